@@ -24,7 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 
 CUDA_SOURCES = ["pkv_attention.cu", "pkv_append.cu", "pkv_static.cu", "pkv_devplan.cu"]
 CXX_SOURCES = ["pkv_api.cpp"]
-HEADERS = ["pkv_internal.h"]
+HEADERS = ["pkv_internal.h", "pkv_device.cuh", "pkv_merge.cuh", "pkv_devplan.cuh", "pkv_slots.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
