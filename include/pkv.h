@@ -263,6 +263,109 @@ int pkv_append(const void *k_new, const void *v_new, void *k_pages, void *v_page
                const int32_t *block_table_d, int32_t *seq_lens_d, pkv_plan_t plan,
                pkv_stream_t stream);
 
+/*
+ * Rotary position embedding of queries and keys ("GPUOS", arXiv 2604.17861,
+ * section 4 operator library: the rotary operator).  A token at position p turns
+ * pair m of a head's first `dim` elements by the angle p * inv_freq[m]:
+ *     (x, y) -> scale * (x cos - y sin, y cos + x sin)
+ * with (x, y) = elements (m, m + dim / 2), or (2m, 2m + 1) if interleaved; the
+ * elements from `dim` on pass unchanged.  The angle is exact to about 2^-32 of a
+ * turn at any position.
+ *   pkv_rotary_init   fills *rotary (a plain value: copy it freely, nothing is
+ *                     owned).  inv_freq_h host double [dim / 2], radians per
+ *                     token, finite; dim a multiple of 16 up to
+ *                     PKV_ROTARY_MAX_DIM; interleaved 0 or 1; scale finite (1
+ *                     for the plain rotation).  PKV_EINVAL otherwise.  No device
+ *                     is touched
+ */
+#define PKV_ROTARY_MAX_DIM 128
+typedef struct {
+    int32_t dim;                             /* rotated elements of a head; 0: no rotation */
+    int32_t interleaved;                     /* pairs (2m, 2m + 1) instead of (m, m + dim / 2) */
+    float scale;                             /* factor on the rotated elements */
+    int32_t reserved;
+    uint64_t step[PKV_ROTARY_MAX_DIM / 2];   /* inv_freq[m] / 2 pi, in 2^-64 turns per token */
+} pkv_rotary;
+int pkv_rotary_init(const double *inv_freq_h, int32_t dim, int32_t interleaved, float scale, pkv_rotary *rotary);
+
+/*
+ * New tokens of the plan's rows: row b's are tokens [cu_tokens_d[b],
+ * cu_tokens_d[b + 1]) of q / k / v, in order, any number from 0 on; without
+ * offsets, token b is row b's one new token.
+ *   k, v         device bf16, token t's heads at k + t * k_stride: [Hkv][D] dense
+ *   q, q_out     device bf16 [Hq][D] per token, or both NULL: the rotated queries
+ *                go to q_out, which may be q itself (with the same stride)
+ *   *_stride     elements from one token to the next, a multiple of 8 and at
+ *                least the token's own size; 0: dense.  A slice of a fused
+ *                projection's output needs no copy
+ *   cu_tokens_d  device int32 [B + 1], ascending from 0 to total_tokens, or NULL
+ *   total_tokens tokens in k / v / q; B without offsets
+ */
+typedef struct {
+    const void *q;
+    void *q_out;
+    const void *k;
+    const void *v;
+    int64_t q_stride, q_out_stride, k_stride, v_stride;
+    const int32_t *cu_tokens_d;
+    int32_t total_tokens;
+} pkv_tokens;
+
+/*
+ * Append every row's new tokens to a bf16 cache, keys rotated by their
+ * positions: token i of row b goes to position seq_lens_d[b] + i (page and slot
+ * as in pkv_append; the pages must be in the table), and new_lens_d[b] receives
+ * seq_lens_d[b] plus the row's tokens.  seq_lens_d is not changed, so a model's
+ * layers can all append with the same lengths, and a repeated call writes the
+ * same cache; new_lens_d must not overlap it.  The rest of the pages is left as
+ * it was.  Values are rotated in fp32 and rounded once to bf16.
+ *   rotary       NULL: no rotation (q is then copied to q_out)
+ *   plan         gives the geometry, the page size and the status word only; it may
+ *                be stale, and calls that share it may overlap
+ * A row is left unchanged (no byte written, new_lens_d[b] = seq_lens_d[b], its
+ * queries not written) and flagged if a page of its new tokens is missing
+ * (PKV_DEV_ROW_FULL: past the table's end, or a negative entry; also a negative
+ * length), lies outside the pool (PKV_DEV_PAGE_OOB), or its offsets do not lie
+ * ascending in [0, total_tokens] (PKV_DEV_PLAN_MISMATCH).  Two rows must not
+ * append to one page.  One kernel on `stream`; needs no memory of its own.
+ * Errors: PKV_EINVAL (null or misaligned pointer, bad stride or count, a rotary
+ * dim above D, another current device than the plan's), PKV_ECUDA.
+ */
+int pkv_append_rotary(const pkv_tokens *tokens, const pkv_rotary *rotary, void *k_pages, void *v_pages,
+                      const int32_t *block_table_d, const int32_t *seq_lens_d, int32_t *new_lens_d, pkv_plan_t plan,
+                      pkv_stream_t stream);
+
+/*
+ * The 8-bit cache.  k_pages / v_pages: e4m3 codes [num_pages][page_size][Hkv][D];
+ * k_scales / v_scales: fp32 [num_pages][page_size / PKV_Q8_BLOCK][Hkv], one scale
+ * for each block of PKV_Q8_BLOCK tokens and KV head; a code stands for code *
+ * scale.
+ *
+ * pkv_append_q8 is pkv_append_rotary into such a cache.  A block's scale becomes
+ * the least power of two s (2^-120 to 2^120) with |x| / s <= 448 for every finite
+ * new value x of the block, but not less than the scale of the tokens of the row
+ * that the block already holds; if it rises, the codes of those tokens are
+ * requantised to it.  A block that the new tokens begin starts afresh, whatever
+ * its page held.  New values are rotated in fp32 and rounded once, to nearest
+ * even, to e4m3; a value that is not finite is stored as NaN.  The slots behind
+ * the row's last token are left as they were.  Rows, flags and errors as in
+ * pkv_append_rotary.
+ *
+ * pkv_decode_q8 is pkv_decode over such a cache (any scales, also ones not made
+ * by pkv_append_q8): the same plan with every route and merge of it, outputs,
+ * flags and errors.  The softmax and all sums are fp32; codes and queries enter
+ * the products exactly.  A slot behind the row's last token may hold anything.
+ * PKV_EUNSUPPORTED for a plan with math = PKV_MATH_FMA; the plan's copy option
+ * has no effect.
+ */
+#define PKV_Q8_BLOCK 16
+int pkv_append_q8(const pkv_tokens *tokens, const pkv_rotary *rotary, void *k_pages, void *v_pages, float *k_scales,
+                  float *v_scales, const int32_t *block_table_d, const int32_t *seq_lens_d, int32_t *new_lens_d,
+                  pkv_plan_t plan, pkv_stream_t stream);
+int pkv_decode_q8(const void *q, const void *k_pages, const void *v_pages, const float *k_scales,
+                  const float *v_scales, const int32_t *block_table_d, const int32_t *seq_lens_d, pkv_plan_t plan,
+                  float *out, float *lse, pkv_stream_t stream);
+
 /* Read and clear the plan's device status word (synchronises `stream`). */
 int pkv_status(pkv_plan_t plan, pkv_stream_t stream, uint32_t *status);
 

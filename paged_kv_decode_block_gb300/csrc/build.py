@@ -22,7 +22,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpkv.so")
 INCLUDE = os.path.join(ROOT, "include")
 
-CUDA_SOURCES = ["pkv_attention.cu", "pkv_append.cu", "pkv_static.cu", "pkv_devplan.cu"]
+CUDA_SOURCES = ["pkv_attention.cu", "pkv_append.cu", "pkv_static.cu", "pkv_devplan.cu",
+                "pkv_append_tokens.cu", "pkv_attention_q8.cu"]
 CXX_SOURCES = ["pkv_api.cpp"]
 HEADERS = ["pkv_internal.h", "pkv_device.cuh", "pkv_merge.cuh", "pkv_devplan.cuh", "pkv_slots.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -27,6 +27,7 @@
 
 #include <algorithm>
 #include <chrono>
+#include <cmath>
 #include <deque>
 #include <mutex>
 #include <new>
@@ -669,7 +670,7 @@ enum class PlanSource {
 int prepare_decode(pkv_plan_t p, const void* q, const void* k_pages, const void* v_pages,
                    const int32_t* block_table_d, const int32_t* seq_lens_d, float* out, float* lse, cudaStream_t s,
                    const DevicePlan* dp, pkv::AttnParams* a_out, int* grid_out, bool* need_merge_out,
-                   PlanSource src = PlanSource::kUpload) {
+                   PlanSource src = PlanSource::kUpload, bool tma_maps = true) {
     if (!q || !k_pages || !v_pages || !block_table_d || !seq_lens_d || !out || !lse) return PKV_EINVAL;
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
         (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(block_table_d) & 3u) ||
@@ -692,12 +693,12 @@ int prepare_decode(pkv_plan_t p, const void* q, const void* k_pages, const void*
         p->upload_recorded = true;
         p->dirty = false;
     }
-    if (k_pages != p->map_k) {
+    if (tma_maps && k_pages != p->map_k) {
         int rc = encode_pool_map(&p->kmap, k_pages, p->g, p->page_size);
         if (rc) return rc;
         p->map_k = k_pages;
     }
-    if (v_pages != p->map_v) {
+    if (tma_maps && v_pages != p->map_v) {
         int rc = encode_pool_map(&p->vmap, v_pages, p->g, p->page_size);
         if (rc) return rc;
         p->map_v = v_pages;
@@ -766,16 +767,26 @@ int prepare_decode(pkv_plan_t p, const void* q, const void* k_pages, const void*
     return PKV_OK;
 }
 
+// The scales of an e4m3 cache (pkv_decode_q8).
+struct Q8Scales {
+    const float* k;
+    const float* v;
+};
+
 int enqueue_decode(pkv_plan_t p, const void* q, const void* k_pages, const void* v_pages,
                    const int32_t* block_table_d, const int32_t* seq_lens_d, float* out, float* lse, cudaStream_t s,
-                   const DevicePlan* dp, PlanSource src = PlanSource::kUpload) {
+                   const DevicePlan* dp, PlanSource src = PlanSource::kUpload, const Q8Scales* q8 = nullptr) {
     if (p->g.batch == 0) return PKV_OK;
     pkv::AttnParams a{};
     int grid = 0;
     bool need_merge = false;
     int rc = prepare_decode(p, q, k_pages, v_pages, block_table_d, seq_lens_d, out, lse, s, dp, &a, &grid, &need_merge,
-                            src);
+                            src, q8 == nullptr);
     if (rc) return rc;
+    auto launch = [&](bool cooperative) {
+        if (q8) return pkv::launch_attention_q8(pkv::AttnQ8Params{a, q8->k, q8->v}, grid, s, cooperative);
+        return pkv::launch_attention(a, p->kmap, p->vmap, grid, s, cooperative);
+    };
 
     if (p->profile) {
         for (auto& ev : p->ev)
@@ -796,13 +807,13 @@ int enqueue_decode(pkv_plan_t p, const void* q, const void* k_pages, const void*
     }
     int n = 0;
     if (grid > 0) {
-        cudaError_t e = pkv::launch_attention(a, p->kmap, p->vmap, grid, s, a.all_merge != 0);
+        cudaError_t e = launch(a.all_merge != 0);
         if (e == cudaErrorCooperativeLaunchTooLarge && a.all_merge) {
             // the device holds fewer CTAs right now than planned for: the last
             // arriving split merges instead (the counters are untouched)
             (void)cudaGetLastError();
             a.all_merge = 0;
-            e = pkv::launch_attention(a, p->kmap, p->vmap, grid, s, false);
+            e = launch(false);
         }
         PKV_CUDA(e);
         ++n;
@@ -888,6 +899,129 @@ int pkv_append(const void* k_new, const void* v_new, void* k_pages, void* v_page
                                 p->g.max_pages_per_seq, p->g.num_pages, &p->ctr->status,
                                 reinterpret_cast<cudaStream_t>(stream)));
     return PKV_OK;
+}
+
+int pkv_rotary_init(const double* inv_freq_h, int32_t dim, int32_t interleaved, float scale, pkv_rotary* rotary) {
+    if (!inv_freq_h || !rotary || dim <= 0 || dim > PKV_ROTARY_MAX_DIM || dim % 16 || (interleaved & ~1) ||
+        !std::isfinite(scale))
+        return PKV_EINVAL;
+    for (int m = 0; m < dim / 2; ++m)
+        if (!std::isfinite(inv_freq_h[m])) return PKV_EINVAL;
+    pkv_rotary r{};
+    r.dim = dim;
+    r.interleaved = interleaved;
+    r.scale = scale;
+    for (int m = 0; m < dim / 2; ++m) {
+        const double turns = inv_freq_h[m] / 6.283185307179586476925;
+        const double part = ldexp(turns - floor(turns), 64);   // in [0, 2^64]; a whole turn is none
+        r.step[m] = part < 18446744073709551616.0 ? static_cast<uint64_t>(part) : 0;
+    }
+    *rotary = r;
+    return PKV_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+int append_tokens(const pkv_tokens* t, const pkv_rotary* rotary, void* k_pages, void* v_pages, float* k_scales,
+                  float* v_scales, const int32_t* block_table_d, const int32_t* seq_lens_d, int32_t* new_lens_d,
+                  pkv_plan_t p, cudaStream_t s) {
+    if (!p || !t) return PKV_EINVAL;
+    const pkv_geom& g = p->g;
+    const int64_t kv_row = static_cast<int64_t>(g.num_kv_heads) * g.head_dim;
+    const int64_t q_row = static_cast<int64_t>(g.num_q_heads) * g.head_dim;
+    if (t->total_tokens < 0 || (!t->cu_tokens_d && t->total_tokens != g.batch)) return PKV_EINVAL;
+    if (rotary && (rotary->dim < 0 || rotary->dim % 16 || rotary->dim > g.head_dim || (rotary->interleaved & ~1)))
+        return PKV_EINVAL;
+    if (g.batch == 0) return t->total_tokens == 0 ? PKV_OK : PKV_EINVAL;
+    if (!k_pages || !v_pages || !block_table_d || !seq_lens_d || !new_lens_d) return PKV_EINVAL;
+    if (t->total_tokens > 0 && (!t->k || !t->v || !t->q != !t->q_out)) return PKV_EINVAL;
+    if (!aligned16(t->q) || !aligned16(t->q_out) || !aligned16(t->k) || !aligned16(t->v) || !aligned16(k_pages) ||
+        !aligned16(v_pages))
+        return PKV_EINVAL;
+    const uintptr_t words = reinterpret_cast<uintptr_t>(t->cu_tokens_d) | reinterpret_cast<uintptr_t>(k_scales) |
+                            reinterpret_cast<uintptr_t>(v_scales) | reinterpret_cast<uintptr_t>(block_table_d) |
+                            reinterpret_cast<uintptr_t>(seq_lens_d) | reinterpret_cast<uintptr_t>(new_lens_d);
+    if (words & 3u) return PKV_EINVAL;
+    if (seq_lens_d < new_lens_d + g.batch && new_lens_d < seq_lens_d + g.batch) return PKV_EINVAL;
+    // strides: 0 is dense; whole 16-byte vectors, and no two tokens in one place
+    pkv::AppendTokensParams a{};
+    const struct {
+        int64_t given, row;
+        int64_t* to;
+    } strides[4] = {{t->q_stride, q_row, &a.q_stride},
+                    {t->q_out_stride, q_row, &a.q_out_stride},
+                    {t->k_stride, kv_row, &a.k_stride},
+                    {t->v_stride, kv_row, &a.v_stride}};
+    for (const auto& x : strides) {
+        if (x.given != 0 && (x.given % 8 || x.given < x.row)) return PKV_EINVAL;
+        *x.to = x.given ? x.given : x.row;
+    }
+    if (t->q && t->q == t->q_out && a.q_stride != a.q_out_stride) return PKV_EINVAL;
+    int dev = -1;
+    PKV_CUDA(cudaGetDevice(&dev));
+    if (dev != p->device) return PKV_EINVAL;
+    a.q = static_cast<const uint16_t*>(t->q);
+    a.q_out = static_cast<uint16_t*>(t->q_out);
+    a.k = static_cast<const uint16_t*>(t->k);
+    a.v = static_cast<const uint16_t*>(t->v);
+    a.cu = t->cu_tokens_d;
+    a.T = t->total_tokens;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.block_table = block_table_d;
+    a.seq_lens = seq_lens_d;
+    a.new_lens = new_lens_d;
+    a.status = &p->ctr->status;
+    a.B = g.batch;
+    a.Hq = g.num_q_heads;
+    a.Hkv = g.num_kv_heads;
+    a.D = g.head_dim;
+    a.page_size = p->page_size;
+    a.max_pages = g.max_pages_per_seq;
+    a.num_pages = g.num_pages;
+    if (rotary) a.rot = *rotary;
+    PKV_CUDA(pkv::launch_append_tokens(a, s));
+    return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkv_append_rotary(const pkv_tokens* tokens, const pkv_rotary* rotary, void* k_pages, void* v_pages,
+                      const int32_t* block_table_d, const int32_t* seq_lens_d, int32_t* new_lens_d, pkv_plan_t p,
+                      pkv_stream_t stream) {
+    NvtxRange range("pkv_append_rotary");
+    return append_tokens(tokens, rotary, k_pages, v_pages, nullptr, nullptr, block_table_d, seq_lens_d, new_lens_d, p,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+int pkv_append_q8(const pkv_tokens* tokens, const pkv_rotary* rotary, void* k_pages, void* v_pages, float* k_scales,
+                  float* v_scales, const int32_t* block_table_d, const int32_t* seq_lens_d, int32_t* new_lens_d,
+                  pkv_plan_t p, pkv_stream_t stream) {
+    NvtxRange range("pkv_append_q8");
+    if (!k_scales || !v_scales) return PKV_EINVAL;
+    return append_tokens(tokens, rotary, k_pages, v_pages, k_scales, v_scales, block_table_d, seq_lens_d, new_lens_d, p,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+int pkv_decode_q8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                  const float* v_scales, const int32_t* block_table_d, const int32_t* seq_lens_d, pkv_plan_t p,
+                  float* out, float* lse, pkv_stream_t stream) {
+    NvtxRange range("pkv_decode_q8");
+    if (!p) return PKV_EINVAL;
+    if (p->opts.math == PKV_MATH_FMA) return PKV_EUNSUPPORTED;
+    if (p->g.batch == 0) return PKV_OK;
+    if (!k_scales || !v_scales || (reinterpret_cast<uintptr_t>(k_scales) & 3u) ||
+        (reinterpret_cast<uintptr_t>(v_scales) & 3u))
+        return PKV_EINVAL;
+    const Q8Scales scales{k_scales, v_scales};
+    return enqueue_decode(p, q, k_pages, v_pages, block_table_d, seq_lens_d, out, lse,
+                          reinterpret_cast<cudaStream_t>(stream), nullptr, PlanSource::kUpload, &scales);
 }
 
 int pkv_status(pkv_plan_t p, pkv_stream_t stream, uint32_t* status) {

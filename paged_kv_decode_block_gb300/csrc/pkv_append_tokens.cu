@@ -1,0 +1,374 @@
+// pkv_append_tokens.cu -- ragged append of rotated keys and values to a paged
+// cache, in bf16 or quantised to e4m3 with one scale per 16-token block and KV
+// head.
+//
+// Layout and role as in pkv_append.cu ("PersistentKV: Page-Aware Decode
+// Scheduling for Long-Context LLM Serving on Commodity GPUs", gist.science
+// summary, Methodology section 1 "Layout"; the KV-cache update and rotary
+// operators of "GPUOS", arXiv 2604.17861, section 4).
+//
+// Mathematics.  Token i of row b has position p = seq_lens[b] + i.  Of its first
+// `dim` elements the pair (x, y) number m turns by the angle p * inv_freq[m]:
+//     (x, y) -> scale * (x cos - y sin, y cos + x sin).
+// The angle is reduced in integers: step[m] is inv_freq[m] / 2 pi in units of
+// 2^-64 turns, so p * step[m] mod 2^64 is the phase, exact but for step's own
+// rounding however far the position; its nearest quarter turn is taken off in
+// integers too, and sincospif sees at most an eighth of a turn.
+// An e4m3 block stores x / s with s the least power of two that brings the
+// largest finite |x| of the block's new tokens to at most 448, and at least the
+// scale of the tokens the block already holds.  e4m3 keeps four significant
+// bits at any scale, so a power of two costs no precision, and when a later
+// token raises the scale the older codes move to it exactly, save those that
+// fall below e4m3's normal range (2^-6 of the new scale), which round again.
+//
+// What bounds it: HBM, (2 * Hq + 4 * Hkv) * D * 2 bytes per token in bf16 (Hkv * D
+// * 2 less for e4m3).  One CTA per (16-token block, KV head): the block's scale
+// needs no other CTA, a thread owns 16 elements of one token of every head of
+// the group, so its eight sines and cosines serve the K head and the G query
+// heads, and every access is 16 bytes (8 for e4m3 codes of half pairs).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace {
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Two floats to two e4m3 codes (a in the low byte), round to nearest even.
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+__device__ __forceinline__ float2 unpack_e4m3(uint32_t two) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// |x| if x is finite, else 0: what the block's scale is taken from.
+__device__ __forceinline__ uint32_t finite_magnitude(float x) {
+    const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
+    return u < 0x7f800000u ? u : 0u;
+}
+
+// The least power of two s in [2^-120, 2^120] with amax / s <= 448 = 0.875 * 2^9.
+__device__ __forceinline__ float block_scale(uint32_t amax_bits) {
+    // amax = 1.m * 2^e: 448 = 1.75 * 2^8, so s = 2^(e - 8), or 2^(e - 7) if 1.m > 1.75
+    int e = static_cast<int>(amax_bits >> 23) - 127 - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    e = max(-120, min(120, e));   // (zero and subnormal maxima end at -120)
+    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// What a row asks for, checked by the whole CTA before any byte of it is written.
+struct RowWork {
+    int tok0;      // its first token in k / v / q
+    int n;         // new tokens
+    int pos0;      // position of the first one
+    uint32_t bad;  // status bits of a row that cannot take its tokens
+};
+
+template <int kThreadsT>
+__device__ RowWork row_work(const AppendTokensParams& p, int b) {
+    RowWork w;
+    w.pos0 = p.seq_lens[b];
+    w.tok0 = b;
+    w.n = 1;
+    uint32_t bad = 0;
+    if (p.cu) {
+        const int end = p.cu[b + 1];
+        w.tok0 = p.cu[b];
+        if (w.tok0 < 0 || end < w.tok0 || end > p.T) {   // offsets that do not describe T tokens
+            bad = PKV_DEV_PLAN_MISMATCH;
+            w.n = 0;
+        } else {
+            w.n = end - w.tok0;
+        }
+    }
+    if (w.n > 0) {
+        if (w.pos0 < 0 || static_cast<int64_t>(w.pos0) + w.n > static_cast<int64_t>(p.max_pages) * p.page_size) {
+            bad = PKV_DEV_ROW_FULL;
+        } else {
+            const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
+            const int last = (w.pos0 + w.n - 1) / p.page_size;
+            for (int i = w.pos0 / p.page_size + static_cast<int>(threadIdx.x); i <= last; i += kThreadsT) {
+                const int page = row[i];
+                if (page < 0)
+                    bad |= PKV_DEV_ROW_FULL;
+                else if (page >= p.num_pages)
+                    bad |= PKV_DEV_PAGE_OOB;
+            }
+        }
+    }
+    w.bad = (__syncthreads_or(bad & PKV_DEV_ROW_FULL) ? PKV_DEV_ROW_FULL : 0u) |
+            (__syncthreads_or(bad & PKV_DEV_PAGE_OOB) ? PKV_DEV_PAGE_OOB : 0u) |
+            (__syncthreads_or(bad & PKV_DEV_PLAN_MISMATCH) ? PKV_DEV_PLAN_MISMATCH : 0u);
+    return w;
+}
+
+// A thread's 16 elements of one head of one token: two runs of eight, at
+// elements e0 and e1 of the head.
+struct Slice {
+    uint4 a, b;
+};
+
+__device__ __forceinline__ Slice load_slice(const uint16_t* head, int e0, int e1) {
+    Slice s;
+    s.a = *reinterpret_cast<const uint4*>(head + e0);
+    s.b = *reinterpret_cast<const uint4*>(head + e1);
+    return s;
+}
+
+// Turn a slice by the thread's eight angles (cos and sin already scaled).
+// Half pairs: x runs through a, y through b.  Neighbouring pairs: (x, y) are
+// (0, 1), (2, 3), ... of a, then of b.  A slice past the rotated elements is
+// only widened.
+__device__ __forceinline__ void turn(const Slice& s, bool rotate, bool pairs, const float (&c)[8], const float (&sn)[8],
+                                     float (&x)[16]) {
+    float a[8], b[8];
+    unpack_bf16x8(s.a, a);
+    unpack_bf16x8(s.b, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[i] = a[i];
+        x[8 + i] = b[i];
+    }
+    if (!rotate) return;
+    if (pairs) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u = x[2 * i], w = x[2 * i + 1];
+            x[2 * i] = fmaf(u, c[i], -w * sn[i]);
+            x[2 * i + 1] = fmaf(w, c[i], u * sn[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u = x[i], w = x[8 + i];
+            x[i] = fmaf(u, c[i], -w * sn[i]);
+            x[8 + i] = fmaf(w, c[i], u * sn[i]);
+        }
+    }
+}
+
+__device__ __forceinline__ void store_bf16(uint16_t* head, int e0, int e1, const float (&x)[16]) {
+    *reinterpret_cast<uint4*>(head + e0) =
+        make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    *reinterpret_cast<uint4*>(head + e1) =
+        make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]), pack_bf16(x[12], x[13]), pack_bf16(x[14], x[15]));
+}
+
+// Eight values to eight codes.  A value that is not finite becomes NaN (x * 0
+// is NaN for it and +-0 otherwise), not the largest code.
+__device__ __forceinline__ uint2 codes8(const float* x, float inv) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], 0.f, x[i] * inv);
+    return make_uint2(pack_e4m3(y[0], y[1]) | pack_e4m3(y[2], y[3]) << 16,
+                      pack_e4m3(y[4], y[5]) | pack_e4m3(y[6], y[7]) << 16);
+}
+
+// Move 16 codes from one scale to a larger one.
+__device__ __forceinline__ uint32_t requantise4(uint32_t w, float ratio) {
+    const float2 lo = unpack_e4m3(w & 0xffffu), hi = unpack_e4m3(w >> 16);
+    return pack_e4m3(lo.x * ratio, lo.y * ratio) | pack_e4m3(hi.x * ratio, hi.y * ratio) << 16;
+}
+
+__device__ __forceinline__ void requantise16(uint8_t* codes, float ratio) {
+    uint4 w = *reinterpret_cast<const uint4*>(codes);
+    w = make_uint4(requantise4(w.x, ratio), requantise4(w.y, ratio), requantise4(w.z, ratio), requantise4(w.w, ratio));
+    *reinterpret_cast<uint4*>(codes) = w;
+}
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant__ AppendTokensParams p) {
+    constexpr int kTpt = D / 16;               // threads per token
+    constexpr int kCta = kBlockRows * kTpt;    // = D
+    __shared__ int s_row;
+    __shared__ uint32_t s_max[2][kCta / 32];
+    grid_dependency_wait();
+    launch_dependents();
+
+    const int piece = blockIdx.x, kvh = blockIdx.y;
+    // The row of this piece.  With offsets, row r owns the pieces from
+    // floor(cu[r] / 16) + 2 r on: at least as many as 16-token blocks that
+    // cu[r + 1] - cu[r] tokens can touch from any start inside a block.
+    int b = piece, first = piece;
+    if (p.cu) {
+        if (threadIdx.x == 0) s_row = -1;
+        __syncthreads();
+        for (int r = threadIdx.x; r < p.B; r += kCta) {
+            const int64_t lo = p.cu[r] / kBlockRows + 2ll * r, hi = p.cu[r + 1] / kBlockRows + 2ll * (r + 1);
+            if (lo <= piece && piece < hi) s_row = r;
+        }
+        __syncthreads();
+        b = s_row;
+        if (b >= 0) first = p.cu[b] / kBlockRows + 2 * b;
+    }
+    RowWork w{};
+    if (b >= 0) w = row_work<kCta>(p, b);
+
+    // the lengths after: one CTA per row, whichever piece it holds
+    if (kvh == 0 && piece < p.B) {
+        const RowWork o = p.cu ? row_work<kCta>(p, piece) : w;
+        if (threadIdx.x == 0) {
+            p.new_lens[piece] = p.seq_lens[piece] + (o.bad ? 0 : o.n);
+            if (o.bad) atomicOr(p.status, o.bad);
+        }
+    }
+    if (b < 0 || w.bad || w.n == 0) return;
+
+    const int blk = w.pos0 / kBlockRows + (piece - first);       // 16-token block of the row
+    const int blk0 = blk * kBlockRows;
+    const int lo = max(blk0, w.pos0), hi = min(blk0 + kBlockRows, w.pos0 + w.n);
+    if (lo >= hi) return;
+    const int slot = static_cast<int>(threadIdx.x) / kTpt, j = static_cast<int>(threadIdx.x) % kTpt;
+    const int pos = blk0 + slot;
+    const bool live = pos >= lo && pos < hi;
+    const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + blk0 / p.page_size];
+    const size_t prow0 = static_cast<size_t>(page) * p.page_size + blk0 % p.page_size;   // token row of the block
+    const int64_t tok = static_cast<int64_t>(w.tok0) + (pos - w.pos0);
+
+    // the thread's elements of a head
+    const int dim = p.rot.dim;
+    const bool rotate = j < dim / 16, pairs = p.rot.interleaved != 0;
+    int e0, e1;
+    if (rotate && !pairs) {
+        e0 = 8 * j;
+        e1 = dim / 2 + 8 * j;
+    } else {   // sixteen neighbours: pairs, or past the rotated elements
+        e0 = 16 * j;
+        e1 = e0 + 8;
+    }
+
+    Slice ks{}, vs{};
+    if (live) {
+        ks = load_slice(p.k + tok * p.k_stride + static_cast<int64_t>(kvh) * D, e0, e1);
+        vs = load_slice(p.v + tok * p.v_stride + static_cast<int64_t>(kvh) * D, e0, e1);
+    }
+    float c[8], sn[8];
+    if (live && rotate) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t turn32 = static_cast<uint32_t>((p.rot.step[8 * j + i] * static_cast<uint64_t>(pos)) >> 32);
+            const uint32_t quarter = (turn32 + 0x20000000u) >> 30;                       // nearest quarter turn
+            const int rest = static_cast<int>(turn32 - (quarter << 30));                 // in [-2^29, 2^29)
+            float s0, c0;
+            sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &s0, &c0);      // rest * 2^-31 half turns
+            s0 *= p.rot.scale;
+            c0 *= p.rot.scale;
+            const bool odd = quarter & 1u;
+            const float cc = odd ? s0 : c0, ss = odd ? c0 : s0;
+            c[i] = (quarter == 1u || quarter == 2u) ? -cc : cc;
+            sn[i] = (quarter & 2u) ? -ss : ss;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = sn[i] = 0.f;
+    }
+
+    float x[16];
+    turn(ks, rotate, pairs, c, sn, x);
+    const size_t prow = prow0 + slot;
+    const size_t head_off = (prow * p.Hkv + kvh) * D;
+    if constexpr (!Q8) {
+        if (live) {
+            store_bf16(static_cast<uint16_t*>(p.k_pages) + head_off, e0, e1, x);
+            uint16_t* vh = static_cast<uint16_t*>(p.v_pages) + head_off;
+            *reinterpret_cast<uint4*>(vh + e0) = vs.a;
+            *reinterpret_cast<uint4*>(vh + e1) = vs.b;
+        }
+    } else {
+        float y[16];
+        turn(vs, false, false, c, sn, y);
+        uint32_t km = 0, vm = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {   // (a slot without a new token holds zeros)
+            km = max(km, finite_magnitude(x[i]));
+            vm = max(vm, finite_magnitude(y[i]));
+        }
+        km = __reduce_max_sync(kFull, km);
+        vm = __reduce_max_sync(kFull, vm);
+        if (threadIdx.x % 32 == 0) {
+            s_max[0][threadIdx.x / 32] = km;
+            s_max[1][threadIdx.x / 32] = vm;
+        }
+        const size_t sidx = prow0 / kBlockRows * p.Hkv + kvh;
+        const bool held = lo > blk0;   // the block holds tokens of the row already
+        const float k_old = held ? p.k_scales[sidx] : 0.f, v_old = held ? p.v_scales[sidx] : 0.f;
+        __syncthreads();   // the maxima; and every thread has read the old scales
+#pragma unroll
+        for (int i = 0; i < kCta / 32; ++i) {
+            km = max(km, s_max[0][i]);
+            vm = max(vm, s_max[1][i]);
+        }
+        const float k_new = fmaxf(block_scale(km), k_old), v_new = fmaxf(block_scale(vm), v_old);
+        uint8_t* kp = static_cast<uint8_t*>(p.k_pages) + head_off;
+        uint8_t* vp = static_cast<uint8_t*>(p.v_pages) + head_off;
+        if (live) {
+            const float ki = 1.f / k_new, vi = 1.f / v_new;
+            *reinterpret_cast<uint2*>(kp + e0) = codes8(x, ki);
+            *reinterpret_cast<uint2*>(kp + e1) = codes8(x + 8, ki);
+            *reinterpret_cast<uint2*>(vp + e0) = codes8(y, vi);
+            *reinterpret_cast<uint2*>(vp + e1) = codes8(y + 8, vi);
+        } else if (pos < lo) {   // an older token of the block
+            if (k_new != k_old) requantise16(kp + 16 * j, k_old / k_new);
+            if (v_new != v_old) requantise16(vp + 16 * j, v_old / v_new);
+        }
+        if (threadIdx.x == 0) {
+            p.k_scales[sidx] = k_new;
+            p.v_scales[sidx] = v_new;
+        }
+    }
+
+    if (p.q && live) {
+        const int G = p.Hq / p.Hkv;
+        const uint16_t* qh = p.q + tok * p.q_stride + static_cast<int64_t>(kvh) * G * D;
+        uint16_t* oh = p.q_out + tok * p.q_out_stride + static_cast<int64_t>(kvh) * G * D;
+        for (int g = 0; g < G; ++g) {   // in place is fine: a thread writes only what it has read
+            const Slice qs = load_slice(qh + g * D, e0, e1);
+            float z[16];
+            turn(qs, rotate, pairs, c, sn, z);
+            store_bf16(oh + g * D, e0, e1, z);
+        }
+    }
+}
+
+template <int D, bool Q8>
+cudaError_t launch_t(const AppendTokensParams& p, cudaStream_t stream) {
+    const int64_t pieces = p.cu ? static_cast<int64_t>(p.T) / kBlockRows + 2ll * p.B : p.B;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(pieces), static_cast<unsigned>(p.Hkv));
+    cfg.blockDim = dim3(D);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, append_tokens_kernel<D, Q8>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_append_tokens(const AppendTokensParams& p, cudaStream_t stream) {
+    const bool q8 = p.k_scales != nullptr;
+    switch (p.D) {
+        case 64: return q8 ? launch_t<64, true>(p, stream) : launch_t<64, false>(p, stream);
+        case 128: return q8 ? launch_t<128, true>(p, stream) : launch_t<128, false>(p, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace pkv

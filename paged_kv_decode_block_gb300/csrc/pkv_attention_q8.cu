@@ -1,0 +1,614 @@
+// pkv_attention_q8.cu -- paged GQA decode attention over an e4m3 cache with one
+// scale per 16-token block and KV head.
+//
+// The method, the tiles and the merges are those of pkv_attention.cu
+// ("PersistentKV: Page-Aware Decode Scheduling for Long-Context LLM Serving on
+// Commodity GPUs", gist.science summary, Methodology section 1); the plan is
+// the same object, and every route and merge of it runs.
+//
+// Mathematics.  With codes k, v and block scales ks, vs of token t's block B:
+//     s_t = (ks_B * log2(e) / sqrt(D)) * <q, k_t>,   out = sum_t 2^(s_t - m) vs_B v_t / sum_t 2^(s_t - m).
+// e4m3 codes are exact in f16, so both products run on f16 tensor cores
+// (mma.m16n8k16, fp32 accumulation).  q (bf16) is scaled per head by the power
+// of two that brings its largest element to [1, 2), so it is exact in f16 down to
+// 2^-14 of that element and rounded by at most 2^-25 of it below.  A weight
+// 2^(s - m) * vs_B / r (r: the largest block scale so far, rounded up to a power of
+// two) is split into f16 hi + lo, about 22 bits; rows 0-7 of the product's A
+// operand hold the group's hi parts and rows 8-15 the lo parts.  Statistics and
+// sums are fp32.  m follows the running maximum lazily: weights may grow to 2^14
+// (within f16) before the accumulators move to a new reference that puts the
+// block's maximum at 2^6.
+//
+// What bounds it: HBM, 2 * D + 8 / 16 bytes per token and KV head against 4 * G * D
+// flops (G flop per byte).  Layout of the work:
+//   * one CTA per tile, eight warps; warp w owns blocks w, w + 8, ... of the tile
+//     with a private softmax state, so the loop has no barrier and no shared state;
+//   * contraction indices may be permuted freely, so each thread fetches whole
+//     16-byte pieces: of K, the pieces of the two token rows whose B fragments
+//     it holds; of V, the same 16 dimensions of its four tokens.  What a thread
+//     copies (cp.async into a private ring) only that thread reads, so a
+//     per-thread wait on its own copies is the pipeline's only synchronisation;
+//   * S = Q K^T comes out in the layout in which P V needs P: no exchange of P;
+//   * the block table and the scales are fetched 32 blocks at a time, one per lane.
+// Bad page ids set PKV_DEV_PAGE_OOB and poison the tile; page 0 is read in place
+// of such a page.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+#include "pkv_merge.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kWarps = kThreads / 32;
+constexpr float kHeadroom = 6.f;     // a new reference puts the block's largest weight at 2^6
+constexpr float kGrowth = 14.f;      // and holds until a weight would pass 2^14
+
+template <int D>
+struct Q8Cfg {
+    static constexpr int kBlockBytes = 2 * kBlockRows * D;   // K and V codes of one block
+    static constexpr int kStages = D == 128 ? 3 : 6;         // 12 KB in flight per warp, 96 KB per CTA
+    static constexpr int kKPieces = D / 32;                  // 16-byte pieces of K per thread and block
+    static constexpr int kVBytes = D / 8;                    // bytes of one token's V per thread
+    static_assert(D == 64 || D == 128, "head_dim");
+};
+
+template <int D, int G>
+struct Q8Smem {
+    static constexpr int kRing = Q8Cfg<D>::kStages * Q8Cfg<D>::kBlockBytes;   // one warp's ring
+    static constexpr int kScratchBytes = kWarps * kRing;
+    static constexpr int kAccRow = D + 4;   // floats of one head's partial (padded against bank conflicts)
+    __device__ uint8_t* scratch() { return &ring[0][0]; }
+    alignas(128) uint8_t ring[kWarps][kRing];   // staged blocks; at the tile's end each warp's partial
+    float m[kWarps][G], l[kWarps][G];
+    int poisoned[kWarps];
+    float merge_m[G], merge_inv[G];
+    int merge_nan_h[G];
+    int abort;
+    int tile_slot[2];
+    int tile_fin, tile_splits, tile_base;
+    uint64_t tr[kTraceWords];
+    static_assert(G * kAccRow * 4 <= kRing, "a warp's partial fits its ring");
+};
+
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+
+// Four e4m3 codes to two f16x2: bytes 0, 1 and bytes 2, 3.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+// D (16x8 fp32) += A (16x16 f16, row-major) * B (16x8 f16, column-major)
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float2 unpack_half(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+
+// The least power of two not below x > 0 (x a finite fp32; the exponent saturates at 2^126).
+__device__ __forceinline__ float power_of_two_above(float x) {
+    const uint32_t u = __float_as_uint(x);
+    int e = static_cast<int>(u >> 23) + ((u & 0x7fffffu) ? 1 : 0);
+    e = max(1, min(253, e));
+    return __uint_as_float(static_cast<uint32_t>(e) << 23);
+}
+
+// One tile: every warp reduces its blocks, then the eight states are combined
+// and written (to out / lse, or to the workspace for a split).
+// Fragment coordinates: g = lane / 4 (a head in A and C, a token or a dimension
+// column in B), t = lane % 4.
+template <int D, int G>
+__device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork tw) {
+    using C = Q8Cfg<D>;
+    const AttnParams& p = qp.attn;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int g = lane >> 2, t = lane & 3;
+    if (tw.lazy) tile_finish(p, tw);
+    if (threadIdx.x == 0) {
+        sm.tile_fin = tw.finalize;
+        sm.tile_splits = tw.splits;
+        sm.tile_base = tw.slot - tw.split;
+    }
+    const int ntok = tw.t1 > tw.t0 ? tw.t1 - tw.t0 : 0;
+    const int nblk = (ntok + kBlockRows - 1) / kBlockRows;
+    const int mine = nblk > warp ? (nblk - warp + kWarps - 1) / kWarps : 0;   // this warp's blocks: warp + 8 i
+    int poisoned = tw.poisoned;
+
+    const uint8_t* kpool = reinterpret_cast<const uint8_t*>(p.k_pages) + static_cast<size_t>(tw.kvh) * D;
+    const uint8_t* vpool = reinterpret_cast<const uint8_t*>(p.v_pages) + static_cast<size_t>(tw.kvh) * D;
+    const size_t pitch = static_cast<size_t>(p.Hkv) * D;   // bytes between tokens
+    const uint32_t k_off = static_cast<uint32_t>(g * pitch + t * 16);
+    const uint32_t v_off = static_cast<uint32_t>(2 * t * pitch + g * C::kVBytes);
+    const uint32_t ring = smem_addr(sm.ring[warp]);
+    const uint64_t policy = l2_evict_first_policy();
+    const int32_t* bt_row = p.block_table + static_cast<size_t>(tw.b) * p.max_pages;
+
+    // 32 of the warp's blocks at a time: lane i holds block i's token row in the
+    // pool and its scales.  The copies run ahead of the arithmetic, so the scales
+    // of the batch being copied (k/v_next) and of the one being reduced differ for
+    // a few blocks; the table entries are read one batch further ahead.
+    int row_i = 0, entry = 0;
+    float k_next = 0.f, v_next = 0.f, k_now = 0.f, v_now = 0.f;
+    auto block_token = [&](int i) { return tw.t0 + (warp + kWarps * i) * kBlockRows; };
+    auto read_entry = [&](int i0) {
+        if (i0 + lane < mine) entry = __ldg(bt_row + block_token(i0 + lane) / p.page_size);
+    };
+    auto fetch_batch = [&](int i0) {
+        if (i0 + lane < mine) {
+            int page = entry;
+            if (page < 0 || page >= p.num_pages) {
+                atomicOr(&p.ctr->status, static_cast<uint32_t>(PKV_DEV_PAGE_OOB));
+                poisoned = 1;
+                page = 0;
+            }
+            row_i = page * p.page_size + block_token(i0 + lane) % p.page_size;
+            const size_t s = static_cast<size_t>(row_i / kBlockRows) * p.Hkv + tw.kvh;
+            k_next = __ldg(qp.k_scales + s);
+            v_next = __ldg(qp.v_scales + s);
+        }
+        read_entry(i0 + 32);
+    };
+    auto issue = [&](int i, int stage) {   // block i of the current batch into the thread's slots of `stage`
+        const size_t off = static_cast<size_t>(__shfl_sync(kFull, row_i, i & 31)) * pitch;
+        const uint32_t dst = ring + stage * C::kBlockBytes + lane * 16;
+#pragma unroll
+        for (int x = 0; x < C::kKPieces; ++x)   // rows g, g + 8; pieces t, t + 4
+            cp_async16(dst + x * 512, kpool + off + k_off + (x & 1) * 8 * pitch + (x >> 1) * 64, policy);
+        const uint32_t vdst = ring + stage * C::kBlockBytes + C::kKPieces * 512 + lane * C::kVBytes;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {   // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+            const uint8_t* src = vpool + off + v_off + ((x & 1) + (x >> 1) * 8) * pitch;
+            if constexpr (D == 128)
+                cp_async16(vdst + x * 512, src, policy);
+            else
+                cp_async8(vdst + x * 256, src);
+        }
+    };
+
+    // the ring's first blocks, then q while they are in flight
+    read_entry(0);
+    fetch_batch(0);
+#pragma unroll
+    for (int s = 0; s < C::kStages; ++s) {
+        if (s < mine) issue(s, s);
+        cp_async_commit();
+    }
+    // A fragments of Q: row g is query head g, k-step j holds the elements of the
+    // thread's j-th 4-byte word of a K row (the same permutation on both sides)
+    uint32_t qa[D / 16][2];
+    float qscale;   // what the dot products of head g are multiplied by, before ks
+    {
+        uint4 raw[D / 32];
+        const uint16_t* qh = p.q + (static_cast<size_t>(tw.b) * p.Hq + tw.kvh * G + (g < G ? g : 0)) * D + t * 16;
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x)   // elements 16 t .. 16 t + 15, then 64 on
+            raw[x] = g < G ? __ldg(reinterpret_cast<const uint4*>(qh + (x >> 1) * 64 + (x & 1) * 8)) : make_uint4(0, 0, 0, 0);
+        uint32_t big = 0;
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+            const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) big = max(big, max((w[i] & 0x7fffu) << 16, w[i] & 0x7fff0000u));
+        }
+        big = max(big, __shfl_xor_sync(kFull, big, 1));
+        big = max(big, __shfl_xor_sync(kFull, big, 2));
+        const int e = max(-126, min(126, static_cast<int>(big >> 23) - 127));
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        qscale = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+            float f[8];
+            unpack_bf16x8(raw[x], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] *= down;
+            qa[2 * x][0] = pack_half(f[0], f[1]);
+            qa[2 * x][1] = pack_half(f[2], f[3]);
+            qa[2 * x + 1][0] = pack_half(f[4], f[5]);
+            qa[2 * x + 1][1] = pack_half(f[6], f[7]);
+        }
+    }
+
+    float m = -INFINITY, l = 0.f;      // head g: reference, and this lane's share of the sum
+    float vref = 1.1754944e-38f;       // power of two not below any block's V scale so far
+    float vinv = 8.5070592e37f;
+    float o[D / 8][4];                 // head g: hi parts in [0], [1], lo parts in [2], [3]
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+
+    int stage = 0;
+    for (int i = 0; i < mine; ++i) {
+        cp_async_wait<C::kStages - 1>();
+        if (i == 0 && p.trace && threadIdx.x == 0 && sm.tr[kTrFirstBlock] == 0) sm.tr[kTrFirstBlock] = globaltimer_ns();
+        const int valid = ntok - (warp + kWarps * i) * kBlockRows;   // tokens of this block (16 or more: all)
+        if ((i & 31) == 0) {
+            k_now = k_next;
+            v_now = v_next;
+        }
+        const float ks = __shfl_sync(kFull, k_now, i & 31), vs = __shfl_sync(kFull, v_now, i & 31);
+        const uint32_t src = ring + stage * C::kBlockBytes + lane * 16;
+
+        // S = Q K^T: tokens 0-7 and 8-15 are two column tiles
+        float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < C::kKPieces; x += 2) {
+            const uint4 ka = lds128(src + x * 512), kb = lds128(src + (x + 1) * 512);
+            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                uint32_t b0, b1;
+                widen4(wa[y], b0, b1);
+                mma_f16(s0, qa[2 * x + y][0], 0u, qa[2 * x + y][1], 0u, b0, b1);
+                widen4(wb[y], b0, b1);
+                mma_f16(s1, qa[2 * x + y][0], 0u, qa[2 * x + y][1], 0u, b0, b1);
+            }
+        }
+        const float sc = ks * qscale;
+        float z[4] = {s0[0] * sc, s0[1] * sc, s1[0] * sc, s1[1] * sc};   // tokens 2t, 2t+1, 2t+8, 2t+9
+        if (valid < kBlockRows) {
+            if (2 * t >= valid) z[0] = -INFINITY;
+            if (2 * t + 1 >= valid) z[1] = -INFINITY;
+            if (2 * t + 8 >= valid) z[2] = -INFINITY;
+            if (2 * t + 9 >= valid) z[3] = -INFINITY;
+        }
+
+        // the reference moves when a weight would pass 2^14, or a block's scale passes r
+        float bm = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+        bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 1));
+        bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 2));
+        const bool grow = bm > m + kGrowth;   // (m = -inf at first)
+        if (__any_sync(kFull, grow) || fabsf(vs) > vref) {
+            const float mn = grow ? bm - kHeadroom : m;
+            float f = m == mn ? 1.f : exp2f(m - mn);   // from m = -inf: 0
+            l *= f;
+            m = mn;
+            if (fabsf(vs) > vref) {
+                const float vn = power_of_two_above(fabsf(vs));
+                f *= vref / vn;
+                vref = vn;
+                vinv = 1.f / vn;
+            }
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[n][k] *= f;
+        }
+        const float vw = vs * vinv;
+        float w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float e = exp2f(z[k] - m);   // masked: 0
+            l += e;
+            w[k] = e * vw;
+        }
+        const uint32_t h0 = pack_half(w[0], w[1]), h1 = pack_half(w[2], w[3]);
+        const float2 u0 = unpack_half(h0), u1 = unpack_half(h1);
+        const uint32_t l0 = pack_half(w[0] - u0.x, w[1] - u0.y), l1 = pack_half(w[2] - u1.x, w[3] - u1.y);
+
+        // O += P V: column tile n is dimension (D / 8) * g + n of every g
+        const uint32_t vsrc = ring + stage * C::kBlockBytes + C::kKPieces * 512 + lane * C::kVBytes;
+        uint32_t vw_[4][C::kVBytes / 4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if constexpr (D == 128) {
+                const uint4 r = lds128(vsrc + x * 512);
+                vw_[x][0] = r.x;
+                vw_[x][1] = r.y;
+                vw_[x][2] = r.z;
+                vw_[x][3] = r.w;
+            } else {
+                const uint2 r = lds64(vsrc + x * 256);
+                vw_[x][0] = r.x;
+                vw_[x][1] = r.y;
+            }
+            // slots past the row's end may hold anything, NaN codes too (0 * NaN = NaN)
+            if (valid < kBlockRows && 2 * t + (x & 1) + (x >> 1) * 8 >= valid)
+#pragma unroll
+                for (int y = 0; y < C::kVBytes / 4; ++y) vw_[x][y] = 0u;
+        }
+#pragma unroll
+        for (int y = 0; y < C::kVBytes / 4; ++y) {
+            // (token pair, dimension) order: two tokens' bytes of one dimension side by side
+            const uint32_t a01 = __byte_perm(vw_[0][y], vw_[1][y], 0x5140), a23 = __byte_perm(vw_[0][y], vw_[1][y], 0x7362);
+            const uint32_t b01 = __byte_perm(vw_[2][y], vw_[3][y], 0x5140), b23 = __byte_perm(vw_[2][y], vw_[3][y], 0x7362);
+            uint32_t f0, f1, f2, f3, q0, q1, q2, q3;
+            widen4(a01, f0, f1);
+            widen4(a23, f2, f3);
+            widen4(b01, q0, q1);
+            widen4(b23, q2, q3);
+            mma_f16(o[4 * y + 0], h0, l0, h1, l1, f0, q0);
+            mma_f16(o[4 * y + 1], h0, l0, h1, l1, f1, q1);
+            mma_f16(o[4 * y + 2], h0, l0, h1, l1, f2, q2);
+            mma_f16(o[4 * y + 3], h0, l0, h1, l1, f3, q3);
+        }
+
+        // the slot is read (by this thread alone): its next block
+        const int next = i + C::kStages;
+        if (next < mine) {
+            if ((next & 31) == 0) fetch_batch(next);
+            issue(next, stage);
+        }
+        cp_async_commit();
+        stage = stage + 1 == C::kStages ? 0 : stage + 1;
+    }
+    trace_stamp(sm, p, kTrStreamEnd);
+
+    // publish the warp's state: column 2t (+ 1) of tile n is dimension
+    // (D / 8) * (2t (+ 1)) + n, so a lane holds two runs of D / 8 dimensions
+    l += __shfl_xor_sync(kFull, l, 1);
+    l += __shfl_xor_sync(kFull, l, 2);
+    poisoned = __any_sync(kFull, poisoned) ? 1 : 0;
+    __syncwarp();   // every lane has read its slots: the ring takes the partial
+    if (g < G) {
+        float* acc = reinterpret_cast<float*>(sm.ring[warp]) + g * Q8Smem<D, G>::kAccRow;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int n = 0; n < D / 8; n += 4)
+                *reinterpret_cast<float4*>(acc + (D / 8) * (2 * t + half) + n) =
+                    make_float4((o[n][half] + o[n][2 + half]) * vref, (o[n + 1][half] + o[n + 1][2 + half]) * vref,
+                                (o[n + 2][half] + o[n + 2][2 + half]) * vref, (o[n + 3][half] + o[n + 3][2 + half]) * vref);
+        if (t == 0) {
+            sm.m[warp][g] = m;
+            sm.l[warp][g] = l;
+        }
+    }
+    if (lane == 0) sm.poisoned[warp] = poisoned;
+    __syncthreads();
+
+    // exact combine of the eight states, one float4 (head h, d .. d+3) per thread and pass
+    bool any_poison = false;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) any_poison |= sm.poisoned[w] != 0;
+    for (int i = threadIdx.x; i < G * D / 4; i += kThreads) {
+        const int h = i / (D / 4), d = (i % (D / 4)) * 4;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][h]);
+        float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+        float lse2 = -INFINITY;
+        if (nblk > 0) {
+            float lsum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float mw = sm.m[w][h];
+                const float f = mw == -INFINITY && sm.l[w][h] == 0.f ? 0.f : exp2f(mw - M);   // idle warp: 0
+                lsum = fmaf(sm.l[w][h], f, lsum);
+                const float4 a = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w]) +
+                                                                  h * Q8Smem<D, G>::kAccRow + d);
+                r.x = fmaf(a.x, f, r.x);
+                r.y = fmaf(a.y, f, r.y);
+                r.z = fmaf(a.z, f, r.z);
+                r.w = fmaf(a.w, f, r.w);
+            }
+            const float inv = 1.f / lsum;
+            r = make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv);
+            lse2 = M + log2f(lsum);
+        }
+        if (any_poison) {
+            r = make_float4(NAN, NAN, NAN, NAN);
+            lse2 = NAN;
+        }
+        if (tw.finalize) {
+            const int qh = tw.kvh * G + h;
+            *reinterpret_cast<float4*>(p.out + (static_cast<size_t>(tw.b) * p.Hq + qh) * D + d) = r;
+            if (d == 0) p.lse[static_cast<size_t>(tw.b) * p.Hq + qh] = lse2 * kLn2;
+        } else {
+            *reinterpret_cast<float4*>(p.ws_o + (static_cast<size_t>(tw.slot) * G + h) * D + d) = r;
+            if (d == 0) p.ws_lse[static_cast<size_t>(tw.slot) * G + h] = lse2;
+        }
+    }
+    if (p.trace && threadIdx.x == 0) {
+        sm.tr[kTrCombineEnd] = globaltimer_ns();
+        sm.tr[kTrLastTile] = (static_cast<uint64_t>(tw.b) << 40) | (static_cast<uint64_t>(tw.kvh) << 20) |
+                             static_cast<uint64_t>(tw.split);
+        sm.tr[kTrTiles] += 1;
+    }
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, 2) attention_q8_kernel(const __grid_constant__ AttnQ8Params qp) {
+    extern __shared__ __align__(128) uint8_t smem_q8[];
+    Q8Smem<D, G>& sm = *reinterpret_cast<Q8Smem<D, G>*>(smem_q8);
+    const AttnParams& p = qp.attn;
+    if (p.trace && threadIdx.x == 0) {
+        for (int i = 0; i < kTraceWords; ++i) sm.tr[i] = 0;
+        sm.tr[kTrEntry] = globaltimer_ns();
+        sm.tr[kTrSm] = smid();
+    }
+    if (threadIdx.x == 0) sm.abort = 0;
+    // Before the grid dependency wait, only what no kernel writes may be used: a
+    // host-staged queue entry.  L2 is warmed with the blocks the ring starts with,
+    // through a speculative read of the block table; prefetches change no value.
+    const bool staged = p.route == kRouteQueue && p.queue_host_staged && static_cast<int>(blockIdx.x) < p.num_tiles;
+    pkv_work_item item{};
+    if (staged) {
+        item = p.queue[blockIdx.x];
+        if (item.b >= 0 && item.b < p.B && item.kvh >= 0 && item.kvh < p.Hkv && item.page_begin >= 0 &&
+            item.page_end <= p.max_pages) {
+            const int t0 = item.page_begin * p.page_size;
+            const int t_end = min(item.page_end * p.page_size, t0 + kWarps * Q8Cfg<D>::kStages * kBlockRows);
+            const int32_t* bt_row = p.block_table + static_cast<size_t>(item.b) * p.max_pages;
+            for (int tok = t0 + static_cast<int>(threadIdx.x); tok < t_end; tok += kThreads) {
+                const int page = ld_volatile_i32(bt_row + tok / p.page_size);
+                if (page < 0 || page >= p.num_pages) continue;
+                const size_t row = static_cast<size_t>(page) * p.page_size + tok % p.page_size;
+                const size_t off = (row * p.Hkv + item.kvh) * D;
+                prefetch_l2(reinterpret_cast<const uint8_t*>(p.k_pages) + off);
+                prefetch_l2(reinterpret_cast<const uint8_t*>(p.v_pages) + off);
+                if (row % kBlockRows == 0) {
+                    prefetch_l2(qp.k_scales + row / kBlockRows * p.Hkv + item.kvh);
+                    prefetch_l2(qp.v_scales + row / kBlockRows * p.Hkv + item.kvh);
+                }
+            }
+        }
+    }
+    grid_dependency_wait();
+    trace_stamp(sm, p, kTrWaitDone);
+    __syncthreads();
+    auto trace_flush = [&]() {
+        if (p.trace && threadIdx.x == 0) {
+            sm.tr[kTrExit] = globaltimer_ns();
+            uint64_t* row = p.trace + static_cast<size_t>(blockIdx.x) * kTraceWords;
+            for (int i = 0; i < kTraceWords; ++i) row[i] = sm.tr[i];
+        }
+    };
+    auto neutral_rows = [&]() {   // rows with no tokens get no tiles
+        if (p.no_empty_rows) return;
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+            if (p.row_splits[b] == 0) write_neutral_row(p, b, threadIdx.x, blockDim.x);
+    };
+
+    if (p.route == kRoutePersistent) {
+        while (true) {
+            if (threadIdx.x == 0) sm.tile_slot[0] = static_cast<int>(atomicAdd(&p.ctr->next_tile, 1u));
+            __syncthreads();
+            const int i = sm.tile_slot[0];
+            if (i >= p.num_tiles) break;
+            const TileWork tw = tile_from_item(p, p.queue[p.order[i]]);
+            run_tile_q8<D, G>(sm, qp, tw);
+            __syncthreads();
+            if (!sm.tile_fin && p.fused_merge) merge_if_last<D, G>(sm, p, tw.b, tw.kvh, sm.tile_splits);
+            __syncthreads();
+        }
+        launch_dependents();
+        neutral_rows();
+        if (threadIdx.x == 0 && atomicAdd(&p.ctr->done_ctas, 1u) == gridDim.x - 1) {
+            p.ctr->next_tile = 0;   // the last CTA out rewinds the queue for the next launch
+            p.ctr->done_ctas = 0;
+        }
+        trace_flush();
+        return;
+    }
+
+    TileWork tw{};
+    if (p.route == kRouteDirect) {
+        tw.b = blockIdx.x / p.Hkv;
+        tw.kvh = blockIdx.x % p.Hkv;
+        tw.t1 = p.seq_lens[tw.b];
+        tw.finalize = 1;
+        tw.splits = 1;
+        if (tw.t1 < 0 || tw.t1 > p.max_pages * p.page_size) {   // would read past the table row
+            tw.poisoned = 1;
+            tw.t1 = 0;
+            if (threadIdx.x == 0) atomicOr(&p.ctr->status, static_cast<uint32_t>(PKV_DEV_PLAN_MISMATCH));
+        }
+    } else if (p.route == kRouteQueue) {
+        if (static_cast<int>(blockIdx.x) >= p.num_tiles) {   // launched only for the neutral rows
+            launch_dependents();
+            neutral_rows();
+            trace_flush();
+            return;
+        }
+        tw = tile_from_item(p, staged ? item : p.queue[blockIdx.x]);
+    } else {   // padded grid: (b, kvh, s) from the block index, ranges from the device lengths
+        const int per_row = p.Hkv * p.max_splits;
+        tw.b = blockIdx.x / per_row;
+        tw.kvh = (blockIdx.x % per_row) / p.max_splits;
+        tw.split = blockIdx.x % p.max_splits;
+        const int n = p.seq_lens[tw.b];
+        const int pages = (n + p.page_size - 1) / p.page_size;
+        tw.poisoned = n < 0 || pages > p.max_splits * p.chunk_pages || n > p.max_pages * p.page_size;
+        if (tw.poisoned && threadIdx.x == 0) atomicOr(&p.ctr->status, static_cast<uint32_t>(PKV_DEV_PLAN_MISMATCH));
+        const int pb = max(0, min(tw.split * p.chunk_pages, pages));
+        const int pe = max(0, min((tw.split + 1) * p.chunk_pages, pages));
+        tw.t0 = pb * p.page_size;
+        tw.t1 = tw.poisoned ? tw.t0 : min(pe * p.page_size, n);
+        tw.finalize = p.max_splits == 1;
+        tw.splits = p.max_splits;
+        tw.slot = blockIdx.x;
+    }
+    run_tile_q8<D, G>(sm, qp, tw);
+    __syncthreads();
+    launch_dependents();   // the next grid may start its CTAs in the slots this tail frees
+    if (!sm.tile_fin && p.fused_merge) {
+        if (p.all_merge)
+            merge_all_splits<D, G>(sm, p, tw.b, tw.kvh, tw.split, sm.tile_splits);
+        else
+            merge_if_last<D, G>(sm, p, tw.b, tw.kvh, sm.tile_splits);
+    }
+    if (p.route == kRouteQueue) neutral_rows();
+    trace_flush();
+}
+
+template <int D, int G>
+cudaError_t launch_q8_t(const AttnQ8Params& p, int grid, cudaStream_t stream, bool cooperative) {
+    constexpr size_t smem = sizeof(Q8Smem<D, G>);
+    cudaError_t e = cudaFuncSetAttribute(attention_q8_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+    if (cooperative) {
+        attr[n].id = cudaLaunchAttributeCooperative;
+        attr[n].val.cooperative = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, attention_q8_kernel<D, G>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_q8(const AttnQ8Params& p, int grid, cudaStream_t stream, bool cooperative) {
+    const int G = p.attn.Hq / p.attn.Hkv;
+    switch (p.attn.D * 16 + G) {
+        case 64 * 16 + 1: return launch_q8_t<64, 1>(p, grid, stream, cooperative);
+        case 64 * 16 + 2: return launch_q8_t<64, 2>(p, grid, stream, cooperative);
+        case 64 * 16 + 4: return launch_q8_t<64, 4>(p, grid, stream, cooperative);
+        case 64 * 16 + 8: return launch_q8_t<64, 8>(p, grid, stream, cooperative);
+        case 128 * 16 + 1: return launch_q8_t<128, 1>(p, grid, stream, cooperative);
+        case 128 * 16 + 2: return launch_q8_t<128, 2>(p, grid, stream, cooperative);
+        case 128 * 16 + 4: return launch_q8_t<128, 4>(p, grid, stream, cooperative);
+        case 128 * 16 + 8: return launch_q8_t<128, 8>(p, grid, stream, cooperative);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace pkv

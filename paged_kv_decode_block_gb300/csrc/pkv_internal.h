@@ -147,6 +147,37 @@ struct AppendStepParams {
     int32_t B, Hkv, D, page_size, max_pages, num_pages;
 };
 cudaError_t launch_append_step(const AppendStepParams& p, cudaStream_t stream);
+// Ragged append with rotation (pkv_append_rotary / pkv_append_q8).
+struct AppendTokensParams {
+    const uint16_t* q;          // bf16 [T][Hq][D] at q_stride, or null
+    uint16_t* q_out;            // its rotation, at q_out_stride (may be q itself)
+    const uint16_t* k;          // bf16 [T][Hkv][D] at k_stride / v_stride
+    const uint16_t* v;
+    int64_t q_stride, q_out_stride, k_stride, v_stride;   // elements between tokens
+    const int32_t* cu;          // [B + 1] first token of each row, or null: one token per row
+    int32_t T;                  // tokens in q / k / v
+    void* k_pages;              // bf16 or e4m3 [num_pages][page_size][Hkv][D]
+    void* v_pages;
+    float* k_scales;            // e4m3 pages: [num_pages][page_size / kBlockRows][Hkv]; null: bf16 pages
+    float* v_scales;
+    const int32_t* block_table;
+    const int32_t* seq_lens;    // [B] lengths before
+    int32_t* new_lens;          // [B] lengths after
+    uint32_t* status;
+    int32_t B, Hq, Hkv, D, page_size, max_pages, num_pages;
+    pkv_rotary rot;             // dim 0: no rotation
+};
+cudaError_t launch_append_tokens(const AppendTokensParams& p, cudaStream_t stream);
+
+// Decode over an e4m3 cache (pkv_decode_q8): AttnParams with k_pages / v_pages
+// pointing to e4m3 codes, and their scales.
+struct AttnQ8Params {
+    AttnParams attn;
+    const float* k_scales;      // [num_pages][page_size / kBlockRows][Hkv]
+    const float* v_scales;
+};
+cudaError_t launch_attention_q8(const AttnQ8Params& p, int grid, cudaStream_t stream, bool cooperative);
+
 // Slot admit / evict (pkv_session_evict / pkv_session_admit / pkv_resident_*).
 // One request per row; evictions are applied before admissions, each in the
 // order listed.  32 bytes.

@@ -69,6 +69,21 @@ class PlanInfo(ctypes.Structure):
         return d
 
 
+ROTARY_MAX_DIM = 128
+Q8_BLOCK = 16   # tokens of one scale of an 8-bit cache
+
+
+class RotaryParams(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("step", ctypes.c_uint64 * (ROTARY_MAX_DIM // 2))]
+
+
+class Tokens(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("cu_tokens_d", ctypes.c_void_p), ("total_tokens", ctypes.c_int32)]
+
+
 # symbol -> (restype, argtypes); the full C ABI of include/pkv.h
 _P, _I32, _I64, _U32P = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(ctypes.c_uint32)
 _I32P = ctypes.POINTER(ctypes.c_int32)
@@ -84,6 +99,13 @@ SIGNATURES = {
     "pkv_decode": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "pkv_decode_host": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "pkv_append": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P]),
+    "pkv_rotary_init": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), _I32, _I32, ctypes.c_float,
+                                       ctypes.POINTER(RotaryParams)]),
+    "pkv_append_rotary": (ctypes.c_int, [ctypes.POINTER(Tokens), ctypes.POINTER(RotaryParams), _P, _P, _P, _P, _P, _P,
+                                         _P]),
+    "pkv_append_q8": (ctypes.c_int, [ctypes.POINTER(Tokens), ctypes.POINTER(RotaryParams), _P, _P, _P, _P, _P, _P, _P,
+                                     _P, _P]),
+    "pkv_decode_q8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "pkv_status": (ctypes.c_int, [_P, _P, _U32P]),
     "pkv_read_workspace": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I32P]),
     "pkv_profile_enable": (ctypes.c_int, [_P, _I32]),
@@ -395,6 +417,131 @@ def append(k_new, v_new, k_pages, v_pages, block_table, seq_lens, plan: Plan, st
                            _dev_ptr(block_table, "block_table", (torch.int32,)),
                            _dev_ptr(seq_lens, "seq_lens", (torch.int32,)), plan.handle, _stream_handle(stream))
     _check(rc, "pkv_append")
+
+
+class Rotary:
+    """Rotary position embedding (pkv_rotary_init): the first `dim` elements of a head turn by
+    position * inv_freq[m], inv_freq[m] = base ** (-2 m / dim) unless given (float64 [dim // 2])."""
+
+    def __init__(self, dim: int, base: float = 10000.0, inv_freq=None, interleaved: bool = False, scale: float = 1.0):
+        dim = int(dim)
+        if inv_freq is None:
+            inv_freq = float(base) ** (-np.arange(0, max(dim, 0), 2, dtype=np.float64) / dim) if dim else np.zeros(0)
+        freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+        if freq.shape != (dim // 2,):
+            raise ValueError(f"inv_freq: shape {freq.shape}, expected {(dim // 2,)}")
+        self.params = RotaryParams()
+        _check(load().pkv_rotary_init(freq.ctypes.data_as(ctypes.POINTER(ctypes.c_double)), dim,
+                                      int(bool(interleaved)), float(scale), ctypes.byref(self.params)),
+               "pkv_rotary_init")
+
+
+def _shaped(t, name, shape, dtypes, device=None):
+    """Device address of a contiguous CUDA tensor of this shape on the plan's device."""
+    ptr = _dev_ptr(t, name, dtypes)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name}: on device {t.get_device()}, expected {device}")
+    return ptr
+
+
+def _token_ptr(t, name, tokens, heads, D):
+    """(address, elements between tokens) of bf16 [tokens][heads][D], each token's heads dense."""
+    if not getattr(t, "is_cuda", False):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _bf16_types():
+        raise TypeError(f"{name}: dtype {t.dtype} not in {_bf16_types()}")
+    if tuple(t.shape) != (tokens, heads, D):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(tokens, heads, D)}")
+    if tokens == 0:
+        return None, 0
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: a token's heads must be dense (strides {t.stride()})")
+    return t.data_ptr(), (t.stride(0) if tokens > 1 else 0)
+
+
+_F8T = None
+
+
+def _f8_types():
+    global _F8T
+    if _F8T is None:
+        import torch
+        _F8T = (torch.float8_e4m3fn, torch.uint8)
+    return _F8T
+
+
+def _append_tokens(what, k_new, v_new, k_pages, v_pages, scales, block_table, seq_lens, new_lens, plan, rotary, q, q_out,
+                   cu_tokens, stream):
+    bf = _bf16_types()
+    g, D = plan.geom, plan.D
+    dev = block_table.get_device()
+    T = int(k_new.shape[0])
+    t = Tokens()
+    t.total_tokens = T
+    t.k, t.k_stride = _token_ptr(k_new, "k_new", T, g.num_kv_heads, D)
+    t.v, t.v_stride = _token_ptr(v_new, "v_new", T, g.num_kv_heads, D)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out: give both or neither")
+    if q is not None:
+        t.q, t.q_stride = _token_ptr(q, "q", T, g.num_q_heads, D)
+        t.q_out, t.q_out_stride = _token_ptr(q_out, "q_out", T, g.num_q_heads, D)
+    if cu_tokens is not None:
+        t.cu_tokens_d = _shaped(cu_tokens, "cu_tokens", (g.batch + 1,), _I32T, dev)
+    for x, name in ((k_new, "k_new"), (v_new, "v_new"), (q, "q"), (q_out, "q_out")):
+        if x is not None and x.get_device() != dev:
+            raise ValueError(f"{name}: on device {x.get_device()}, expected {dev}")
+    pool = (g.num_pages, plan.page_size, g.num_kv_heads, D)
+    types = bf if scales is None else _f8_types()
+    args = [_shaped(k_pages, "k_pages", pool, types, dev), _shaped(v_pages, "v_pages", pool, types, dev)]
+    if scales is not None:
+        blocks = (g.num_pages, plan.page_size // Q8_BLOCK, g.num_kv_heads)
+        args += [_shaped(scales[0], "k_scales", blocks, _F32T, dev), _shaped(scales[1], "v_scales", blocks, _F32T, dev)]
+    args += [_shaped(block_table, "block_table", (g.batch, g.max_pages_per_seq), _I32T, dev),
+             _shaped(seq_lens, "seq_lens", (g.batch,), _I32T, dev),
+             _shaped(new_lens, "new_lens", (g.batch,), _I32T, dev)]
+    rc = getattr(_lib or load(), what)(ctypes.byref(t), ctypes.byref(rotary.params) if rotary is not None else None,
+                                       *args, plan.handle, _stream_handle(stream))
+    if rc:
+        _check(rc, what)
+
+
+def append_rotary(k_new, v_new, k_pages, v_pages, block_table, seq_lens, new_lens, plan: Plan, rotary: Rotary | None,
+                  q=None, q_out=None, cu_tokens=None, stream=None):
+    """pkv_append_rotary: row b's tokens cu_tokens[b]..cu_tokens[b + 1] (without cu_tokens: its one
+    token) go to positions seq_lens[b] on, keys and queries rotated; new_lens = the lengths after.
+    k_new / v_new / q: bf16 [T][heads][D], also slices of one projection's output."""
+    _append_tokens("pkv_append_rotary", k_new, v_new, k_pages, v_pages, None, block_table, seq_lens, new_lens, plan,
+                   rotary, q, q_out, cu_tokens, stream)
+
+
+def append_q8(k_new, v_new, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, new_lens, plan: Plan,
+              rotary: Rotary | None = None, q=None, q_out=None, cu_tokens=None, stream=None):
+    """pkv_append_q8: append_rotary into an 8-bit cache (pages float8_e4m3fn [num_pages][page_size][Hkv][D],
+    scales fp32 [num_pages][page_size // Q8_BLOCK][Hkv])."""
+    _append_tokens("pkv_append_q8", k_new, v_new, k_pages, v_pages, (k_scales, v_scales), block_table, seq_lens,
+                   new_lens, plan, rotary, q, q_out, cu_tokens, stream)
+
+
+def decode_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, plan: Plan, out, lse, stream=None):
+    """pkv_decode_q8: decode over an 8-bit cache (see append_q8)."""
+    bf = _bf16_types()
+    f8 = _f8_types()
+    g, D = plan.geom, plan.D
+    dev = block_table.get_device()
+    pool = (g.num_pages, plan.page_size, g.num_kv_heads, D)
+    blocks = (g.num_pages, plan.page_size // Q8_BLOCK, g.num_kv_heads)
+    heads = (g.batch, g.num_q_heads)
+    rc = (_lib or load()).pkv_decode_q8(
+        _shaped(q, "q", heads + (D,), bf, dev), _shaped(k_pages, "k_pages", pool, f8, dev),
+        _shaped(v_pages, "v_pages", pool, f8, dev), _shaped(k_scales, "k_scales", blocks, _F32T, dev),
+        _shaped(v_scales, "v_scales", blocks, _F32T, dev),
+        _shaped(block_table, "block_table", (g.batch, g.max_pages_per_seq), _I32T, dev),
+        _shaped(seq_lens, "seq_lens", (g.batch,), _I32T, dev), plan.handle,
+        _shaped(out, "out", heads + (D,), _F32T, dev), _shaped(lse, "lse", heads, _F32T, dev), _stream_handle(stream))
+    if rc:
+        _check(rc, "pkv_decode_q8")
 
 
 class Pool:
