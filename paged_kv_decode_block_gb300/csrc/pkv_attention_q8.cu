@@ -13,9 +13,9 @@
 // of two that brings its largest element to [1, 2), so it is exact in f16 down to
 // 2^-14 of that element and rounded by at most 2^-25 of it below.  A weight
 // 2^(s - m) * vs_B / r (r: the largest block scale so far, rounded up to a power of
-// two) is split into f16 hi + lo, about 22 bits; rows 0-7 of the product's A
-// operand hold the group's hi parts and rows 8-15 the lo parts.  Statistics and
-// sums are fp32.  m follows the running maximum lazily: weights may grow to 2^14
+// two) is split into f16 hi + lo, about 22 bits; the parts are columns of the
+// products' right operand (with G = 8, of a second one).  Statistics and sums are
+// fp32.  m follows the running maximum lazily: weights may grow to 2^14
 // (within f16) before the accumulators move to a new reference that puts the
 // block's maximum at 2^6.
 //
@@ -24,11 +24,12 @@
 //   * one CTA per tile, eight warps; warp w owns blocks w, w + 8, ... of the tile
 //     with a private softmax state, so the loop has no barrier and no shared state;
 //   * contraction indices may be permuted freely, so each thread fetches whole
-//     16-byte pieces: of K, the pieces of the two token rows whose B fragments
+//     16-byte pieces: of K, the pieces of the two token rows whose A fragments
 //     it holds; of V, the same 16 dimensions of its four tokens.  What a thread
 //     copies (cp.async into a private ring) only that thread reads, so a
 //     per-thread wait on its own copies is the pipeline's only synchronisation;
-//   * S = Q K^T comes out in the layout in which P V needs P: no exchange of P;
+//   * S^T = K Q^T and O^T += V^T P^T, with the query group as the 8 columns: no row
+//     of a product is padding; P^T goes from one to the other through movmatrix;
 //   * the block table and the scales are fetched 32 blocks at a time, one per lane.
 // Bad page ids set PKV_DEV_PAGE_OOB and poison the tile; page 0 is read in place
 // of such a page.
@@ -48,18 +49,19 @@ constexpr int kWarps = kThreads / 32;
 constexpr float kHeadroom = 6.f;     // a new reference puts the block's largest weight at 2^6
 constexpr float kGrowth = 14.f;      // and holds until a weight would pass 2^14
 
-template <int D>
+template <int D, int G>
 struct Q8Cfg {
     static constexpr int kBlockBytes = 2 * kBlockRows * D;   // K and V codes of one block
     static constexpr int kStages = D == 128 ? 3 : 6;         // 12 KB in flight per warp, 96 KB per CTA
     static constexpr int kKPieces = D / 32;                  // 16-byte pieces of K per thread and block
     static constexpr int kVBytes = D / 8;                    // bytes of one token's V per thread
+    static constexpr int kParts = G == 8 ? 2 : 1;            // P^T column tiles: the lo parts share one while 2G <= 8
     static_assert(D == 64 || D == 128, "head_dim");
 };
 
 template <int D, int G>
 struct Q8Smem {
-    static constexpr int kRing = Q8Cfg<D>::kStages * Q8Cfg<D>::kBlockBytes;   // one warp's ring
+    static constexpr int kRing = Q8Cfg<D, G>::kStages * Q8Cfg<D, G>::kBlockBytes;   // one warp's ring
     static constexpr int kScratchBytes = kWarps * kRing;
     static constexpr int kAccRow = D + 4;   // floats of one head's partial (padded against bank conflicts)
     __device__ uint8_t* scratch() { return &ring[0][0]; }
@@ -121,6 +123,27 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
 
 __device__ __forceinline__ float2 unpack_half(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
+// 2^x (ex2.approx: about 2^-22 relative; results below 2^-126 are zero).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// An 8 x 8 tile of 16-bit values held as mma fragments (row lane / 4, columns
+// 2 (lane % 4) and + 1), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Two columns' f16: each takes its half of `hi` (part 0), of `lo` (1), or zero (2).
+__device__ __forceinline__ uint32_t pick(int part0, int part1, uint32_t hi, uint32_t lo) {
+    const uint32_t a = part0 == 0 ? hi : part0 == 1 ? lo : 0u, b = part1 == 0 ? hi : part1 == 1 ? lo : 0u;
+    return __byte_perm(a, b, 0x7610);
+}
+
 // The least power of two not below x > 0 (x a finite fp32; the exponent saturates at 2^126).
 __device__ __forceinline__ float power_of_two_above(float x) {
     const uint32_t u = __float_as_uint(x);
@@ -131,11 +154,12 @@ __device__ __forceinline__ float power_of_two_above(float x) {
 
 // One tile: every warp reduces its blocks, then the eight states are combined
 // and written (to out / lse, or to the workspace for a split).
-// Fragment coordinates: g = lane / 4 (a head in A and C, a token or a dimension
-// column in B), t = lane % 4.
+// Fragment coordinates: g = lane / 4 (a row of A and C: tokens g, g + 8 of K,
+// two dimensions of V^T; a column of B: a head), t = lane % 4 (k pairs of A and
+// B, columns 2t, 2t + 1 of C).
 template <int D, int G>
 __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork tw) {
-    using C = Q8Cfg<D>;
+    using C = Q8Cfg<D, G>;
     const AttnParams& p = qp.attn;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = lane >> 2, t = lane & 3;
@@ -150,11 +174,9 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
     const int mine = nblk > warp ? (nblk - warp + kWarps - 1) / kWarps : 0;   // this warp's blocks: warp + 8 i
     int poisoned = tw.poisoned;
 
-    const uint8_t* kpool = reinterpret_cast<const uint8_t*>(p.k_pages) + static_cast<size_t>(tw.kvh) * D;
-    const uint8_t* vpool = reinterpret_cast<const uint8_t*>(p.v_pages) + static_cast<size_t>(tw.kvh) * D;
-    const size_t pitch = static_cast<size_t>(p.Hkv) * D;   // bytes between tokens
-    const uint32_t k_off = static_cast<uint32_t>(g * pitch + t * 16);
-    const uint32_t v_off = static_cast<uint32_t>(2 * t * pitch + g * C::kVBytes);
+    const uint32_t pitch = static_cast<uint32_t>(p.Hkv) * D, eight = 8 * pitch;   // bytes between tokens
+    const uint8_t* kpool = reinterpret_cast<const uint8_t*>(p.k_pages) + tw.kvh * D + g * pitch + t * 16;
+    const uint8_t* vpool = reinterpret_cast<const uint8_t*>(p.v_pages) + tw.kvh * D + 2 * t * pitch + g * C::kVBytes;
     const uint32_t ring = smem_addr(sm.ring[warp]);
     const uint64_t policy = l2_evict_first_policy();
     const int32_t* bt_row = p.block_table + static_cast<size_t>(tw.b) * p.max_pages;
@@ -186,14 +208,16 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
     };
     auto issue = [&](int i, int stage) {   // block i of the current batch into the thread's slots of `stage`
         const size_t off = static_cast<size_t>(__shfl_sync(kFull, row_i, i & 31)) * pitch;
+        const uint8_t* ksrc = kpool + off;
+        const uint8_t* vsrc = vpool + off;
         const uint32_t dst = ring + stage * C::kBlockBytes + lane * 16;
 #pragma unroll
         for (int x = 0; x < C::kKPieces; ++x)   // rows g, g + 8; pieces t, t + 4
-            cp_async16(dst + x * 512, kpool + off + k_off + (x & 1) * 8 * pitch + (x >> 1) * 64, policy);
+            cp_async16(dst + x * 512, ksrc + ((x & 1) ? eight : 0) + (x >> 1) * 64, policy);
         const uint32_t vdst = ring + stage * C::kBlockBytes + C::kKPieces * 512 + lane * C::kVBytes;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {   // tokens 2t, 2t + 1, 2t + 8, 2t + 9
-            const uint8_t* src = vpool + off + v_off + ((x & 1) + (x >> 1) * 8) * pitch;
+            const uint8_t* src = vsrc + ((x & 1) ? pitch : 0) + ((x >> 1) ? eight : 0);
             if constexpr (D == 128)
                 cp_async16(vdst + x * 512, src, policy);
             else
@@ -209,16 +233,18 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         if (s < mine) issue(s, s);
         cp_async_commit();
     }
-    // A fragments of Q: row g is query head g, k-step j holds the elements of the
-    // thread's j-th 4-byte word of a K row (the same permutation on both sides)
-    uint32_t qa[D / 16][2];
-    float qscale;   // what the dot products of head g are multiplied by, before ks
+    // B fragments of Q^T: column g is query head g % G (so with G <= 4 the columns
+    // repeat the group: one copy serves P's hi parts, the next its lo parts); k-step
+    // j holds the elements of the thread's j-th 4-byte word of a K row (the same
+    // permutation on both sides)
+    uint32_t qb[D / 16][2];
+    float qs[2];   // what the dot products of columns 2t, 2t + 1 are multiplied by, before ks
     {
         uint4 raw[D / 32];
-        const uint16_t* qh = p.q + (static_cast<size_t>(tw.b) * p.Hq + tw.kvh * G + (g < G ? g : 0)) * D + t * 16;
+        const uint16_t* qh = p.q + (static_cast<size_t>(tw.b) * p.Hq + tw.kvh * G + g % G) * D + t * 16;
 #pragma unroll
         for (int x = 0; x < D / 32; ++x)   // elements 16 t .. 16 t + 15, then 64 on
-            raw[x] = g < G ? __ldg(reinterpret_cast<const uint4*>(qh + (x >> 1) * 64 + (x & 1) * 8)) : make_uint4(0, 0, 0, 0);
+            raw[x] = __ldg(reinterpret_cast<const uint4*>(qh + (x >> 1) * 64 + (x & 1) * 8));
         uint32_t big = 0;
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) {
@@ -230,28 +256,34 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         big = max(big, __shfl_xor_sync(kFull, big, 2));
         const int e = max(-126, min(126, static_cast<int>(big >> 23) - 127));
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        qscale = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        const float up = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        qs[0] = __shfl_sync(kFull, up, 8 * t);       // column 2t: the lanes of g = 2t hold its head
+        qs[1] = __shfl_sync(kFull, up, 8 * t + 4);
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) {
             float f[8];
             unpack_bf16x8(raw[x], f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] *= down;
-            qa[2 * x][0] = pack_half(f[0], f[1]);
-            qa[2 * x][1] = pack_half(f[2], f[3]);
-            qa[2 * x + 1][0] = pack_half(f[4], f[5]);
-            qa[2 * x + 1][1] = pack_half(f[6], f[7]);
+            qb[2 * x][0] = pack_half(f[0], f[1]);
+            qb[2 * x][1] = pack_half(f[2], f[3]);
+            qb[2 * x + 1][0] = pack_half(f[4], f[5]);
+            qb[2 * x + 1][1] = pack_half(f[6], f[7]);
         }
     }
+    // which part of P the lane's columns 2t, 2t + 1 carry: 0 hi, 1 lo, 2 none
+    const int part0 = G == 8 ? 0 : min(2 * t / G, 2), part1 = G == 8 ? 0 : min((2 * t + 1) / G, 2);
 
-    float m = -INFINITY, l = 0.f;      // head g: reference, and this lane's share of the sum
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // columns 2t, 2t + 1: reference, this lane's share of the sum
     float vref = 1.1754944e-38f;       // power of two not below any block's V scale so far
     float vinv = 8.5070592e37f;
-    float o[D / 8][4];                 // head g: hi parts in [0], [1], lo parts in [2], [3]
+    float o[C::kParts][D / 16][4];     // O^T accumulators
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
+    for (int x = 0; x < C::kParts; ++x)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+        for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[x][n][i] = 0.f;
 
     int stage = 0;
     for (int i = 0; i < mine; ++i) {
@@ -265,64 +297,84 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         const float ks = __shfl_sync(kFull, k_now, i & 31), vs = __shfl_sync(kFull, v_now, i & 31);
         const uint32_t src = ring + stage * C::kBlockBytes + lane * 16;
 
-        // S = Q K^T: tokens 0-7 and 8-15 are two column tiles
-        float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+        // S^T = K Q^T: rows g and g + 8 are tokens g and g + 8
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};   // two chains, for the product's latency
 #pragma unroll
         for (int x = 0; x < C::kKPieces; x += 2) {
             const uint4 ka = lds128(src + x * 512), kb = lds128(src + (x + 1) * 512);
             const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-                uint32_t b0, b1;
-                widen4(wa[y], b0, b1);
-                mma_f16(s0, qa[2 * x + y][0], 0u, qa[2 * x + y][1], 0u, b0, b1);
-                widen4(wb[y], b0, b1);
-                mma_f16(s1, qa[2 * x + y][0], 0u, qa[2 * x + y][1], 0u, b0, b1);
+                uint32_t a0, a1, a2, a3;
+                widen4(wa[y], a0, a2);
+                widen4(wb[y], a1, a3);
+                mma_f16(y & 1 ? s2 : s, a0, a1, a2, a3, qb[2 * x + y][0], qb[2 * x + y][1]);
             }
         }
-        const float sc = ks * qscale;
-        float z[4] = {s0[0] * sc, s0[1] * sc, s1[0] * sc, s1[1] * sc};   // tokens 2t, 2t+1, 2t+8, 2t+9
+        const float sc0 = ks * qs[0], sc1 = ks * qs[1];
+        float z[4] = {(s[0] + s2[0]) * sc0, (s[1] + s2[1]) * sc1, (s[2] + s2[2]) * sc0, (s[3] + s2[3]) * sc1};
         if (valid < kBlockRows) {
-            if (2 * t >= valid) z[0] = -INFINITY;
-            if (2 * t + 1 >= valid) z[1] = -INFINITY;
-            if (2 * t + 8 >= valid) z[2] = -INFINITY;
-            if (2 * t + 9 >= valid) z[3] = -INFINITY;
+            if (g >= valid) z[0] = z[1] = -INFINITY;
+            if (g + 8 >= valid) z[2] = z[3] = -INFINITY;
         }
 
-        // the reference moves when a weight would pass 2^14, or a block's scale passes r
-        float bm = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
-        bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 1));
-        bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 2));
-        const bool grow = bm > m + kGrowth;   // (m = -inf at first)
-        if (__any_sync(kFull, grow) || fabsf(vs) > vref) {
-            const float mn = grow ? bm - kHeadroom : m;
-            float f = m == mn ? 1.f : exp2f(m - mn);   // from m = -inf: 0
-            l *= f;
-            m = mn;
+        // a reference moves when one of its weights would pass 2^14 (m = -inf: at
+        // once), or the block's V scale passes r; neither happens often, so the
+        // block's exact maximum is found only then
+        const bool big = fmaxf(z[0], z[2]) > m[0] + kGrowth || fmaxf(z[1], z[3]) > m[1] + kGrowth;
+        if (__any_sync(kFull, big) || fabsf(vs) > vref) {
+            float bm0 = fmaxf(z[0], z[2]), bm1 = fmaxf(z[1], z[3]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+                bm0 = fmaxf(bm0, __shfl_xor_sync(kFull, bm0, x));
+                bm1 = fmaxf(bm1, __shfl_xor_sync(kFull, bm1, x));
+            }
+            const float mn0 = bm0 > m[0] + kGrowth ? bm0 - kHeadroom : m[0];
+            const float mn1 = bm1 > m[1] + kGrowth ? bm1 - kHeadroom : m[1];
+            float f0 = m[0] == mn0 ? 1.f : exp2f(m[0] - mn0);   // from m = -inf: 0
+            float f1 = m[1] == mn1 ? 1.f : exp2f(m[1] - mn1);
+            m[0] = mn0;
+            m[1] = mn1;
+            l[0] *= f0;
+            l[1] *= f1;
             if (fabsf(vs) > vref) {
                 const float vn = power_of_two_above(fabsf(vs));
-                f *= vref / vn;
+                f0 *= vref / vn;
+                f1 *= vref / vn;
                 vref = vn;
                 vinv = 1.f / vn;
             }
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n)
+            for (int x = 0; x < C::kParts; ++x)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[n][k] *= f;
+                for (int n = 0; n < D / 16; ++n) {
+                    o[x][n][0] *= f0;
+                    o[x][n][1] *= f1;
+                    o[x][n][2] *= f0;
+                    o[x][n][3] *= f1;
+                }
         }
         const float vw = vs * vinv;
-        float w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float e = exp2f(z[k] - m);   // masked: 0
-            l += e;
-            w[k] = e * vw;
+        const float p0 = ex2(z[0] - m[0]), p1 = ex2(z[1] - m[1]), p2 = ex2(z[2] - m[0]), p3 = ex2(z[3] - m[1]);   // masked: 0
+        l[0] += p0 + p2;
+        l[1] += p1 + p3;
+        const float w0 = p0 * vw, w1 = p1 * vw, w2 = p2 * vw, w3 = p3 * vw;
+        const uint32_t ha = pack_half(w0, w1), hb = pack_half(w2, w3);   // tokens g and g + 8
+        const float2 ua = unpack_half(ha), ub = unpack_half(hb);
+        const uint32_t la = pack_half(w0 - ua.x, w1 - ua.y), lb = pack_half(w2 - ub.x, w3 - ub.y);
+        // B fragments of P^T: the 8 x 8 transposes of the token-major tiles
+        uint32_t pb[C::kParts][2];
+        if constexpr (C::kParts == 2) {
+            pb[0][0] = transpose8(ha);
+            pb[0][1] = transpose8(hb);
+            pb[1][0] = transpose8(la);
+            pb[1][1] = transpose8(lb);
+        } else {
+            pb[0][0] = transpose8(pick(part0, part1, ha, la));
+            pb[0][1] = transpose8(pick(part0, part1, hb, lb));
         }
-        const uint32_t h0 = pack_half(w[0], w[1]), h1 = pack_half(w[2], w[3]);
-        const float2 u0 = unpack_half(h0), u1 = unpack_half(h1);
-        const uint32_t l0 = pack_half(w[0] - u0.x, w[1] - u0.y), l1 = pack_half(w[2] - u1.x, w[3] - u1.y);
 
-        // O += P V: column tile n is dimension (D / 8) * g + n of every g
+        // O^T += V^T P^T: rows g and g + 8 of tile n are dimensions (D / 8) g + 2n and + 1
         const uint32_t vsrc = ring + stage * C::kBlockBytes + C::kKPieces * 512 + lane * C::kVBytes;
         uint32_t vw_[4][C::kVBytes / 4];
 #pragma unroll
@@ -338,25 +390,28 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
                 vw_[x][0] = r.x;
                 vw_[x][1] = r.y;
             }
-            // slots past the row's end may hold anything, NaN codes too (0 * NaN = NaN)
-            if (valid < kBlockRows && 2 * t + (x & 1) + (x >> 1) * 8 >= valid)
+        }
+        if (valid < kBlockRows) {   // slots past the row's end may hold anything, NaN codes too (0 * NaN = NaN)
 #pragma unroll
-                for (int y = 0; y < C::kVBytes / 4; ++y) vw_[x][y] = 0u;
+            for (int x = 0; x < 4; ++x)
+                if (2 * t + (x & 1) + (x >> 1) * 8 >= valid)
+#pragma unroll
+                    for (int y = 0; y < C::kVBytes / 4; ++y) vw_[x][y] = 0u;
         }
 #pragma unroll
         for (int y = 0; y < C::kVBytes / 4; ++y) {
             // (token pair, dimension) order: two tokens' bytes of one dimension side by side
-            const uint32_t a01 = __byte_perm(vw_[0][y], vw_[1][y], 0x5140), a23 = __byte_perm(vw_[0][y], vw_[1][y], 0x7362);
-            const uint32_t b01 = __byte_perm(vw_[2][y], vw_[3][y], 0x5140), b23 = __byte_perm(vw_[2][y], vw_[3][y], 0x7362);
-            uint32_t f0, f1, f2, f3, q0, q1, q2, q3;
-            widen4(a01, f0, f1);
-            widen4(a23, f2, f3);
-            widen4(b01, q0, q1);
-            widen4(b23, q2, q3);
-            mma_f16(o[4 * y + 0], h0, l0, h1, l1, f0, q0);
-            mma_f16(o[4 * y + 1], h0, l0, h1, l1, f1, q1);
-            mma_f16(o[4 * y + 2], h0, l0, h1, l1, f2, q2);
-            mma_f16(o[4 * y + 3], h0, l0, h1, l1, f3, q3);
+            const uint32_t t01 = __byte_perm(vw_[0][y], vw_[1][y], 0x5140), t23 = __byte_perm(vw_[0][y], vw_[1][y], 0x7362);
+            const uint32_t u01 = __byte_perm(vw_[2][y], vw_[3][y], 0x5140), u23 = __byte_perm(vw_[2][y], vw_[3][y], 0x7362);
+            uint32_t a0, a1, a2, a3;
+            widen4(t01, a0, a1);
+            widen4(u01, a2, a3);
+#pragma unroll
+            for (int x = 0; x < C::kParts; ++x) mma_f16(o[x][2 * y], a0, a1, a2, a3, pb[x][0], pb[x][1]);
+            widen4(t23, a0, a1);
+            widen4(u23, a2, a3);
+#pragma unroll
+            for (int x = 0; x < C::kParts; ++x) mma_f16(o[x][2 * y + 1], a0, a1, a2, a3, pb[x][0], pb[x][1]);
         }
 
         // the slot is read (by this thread alone): its next block
@@ -370,25 +425,48 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
     }
     trace_stamp(sm, p, kTrStreamEnd);
 
-    // publish the warp's state: column 2t (+ 1) of tile n is dimension
-    // (D / 8) * (2t (+ 1)) + n, so a lane holds two runs of D / 8 dimensions
-    l += __shfl_xor_sync(kFull, l, 1);
-    l += __shfl_xor_sync(kFull, l, 2);
+    // publish the warp's state: fold the lo parts into the hi parts; a lane then
+    // holds D / 8 neighbouring dimensions of its columns' heads
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+        l[0] += __shfl_xor_sync(kFull, l[0], x);
+        l[1] += __shfl_xor_sync(kFull, l[1], x);
+    }
     poisoned = __any_sync(kFull, poisoned) ? 1 : 0;
     __syncwarp();   // every lane has read its slots: the ring takes the partial
-    if (g < G) {
-        float* acc = reinterpret_cast<float*>(sm.ring[warp]) + g * Q8Smem<D, G>::kAccRow;
+    float* acc = reinterpret_cast<float*>(sm.ring[warp]) + (D / 8) * g;
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+    for (int n = 0; n < D / 16; n += 2) {
+        float f[2][4];   // columns 2t, 2t + 1: four dimensions
 #pragma unroll
-            for (int n = 0; n < D / 8; n += 4)
-                *reinterpret_cast<float4*>(acc + (D / 8) * (2 * t + half) + n) =
-                    make_float4((o[n][half] + o[n][2 + half]) * vref, (o[n + 1][half] + o[n + 1][2 + half]) * vref,
-                                (o[n + 2][half] + o[n + 2][2 + half]) * vref, (o[n + 3][half] + o[n + 3][2 + half]) * vref);
-        if (t == 0) {
-            sm.m[warp][g] = m;
-            sm.l[warp][g] = l;
+        for (int c = 0; c < 2; ++c) {
+            f[c][0] = o[0][n][c];
+            f[c][1] = o[0][n][2 + c];
+            f[c][2] = o[0][n + 1][c];
+            f[c][3] = o[0][n + 1][2 + c];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (C::kParts == 2) f[c][k] += o[1][n + k / 2][2 * (k & 1) + c];
+                else if constexpr (G > 1) f[c][k] += __shfl_xor_sync(kFull, f[c][k], G / 2);
+            }
         }
+        if constexpr (G == 1) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[0][k] += f[1][k];
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            if (2 * t + c < G)
+                *reinterpret_cast<float4*>(acc + (2 * t + c) * Q8Smem<D, G>::kAccRow + 2 * n) =
+                    make_float4(f[c][0] * vref, f[c][1] * vref, f[c][2] * vref, f[c][3] * vref);
+    }
+    if (g == 0) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            if (2 * t + c < G) {
+                sm.m[warp][2 * t + c] = m[c];
+                sm.l[warp][2 * t + c] = l[c];
+            }
     }
     if (lane == 0) sm.poisoned[warp] = poisoned;
     __syncthreads();
@@ -464,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q8_kernel(const __grid_
         if (item.b >= 0 && item.b < p.B && item.kvh >= 0 && item.kvh < p.Hkv && item.page_begin >= 0 &&
             item.page_end <= p.max_pages) {
             const int t0 = item.page_begin * p.page_size;
-            const int t_end = min(item.page_end * p.page_size, t0 + kWarps * Q8Cfg<D>::kStages * kBlockRows);
+            const int t_end = min(item.page_end * p.page_size, t0 + kWarps * Q8Cfg<D, G>::kStages * kBlockRows);
             const int32_t* bt_row = p.block_table + static_cast<size_t>(item.b) * p.max_pages;
             for (int tok = t0 + static_cast<int>(threadIdx.x); tok < t_end; tok += kThreads) {
                 const int page = ld_volatile_i32(bt_row + tok / p.page_size);
