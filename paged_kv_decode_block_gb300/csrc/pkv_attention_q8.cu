@@ -23,11 +23,11 @@
 // flops (G flop per byte).  Layout of the work:
 //   * one CTA per tile, eight warps; warp w owns blocks w, w + 8, ... of the tile
 //     with a private softmax state, so the loop has no barrier and no shared state;
-//   * contraction indices may be permuted freely, so each thread fetches whole
-//     16-byte pieces: of K, the pieces of the two token rows whose A fragments
-//     it holds; of V, the same 16 dimensions of its four tokens.  What a thread
-//     copies (cp.async into a private ring) only that thread reads, so a
-//     per-thread wait on its own copies is the pipeline's only synchronisation;
+//   * a warp copies its blocks by whole rows (cp.async, 16 bytes a lane) into a ring
+//     of its own and waits for its own copies only; ldmatrix brings the codes out
+//     conflict-free, four per register, in the order the fragments need (K as it
+//     lies, V transposed), the contraction order being free; the ring slot is
+//     refilled before the block's softmax;
 //   * S^T = K Q^T and O^T += V^T P^T, with the query group as the 8 columns: no row
 //     of a product is padding; P^T goes from one to the other through movmatrix;
 //   * the block table and the scales are fetched 32 blocks at a time, one per lane.
@@ -53,8 +53,8 @@ template <int D, int G>
 struct Q8Cfg {
     static constexpr int kBlockBytes = 2 * kBlockRows * D;   // K and V codes of one block
     static constexpr int kStages = D == 128 ? 3 : 6;         // 12 KB in flight per warp, 96 KB per CTA
-    static constexpr int kKPieces = D / 32;                  // 16-byte pieces of K per thread and block
-    static constexpr int kVBytes = D / 8;                    // bytes of one token's V per thread
+    static constexpr int kMatBytes = kBlockRows * D;         // one K or V block: 16 rows of D bytes
+    static constexpr int kChunks = D / 16;                   // 16-byte chunks of a row
     static constexpr int kParts = G == 8 ? 2 : 1;            // P^T column tiles: the lo parts share one while 2G <= 8
     static_assert(D == 64 || D == 128, "head_dim");
 };
@@ -77,24 +77,19 @@ struct Q8Smem {
     static_assert(G * kAccRow * 4 <= kRing, "a warp's partial fits its ring");
 };
 
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-    return v;
+// Byte offset of 16-byte chunk `c` of row `r` in a staged block.  Chunks are
+// exchanged within a row (by r mod 8 in 128-byte rows, by r / 2 mod 4 in 64-byte
+// rows) so that one chunk index of eight neighbouring rows hits eight distinct
+// bank groups.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_offset(int r, int c) {
+    return static_cast<uint32_t>(r * D + ((c ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4));
 }
 
 // Four e4m3 codes to two f16x2: bytes 0, 1 and bytes 2, 3.
@@ -174,9 +169,13 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
     const int mine = nblk > warp ? (nblk - warp + kWarps - 1) / kWarps : 0;   // this warp's blocks: warp + 8 i
     int poisoned = tw.poisoned;
 
-    const uint32_t pitch = static_cast<uint32_t>(p.Hkv) * D, eight = 8 * pitch;   // bytes between tokens
-    const uint8_t* kpool = reinterpret_cast<const uint8_t*>(p.k_pages) + tw.kvh * D + g * pitch + t * 16;
-    const uint8_t* vpool = reinterpret_cast<const uint8_t*>(p.v_pages) + tw.kvh * D + 2 * t * pitch + g * C::kVBytes;
+    // the lane's share of a copy: 16-byte chunk lane % kChunks of rows lane /
+    // kChunks, + kRows, ... (a warp moves whole rows)
+    constexpr int kRows = 32 / C::kChunks;
+    const uint32_t pitch = static_cast<uint32_t>(p.Hkv) * D;   // bytes between tokens
+    const uint32_t lane_off = tw.kvh * D + (lane / C::kChunks) * pitch + (lane % C::kChunks) * 16;
+    const uint8_t* kpool = reinterpret_cast<const uint8_t*>(p.k_pages) + lane_off;
+    const uint8_t* vpool = reinterpret_cast<const uint8_t*>(p.v_pages) + lane_off;
     const uint32_t ring = smem_addr(sm.ring[warp]);
     const uint64_t policy = l2_evict_first_policy();
     const int32_t* bt_row = p.block_table + static_cast<size_t>(tw.b) * p.max_pages;
@@ -206,22 +205,14 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         }
         read_entry(i0 + 32);
     };
-    auto issue = [&](int i, int stage) {   // block i of the current batch into the thread's slots of `stage`
+    auto issue = [&](int i, int stage) {   // block i of the current batch into `stage`
         const size_t off = static_cast<size_t>(__shfl_sync(kFull, row_i, i & 31)) * pitch;
-        const uint8_t* ksrc = kpool + off;
-        const uint8_t* vsrc = vpool + off;
-        const uint32_t dst = ring + stage * C::kBlockBytes + lane * 16;
+        const uint32_t dst = ring + stage * C::kBlockBytes;
 #pragma unroll
-        for (int x = 0; x < C::kKPieces; ++x)   // rows g, g + 8; pieces t, t + 4
-            cp_async16(dst + x * 512, ksrc + ((x & 1) ? eight : 0) + (x >> 1) * 64, policy);
-        const uint32_t vdst = ring + stage * C::kBlockBytes + C::kKPieces * 512 + lane * C::kVBytes;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {   // tokens 2t, 2t + 1, 2t + 8, 2t + 9
-            const uint8_t* src = vsrc + ((x & 1) ? pitch : 0) + ((x >> 1) ? eight : 0);
-            if constexpr (D == 128)
-                cp_async16(vdst + x * 512, src, policy);
-            else
-                cp_async8(vdst + x * 256, src);
+        for (int x = 0; x < kBlockRows / kRows; ++x) {
+            const uint32_t at = dst + chunk_offset<D>(lane / C::kChunks + x * kRows, lane % C::kChunks);
+            cp_async16(at, kpool + off + x * kRows * pitch, policy);
+            cp_async16(at + C::kMatBytes, vpool + off + x * kRows * pitch, policy);
         }
     };
 
@@ -234,23 +225,21 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         cp_async_commit();
     }
     // B fragments of Q^T: column g is query head g % G (so with G <= 4 the columns
-    // repeat the group: one copy serves P's hi parts, the next its lo parts); k-step
-    // j holds the elements of the thread's j-th 4-byte word of a K row (the same
-    // permutation on both sides)
+    // repeat the group: one copy serves P's hi parts, the next its lo parts).  A K
+    // word is four neighbouring elements, 16 j + 4 t on for k-step j, so q's fragments
+    // hold the same four
     uint32_t qb[D / 16][2];
     float qs[2];   // what the dot products of columns 2t, 2t + 1 are multiplied by, before ks
     {
-        uint4 raw[D / 32];
-        const uint16_t* qh = p.q + (static_cast<size_t>(tw.b) * p.Hq + tw.kvh * G + g % G) * D + t * 16;
+        uint2 raw[D / 16];
+        const uint16_t* qh = p.q + (static_cast<size_t>(tw.b) * p.Hq + tw.kvh * G + g % G) * D + t * 4;
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x)   // elements 16 t .. 16 t + 15, then 64 on
-            raw[x] = __ldg(reinterpret_cast<const uint4*>(qh + (x >> 1) * 64 + (x & 1) * 8));
+        for (int j = 0; j < D / 16; ++j) raw[j] = __ldg(reinterpret_cast<const uint2*>(qh + 16 * j));
         uint32_t big = 0;
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-            const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) big = max(big, max((w[i] & 0x7fffu) << 16, w[i] & 0x7fff0000u));
+        for (int j = 0; j < D / 16; ++j) {
+            big = max(big, max((raw[j].x & 0x7fffu) << 16, raw[j].x & 0x7fff0000u));
+            big = max(big, max((raw[j].y & 0x7fffu) << 16, raw[j].y & 0x7fff0000u));
         }
         big = max(big, __shfl_xor_sync(kFull, big, 1));
         big = max(big, __shfl_xor_sync(kFull, big, 2));
@@ -260,15 +249,9 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         qs[0] = __shfl_sync(kFull, up, 8 * t);       // column 2t: the lanes of g = 2t hold its head
         qs[1] = __shfl_sync(kFull, up, 8 * t + 4);
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-            float f[8];
-            unpack_bf16x8(raw[x], f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] *= down;
-            qb[2 * x][0] = pack_half(f[0], f[1]);
-            qb[2 * x][1] = pack_half(f[2], f[3]);
-            qb[2 * x + 1][0] = pack_half(f[4], f[5]);
-            qb[2 * x + 1][1] = pack_half(f[6], f[7]);
+        for (int j = 0; j < D / 16; ++j) {
+            qb[j][0] = pack_half(__uint_as_float(raw[j].x << 16) * down, __uint_as_float(raw[j].x & 0xffff0000u) * down);
+            qb[j][1] = pack_half(__uint_as_float(raw[j].y << 16) * down, __uint_as_float(raw[j].y & 0xffff0000u) * down);
         }
     }
     // which part of P the lane's columns 2t, 2t + 1 carry: 0 hi, 1 lo, 2 none
@@ -285,9 +268,12 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[x][n][i] = 0.f;
 
+    // a lane's row address for ldmatrix: matrices 0, 1 are rows 0-7 and 8-15 of a chunk, 2, 3 of the next chunk
+    const uint32_t frag_off = chunk_offset<D>((lane & 7) + (lane & 8), lane >> 4);
     int stage = 0;
     for (int i = 0; i < mine; ++i) {
         cp_async_wait<C::kStages - 1>();
+        __syncwarp();   // every lane's copies of the block have landed
         if (i == 0 && p.trace && threadIdx.x == 0 && sm.tr[kTrFirstBlock] == 0) sm.tr[kTrFirstBlock] = globaltimer_ns();
         const int valid = ntok - (warp + kWarps * i) * kBlockRows;   // tokens of this block (16 or more: all)
         if ((i & 31) == 0) {
@@ -295,22 +281,33 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
             v_now = v_next;
         }
         const float ks = __shfl_sync(kFull, k_now, i & 31), vs = __shfl_sync(kFull, v_now, i & 31);
-        const uint32_t src = ring + stage * C::kBlockBytes + lane * 16;
-
         // S^T = K Q^T: rows g and g + 8 are tokens g and g + 8
+        const uint32_t src = ring + stage * C::kBlockBytes + frag_off;
         float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};   // two chains, for the product's latency
 #pragma unroll
-        for (int x = 0; x < C::kKPieces; x += 2) {
-            const uint4 ka = lds128(src + x * 512), kb = lds128(src + (x + 1) * 512);
-            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                uint32_t a0, a1, a2, a3;
-                widen4(wa[y], a0, a2);
-                widen4(wb[y], a1, a3);
-                mma_f16(y & 1 ? s2 : s, a0, a1, a2, a3, qb[2 * x + y][0], qb[2 * x + y][1]);
-            }
+        for (int c = 0; c < C::kChunks; c += 2) {
+            uint32_t w[4], a0, a1, a2, a3;
+            ldsm_x4(w, src ^ (c << 4));
+            widen4(w[0], a0, a2);
+            widen4(w[1], a1, a3);
+            mma_f16(s, a0, a1, a2, a3, qb[c][0], qb[c][1]);
+            widen4(w[2], a0, a2);
+            widen4(w[3], a1, a3);
+            mma_f16(s2, a0, a1, a2, a3, qb[c + 1][0], qb[c + 1][1]);
         }
+        // V to registers, and the stage is free for its next block
+        uint32_t vf[C::kChunks / 2][4];
+#pragma unroll
+        for (int c = 0; c < C::kChunks; c += 2) ldsm_x4_trans(vf[c / 2], (src ^ (c << 4)) + C::kMatBytes);
+        __syncwarp();
+        const int next = i + C::kStages;
+        if (next < mine) {
+            if ((next & 31) == 0) fetch_batch(next);
+            issue(next, stage);
+        }
+        cp_async_commit();
+        stage = stage + 1 == C::kStages ? 0 : stage + 1;
+
         const float sc0 = ks * qs[0], sc1 = ks * qs[1];
         float z[4] = {(s[0] + s2[0]) * sc0, (s[1] + s2[1]) * sc1, (s[2] + s2[2]) * sc0, (s[3] + s2[3]) * sc1};
         if (valid < kBlockRows) {
@@ -374,54 +371,27 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
             pb[0][1] = transpose8(pick(part0, part1, hb, lb));
         }
 
-        // O^T += V^T P^T: rows g and g + 8 of tile n are dimensions (D / 8) g + 2n and + 1
-        const uint32_t vsrc = ring + stage * C::kBlockBytes + C::kKPieces * 512 + lane * C::kVBytes;
-        uint32_t vw_[4][C::kVBytes / 4];
+        // O^T += V^T P^T: rows g and g + 8 of tile c are dimensions 16 c + 2 g and + 1.  A
+        // transposed word holds (token 2t: both dimensions), (token 2t + 1: both)
+        if (valid < kBlockRows) {   // slots past the row's end may hold anything, NaN codes too (0 * NaN = NaN)
+            const uint32_t lo = (2 * t < valid ? 0xffffu : 0u) | (2 * t + 1 < valid ? 0xffff0000u : 0u);
+            const uint32_t hi = (2 * t + 8 < valid ? 0xffffu : 0u) | (2 * t + 9 < valid ? 0xffff0000u : 0u);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            if constexpr (D == 128) {
-                const uint4 r = lds128(vsrc + x * 512);
-                vw_[x][0] = r.x;
-                vw_[x][1] = r.y;
-                vw_[x][2] = r.z;
-                vw_[x][3] = r.w;
-            } else {
-                const uint2 r = lds64(vsrc + x * 256);
-                vw_[x][0] = r.x;
-                vw_[x][1] = r.y;
+            for (int c = 0; c < C::kChunks / 2; ++c) {
+                vf[c][0] &= lo;
+                vf[c][1] &= hi;
+                vf[c][2] &= lo;
+                vf[c][3] &= hi;
             }
         }
-        if (valid < kBlockRows) {   // slots past the row's end may hold anything, NaN codes too (0 * NaN = NaN)
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                if (2 * t + (x & 1) + (x >> 1) * 8 >= valid)
-#pragma unroll
-                    for (int y = 0; y < C::kVBytes / 4; ++y) vw_[x][y] = 0u;
-        }
-#pragma unroll
-        for (int y = 0; y < C::kVBytes / 4; ++y) {
-            // (token pair, dimension) order: two tokens' bytes of one dimension side by side
-            const uint32_t t01 = __byte_perm(vw_[0][y], vw_[1][y], 0x5140), t23 = __byte_perm(vw_[0][y], vw_[1][y], 0x7362);
-            const uint32_t u01 = __byte_perm(vw_[2][y], vw_[3][y], 0x5140), u23 = __byte_perm(vw_[2][y], vw_[3][y], 0x7362);
+        for (int c = 0; c < C::kChunks; ++c) {
             uint32_t a0, a1, a2, a3;
-            widen4(t01, a0, a1);
-            widen4(u01, a2, a3);
+            widen4(__byte_perm(vf[c / 2][2 * (c & 1)], 0, 0x3120), a0, a1);
+            widen4(__byte_perm(vf[c / 2][2 * (c & 1) + 1], 0, 0x3120), a2, a3);
 #pragma unroll
-            for (int x = 0; x < C::kParts; ++x) mma_f16(o[x][2 * y], a0, a1, a2, a3, pb[x][0], pb[x][1]);
-            widen4(t23, a0, a1);
-            widen4(u23, a2, a3);
-#pragma unroll
-            for (int x = 0; x < C::kParts; ++x) mma_f16(o[x][2 * y + 1], a0, a1, a2, a3, pb[x][0], pb[x][1]);
+            for (int x = 0; x < C::kParts; ++x) mma_f16(o[x][c], a0, a1, a2, a3, pb[x][0], pb[x][1]);
         }
-
-        // the slot is read (by this thread alone): its next block
-        const int next = i + C::kStages;
-        if (next < mine) {
-            if ((next & 31) == 0) fetch_batch(next);
-            issue(next, stage);
-        }
-        cp_async_commit();
-        stage = stage + 1 == C::kStages ? 0 : stage + 1;
     }
     trace_stamp(sm, p, kTrStreamEnd);
 
@@ -434,31 +404,25 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
     }
     poisoned = __any_sync(kFull, poisoned) ? 1 : 0;
     __syncwarp();   // every lane has read its slots: the ring takes the partial
-    float* acc = reinterpret_cast<float*>(sm.ring[warp]) + (D / 8) * g;
+    float* acc = reinterpret_cast<float*>(sm.ring[warp]) + 2 * g;
 #pragma unroll
-    for (int n = 0; n < D / 16; n += 2) {
-        float f[2][4];   // columns 2t, 2t + 1: four dimensions
+    for (int n = 0; n < D / 16; ++n) {
+        float f[4];   // column 2t: dimensions 16 n + 2 g and + 1; column 2t + 1: the same
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            f[c][0] = o[0][n][c];
-            f[c][1] = o[0][n][2 + c];
-            f[c][2] = o[0][n + 1][c];
-            f[c][3] = o[0][n + 1][2 + c];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if constexpr (C::kParts == 2) f[c][k] += o[1][n + k / 2][2 * (k & 1) + c];
-                else if constexpr (G > 1) f[c][k] += __shfl_xor_sync(kFull, f[c][k], G / 2);
-            }
+        for (int k = 0; k < 4; ++k) {
+            f[k] = o[0][n][(k >> 1) + 2 * (k & 1)];
+            if constexpr (C::kParts == 2) f[k] += o[1][n][(k >> 1) + 2 * (k & 1)];
+            else if constexpr (G > 1) f[k] += __shfl_xor_sync(kFull, f[k], G / 2);
         }
         if constexpr (G == 1) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) f[0][k] += f[1][k];
+            f[0] += f[2];
+            f[1] += f[3];
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c)
             if (2 * t + c < G)
-                *reinterpret_cast<float4*>(acc + (2 * t + c) * Q8Smem<D, G>::kAccRow + 2 * n) =
-                    make_float4(f[c][0] * vref, f[c][1] * vref, f[c][2] * vref, f[c][3] * vref);
+                *reinterpret_cast<float2*>(acc + (2 * t + c) * Q8Smem<D, G>::kAccRow + 16 * n) =
+                    make_float2(f[2 * c] * vref, f[2 * c + 1] * vref);
     }
     if (g == 0) {
 #pragma unroll
