@@ -39,6 +39,8 @@
 namespace pkv {
 namespace {
 
+constexpr int kQueries = 4;   // query heads whose loads a thread has in flight at once
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -71,50 +73,51 @@ __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// What a row asks for, checked by the whole CTA before any byte of it is written.
+// What a row asks for, from its length and offsets alone (the same in every
+// thread); `bad`: status bits of a row that cannot take its tokens.
 struct RowWork {
     int tok0;      // its first token in k / v / q
     int n;         // new tokens
     int pos0;      // position of the first one
-    uint32_t bad;  // status bits of a row that cannot take its tokens
+    uint32_t bad;
 };
 
-template <int kThreadsT>
-__device__ RowWork row_work(const AppendTokensParams& p, int b) {
-    RowWork w;
-    w.pos0 = p.seq_lens[b];
-    w.tok0 = b;
-    w.n = 1;
-    uint32_t bad = 0;
+__device__ __forceinline__ RowWork row_work(const AppendTokensParams& p, int b) {
+    RowWork w{b, 1, p.seq_lens[b], 0u};
     if (p.cu) {
         const int end = p.cu[b + 1];
         w.tok0 = p.cu[b];
         if (w.tok0 < 0 || end < w.tok0 || end > p.T) {   // offsets that do not describe T tokens
-            bad = PKV_DEV_PLAN_MISMATCH;
+            w.bad = PKV_DEV_PLAN_MISMATCH;
             w.n = 0;
-        } else {
-            w.n = end - w.tok0;
+            return w;
         }
+        w.n = end - w.tok0;
     }
-    if (w.n > 0) {
-        if (w.pos0 < 0 || static_cast<int64_t>(w.pos0) + w.n > static_cast<int64_t>(p.max_pages) * p.page_size) {
-            bad = PKV_DEV_ROW_FULL;
-        } else {
-            const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
-            const int last = (w.pos0 + w.n - 1) / p.page_size;
-            for (int i = w.pos0 / p.page_size + static_cast<int>(threadIdx.x); i <= last; i += kThreadsT) {
-                const int page = row[i];
-                if (page < 0)
-                    bad |= PKV_DEV_ROW_FULL;
-                else if (page >= p.num_pages)
-                    bad |= PKV_DEV_PAGE_OOB;
-            }
-        }
-    }
-    w.bad = (__syncthreads_or(bad & PKV_DEV_ROW_FULL) ? PKV_DEV_ROW_FULL : 0u) |
-            (__syncthreads_or(bad & PKV_DEV_PAGE_OOB) ? PKV_DEV_PAGE_OOB : 0u) |
-            (__syncthreads_or(bad & PKV_DEV_PLAN_MISMATCH) ? PKV_DEV_PLAN_MISMATCH : 0u);
+    if (w.n > 0 && (w.pos0 < 0 || static_cast<int64_t>(w.pos0) + w.n > static_cast<int64_t>(p.max_pages) * p.page_size))
+        w.bad = PKV_DEV_ROW_FULL;
     return w;
+}
+
+// The rest of the check, over the table entries of all of the row's new tokens,
+// by the whole CTA (a barrier): a row is refused before any byte of it is written.
+__device__ __forceinline__ uint32_t row_pages_bad(const AppendTokensParams& p, int b, const RowWork& w) {
+    uint32_t bad = w.bad;
+    if (!bad && w.n > 0) {
+        const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
+        const int last = (w.pos0 + w.n - 1) / p.page_size;
+        for (int i = w.pos0 / p.page_size + static_cast<int>(threadIdx.x); i <= last; i += static_cast<int>(blockDim.x)) {
+            const int page = row[i];
+            if (page < 0)
+                bad |= PKV_DEV_ROW_FULL;
+            else if (page >= p.num_pages)
+                bad |= PKV_DEV_PAGE_OOB;
+        }
+    }
+    if (!__syncthreads_or(static_cast<int>(bad))) return 0u;
+    return (__syncthreads_or(bad & PKV_DEV_ROW_FULL) ? PKV_DEV_ROW_FULL : 0u) |
+           (__syncthreads_or(bad & PKV_DEV_PAGE_OOB) ? PKV_DEV_PAGE_OOB : 0u) |
+           (__syncthreads_or(bad & PKV_DEV_PLAN_MISMATCH) ? PKV_DEV_PLAN_MISMATCH : 0u);
 }
 
 // A thread's 16 elements of one head of one token: two runs of eight, at
@@ -185,10 +188,8 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t w, float ratio) {
     return pack_e4m3(lo.x * ratio, lo.y * ratio) | pack_e4m3(hi.x * ratio, hi.y * ratio) << 16;
 }
 
-__device__ __forceinline__ void requantise16(uint8_t* codes, float ratio) {
-    uint4 w = *reinterpret_cast<const uint4*>(codes);
-    w = make_uint4(requantise4(w.x, ratio), requantise4(w.y, ratio), requantise4(w.z, ratio), requantise4(w.w, ratio));
-    *reinterpret_cast<uint4*>(codes) = w;
+__device__ __forceinline__ uint4 requantise16(const uint4& w, float ratio) {
+    return make_uint4(requantise4(w.x, ratio), requantise4(w.y, ratio), requantise4(w.z, ratio), requantise4(w.w, ratio));
 }
 
 template <int D, bool Q8>
@@ -216,28 +217,14 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
         b = s_row;
         if (b >= 0) first = p.cu[b] / kBlockRows + 2 * b;
     }
-    RowWork w{};
-    if (b >= 0) w = row_work<kCta>(p, b);
-
-    // the lengths after: one CTA per row, whichever piece it holds
-    if (kvh == 0 && piece < p.B) {
-        const RowWork o = p.cu ? row_work<kCta>(p, piece) : w;
-        if (threadIdx.x == 0) {
-            p.new_lens[piece] = p.seq_lens[piece] + (o.bad ? 0 : o.n);
-            if (o.bad) atomicOr(p.status, o.bad);
-        }
-    }
-    if (b < 0 || w.bad || w.n == 0) return;
-
-    const int blk = w.pos0 / kBlockRows + (piece - first);       // 16-token block of the row
-    const int blk0 = blk * kBlockRows;
+    // a CTA without a piece (b < 0) still writes its row's length below
+    const RowWork w = b >= 0 ? row_work(p, b) : RowWork{0, 0, 0, 0u};
+    const int blk0 = (w.pos0 / kBlockRows + (piece - first)) * kBlockRows;   // first position of the 16-token block
     const int lo = max(blk0, w.pos0), hi = min(blk0 + kBlockRows, w.pos0 + w.n);
-    if (lo >= hi) return;
+    const bool work = !w.bad && lo < hi;
     const int slot = static_cast<int>(threadIdx.x) / kTpt, j = static_cast<int>(threadIdx.x) % kTpt;
     const int pos = blk0 + slot;
-    const bool live = pos >= lo && pos < hi;
-    const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + blk0 / p.page_size];
-    const size_t prow0 = static_cast<size_t>(page) * p.page_size + blk0 % p.page_size;   // token row of the block
+    const bool live = work && pos >= lo && pos < hi;
     const int64_t tok = static_cast<int64_t>(w.tok0) + (pos - w.pos0);
 
     // the thread's elements of a head
@@ -252,11 +239,53 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
         e1 = e0 + 8;
     }
 
-    Slice ks{}, vs{};
+    // all loads that need no page are in flight before the row's pages are checked
+    const int G = p.Hq / p.Hkv;
+    const uint16_t* qh = p.q + tok * p.q_stride + static_cast<int64_t>(kvh) * G * D;
+    uint16_t* oh = p.q_out + tok * p.q_out_stride + static_cast<int64_t>(kvh) * G * D;
+    Slice ks{}, vs{}, qs[kQueries] = {};
     if (live) {
         ks = load_slice(p.k + tok * p.k_stride + static_cast<int64_t>(kvh) * D, e0, e1);
         vs = load_slice(p.v + tok * p.v_stride + static_cast<int64_t>(kvh) * D, e0, e1);
+        if (p.q)
+#pragma unroll
+            for (int g = 0; g < kQueries; ++g)
+                if (g < G) qs[g] = load_slice(qh + g * D, e0, e1);
     }
+    const uint32_t bad = row_pages_bad(p, max(b, 0), w);
+
+    // the lengths after: one CTA per row, whichever piece it holds
+    if (kvh == 0 && piece < p.B) {
+        RowWork o = w;
+        uint32_t o_bad = bad;
+        if (p.cu) {
+            o = row_work(p, piece);
+            o_bad = row_pages_bad(p, piece, o);
+        }
+        if (threadIdx.x == 0) {
+            p.new_lens[piece] = p.seq_lens[piece] + (o_bad ? 0 : o.n);
+            if (o_bad) atomicOr(p.status, o_bad);
+        }
+    }
+    if (bad || !work) return;
+    const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + blk0 / p.page_size];
+    const size_t prow0 = static_cast<size_t>(page) * p.page_size + blk0 % p.page_size;   // token row of the block
+    const size_t head_off = ((prow0 + slot) * p.Hkv + kvh) * D;
+    // what the block holds already
+    [[maybe_unused]] const size_t sidx = prow0 / kBlockRows * p.Hkv + kvh;
+    [[maybe_unused]] float k_old = 0.f, v_old = 0.f;
+    [[maybe_unused]] uint4 k_held, v_held;
+    if constexpr (Q8) {
+        if (lo > blk0) {
+            k_old = p.k_scales[sidx];
+            v_old = p.v_scales[sidx];
+            if (pos < lo) {
+                k_held = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_pages) + head_off + 16 * j);
+                v_held = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.v_pages) + head_off + 16 * j);
+            }
+        }
+    }
+
     float c[8], sn[8];
     if (live && rotate) {
 #pragma unroll
@@ -280,8 +309,6 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
 
     float x[16];
     turn(ks, rotate, pairs, c, sn, x);
-    const size_t prow = prow0 + slot;
-    const size_t head_off = (prow * p.Hkv + kvh) * D;
     if constexpr (!Q8) {
         if (live) {
             store_bf16(static_cast<uint16_t*>(p.k_pages) + head_off, e0, e1, x);
@@ -304,10 +331,7 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
             s_max[0][threadIdx.x / 32] = km;
             s_max[1][threadIdx.x / 32] = vm;
         }
-        const size_t sidx = prow0 / kBlockRows * p.Hkv + kvh;
-        const bool held = lo > blk0;   // the block holds tokens of the row already
-        const float k_old = held ? p.k_scales[sidx] : 0.f, v_old = held ? p.v_scales[sidx] : 0.f;
-        __syncthreads();   // the maxima; and every thread has read the old scales
+        __syncthreads();   // the maxima; and every thread has read the old scales and codes
 #pragma unroll
         for (int i = 0; i < kCta / 32; ++i) {
             km = max(km, s_max[0][i]);
@@ -323,8 +347,8 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
             *reinterpret_cast<uint2*>(vp + e0) = codes8(y, vi);
             *reinterpret_cast<uint2*>(vp + e1) = codes8(y + 8, vi);
         } else if (pos < lo) {   // an older token of the block
-            if (k_new != k_old) requantise16(kp + 16 * j, k_old / k_new);
-            if (v_new != v_old) requantise16(vp + 16 * j, v_old / v_new);
+            if (k_new != k_old) *reinterpret_cast<uint4*>(kp + 16 * j) = requantise16(k_held, k_old / k_new);
+            if (v_new != v_old) *reinterpret_cast<uint4*>(vp + 16 * j) = requantise16(v_held, v_old / v_new);
         }
         if (threadIdx.x == 0) {
             p.k_scales[sidx] = k_new;
@@ -333,14 +357,19 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
     }
 
     if (p.q && live) {
-        const int G = p.Hq / p.Hkv;
-        const uint16_t* qh = p.q + tok * p.q_stride + static_cast<int64_t>(kvh) * G * D;
-        uint16_t* oh = p.q_out + tok * p.q_out_stride + static_cast<int64_t>(kvh) * G * D;
-        for (int g = 0; g < G; ++g) {   // in place is fine: a thread writes only what it has read
-            const Slice qs = load_slice(qh + g * D, e0, e1);
-            float z[16];
-            turn(qs, rotate, pairs, c, sn, z);
-            store_bf16(oh + g * D, e0, e1, z);
+        for (int g0 = 0; g0 < G; g0 += kQueries) {   // in place is fine: a thread writes only what it has read
+#pragma unroll
+            for (int g = 0; g < kQueries; ++g) {
+                if (g0 + g >= G) break;
+                if (g0 > 0) qs[g] = load_slice(qh + (g0 + g) * D, e0, e1);
+            }
+#pragma unroll
+            for (int g = 0; g < kQueries; ++g) {
+                if (g0 + g >= G) break;
+                float z[16];
+                turn(qs[g], rotate, pairs, c, sn, z);
+                store_bf16(oh + (g0 + g) * D, e0, e1, z);
+            }
         }
     }
 }

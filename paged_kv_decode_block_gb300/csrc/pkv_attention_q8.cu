@@ -38,6 +38,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_merge.cuh"
@@ -65,7 +67,7 @@ struct Q8Smem {
     static constexpr int kScratchBytes = kWarps * kRing;
     static constexpr int kAccRow = D + 4;   // floats of one head's partial (padded against bank conflicts)
     __device__ uint8_t* scratch() { return &ring[0][0]; }
-    alignas(128) uint8_t ring[kWarps][kRing];   // staged blocks; at the tile's end each warp's partial
+    alignas(1024) uint8_t ring[kWarps][kRing];   // staged blocks; at the tile's end each warp's partial
     float m[kWarps][G], l[kWarps][G];
     int poisoned[kWarps];
     float merge_m[G], merge_inv[G];
@@ -75,6 +77,7 @@ struct Q8Smem {
     int tile_fin, tile_splits, tile_base;
     uint64_t tr[kTraceWords];
     static_assert(G * kAccRow * 4 <= kRing, "a warp's partial fits its ring");
+    static_assert(kRing % 512 == 0 && Q8Cfg<D, G>::kBlockBytes % 512 == 0, "chunk addresses are formed by exclusive or");
 };
 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -174,6 +177,8 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
     constexpr int kRows = 32 / C::kChunks;
     const uint32_t pitch = static_cast<uint32_t>(p.Hkv) * D;   // bytes between tokens
     const uint32_t lane_off = tw.kvh * D + (lane / C::kChunks) * pitch + (lane % C::kChunks) * 16;
+    const uint32_t step = kRows * pitch;
+    const uint32_t lane_chunk = chunk_offset<D>(lane / C::kChunks, lane % C::kChunks);   // below the ring's alignment
     const uint8_t* kpool = reinterpret_cast<const uint8_t*>(p.k_pages) + lane_off;
     const uint8_t* vpool = reinterpret_cast<const uint8_t*>(p.v_pages) + lane_off;
     const uint32_t ring = smem_addr(sm.ring[warp]);
@@ -207,12 +212,17 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
     };
     auto issue = [&](int i, int stage) {   // block i of the current batch into `stage`
         const size_t off = static_cast<size_t>(__shfl_sync(kFull, row_i, i & 31)) * pitch;
-        const uint32_t dst = ring + stage * C::kBlockBytes;
+        const uint32_t dst = (ring + stage * C::kBlockBytes) ^ lane_chunk;
+        const uint8_t* ksrc = kpool + off;
+        const uint8_t* vsrc = vpool + off;
 #pragma unroll
         for (int x = 0; x < kBlockRows / kRows; ++x) {
-            const uint32_t at = dst + chunk_offset<D>(lane / C::kChunks + x * kRows, lane % C::kChunks);
-            cp_async16(at, kpool + off + x * kRows * pitch, policy);
-            cp_async16(at + C::kMatBytes, vpool + off + x * kRows * pitch, policy);
+            // (128-byte rows: row + 4 flips the exchange's bit 2)
+            const uint32_t at = (D == 128 && (x & 1) ? dst ^ 64u : dst) + x * kRows * D;
+            cp_async16(at, ksrc, policy);
+            cp_async16(at + C::kMatBytes, vsrc, policy);
+            ksrc += step;
+            vsrc += step;
         }
     };
 
@@ -487,7 +497,7 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
 
 template <int D, int G>
 __global__ void __launch_bounds__(kThreads, 2) attention_q8_kernel(const __grid_constant__ AttnQ8Params qp) {
-    extern __shared__ __align__(128) uint8_t smem_q8[];
+    extern __shared__ __align__(1024) uint8_t smem_q8[];
     Q8Smem<D, G>& sm = *reinterpret_cast<Q8Smem<D, G>*>(smem_q8);
     const AttnParams& p = qp.attn;
     if (p.trace && threadIdx.x == 0) {
@@ -613,9 +623,17 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q8_kernel(const __grid_
 template <int D, int G>
 cudaError_t launch_q8_t(const AttnQ8Params& p, int grid, cudaStream_t stream, bool cooperative) {
     constexpr size_t smem = sizeof(Q8Smem<D, G>);
-    cudaError_t e = cudaFuncSetAttribute(attention_q8_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    static std::atomic<uint64_t> configured{0};   // devices whose copy of the kernel may use that much
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(configured.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(attention_q8_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);

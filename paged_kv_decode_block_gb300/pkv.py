@@ -233,6 +233,19 @@ def _stream_handle(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_raw_current_stream = None
+
+
+def _raw_stream(device: int) -> int:
+    """cudaStream_t of torch's current stream on `device`."""
+    global _raw_current_stream
+    if _raw_current_stream is None:
+        import torch
+        _raw_current_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+                               (lambda d: torch.cuda.current_stream(d).cuda_stream))
+    return _raw_current_stream(device)
+
+
 class Plan:
     """An opaque pkv plan (see pkv_plan in include/pkv.h)."""
 
@@ -249,6 +262,14 @@ class Plan:
         _check(lib.pkv_plan(_ptr_i32(lens), _ptr_i32(table), self.page_size, ctypes.byref(self.geom),
                             ctypes.byref(o), ctypes.byref(h)), "pkv_plan")
         self._h = h
+        import torch
+        self.device = torch.cuda.current_device()   # the device the plan is bound to
+        # the shapes of the tensors that go with the plan
+        self.Hq, self.Hkv = int(Hq), int(Hkv)
+        self.pool_shape = (int(num_pages), self.page_size, self.Hkv, self.D)
+        self.scales_shape = (int(num_pages), self.page_size // Q8_BLOCK, self.Hkv)
+        self.table_shape, self.rows_shape = (int(B), int(max_pages)), (int(B),)
+        self.out_shape, self.lse_shape = (int(B), self.Hq, self.D), (int(B), self.Hq)
 
     @property
     def handle(self):
@@ -436,73 +457,72 @@ class Rotary:
                "pkv_rotary_init")
 
 
-def _shaped(t, name, shape, dtypes, device=None):
-    """Device address of a contiguous CUDA tensor of this shape on the plan's device."""
-    ptr = _dev_ptr(t, name, dtypes)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if device is not None and t.get_device() != device:
-        raise ValueError(f"{name}: on device {t.get_device()}, expected {device}")
-    return ptr
+def _arg(t, name, dtypes, shape, dev):
+    """Device address of a contiguous tensor of this type and shape on device `dev`."""
+    if t.shape == shape and t.dtype in dtypes and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _dev_ptr(t, name, dtypes)
+    raise ValueError(f"{name}: shape {tuple(t.shape)} on device {t.get_device()}, expected {shape} on device {dev}")
 
 
-def _token_ptr(t, name, tokens, heads, D):
+def _tokens_arg(t, name, shape, dev):
     """(address, elements between tokens) of bf16 [tokens][heads][D], each token's heads dense."""
-    if not getattr(t, "is_cuda", False):
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _bf16_types():
-        raise TypeError(f"{name}: dtype {t.dtype} not in {_bf16_types()}")
-    if tuple(t.shape) != (tokens, heads, D):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(tokens, heads, D)}")
-    if tokens == 0:
-        return None, 0
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+    if t.shape == shape and t.dtype in _BF16 and t.get_device() == dev:
+        T, heads, D = shape
+        if T == 0:
+            return None, 0
+        between, head, one = t.stride()
+        if one == 1 and (head == D or heads == 1):
+            return t.data_ptr(), (between if T > 1 else 0)
         raise ValueError(f"{name}: a token's heads must be dense (strides {t.stride()})")
-    return t.data_ptr(), (t.stride(0) if tokens > 1 else 0)
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _BF16:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {_BF16}")
+    raise ValueError(f"{name}: shape {tuple(t.shape)} on device {t.get_device()}, expected {shape} on device {dev}")
 
 
-_F8T = None
+_F8 = None
 
 
 def _f8_types():
-    global _F8T
-    if _F8T is None:
+    global _F8
+    if _F8 is None:
         import torch
-        _F8T = (torch.float8_e4m3fn, torch.uint8)
-    return _F8T
+        _F8 = (torch.float8_e4m3fn, torch.uint8)
+    return _F8
 
 
-def _append_tokens(what, k_new, v_new, k_pages, v_pages, scales, block_table, seq_lens, new_lens, plan, rotary, q, q_out,
-                   cu_tokens, stream):
-    bf = _bf16_types()
-    g, D = plan.geom, plan.D
-    dev = block_table.get_device()
-    T = int(k_new.shape[0])
-    t = Tokens()
-    t.total_tokens = T
-    t.k, t.k_stride = _token_ptr(k_new, "k_new", T, g.num_kv_heads, D)
-    t.v, t.v_stride = _token_ptr(v_new, "v_new", T, g.num_kv_heads, D)
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out: give both or neither")
-    if q is not None:
-        t.q, t.q_stride = _token_ptr(q, "q", T, g.num_q_heads, D)
-        t.q_out, t.q_out_stride = _token_ptr(q_out, "q_out", T, g.num_q_heads, D)
-    if cu_tokens is not None:
-        t.cu_tokens_d = _shaped(cu_tokens, "cu_tokens", (g.batch + 1,), _I32T, dev)
-    for x, name in ((k_new, "k_new"), (v_new, "v_new"), (q, "q"), (q_out, "q_out")):
-        if x is not None and x.get_device() != dev:
-            raise ValueError(f"{name}: on device {x.get_device()}, expected {dev}")
-    pool = (g.num_pages, plan.page_size, g.num_kv_heads, D)
-    types = bf if scales is None else _f8_types()
-    args = [_shaped(k_pages, "k_pages", pool, types, dev), _shaped(v_pages, "v_pages", pool, types, dev)]
-    if scales is not None:
-        blocks = (g.num_pages, plan.page_size // Q8_BLOCK, g.num_kv_heads)
-        args += [_shaped(scales[0], "k_scales", blocks, _F32T, dev), _shaped(scales[1], "v_scales", blocks, _F32T, dev)]
-    args += [_shaped(block_table, "block_table", (g.batch, g.max_pages_per_seq), _I32T, dev),
-             _shaped(seq_lens, "seq_lens", (g.batch,), _I32T, dev),
-             _shaped(new_lens, "new_lens", (g.batch,), _I32T, dev)]
-    rc = getattr(_lib or load(), what)(ctypes.byref(t), ctypes.byref(rotary.params) if rotary is not None else None,
-                                       *args, plan.handle, _stream_handle(stream))
+def _append_tokens(what, fn, k_new, v_new, k_pages, v_pages, scales, block_table, seq_lens, new_lens, plan, rotary, q,
+                   q_out, cu_tokens, stream):
+    bf, g, dev = _BF16 or _bf16_types(), plan.geom, plan.device
+    try:
+        T = k_new.shape[0]
+        kv = (T, plan.Hkv, plan.D)
+        k, k_stride = _tokens_arg(k_new, "k_new", kv, dev)
+        v, v_stride = _tokens_arg(v_new, "v_new", kv, dev)
+        qp = qo = None
+        q_stride = qo_stride = 0
+        if q is not None and q_out is not None:
+            heads = (T, plan.Hq, plan.D)
+            qp, q_stride = _tokens_arg(q, "q", heads, dev)
+            qo, qo_stride = _tokens_arg(q_out, "q_out", heads, dev)
+        elif q is not None or q_out is not None:
+            raise ValueError("q and q_out: give both or neither")
+        cu = _arg(cu_tokens, "cu_tokens", _I32T, (g.batch + 1,), dev) if cu_tokens is not None else None
+        types = bf if scales is None else _F8 or _f8_types()
+        pages = (_arg(k_pages, "k_pages", types, plan.pool_shape, dev), _arg(v_pages, "v_pages", types, plan.pool_shape, dev))
+        if scales is not None:
+            pages += (_arg(scales[0], "k_scales", _F32T, plan.scales_shape, dev),
+                      _arg(scales[1], "v_scales", _F32T, plan.scales_shape, dev))
+        rows = plan.rows_shape
+        rc = fn(ctypes.byref(Tokens(qp, qo, k, v, q_stride, qo_stride, k_stride, v_stride, cu, T)),
+                rotary.params if rotary is not None else None, *pages,
+                _arg(block_table, "block_table", _I32T, plan.table_shape, dev), _arg(seq_lens, "seq_lens", _I32T, rows, dev),
+                _arg(new_lens, "new_lens", _I32T, rows, dev), plan.handle,
+                _raw_stream(dev) if stream is None else _stream_handle(stream))
+    except AttributeError as e:
+        raise TypeError(f"{what}: arguments must be CUDA tensors ({e})") from None
     if rc:
         _check(rc, what)
 
@@ -512,34 +532,32 @@ def append_rotary(k_new, v_new, k_pages, v_pages, block_table, seq_lens, new_len
     """pkv_append_rotary: row b's tokens cu_tokens[b]..cu_tokens[b + 1] (without cu_tokens: its one
     token) go to positions seq_lens[b] on, keys and queries rotated; new_lens = the lengths after.
     k_new / v_new / q: bf16 [T][heads][D], also slices of one projection's output."""
-    _append_tokens("pkv_append_rotary", k_new, v_new, k_pages, v_pages, None, block_table, seq_lens, new_lens, plan,
-                   rotary, q, q_out, cu_tokens, stream)
+    _append_tokens("pkv_append_rotary", (_lib or load()).pkv_append_rotary, k_new, v_new, k_pages, v_pages, None,
+                   block_table, seq_lens, new_lens, plan, rotary, q, q_out, cu_tokens, stream)
 
 
 def append_q8(k_new, v_new, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, new_lens, plan: Plan,
               rotary: Rotary | None = None, q=None, q_out=None, cu_tokens=None, stream=None):
     """pkv_append_q8: append_rotary into an 8-bit cache (pages float8_e4m3fn [num_pages][page_size][Hkv][D],
     scales fp32 [num_pages][page_size // Q8_BLOCK][Hkv])."""
-    _append_tokens("pkv_append_q8", k_new, v_new, k_pages, v_pages, (k_scales, v_scales), block_table, seq_lens,
-                   new_lens, plan, rotary, q, q_out, cu_tokens, stream)
+    _append_tokens("pkv_append_q8", (_lib or load()).pkv_append_q8, k_new, v_new, k_pages, v_pages, (k_scales, v_scales),
+                   block_table, seq_lens, new_lens, plan, rotary, q, q_out, cu_tokens, stream)
 
 
 def decode_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, plan: Plan, out, lse, stream=None):
     """pkv_decode_q8: decode over an 8-bit cache (see append_q8)."""
-    bf = _bf16_types()
-    f8 = _f8_types()
-    g, D = plan.geom, plan.D
-    dev = block_table.get_device()
-    pool = (g.num_pages, plan.page_size, g.num_kv_heads, D)
-    blocks = (g.num_pages, plan.page_size // Q8_BLOCK, g.num_kv_heads)
-    heads = (g.batch, g.num_q_heads)
-    rc = (_lib or load()).pkv_decode_q8(
-        _shaped(q, "q", heads + (D,), bf, dev), _shaped(k_pages, "k_pages", pool, f8, dev),
-        _shaped(v_pages, "v_pages", pool, f8, dev), _shaped(k_scales, "k_scales", blocks, _F32T, dev),
-        _shaped(v_scales, "v_scales", blocks, _F32T, dev),
-        _shaped(block_table, "block_table", (g.batch, g.max_pages_per_seq), _I32T, dev),
-        _shaped(seq_lens, "seq_lens", (g.batch,), _I32T, dev), plan.handle,
-        _shaped(out, "out", heads + (D,), _F32T, dev), _shaped(lse, "lse", heads, _F32T, dev), _stream_handle(stream))
+    bf, f8, dev = _BF16 or _bf16_types(), _F8 or _f8_types(), plan.device
+    try:
+        rc = (_lib or load()).pkv_decode_q8(
+            _arg(q, "q", bf, plan.out_shape, dev), _arg(k_pages, "k_pages", f8, plan.pool_shape, dev),
+            _arg(v_pages, "v_pages", f8, plan.pool_shape, dev), _arg(k_scales, "k_scales", _F32T, plan.scales_shape, dev),
+            _arg(v_scales, "v_scales", _F32T, plan.scales_shape, dev),
+            _arg(block_table, "block_table", _I32T, plan.table_shape, dev),
+            _arg(seq_lens, "seq_lens", _I32T, plan.rows_shape, dev), plan.handle,
+            _arg(out, "out", _F32T, plan.out_shape, dev), _arg(lse, "lse", _F32T, plan.lse_shape, dev),
+            _raw_stream(dev) if stream is None else _stream_handle(stream))
+    except AttributeError as e:
+        raise TypeError(f"pkv_decode_q8: arguments must be CUDA tensors ({e})") from None
     if rc:
         _check(rc, "pkv_decode_q8")
 

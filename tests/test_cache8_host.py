@@ -122,12 +122,16 @@ def test_calls_without_a_plan_are_refused():
 def test_cpu_tensors_are_refused():
     class FakePlan:   # the checks come before the plan is used
         geom = pkv.Geom(1, 4, 1, 64, 4, 8)
-        page_size, D, handle = 16, 64, None
+        page_size, D, Hq, Hkv, handle, device = 16, 64, 4, 1, None, 0
+        pool_shape, scales_shape, table_shape, rows_shape = (8, 16, 1, 64), (8, 1, 1), (1, 4), (1,)
+        out_shape, lse_shape = (1, 4, 64), (1, 4)
     k = torch.zeros(1, 1, 64, dtype=torch.bfloat16)
     pages = torch.zeros(8, 16, 1, 64, dtype=torch.bfloat16)
     i = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(TypeError):
         pkv.append_rotary(k, k, pages, pages, torch.zeros(1, 4, dtype=torch.int32), i, i.clone(), FakePlan, None)
+    with pytest.raises(TypeError):
+        pkv.append_q8(None, k, pages, pages, None, None, torch.zeros(1, 4, dtype=torch.int32), i, i.clone(), FakePlan)
     with pytest.raises(TypeError):
         pkv.decode_q8(torch.zeros(1, 4, 64, dtype=torch.bfloat16), pages, pages, i, i, torch.zeros(1, 4, dtype=torch.int32),
                       i, FakePlan, k, k)
