@@ -13,7 +13,8 @@
 // The angle is reduced in integers: step[m] is inv_freq[m] / 2 pi in units of
 // 2^-64 turns, so p * step[m] mod 2^64 is the phase, exact but for step's own
 // rounding however far the position; its nearest quarter turn is taken off in
-// integers too, and sincospif sees at most an eighth of a turn.
+// integers too, which leaves at most an eighth of a turn for the series of sin
+// and cos.
 // An e4m3 block stores x / s with s the least power of two that brings the
 // largest finite |x| of the block's new tokens to at most 448, and at least the
 // scale of the tokens the block already holds.  e4m3 keeps four significant
@@ -39,6 +40,7 @@
 namespace pkv {
 namespace {
 
+constexpr uint32_t kInfinity = 0x7f800000u;
 constexpr int kQueries = 4;   // query heads whose loads a thread has in flight at once
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -59,10 +61,55 @@ __device__ __forceinline__ float2 unpack_e4m3(uint32_t two) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// |x| if x is finite, else 0: what the block's scale is taken from.
-__device__ __forceinline__ uint32_t finite_magnitude(float x) {
-    const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
-    return u < 0x7f800000u ? u : 0u;
+// Largest magnitude of 16 values, as bits: NaN is passed over; 0x7f800000 if one is infinite.
+__device__ __forceinline__ uint32_t magnitude16(const float (&x)[16]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
+    return __float_as_uint(m);
+}
+
+// The same of the finite ones among them.
+__device__ __forceinline__ uint32_t finite_magnitude16(const float (&x)[16]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t u = __float_as_uint(x[i]) & 0x7fffffffu;
+        if (u < kInfinity) m = max(m, u);
+    }
+    return m;
+}
+
+// Largest of all threads' values, over the CTA (one barrier; `part` is shared scratch).
+template <int kWarpsT>
+__device__ __forceinline__ void cta_max(uint32_t& a, uint32_t& b, uint32_t (&part)[2][kWarpsT]) {
+    a = __reduce_max_sync(kFull, a);
+    b = __reduce_max_sync(kFull, b);
+    if (threadIdx.x % 32 == 0) {
+        part[0][threadIdx.x / 32] = a;
+        part[1][threadIdx.x / 32] = b;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWarpsT; ++i) {
+        a = max(a, part[0][i]);
+        b = max(b, part[1][i]);
+    }
+}
+
+// sin and cos of an angle of at most an eighth of a turn (pi / 4): their power
+// series to the terms below 2^-25.
+__device__ __forceinline__ void sincos_eighth(float a, float& s, float& c) {
+    const float u = a * a;
+    s = fmaf(u, 1.f / 362880, -1.f / 5040);
+    s = fmaf(u, s, 1.f / 120);
+    s = fmaf(u, s, -1.f / 6);
+    s = fmaf(a * u, s, a);
+    c = fmaf(u, -1.f / 3628800, 1.f / 40320);
+    c = fmaf(u, c, -1.f / 720);
+    c = fmaf(u, c, 1.f / 24);
+    c = fmaf(u, c, -0.5f);
+    c = fmaf(u, c, 1.f);
 }
 
 // The least power of two s in [2^-120, 2^120] with amax / s <= 448 = 0.875 * 2^9.
@@ -172,12 +219,16 @@ __device__ __forceinline__ void store_bf16(uint16_t* head, int e0, int e1, const
         make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]), pack_bf16(x[12], x[13]), pack_bf16(x[14], x[15]));
 }
 
-// Eight values to eight codes.  A value that is not finite becomes NaN (x * 0
-// is NaN for it and +-0 otherwise), not the largest code.
-__device__ __forceinline__ uint2 codes8(const float* x, float inv) {
+// Eight values to eight codes.  NaN stays NaN; an infinite value becomes NaN too,
+// not the largest code, where the block is known to hold one (x * 0 is NaN for
+// it and +-0 otherwise).
+__device__ __forceinline__ uint2 codes8(const float* x, float inv, bool infinite) {
     float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], 0.f, x[i] * inv);
+    for (int i = 0; i < 8; ++i) y[i] = x[i] * inv;
+    if (infinite)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], 0.f, y[i]);
     return make_uint2(pack_e4m3(y[0], y[1]) | pack_e4m3(y[2], y[3]) << 16,
                       pack_e4m3(y[4], y[5]) | pack_e4m3(y[6], y[7]) << 16);
 }
@@ -290,11 +341,13 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
     if (live && rotate) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t turn32 = static_cast<uint32_t>((p.rot.step[8 * j + i] * static_cast<uint64_t>(pos)) >> 32);
-            const uint32_t quarter = (turn32 + 0x20000000u) >> 30;                       // nearest quarter turn
-            const int rest = static_cast<int>(turn32 - (quarter << 30));                 // in [-2^29, 2^29)
+            const uint64_t step = p.rot.step[8 * j + i];
+            const uint32_t at = static_cast<uint32_t>(pos);
+            const uint32_t turns = __umulhi(static_cast<uint32_t>(step), at) + static_cast<uint32_t>(step >> 32) * at;
+            const uint32_t quarter = (turns + 0x20000000u) >> 30;          // nearest quarter turn
+            const int rest = static_cast<int>(turns - (quarter << 30));    // in [-2^29, 2^29)
             float s0, c0;
-            sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &s0, &c0);      // rest * 2^-31 half turns
+            sincos_eighth(static_cast<float>(rest) * 1.4629180792671596e-9f, s0, c0);   // * 2 pi / 2^32
             s0 *= p.rot.scale;
             c0 *= p.rot.scale;
             const bool odd = quarter & 1u;
@@ -319,33 +372,24 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
     } else {
         float y[16];
         turn(vs, false, false, c, sn, y);
-        uint32_t km = 0, vm = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {   // (a slot without a new token holds zeros)
-            km = max(km, finite_magnitude(x[i]));
-            vm = max(vm, finite_magnitude(y[i]));
-        }
-        km = __reduce_max_sync(kFull, km);
-        vm = __reduce_max_sync(kFull, vm);
-        if (threadIdx.x % 32 == 0) {
-            s_max[0][threadIdx.x / 32] = km;
-            s_max[1][threadIdx.x / 32] = vm;
-        }
-        __syncthreads();   // the maxima; and every thread has read the old scales and codes
-#pragma unroll
-        for (int i = 0; i < kCta / 32; ++i) {
-            km = max(km, s_max[0][i]);
-            vm = max(vm, s_max[1][i]);
+        uint32_t km = magnitude16(x), vm = magnitude16(y);   // (a slot without a new token holds zeros)
+        cta_max(km, vm, s_max);   // and every thread has read the old scales and codes
+        const bool infinite = km == kInfinity || vm == kInfinity;
+        if (infinite) {
+            km = finite_magnitude16(x);
+            vm = finite_magnitude16(y);
+            __syncthreads();   // s_max is read
+            cta_max(km, vm, s_max);
         }
         const float k_new = fmaxf(block_scale(km), k_old), v_new = fmaxf(block_scale(vm), v_old);
         uint8_t* kp = static_cast<uint8_t*>(p.k_pages) + head_off;
         uint8_t* vp = static_cast<uint8_t*>(p.v_pages) + head_off;
         if (live) {
             const float ki = 1.f / k_new, vi = 1.f / v_new;
-            *reinterpret_cast<uint2*>(kp + e0) = codes8(x, ki);
-            *reinterpret_cast<uint2*>(kp + e1) = codes8(x + 8, ki);
-            *reinterpret_cast<uint2*>(vp + e0) = codes8(y, vi);
-            *reinterpret_cast<uint2*>(vp + e1) = codes8(y + 8, vi);
+            *reinterpret_cast<uint2*>(kp + e0) = codes8(x, ki, infinite);
+            *reinterpret_cast<uint2*>(kp + e1) = codes8(x + 8, ki, infinite);
+            *reinterpret_cast<uint2*>(vp + e0) = codes8(y, vi, infinite);
+            *reinterpret_cast<uint2*>(vp + e1) = codes8(y + 8, vi, infinite);
         } else if (pos < lo) {   // an older token of the block
             if (k_new != k_old) *reinterpret_cast<uint4*>(kp + 16 * j) = requantise16(k_held, k_old / k_new);
             if (v_new != v_old) *reinterpret_cast<uint4*>(vp + 16 * j) = requantise16(v_held, v_old / v_new);

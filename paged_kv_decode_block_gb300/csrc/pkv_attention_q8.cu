@@ -161,16 +161,10 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
     const AttnParams& p = qp.attn;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = lane >> 2, t = lane & 3;
-    if (tw.lazy) tile_finish(p, tw);
-    if (threadIdx.x == 0) {
-        sm.tile_fin = tw.finalize;
-        sm.tile_splits = tw.splits;
-        sm.tile_base = tw.slot - tw.split;
-    }
-    const int ntok = tw.t1 > tw.t0 ? tw.t1 - tw.t0 : 0;
-    const int nblk = (ntok + kBlockRows - 1) / kBlockRows;
-    const int mine = nblk > warp ? (nblk - warp + kWarps - 1) / kWarps : 0;   // this warp's blocks: warp + 8 i
-    int poisoned = tw.poisoned;
+    // A queue tile's planned pages are copied at once; the row's length, which masks
+    // its last block, is read meanwhile.
+    const int nplan = (max(tw.t_stream - tw.t0, 0) + kBlockRows - 1) / kBlockRows;
+    int mine = nplan > warp ? (nplan - warp + kWarps - 1) / kWarps : 0;   // this warp's blocks: warp + 8 i
 
     // the lane's share of a copy: 16-byte chunk lane % kChunks of rows lane /
     // kChunks, + kRows, ... (a warp moves whole rows)
@@ -189,7 +183,7 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
     // pool and its scales.  The copies run ahead of the arithmetic, so the scales
     // of the batch being copied (k/v_next) and of the one being reduced differ for
     // a few blocks; the table entries are read one batch further ahead.
-    int row_i = 0, entry = 0;
+    int row_i = 0, entry = 0, poisoned = 0;
     float k_next = 0.f, v_next = 0.f, k_now = 0.f, v_now = 0.f;
     auto block_token = [&](int i) { return tw.t0 + (warp + kWarps * i) * kBlockRows; };
     auto read_entry = [&](int i0) {
@@ -226,14 +220,31 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         }
     };
 
-    // the ring's first blocks, then q while they are in flight
+    // the first table entries, q and the row's length in one round trip
     read_entry(0);
+    uint2 q_raw[D / 16];   // head g % G: elements 16 j + 4 t .. + 3
+    {
+        const uint16_t* qh = p.q + (static_cast<size_t>(tw.b) * p.Hq + tw.kvh * G + g % G) * D + t * 4;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) q_raw[j] = __ldg(reinterpret_cast<const uint2*>(qh + 16 * j));
+    }
+    if (tw.lazy) tile_finish(p, tw);
+    // the ring's first blocks
     fetch_batch(0);
 #pragma unroll
     for (int s = 0; s < C::kStages; ++s) {
         if (s < mine) issue(s, s);
         cp_async_commit();
     }
+    if (threadIdx.x == 0) {
+        sm.tile_fin = tw.finalize;
+        sm.tile_splits = tw.splits;
+        sm.tile_base = tw.slot - tw.split;
+    }
+    const int ntok = tw.t1 > tw.t0 ? tw.t1 - tw.t0 : 0;
+    const int nblk = (ntok + kBlockRows - 1) / kBlockRows;   // at most nplan
+    mine = nblk > warp ? (nblk - warp + kWarps - 1) / kWarps : 0;
+    poisoned |= tw.poisoned;
     // B fragments of Q^T: column g is query head g % G (so with G <= 4 the columns
     // repeat the group: one copy serves P's hi parts, the next its lo parts).  A K
     // word is four neighbouring elements, 16 j + 4 t on for k-step j, so q's fragments
@@ -241,15 +252,11 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
     uint32_t qb[D / 16][2];
     float qs[2];   // what the dot products of columns 2t, 2t + 1 are multiplied by, before ks
     {
-        uint2 raw[D / 16];
-        const uint16_t* qh = p.q + (static_cast<size_t>(tw.b) * p.Hq + tw.kvh * G + g % G) * D + t * 4;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) raw[j] = __ldg(reinterpret_cast<const uint2*>(qh + 16 * j));
         uint32_t big = 0;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
-            big = max(big, max((raw[j].x & 0x7fffu) << 16, raw[j].x & 0x7fff0000u));
-            big = max(big, max((raw[j].y & 0x7fffu) << 16, raw[j].y & 0x7fff0000u));
+            big = max(big, max((q_raw[j].x & 0x7fffu) << 16, q_raw[j].x & 0x7fff0000u));
+            big = max(big, max((q_raw[j].y & 0x7fffu) << 16, q_raw[j].y & 0x7fff0000u));
         }
         big = max(big, __shfl_xor_sync(kFull, big, 1));
         big = max(big, __shfl_xor_sync(kFull, big, 2));
@@ -260,8 +267,8 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         qs[1] = __shfl_sync(kFull, up, 8 * t + 4);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
-            qb[j][0] = pack_half(__uint_as_float(raw[j].x << 16) * down, __uint_as_float(raw[j].x & 0xffff0000u) * down);
-            qb[j][1] = pack_half(__uint_as_float(raw[j].y << 16) * down, __uint_as_float(raw[j].y & 0xffff0000u) * down);
+            qb[j][0] = pack_half(__uint_as_float(q_raw[j].x << 16) * down, __uint_as_float(q_raw[j].x & 0xffff0000u) * down);
+            qb[j][1] = pack_half(__uint_as_float(q_raw[j].y << 16) * down, __uint_as_float(q_raw[j].y & 0xffff0000u) * down);
         }
     }
     // which part of P the lane's columns 2t, 2t + 1 carry: 0 hi, 1 lo, 2 none
@@ -413,7 +420,8 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         l[1] += __shfl_xor_sync(kFull, l[1], x);
     }
     poisoned = __any_sync(kFull, poisoned) ? 1 : 0;
-    __syncwarp();   // every lane has read its slots: the ring takes the partial
+    cp_async_wait<0>();   // (planned blocks past the row's end may still be on their way)
+    __syncwarp();         // every lane has read its slots: the ring takes the partial
     float* acc = reinterpret_cast<float*>(sm.ring[warp]) + 2 * g;
 #pragma unroll
     for (int n = 0; n < D / 16; ++n) {
@@ -582,6 +590,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q8_kernel(const __grid_
             tw.t1 = 0;
             if (threadIdx.x == 0) atomicOr(&p.ctr->status, static_cast<uint32_t>(PKV_DEV_PLAN_MISMATCH));
         }
+        tw.t_stream = tw.t1;
     } else if (p.route == kRouteQueue) {
         if (static_cast<int>(blockIdx.x) >= p.num_tiles) {   // launched only for the neutral rows
             launch_dependents();
@@ -603,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q8_kernel(const __grid_
         const int pe = max(0, min((tw.split + 1) * p.chunk_pages, pages));
         tw.t0 = pb * p.page_size;
         tw.t1 = tw.poisoned ? tw.t0 : min(pe * p.page_size, n);
+        tw.t_stream = tw.t1;
         tw.finalize = p.max_splits == 1;
         tw.splits = p.max_splits;
         tw.slot = blockIdx.x;
