@@ -784,7 +784,11 @@ int enqueue_decode(pkv_plan_t p, const void* q, const void* k_pages, const void*
                             src, q8 == nullptr);
     if (rc) return rc;
     auto launch = [&](bool cooperative) {
-        if (q8) return pkv::launch_attention_q8(pkv::AttnQ8Params{a, q8->k, q8->v}, grid, s, cooperative);
+        if (q8) {
+            const uint32_t bpp = static_cast<uint32_t>(p->page_size / pkv::kBlockRows);
+            const uint32_t magic = bpp > 1 ? static_cast<uint32_t>((1ull << 32) / bpp + 1) : 0u;
+            return pkv::launch_attention_q8(pkv::AttnQ8Params{a, q8->k, q8->v, magic}, grid, s, cooperative);
+        }
         return pkv::launch_attention(a, p->kmap, p->vmap, grid, s, cooperative);
     };
 

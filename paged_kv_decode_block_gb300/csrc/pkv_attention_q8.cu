@@ -39,6 +39,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -54,9 +55,10 @@ constexpr float kGrowth = 14.f;      // and holds until a weight would pass 2^14
 template <int D, int G>
 struct Q8Cfg {
     static constexpr int kBlockBytes = 2 * kBlockRows * D;   // K and V codes of one block
-    static constexpr int kStages = D == 128 ? 3 : 6;         // 12 KB in flight per warp, 96 KB per CTA
+    static constexpr int kStages = D == 128 ? 3 : 5;         // 12 or 10 KB in flight per warp, 80-96 KB per CTA
     static constexpr int kMatBytes = kBlockRows * D;         // one K or V block: 16 rows of D bytes
     static constexpr int kChunks = D / 16;                   // 16-byte chunks of a row
+    static constexpr int kPairFrom = D == 128 ? 40 : 16;     // blocks a warp from which two are reduced at a time
     static constexpr int kParts = G == 8 ? 2 : 1;            // P^T column tiles: the lo parts share one while 2G <= 8
     static_assert(D == 64 || D == 128, "head_dim");
 };
@@ -136,12 +138,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// Two columns' f16: each takes its half of `hi` (part 0), of `lo` (1), or zero (2).
-__device__ __forceinline__ uint32_t pick(int part0, int part1, uint32_t hi, uint32_t lo) {
-    const uint32_t a = part0 == 0 ? hi : part0 == 1 ? lo : 0u, b = part1 == 0 ? hi : part1 == 1 ? lo : 0u;
-    return __byte_perm(a, b, 0x7610);
-}
-
 // The least power of two not below x > 0 (x a finite fp32; the exponent saturates at 2^126).
 __device__ __forceinline__ float power_of_two_above(float x) {
     const uint32_t u = __float_as_uint(x);
@@ -185,9 +181,12 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
     // a few blocks; the table entries are read one batch further ahead.
     int row_i = 0, entry = 0, poisoned = 0;
     float k_next = 0.f, v_next = 0.f, k_now = 0.f, v_now = 0.f;
-    auto block_token = [&](int i) { return tw.t0 + (warp + kWarps * i) * kBlockRows; };
+    auto row_block = [&](int i) { return tw.t0 / kBlockRows + warp + kWarps * i; };   // 16-token block of the row
+    auto page_of = [&](int blk) {   // blk / (blocks per page)
+        return qp.page_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(blk), qp.page_magic)) : blk;
+    };
     auto read_entry = [&](int i0) {
-        if (i0 + lane < mine) entry = __ldg(bt_row + block_token(i0 + lane) / p.page_size);
+        if (i0 + lane < mine) entry = __ldg(bt_row + page_of(row_block(i0 + lane)));
     };
     auto fetch_batch = [&](int i0) {
         if (i0 + lane < mine) {
@@ -197,7 +196,8 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
                 poisoned = 1;
                 page = 0;
             }
-            row_i = page * p.page_size + block_token(i0 + lane) % p.page_size;
+            const int blk = row_block(i0 + lane);
+            row_i = page * p.page_size + blk * kBlockRows - page_of(blk) * p.page_size;
             const size_t s = static_cast<size_t>(row_i / kBlockRows) * p.Hkv + tw.kvh;
             k_next = __ldg(qp.k_scales + s);
             v_next = __ldg(qp.v_scales + s);
@@ -271,8 +271,9 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
             qb[j][1] = pack_half(__uint_as_float(q_raw[j].y << 16) * down, __uint_as_float(q_raw[j].y & 0xffff0000u) * down);
         }
     }
-    // which part of P the lane's columns 2t, 2t + 1 carry: 0 hi, 1 lo, 2 none
-    const int part0 = G == 8 ? 0 : min(2 * t / G, 2), part1 = G == 8 ? 0 : min((2 * t + 1) / G, 2);
+    // Where the parts share a column tile, columns 2t and 2t + 1 carry w - part * f16(w):
+    // with part 0 P's hi parts, with part 1 its lo parts
+    const float part0 = 2 * t < G ? 0.f : 1.f, part1 = 2 * t + 1 < G ? 0.f : 1.f;
 
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // columns 2t, 2t + 1: reference, this lane's share of the sum
     float vref = 1.1754944e-38f;       // power of two not below any block's V scale so far
@@ -288,128 +289,168 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
     // a lane's row address for ldmatrix: matrices 0, 1 are rows 0-7 and 8-15 of a chunk, 2, 3 of the next chunk
     const uint32_t frag_off = chunk_offset<D>((lane & 7) + (lane & 8), lane >> 4);
     int stage = 0;
-    for (int i = 0; i < mine; ++i) {
-        cp_async_wait<C::kStages - 1>();
-        __syncwarp();   // every lane's copies of the block have landed
-        if (i == 0 && p.trace && threadIdx.x == 0 && sm.tr[kTrFirstBlock] == 0) sm.tr[kTrFirstBlock] = globaltimer_ns();
-        const int valid = ntok - (warp + kWarps * i) * kBlockRows;   // tokens of this block (16 or more: all)
-        if ((i & 31) == 0) {
-            k_now = k_next;
-            v_now = v_next;
-        }
-        const float ks = __shfl_sync(kFull, k_now, i & 31), vs = __shfl_sync(kFull, v_now, i & 31);
-        // S^T = K Q^T: rows g and g + 8 are tokens g and g + 8
-        const uint32_t src = ring + stage * C::kBlockBytes + frag_off;
-        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};   // two chains, for the product's latency
-#pragma unroll
-        for (int c = 0; c < C::kChunks; c += 2) {
-            uint32_t w[4], a0, a1, a2, a3;
-            ldsm_x4(w, src ^ (c << 4));
-            widen4(w[0], a0, a2);
-            widen4(w[1], a1, a3);
-            mma_f16(s, a0, a1, a2, a3, qb[c][0], qb[c][1]);
-            widen4(w[2], a0, a2);
-            widen4(w[3], a1, a3);
-            mma_f16(s2, a0, a1, a2, a3, qb[c + 1][0], qb[c + 1][1]);
-        }
-        // V to registers, and the stage is free for its next block
-        uint32_t vf[C::kChunks / 2][4];
-#pragma unroll
-        for (int c = 0; c < C::kChunks; c += 2) ldsm_x4_trans(vf[c / 2], (src ^ (c << 4)) + C::kMatBytes);
-        __syncwarp();
-        const int next = i + C::kStages;
-        if (next < mine) {
-            if ((next & 31) == 0) fetch_batch(next);
-            issue(next, stage);
-        }
-        cp_async_commit();
-        stage = stage + 1 == C::kStages ? 0 : stage + 1;
-
-        const float sc0 = ks * qs[0], sc1 = ks * qs[1];
-        float z[4] = {(s[0] + s2[0]) * sc0, (s[1] + s2[1]) * sc1, (s[2] + s2[2]) * sc0, (s[3] + s2[3]) * sc1};
-        if (valid < kBlockRows) {
-            if (g >= valid) z[0] = z[1] = -INFINITY;
-            if (g + 8 >= valid) z[2] = z[3] = -INFINITY;
-        }
-
-        // a reference moves when one of its weights would pass 2^14 (m = -inf: at
-        // once), or the block's V scale passes r; neither happens often, so the
-        // block's exact maximum is found only then
-        const bool big = fmaxf(z[0], z[2]) > m[0] + kGrowth || fmaxf(z[1], z[3]) > m[1] + kGrowth;
-        if (__any_sync(kFull, big) || fabsf(vs) > vref) {
-            float bm0 = fmaxf(z[0], z[2]), bm1 = fmaxf(z[1], z[3]);
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) {
-                bm0 = fmaxf(bm0, __shfl_xor_sync(kFull, bm0, x));
-                bm1 = fmaxf(bm1, __shfl_xor_sync(kFull, bm1, x));
+    // U blocks at a time; of a last, incomplete turn the missing block is masked whole.
+    auto reduce = [&](auto u_blocks) {
+        constexpr int U = decltype(u_blocks)::value;
+        for (int i = 0; i < mine; i += U) {
+            cp_async_wait<C::kStages - U>();
+            __syncwarp();   // every lane's copies of the blocks have landed
+            if (i == 0 && p.trace && threadIdx.x == 0 && sm.tr[kTrFirstBlock] == 0) sm.tr[kTrFirstBlock] = globaltimer_ns();
+            if ((i & 31) == 0) {
+                k_now = k_next;
+                v_now = v_next;
             }
-            const float mn0 = bm0 > m[0] + kGrowth ? bm0 - kHeadroom : m[0];
-            const float mn1 = bm1 > m[1] + kGrowth ? bm1 - kHeadroom : m[1];
-            float f0 = m[0] == mn0 ? 1.f : exp2f(m[0] - mn0);   // from m = -inf: 0
-            float f1 = m[1] == mn1 ? 1.f : exp2f(m[1] - mn1);
-            m[0] = mn0;
-            m[1] = mn1;
-            l[0] *= f0;
-            l[1] *= f1;
-            if (fabsf(vs) > vref) {
-                const float vn = power_of_two_above(fabsf(vs));
-                f0 *= vref / vn;
-                f1 *= vref / vn;
-                vref = vn;
-                vinv = 1.f / vn;
+            float z[U][4], vs[U];
+            int valid[U], slot[U];
+            uint32_t src[U], vf[C::kChunks / 2][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                valid[u] = ntok - (warp + kWarps * (i + u)) * kBlockRows;   // tokens of the block (16 or more: all)
+                slot[u] = stage;
+                src[u] = ring + stage * C::kBlockBytes + frag_off;
+                stage = stage + 1 == C::kStages ? 0 : stage + 1;
             }
+            // V to registers, and the stage is free for its next block
+            auto take_v = [&](int u) {
 #pragma unroll
-            for (int x = 0; x < C::kParts; ++x)
-#pragma unroll
-                for (int n = 0; n < D / 16; ++n) {
-                    o[x][n][0] *= f0;
-                    o[x][n][1] *= f1;
-                    o[x][n][2] *= f0;
-                    o[x][n][3] *= f1;
+                for (int c = 0; c < C::kChunks; c += 2) ldsm_x4_trans(vf[c / 2], (src[u] ^ (c << 4)) + C::kMatBytes);
+                __syncwarp();
+                const int next = i + u + C::kStages;
+                if (next < mine) {
+                    if ((U == 1 || (u + C::kStages) % U == 0) && (next & 31) == 0) fetch_batch(next);
+                    issue(next, slot[u]);
                 }
-        }
-        const float vw = vs * vinv;
-        const float p0 = ex2(z[0] - m[0]), p1 = ex2(z[1] - m[1]), p2 = ex2(z[2] - m[0]), p3 = ex2(z[3] - m[1]);   // masked: 0
-        l[0] += p0 + p2;
-        l[1] += p1 + p3;
-        const float w0 = p0 * vw, w1 = p1 * vw, w2 = p2 * vw, w3 = p3 * vw;
-        const uint32_t ha = pack_half(w0, w1), hb = pack_half(w2, w3);   // tokens g and g + 8
-        const float2 ua = unpack_half(ha), ub = unpack_half(hb);
-        const uint32_t la = pack_half(w0 - ua.x, w1 - ua.y), lb = pack_half(w2 - ub.x, w3 - ub.y);
-        // B fragments of P^T: the 8 x 8 transposes of the token-major tiles
-        uint32_t pb[C::kParts][2];
-        if constexpr (C::kParts == 2) {
-            pb[0][0] = transpose8(ha);
-            pb[0][1] = transpose8(hb);
-            pb[1][0] = transpose8(la);
-            pb[1][1] = transpose8(lb);
-        } else {
-            pb[0][0] = transpose8(pick(part0, part1, ha, la));
-            pb[0][1] = transpose8(pick(part0, part1, hb, lb));
-        }
-
-        // O^T += V^T P^T: rows g and g + 8 of tile c are dimensions 16 c + 2 g and + 1.  A
-        // transposed word holds (token 2t: both dimensions), (token 2t + 1: both)
-        if (valid < kBlockRows) {   // slots past the row's end may hold anything, NaN codes too (0 * NaN = NaN)
-            const uint32_t lo = (2 * t < valid ? 0xffffu : 0u) | (2 * t + 1 < valid ? 0xffff0000u : 0u);
-            const uint32_t hi = (2 * t + 8 < valid ? 0xffffu : 0u) | (2 * t + 9 < valid ? 0xffff0000u : 0u);
+                cp_async_commit();
+            };
+            // S^T = K Q^T: rows g and g + 8 are tokens g and g + 8
 #pragma unroll
-            for (int c = 0; c < C::kChunks / 2; ++c) {
-                vf[c][0] &= lo;
-                vf[c][1] &= hi;
-                vf[c][2] &= lo;
-                vf[c][3] &= hi;
+            for (int u = 0; u < U; ++u) {
+                float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};   // two chains, for the product's latency
+#pragma unroll
+                for (int c = 0; c < C::kChunks; c += 2) {
+                    uint32_t w[4], a0, a1, a2, a3;
+                    ldsm_x4(w, src[u] ^ (c << 4));
+                    widen4(w[0], a0, a2);
+                    widen4(w[1], a1, a3);
+                    mma_f16(s, a0, a1, a2, a3, qb[c][0], qb[c][1]);
+                    widen4(w[2], a0, a2);
+                    widen4(w[3], a1, a3);
+                    mma_f16(U == 1 ? s2 : s, a0, a1, a2, a3, qb[c + 1][0], qb[c + 1][1]);
+                }
+                const float ks = __shfl_sync(kFull, k_now, (i + u) & 31);
+                vs[u] = __shfl_sync(kFull, v_now, (i + u) & 31);
+                if (U > 1 && i + u >= mine) vs[u] = 0.f;
+                const float sc0 = ks * qs[0], sc1 = ks * qs[1];
+                z[u][0] = (U == 1 ? s[0] + s2[0] : s[0]) * sc0;
+                z[u][1] = (U == 1 ? s[1] + s2[1] : s[1]) * sc1;
+                z[u][2] = (U == 1 ? s[2] + s2[2] : s[2]) * sc0;
+                z[u][3] = (U == 1 ? s[3] + s2[3] : s[3]) * sc1;
+                if (valid[u] < kBlockRows) {
+                    if (g >= valid[u]) z[u][0] = z[u][1] = -INFINITY;
+                    if (g + 8 >= valid[u]) z[u][2] = z[u][3] = -INFINITY;
+                }
+            }
+            if constexpr (U == 1) take_v(0);
+
+            // a reference moves when one of its weights would pass 2^14 (m = -inf: at
+            // once), or a block's V scale passes r; neither happens often, so the exact
+            // maximum is found only then
+            float bm0 = fmaxf(z[0][0], z[0][2]), bm1 = fmaxf(z[0][1], z[0][3]), va = fabsf(vs[0]);
+            if constexpr (U == 2) {
+                bm0 = fmaxf(bm0, fmaxf(z[1][0], z[1][2]));
+                bm1 = fmaxf(bm1, fmaxf(z[1][1], z[1][3]));
+                va = fmaxf(va, fabsf(vs[1]));
+            }
+            if (__any_sync(kFull, bm0 > m[0] + kGrowth || bm1 > m[1] + kGrowth) || va > vref) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+                    bm0 = fmaxf(bm0, __shfl_xor_sync(kFull, bm0, x));
+                    bm1 = fmaxf(bm1, __shfl_xor_sync(kFull, bm1, x));
+                }
+                const float mn0 = bm0 > m[0] + kGrowth ? bm0 - kHeadroom : m[0];
+                const float mn1 = bm1 > m[1] + kGrowth ? bm1 - kHeadroom : m[1];
+                float f0 = m[0] == mn0 ? 1.f : exp2f(m[0] - mn0);   // from m = -inf: 0
+                float f1 = m[1] == mn1 ? 1.f : exp2f(m[1] - mn1);
+                m[0] = mn0;
+                m[1] = mn1;
+                l[0] *= f0;
+                l[1] *= f1;
+                if (va > vref) {
+                    const float vn = power_of_two_above(va);
+                    f0 *= vref / vn;
+                    f1 *= vref / vn;
+                    vref = vn;
+                    vinv = 1.f / vn;
+                }
+#pragma unroll
+                for (int x = 0; x < C::kParts; ++x)
+#pragma unroll
+                    for (int n = 0; n < D / 16; ++n) {
+                        o[x][n][0] *= f0;
+                        o[x][n][1] *= f1;
+                        o[x][n][2] *= f0;
+                        o[x][n][3] *= f1;
+                    }
+            }
+            // B fragments of P^T: the 8 x 8 transposes of the token-major tiles
+            uint32_t pb[U][C::kParts][2];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float vw = vs[u] * vinv;
+                const float p0 = ex2(z[u][0] - m[0]), p1 = ex2(z[u][1] - m[1]);   // token g (masked: 0)
+                const float p2 = ex2(z[u][2] - m[0]), p3 = ex2(z[u][3] - m[1]);   // token g + 8
+                l[0] += p0 + p2;
+                l[1] += p1 + p3;
+                const float w0 = p0 * vw, w1 = p1 * vw, w2 = p2 * vw, w3 = p3 * vw;
+                const uint32_t ha = pack_half(w0, w1), hb = pack_half(w2, w3);
+                const float2 ua = unpack_half(ha), ub = unpack_half(hb);
+                if constexpr (C::kParts == 2) {
+                    pb[u][0][0] = transpose8(ha);
+                    pb[u][0][1] = transpose8(hb);
+                    pb[u][1][0] = transpose8(pack_half(w0 - ua.x, w1 - ua.y));
+                    pb[u][1][1] = transpose8(pack_half(w2 - ub.x, w3 - ub.y));
+                } else {
+                    pb[u][0][0] = transpose8(pack_half(fmaf(-part0, ua.x, w0), fmaf(-part1, ua.y, w1)));
+                    pb[u][0][1] = transpose8(pack_half(fmaf(-part0, ub.x, w2), fmaf(-part1, ub.y, w3)));
+                }
+            }
+
+            // O^T += V^T P^T: rows g and g + 8 of tile c are dimensions 16 c + 2 g and + 1.  A
+            // transposed word holds (token 2t: both dimensions), (token 2t + 1: both)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if constexpr (U > 1) take_v(u);
+                if (valid[u] < kBlockRows) {   // slots past the row's end may hold anything, NaN codes too (0 * NaN = NaN)
+                    const uint32_t lo = (2 * t < valid[u] ? 0xffffu : 0u) | (2 * t + 1 < valid[u] ? 0xffff0000u : 0u);
+                    const uint32_t hi = (2 * t + 8 < valid[u] ? 0xffffu : 0u) | (2 * t + 9 < valid[u] ? 0xffff0000u : 0u);
+#pragma unroll
+                    for (int c = 0; c < C::kChunks / 2; ++c) {
+                        vf[c][0] &= lo;
+                        vf[c][1] &= hi;
+                        vf[c][2] &= lo;
+                        vf[c][3] &= hi;
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < C::kChunks; ++c) {
+                    uint32_t a0, a1, a2, a3;
+                    widen4(__byte_perm(vf[c / 2][2 * (c & 1)], 0, 0x3120), a0, a1);
+                    widen4(__byte_perm(vf[c / 2][2 * (c & 1) + 1], 0, 0x3120), a2, a3);
+#pragma unroll
+                    for (int x = 0; x < C::kParts; ++x) mma_f16(o[x][c], a0, a1, a2, a3, pb[u][x][0], pb[u][x][1]);
+                }
             }
         }
-#pragma unroll
-        for (int c = 0; c < C::kChunks; ++c) {
-            uint32_t a0, a1, a2, a3;
-            widen4(__byte_perm(vf[c / 2][2 * (c & 1)], 0, 0x3120), a0, a1);
-            widen4(__byte_perm(vf[c / 2][2 * (c & 1) + 1], 0, 0x3120), a2, a3);
-#pragma unroll
-            for (int x = 0; x < C::kParts; ++x) mma_f16(o[x][c], a0, a1, a2, a3, pb[x][0], pb[x][1]);
-        }
-    }
+    };
+    // Two blocks at a time share a turn's bookkeeping and overlap their latencies; one
+    // at a time starts earlier and has its loads out earlier.  Measured (one / two at
+    // a time): D = 128, 7 blocks a warp 15.3 / 16.5 us (1 x 32768 tokens), 14 on
+    // average 23.0 / 23.7 us, 32 blocks 84.4 / 86.3 us (64 x 4096), 64 blocks 101.8 /
+    // 95.8 us (38 x 8192); D = 64, 32 blocks 91.1 / 87.7 us (128 x 4096).
+    if (nblk >= C::kPairFrom * kWarps)
+        reduce(std::integral_constant<int, 2>{});
+    else
+        reduce(std::integral_constant<int, 1>{});
     trace_stamp(sm, p, kTrStreamEnd);
 
     // publish the warp's state: fold the lo parts into the hi parts; a lane then
