@@ -326,8 +326,8 @@ typedef struct {
  * queries not written) and flagged if a page of its new tokens is missing
  * (PKV_DEV_ROW_FULL: past the table's end, or a negative entry; also a negative
  * length), lies outside the pool (PKV_DEV_PAGE_OOB), or its offsets do not lie
- * ascending in [0, total_tokens] (PKV_DEV_PLAN_MISMATCH).  Two rows must not
- * append to one page.  One kernel on `stream`; needs no memory of its own.
+ * ascending in [0, total_tokens] (PKV_DEV_PLAN_MISMATCH; where offsets descend,
+ * the rows around may be written in part).  Two rows must not append to one page.  One kernel on `stream`; needs no memory of its own.
  * Errors: PKV_EINVAL (null or misaligned pointer, bad stride or count, a rotary
  * dim above D, another current device than the plan's), PKV_ECUDA.
  */

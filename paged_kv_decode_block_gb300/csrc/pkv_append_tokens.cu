@@ -248,6 +248,7 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
     constexpr int kTpt = D / 16;               // threads per token
     constexpr int kCta = kBlockRows * kTpt;    // = D
     __shared__ int s_row;
+    __shared__ RowWork s_work;
     __shared__ uint32_t s_max[2][kCta / 32];
     grid_dependency_wait();
     launch_dependents();
@@ -255,21 +256,35 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
     const int piece = blockIdx.x, kvh = blockIdx.y;
     // The row of this piece.  With offsets, row r owns the pieces from
     // floor(cu[r] / 16) + 2 r on: at least as many as 16-token blocks that
-    // cu[r + 1] - cu[r] tokens can touch from any start inside a block.
+    // cu[r + 1] - cu[r] tokens can touch from any start inside a block.  The thread
+    // that finds the row has its work in the same round trip.
     int b = piece, first = piece;
+    RowWork w;
     if (p.cu) {
-        if (threadIdx.x == 0) s_row = -1;
+        if (threadIdx.x == 0) {
+            s_row = p.B;
+            s_work = RowWork{0, 0, 0, 0u};   // no row: the CTA still writes a length below
+        }
         __syncthreads();
+        int found = p.B;
         for (int r = threadIdx.x; r < p.B; r += kCta) {
+            const RowWork its = row_work(p, r);
             const int64_t lo = p.cu[r] / kBlockRows + 2ll * r, hi = p.cu[r + 1] / kBlockRows + 2ll * (r + 1);
-            if (lo <= piece && piece < hi) s_row = r;
+            if (lo <= piece && piece < hi && r < found) {   // (two rows can claim a piece only if offsets descend)
+                found = r;
+                w = its;
+                atomicMin(&s_row, r);
+            }
         }
         __syncthreads();
         b = s_row;
-        if (b >= 0) first = p.cu[b] / kBlockRows + 2 * b;
+        if (found == b && b < p.B) s_work = w;
+        __syncthreads();
+        w = s_work;
+        first = w.tok0 / kBlockRows + 2 * b;
+    } else {
+        w = row_work(p, b);
     }
-    // a CTA without a piece (b < 0) still writes its row's length below
-    const RowWork w = b >= 0 ? row_work(p, b) : RowWork{0, 0, 0, 0u};
     const int blk0 = (w.pos0 / kBlockRows + (piece - first)) * kBlockRows;   // first position of the 16-token block
     const int lo = max(blk0, w.pos0), hi = min(blk0 + kBlockRows, w.pos0 + w.n);
     const bool work = !w.bad && lo < hi;
@@ -303,7 +318,7 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
             for (int g = 0; g < kQueries; ++g)
                 if (g < G) qs[g] = load_slice(qh + g * D, e0, e1);
     }
-    const uint32_t bad = row_pages_bad(p, max(b, 0), w);
+    const uint32_t bad = row_pages_bad(p, min(b, p.B - 1), w);   // (no row: no work, nothing read)
 
     // the lengths after: one CTA per row, whichever piece it holds
     if (kvh == 0 && piece < p.B) {
