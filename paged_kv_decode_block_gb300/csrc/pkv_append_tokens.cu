@@ -23,10 +23,15 @@
 // fall below e4m3's normal range (2^-6 of the new scale), which round again.
 //
 // What bounds it: HBM, (2 * Hq + 4 * Hkv) * D * 2 bytes per token in bf16 (Hkv * D
-// * 2 less for e4m3).  One CTA per (16-token block, KV head): the block's scale
-// needs no other CTA, a thread owns 16 elements of one token of every head of
-// the group, so its eight sines and cosines serve the K head and the G query
-// heads, and every access is 16 bytes (8 for e4m3 codes of half pairs).
+// * 2 less for e4m3).  One CTA per (16-token block, KV head or two): the block's
+// scale needs no other CTA, a thread owns 16 elements of one token of every head
+// of the group, so its eight sines and cosines serve the K head and the G query
+// heads, and every access is 16 bytes (8 for e4m3 codes of half pairs).  8 x 128
+// and 32 query heads, prompts of 12.5 thousand tokens in bf16: 49 us, 6.3 TB/s; of
+// 8.8 thousand in e4m3: 35.6 us, 5.5 TB/s, where the arithmetic (about 1000
+// instructions a warp and head, half of the issue slots) bounds it too; one token
+// for each of 64 rows: 4.4 us in a graph, a chain of round trips (length, table
+// entry, scales, then the stores).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -146,14 +151,19 @@ __device__ __forceinline__ RowWork row_work(const AppendTokensParams& p, int b) 
     return w;
 }
 
+// The row's page that holds its 16-token block `blk`: blk / (blocks per page).
+__device__ __forceinline__ int page_of(const AppendTokensParams& p, int blk) {
+    return p.page_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(blk), p.page_magic)) : blk;
+}
+
 // The rest of the check, over the table entries of all of the row's new tokens,
 // by the whole CTA (a barrier): a row is refused before any byte of it is written.
 __device__ __forceinline__ uint32_t row_pages_bad(const AppendTokensParams& p, int b, const RowWork& w) {
     uint32_t bad = w.bad;
     if (!bad && w.n > 0) {
         const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
-        const int last = (w.pos0 + w.n - 1) / p.page_size;
-        for (int i = w.pos0 / p.page_size + static_cast<int>(threadIdx.x); i <= last; i += static_cast<int>(blockDim.x)) {
+        const int last = page_of(p, (w.pos0 + w.n - 1) / kBlockRows);
+        for (int i = page_of(p, w.pos0 / kBlockRows) + static_cast<int>(threadIdx.x); i <= last; i += static_cast<int>(blockDim.x)) {
             const int page = row[i];
             if (page < 0)
                 bad |= PKV_DEV_ROW_FULL;
@@ -184,8 +194,7 @@ __device__ __forceinline__ Slice load_slice(const uint16_t* head, int e0, int e1
 // Half pairs: x runs through a, y through b.  Neighbouring pairs: (x, y) are
 // (0, 1), (2, 3), ... of a, then of b.  A slice past the rotated elements is
 // only widened.
-__device__ __forceinline__ void turn(const Slice& s, bool rotate, bool pairs, const float (&c)[8], const float (&sn)[8],
-                                     float (&x)[16]) {
+__device__ __forceinline__ void widen(const Slice& s, float (&x)[16]) {
     float a[8], b[8];
     unpack_bf16x8(s.a, a);
     unpack_bf16x8(s.b, b);
@@ -194,8 +203,14 @@ __device__ __forceinline__ void turn(const Slice& s, bool rotate, bool pairs, co
         x[i] = a[i];
         x[8 + i] = b[i];
     }
+}
+
+template <bool kPairs>
+__device__ __forceinline__ void turn(const Slice& s, bool rotate, const float (&c)[8], const float (&sn)[8],
+                                     float (&x)[16]) {
+    widen(s, x);
     if (!rotate) return;
-    if (pairs) {
+    if constexpr (kPairs) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float u = x[2 * i], w = x[2 * i + 1];
@@ -243,17 +258,19 @@ __device__ __forceinline__ uint4 requantise16(const uint4& w, float ratio) {
     return make_uint4(requantise4(w.x, ratio), requantise4(w.y, ratio), requantise4(w.z, ratio), requantise4(w.w, ratio));
 }
 
-template <int D, bool Q8>
+template <int D, bool Q8, bool kPairs>
 __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant__ AppendTokensParams p) {
     constexpr int kTpt = D / 16;               // threads per token
     constexpr int kCta = kBlockRows * kTpt;    // = D
     __shared__ int s_row;
     __shared__ RowWork s_work;
-    __shared__ uint32_t s_max[2][kCta / 32];
+    __shared__ uint32_t s_max[2][2][kCta / 32];
+    __shared__ alignas(16) uint64_t s_step[PKV_ROTARY_MAX_DIM / 2];
     grid_dependency_wait();
     launch_dependents();
 
-    const int piece = blockIdx.x, kvh = blockIdx.y;
+    for (int i = threadIdx.x; i < PKV_ROTARY_MAX_DIM / 2; i += kCta) s_step[i] = p.rot.step[i];   // (read after a barrier)
+    const int piece = blockIdx.x, kvh0 = blockIdx.y * p.heads;   // this CTA's KV heads: kvh0 .. kvh0 + heads - 1
     // The row of this piece.  With offsets, row r owns the pieces from
     // floor(cu[r] / 16) + 2 r on: at least as many as 16-token blocks that
     // cu[r + 1] - cu[r] tokens can touch from any start inside a block.  The thread
@@ -295,9 +312,9 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
 
     // the thread's elements of a head
     const int dim = p.rot.dim;
-    const bool rotate = j < dim / 16, pairs = p.rot.interleaved != 0;
+    const bool rotate = j < dim / 16;
     int e0, e1;
-    if (rotate && !pairs) {
+    if (rotate && !kPairs) {
         e0 = 8 * j;
         e1 = dim / 2 + 8 * j;
     } else {   // sixteen neighbours: pairs, or past the rotated elements
@@ -307,21 +324,23 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
 
     // all loads that need no page are in flight before the row's pages are checked
     const int G = p.Hq / p.Hkv;
-    const uint16_t* qh = p.q + tok * p.q_stride + static_cast<int64_t>(kvh) * G * D;
-    uint16_t* oh = p.q_out + tok * p.q_out_stride + static_cast<int64_t>(kvh) * G * D;
     Slice ks{}, vs{}, qs[kQueries] = {};
-    if (live) {
-        ks = load_slice(p.k + tok * p.k_stride + static_cast<int64_t>(kvh) * D, e0, e1);
-        vs = load_slice(p.v + tok * p.v_stride + static_cast<int64_t>(kvh) * D, e0, e1);
-        if (p.q)
+    auto load_head = [&](int kvh) {
+        if (!live) return;
+        ks = load_slice(p.k + tok * p.k_stride + kvh * D, e0, e1);
+        vs = load_slice(p.v + tok * p.v_stride + kvh * D, e0, e1);
+        if (p.q) {
+            const uint16_t* qh = p.q + tok * p.q_stride + static_cast<int64_t>(kvh) * G * D;
 #pragma unroll
             for (int g = 0; g < kQueries; ++g)
                 if (g < G) qs[g] = load_slice(qh + g * D, e0, e1);
-    }
+        }
+    };
+    load_head(kvh0);
     const uint32_t bad = row_pages_bad(p, min(b, p.B - 1), w);   // (no row: no work, nothing read)
 
     // the lengths after: one CTA per row, whichever piece it holds
-    if (kvh == 0 && piece < p.B) {
+    if (kvh0 == 0 && piece < p.B) {
         RowWork o = w;
         uint32_t o_bad = bad;
         if (p.cu) {
@@ -334,29 +353,17 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
         }
     }
     if (bad || !work) return;
-    const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + blk0 / p.page_size];
-    const size_t prow0 = static_cast<size_t>(page) * p.page_size + blk0 % p.page_size;   // token row of the block
-    const size_t head_off = ((prow0 + slot) * p.Hkv + kvh) * D;
-    // what the block holds already
-    [[maybe_unused]] const size_t sidx = prow0 / kBlockRows * p.Hkv + kvh;
-    [[maybe_unused]] float k_old = 0.f, v_old = 0.f;
-    [[maybe_unused]] uint4 k_held, v_held;
-    if constexpr (Q8) {
-        if (lo > blk0) {
-            k_old = p.k_scales[sidx];
-            v_old = p.v_scales[sidx];
-            if (pos < lo) {
-                k_held = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_pages) + head_off + 16 * j);
-                v_held = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.v_pages) + head_off + 16 * j);
-            }
-        }
-    }
+    const int blk = blk0 / kBlockRows, its_page = page_of(p, blk);
+    const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + its_page];
+    // token row of the block in the pool
+    const size_t prow0 = static_cast<size_t>(page) * p.page_size + (blk0 - its_page * p.page_size);
+    const bool held = lo > blk0;   // the block holds older tokens of the row
 
     float c[8], sn[8];
     if (live && rotate) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint64_t step = p.rot.step[8 * j + i];
+            const uint64_t step = s_step[8 * j + i];
             const uint32_t at = static_cast<uint32_t>(pos);
             const uint32_t turns = __umulhi(static_cast<uint32_t>(step), at) + static_cast<uint32_t>(step >> 32) * at;
             const uint32_t quarter = (turns + 0x20000000u) >> 30;          // nearest quarter turn
@@ -375,69 +382,102 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
         for (int i = 0; i < 8; ++i) c[i] = sn[i] = 0.f;
     }
 
-    float x[16];
-    turn(ks, rotate, pairs, c, sn, x);
-    if constexpr (!Q8) {
-        if (live) {
-            store_bf16(static_cast<uint16_t*>(p.k_pages) + head_off, e0, e1, x);
-            uint16_t* vh = static_cast<uint16_t*>(p.v_pages) + head_off;
-            *reinterpret_cast<uint4*>(vh + e0) = vs.a;
-            *reinterpret_cast<uint4*>(vh + e1) = vs.b;
+    for (int h = 0; h < p.heads; ++h) {
+        const int kvh = kvh0 + h;
+        const size_t head_off = ((prow0 + slot) * p.Hkv + kvh) * D;
+        // what the block holds already
+        [[maybe_unused]] const size_t sidx = prow0 / kBlockRows * p.Hkv + kvh;
+        [[maybe_unused]] float k_old = 0.f, v_old = 0.f;
+        [[maybe_unused]] uint4 k_held, v_held;
+        if constexpr (Q8) {
+            if (held) {
+                k_old = p.k_scales[sidx];
+                v_old = p.v_scales[sidx];
+                if (pos < lo) {
+                    k_held = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_pages) + head_off + 16 * j);
+                    v_held = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.v_pages) + head_off + 16 * j);
+                }
+            }
         }
-    } else {
-        float y[16];
-        turn(vs, false, false, c, sn, y);
-        uint32_t km = magnitude16(x), vm = magnitude16(y);   // (a slot without a new token holds zeros)
-        cta_max(km, vm, s_max);   // and every thread has read the old scales and codes
-        const bool infinite = km == kInfinity || vm == kInfinity;
-        if (infinite) {
-            km = finite_magnitude16(x);
-            vm = finite_magnitude16(y);
-            __syncthreads();   // s_max is read
-            cta_max(km, vm, s_max);
+        float x[16];
+        turn<kPairs>(ks, rotate, c, sn, x);
+        if constexpr (!Q8) {
+            if (live) {
+                store_bf16(static_cast<uint16_t*>(p.k_pages) + head_off, e0, e1, x);
+                uint16_t* vh = static_cast<uint16_t*>(p.v_pages) + head_off;
+                *reinterpret_cast<uint4*>(vh + e0) = vs.a;
+                *reinterpret_cast<uint4*>(vh + e1) = vs.b;
+            }
+        } else {
+            float y[16];
+            widen(vs, y);
+            uint32_t km = magnitude16(x), vm = magnitude16(y);   // (a slot without a new token holds zeros)
+            cta_max(km, vm, s_max[h & 1]);   // and every thread has read the old scales and codes
+            const bool infinite = km == kInfinity || vm == kInfinity;
+            if (infinite) {
+                km = finite_magnitude16(x);
+                vm = finite_magnitude16(y);
+                __syncthreads();   // s_max is read
+                cta_max(km, vm, s_max[h & 1]);
+            }
+            const float k_new = fmaxf(block_scale(km), k_old), v_new = fmaxf(block_scale(vm), v_old);
+            uint8_t* kp = static_cast<uint8_t*>(p.k_pages) + head_off;
+            uint8_t* vp = static_cast<uint8_t*>(p.v_pages) + head_off;
+            if (live) {
+                const float ki = 1.f / k_new, vi = 1.f / v_new;
+                *reinterpret_cast<uint2*>(kp + e0) = codes8(x, ki, infinite);
+                *reinterpret_cast<uint2*>(kp + e1) = codes8(x + 8, ki, infinite);
+                *reinterpret_cast<uint2*>(vp + e0) = codes8(y, vi, infinite);
+                *reinterpret_cast<uint2*>(vp + e1) = codes8(y + 8, vi, infinite);
+            } else if (pos < lo) {   // an older token of the block
+                if (k_new != k_old) *reinterpret_cast<uint4*>(kp + 16 * j) = requantise16(k_held, k_old / k_new);
+                if (v_new != v_old) *reinterpret_cast<uint4*>(vp + 16 * j) = requantise16(v_held, v_old / v_new);
+            }
+            if (threadIdx.x == 0) {
+                p.k_scales[sidx] = k_new;
+                p.v_scales[sidx] = v_new;
+            }
         }
-        const float k_new = fmaxf(block_scale(km), k_old), v_new = fmaxf(block_scale(vm), v_old);
-        uint8_t* kp = static_cast<uint8_t*>(p.k_pages) + head_off;
-        uint8_t* vp = static_cast<uint8_t*>(p.v_pages) + head_off;
-        if (live) {
-            const float ki = 1.f / k_new, vi = 1.f / v_new;
-            *reinterpret_cast<uint2*>(kp + e0) = codes8(x, ki, infinite);
-            *reinterpret_cast<uint2*>(kp + e1) = codes8(x + 8, ki, infinite);
-            *reinterpret_cast<uint2*>(vp + e0) = codes8(y, vi, infinite);
-            *reinterpret_cast<uint2*>(vp + e1) = codes8(y + 8, vi, infinite);
-        } else if (pos < lo) {   // an older token of the block
-            if (k_new != k_old) *reinterpret_cast<uint4*>(kp + 16 * j) = requantise16(k_held, k_old / k_new);
-            if (v_new != v_old) *reinterpret_cast<uint4*>(vp + 16 * j) = requantise16(v_held, v_old / v_new);
-        }
-        if (threadIdx.x == 0) {
-            p.k_scales[sidx] = k_new;
-            p.v_scales[sidx] = v_new;
-        }
-    }
 
-    if (p.q && live) {
-        for (int g0 = 0; g0 < G; g0 += kQueries) {   // in place is fine: a thread writes only what it has read
+        if (p.q && live) {
+            const uint16_t* qh = p.q + tok * p.q_stride + static_cast<int64_t>(kvh) * G * D;
+            uint16_t* oh = p.q_out + tok * p.q_out_stride + static_cast<int64_t>(kvh) * G * D;
+            for (int g0 = 0; g0 < G; g0 += kQueries) {   // in place is fine: a thread writes only what it has read
 #pragma unroll
-            for (int g = 0; g < kQueries; ++g) {
-                if (g0 + g >= G) break;
-                if (g0 > 0) qs[g] = load_slice(qh + (g0 + g) * D, e0, e1);
-            }
+                for (int g = 0; g < kQueries; ++g) {
+                    if (g0 + g >= G) break;
+                    if (g0 > 0) qs[g] = load_slice(qh + (g0 + g) * D, e0, e1);
+                }
 #pragma unroll
-            for (int g = 0; g < kQueries; ++g) {
-                if (g0 + g >= G) break;
-                float z[16];
-                turn(qs[g], rotate, pairs, c, sn, z);
-                store_bf16(oh + (g0 + g) * D, e0, e1, z);
+                for (int g = 0; g < kQueries; ++g) {
+                    if (g0 + g >= G) break;
+                    float z[16];
+                    turn<kPairs>(qs[g], rotate, c, sn, z);
+                    store_bf16(oh + (g0 + g) * D, e0, e1, z);
+                }
             }
         }
+        if (h + 1 < p.heads) load_head(kvh + 1);
     }
 }
 
-template <int D, bool Q8>
-cudaError_t launch_t(const AppendTokensParams& p, cudaStream_t stream) {
+// From this many (block, KV head) units on a CTA takes two KV heads one after the
+// other, which share its row look-up and its sines and cosines.  Below, one: the
+// call is a chain of round trips.  Measured, one / two heads, one row, 8 KV heads,
+// e4m3: 512 tokens 4.29 / 4.92 us, 1024 (528 units) 5.64 / 5.85, 2048 (1040) 12.8 /
+// 11.7, 16384 68.7 / 64.9 us; bf16: 3.90 / 4.05, 5.35 / 5.49, 12.2 / 11.1, 68.3 /
+// 67.7 us.  (Loading the second head's inputs during the first's arithmetic costs
+// a fourth CTA per SM its registers: slower.)
+constexpr int64_t kTwoHeadUnits = 1024;
+
+template <int D, bool Q8, bool kPairs>
+cudaError_t launch_t(AppendTokensParams p, cudaStream_t stream) {
     const int64_t pieces = p.cu ? static_cast<int64_t>(p.T) / kBlockRows + 2ll * p.B : p.B;
+    const uint32_t bpp = static_cast<uint32_t>(p.page_size / kBlockRows);
+    p.page_magic = bpp > 1 ? static_cast<uint32_t>((1ull << 32) / bpp + 1) : 0u;
+    p.heads = p.Hkv % 2 == 0 && pieces * p.Hkv >= kTwoHeadUnits ? 2 : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(pieces), static_cast<unsigned>(p.Hkv));
+    cfg.gridDim = dim3(static_cast<unsigned>(pieces), static_cast<unsigned>(p.Hkv / p.heads));
     cfg.blockDim = dim3(D);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -445,7 +485,12 @@ cudaError_t launch_t(const AppendTokensParams& p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, append_tokens_kernel<D, Q8>, p);
+    return cudaLaunchKernelEx(&cfg, append_tokens_kernel<D, Q8, kPairs>, p);
+}
+
+template <int D, bool Q8>
+cudaError_t launch_d(const AppendTokensParams& p, cudaStream_t stream) {
+    return p.rot.interleaved ? launch_t<D, Q8, true>(p, stream) : launch_t<D, Q8, false>(p, stream);
 }
 
 }  // namespace
@@ -453,8 +498,8 @@ cudaError_t launch_t(const AppendTokensParams& p, cudaStream_t stream) {
 cudaError_t launch_append_tokens(const AppendTokensParams& p, cudaStream_t stream) {
     const bool q8 = p.k_scales != nullptr;
     switch (p.D) {
-        case 64: return q8 ? launch_t<64, true>(p, stream) : launch_t<64, false>(p, stream);
-        case 128: return q8 ? launch_t<128, true>(p, stream) : launch_t<128, false>(p, stream);
+        case 64: return q8 ? launch_d<64, true>(p, stream) : launch_d<64, false>(p, stream);
+        case 128: return q8 ? launch_d<128, true>(p, stream) : launch_d<128, false>(p, stream);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -166,6 +166,9 @@ struct AppendTokensParams {
     uint32_t* status;
     int32_t B, Hq, Hkv, D, page_size, max_pages, num_pages;
     pkv_rotary rot;             // dim 0: no rotation
+    // set by launch_append_tokens
+    uint32_t page_magic;        // as AttnQ8Params::page_magic
+    int32_t heads;              // KV heads per CTA
 };
 cudaError_t launch_append_tokens(const AppendTokensParams& p, cudaStream_t stream);
 
