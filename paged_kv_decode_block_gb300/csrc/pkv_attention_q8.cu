@@ -13,11 +13,12 @@
 // of two that brings its largest element to [1, 2), so it is exact in f16 down to
 // 2^-14 of that element and rounded by at most 2^-25 of it below.  A weight
 // 2^(s - m) * vs_B / r (r: the largest block scale so far, rounded up to a power of
-// two) is split into f16 hi + lo, about 22 bits; the parts are columns of the
-// products' right operand (with G = 8, of a second one).  Statistics and sums are
-// fp32.  m follows the running maximum lazily: weights may grow to 2^14
-// (within f16) before the accumulators move to a new reference that puts the
-// block's maximum at 2^6.
+// two) is split into f16 hi + 2^-11 lo, 22 bits, and 2^-36 is the least that is not
+// rounded to zero; the parts are columns of the products' right operand (with G =
+// 8, of a second one).  Statistics and sums are fp32.  m follows the running
+// maximum lazily: weights may grow to 2^14 (within f16) before the accumulators
+// move to a new reference that puts the block's maximum at 2^6, so what a token 2^42
+// times lighter than the heaviest adds is still there.
 //
 // What bounds it: HBM, 2 * D + 8 / 16 bytes per token and KV head against 4 * G * D
 // flops (G flop per byte).  Layout of the work:
@@ -35,6 +36,7 @@
 // of such a page.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -51,6 +53,7 @@ namespace {
 constexpr int kWarps = kThreads / 32;
 constexpr float kHeadroom = 6.f;     // a new reference puts the block's largest weight at 2^6
 constexpr float kGrowth = 14.f;      // and holds until a weight would pass 2^14
+constexpr float kLoUp = 2048.f, kLoDown = 1.f / 2048.f;   // P's lo parts are held times 2^11
 
 template <int D, int G>
 struct Q8Cfg {
@@ -271,9 +274,10 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
             qb[j][1] = pack_half(__uint_as_float(q_raw[j].y << 16) * down, __uint_as_float(q_raw[j].y & 0xffff0000u) * down);
         }
     }
-    // Where the parts share a column tile, columns 2t and 2t + 1 carry w - part * f16(w):
-    // with part 0 P's hi parts, with part 1 its lo parts
-    const float part0 = 2 * t < G ? 0.f : 1.f, part1 = 2 * t + 1 < G ? 0.f : 1.f;
+    // Where the parts share a column tile, columns 2t and 2t + 1 carry up * w - part * f16(w):
+    // P's hi parts (up 1, part 0) or its lo parts (both 2^11)
+    const float up0 = 2 * t < G ? 1.f : kLoUp, up1 = 2 * t + 1 < G ? 1.f : kLoUp;
+    const float part0 = 2 * t < G ? 0.f : kLoUp, part1 = 2 * t + 1 < G ? 0.f : kLoUp;
 
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // columns 2t, 2t + 1: reference, this lane's share of the sum
     float vref = 1.1754944e-38f;       // power of two not below any block's V scale so far
@@ -407,11 +411,11 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
                 if constexpr (C::kParts == 2) {
                     pb[u][0][0] = transpose8(ha);
                     pb[u][0][1] = transpose8(hb);
-                    pb[u][1][0] = transpose8(pack_half(w0 - ua.x, w1 - ua.y));
-                    pb[u][1][1] = transpose8(pack_half(w2 - ub.x, w3 - ub.y));
+                    pb[u][1][0] = transpose8(pack_half((w0 - ua.x) * kLoUp, (w1 - ua.y) * kLoUp));
+                    pb[u][1][1] = transpose8(pack_half((w2 - ub.x) * kLoUp, (w3 - ub.y) * kLoUp));
                 } else {
-                    pb[u][0][0] = transpose8(pack_half(fmaf(-part0, ua.x, w0), fmaf(-part1, ua.y, w1)));
-                    pb[u][0][1] = transpose8(pack_half(fmaf(-part0, ub.x, w2), fmaf(-part1, ub.y, w3)));
+                    pb[u][0][0] = transpose8(pack_half(fmaf(-part0, ua.x, w0 * up0), fmaf(-part1, ua.y, w1 * up1)));
+                    pb[u][0][1] = transpose8(pack_half(fmaf(-part0, ub.x, w2 * up0), fmaf(-part1, ub.y, w3 * up1)));
                 }
             }
 
@@ -470,12 +474,12 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             f[k] = o[0][n][(k >> 1) + 2 * (k & 1)];
-            if constexpr (C::kParts == 2) f[k] += o[1][n][(k >> 1) + 2 * (k & 1)];
-            else if constexpr (G > 1) f[k] += __shfl_xor_sync(kFull, f[k], G / 2);
+            if constexpr (C::kParts == 2) f[k] = fmaf(o[1][n][(k >> 1) + 2 * (k & 1)], kLoDown, f[k]);
+            else if constexpr (G > 1) f[k] = fmaf(__shfl_xor_sync(kFull, f[k], G / 2), kLoDown, f[k]);   // (hi columns' lanes)
         }
         if constexpr (G == 1) {
-            f[0] += f[2];
-            f[1] += f[3];
+            f[0] = fmaf(f[2], kLoDown, f[0]);
+            f[1] = fmaf(f[3], kLoDown, f[1]);
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -542,6 +546,25 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
                              static_cast<uint64_t>(tw.split);
         sm.tr[kTrTiles] += 1;
     }
+}
+
+// The row whose length is the rank-th largest (of equal lengths the lower row
+// first), for B <= kThreads rows; all CTA threads call this.
+template <int D, int G>
+__device__ int row_by_length(Q8Smem<D, G>& sm, const AttnParams& p, int rank) {
+    int* lens = reinterpret_cast<int*>(sm.scratch());   // the idle ring
+    const int r = threadIdx.x, n = r < p.B ? p.seq_lens[r] : INT_MIN;
+    lens[r] = n;
+    __syncthreads();
+    int before = 0;
+    for (int i = 0; i < p.B; i += 4) {   // (past B: INT_MIN, before no row)
+        const int4 x = *reinterpret_cast<const int4*>(lens + i);
+        before += (x.x > n || (x.x == n && i < r)) + (x.y > n || (x.y == n && i + 1 < r)) +
+                  (x.z > n || (x.z == n && i + 2 < r)) + (x.w > n || (x.w == n && i + 3 < r));
+    }
+    if (r < p.B && before == rank) sm.tile_slot[1] = r;
+    __syncthreads();
+    return sm.tile_slot[1];
 }
 
 template <int D, int G>
@@ -623,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q8_kernel(const __grid_
     if (p.route == kRouteDirect) {
         tw.b = blockIdx.x / p.Hkv;
         tw.kvh = blockIdx.x % p.Hkv;
+        if (qp.longest_first) tw.b = row_by_length(sm, p, tw.b);
         tw.t1 = p.seq_lens[tw.b];
         tw.finalize = 1;
         tw.splits = 1;

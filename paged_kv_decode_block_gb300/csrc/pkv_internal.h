@@ -179,6 +179,7 @@ struct AttnQ8Params {
     const float* k_scales;      // [num_pages][page_size / kBlockRows][Hkv]
     const float* v_scales;
     uint32_t page_magic;        // x / (16-token blocks per page) = high word of x * page_magic (x < 2^27); 0: one block
+    int32_t longest_first;      // direct route: CTAs take the rows by length, longest first (B <= 256)
 };
 cudaError_t launch_attention_q8(const AttnQ8Params& p, int grid, cudaStream_t stream, bool cooperative);
 

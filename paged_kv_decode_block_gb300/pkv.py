@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 import numpy as np
 
@@ -262,8 +263,9 @@ class Plan:
         _check(lib.pkv_plan(_ptr_i32(lens), _ptr_i32(table), self.page_size, ctypes.byref(self.geom),
                             ctypes.byref(o), ctypes.byref(h)), "pkv_plan")
         self._h = h
-        import torch
-        self.device = torch.cuda.current_device()   # the device the plan is bound to
+        torch = sys.modules.get("torch")
+        # the device the plan is bound to
+        self.device = torch.cuda.current_device() if torch is not None and torch.cuda.is_available() else 0
         # the shapes of the tensors that go with the plan
         self.Hq, self.Hkv = int(Hq), int(Hkv)
         self.pool_shape = (int(num_pages), self.page_size, self.Hkv, self.D)

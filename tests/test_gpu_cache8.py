@@ -164,6 +164,31 @@ def test_decode_more_than_one_batch_of_blocks():
     c.check()
 
 
+@pytest.mark.parametrize("B", [200, 256, 257])
+def test_decode_many_unequal_rows(B):
+    """More tiles than the GPU holds at once, rows of all lengths (equal ones, empty ones): up to 256 rows are taken
+    longest first, more in row order; the device's lengths decide, also after the plan was made."""
+    rng = np.random.default_rng(B)
+    lens = rng.choice([0, 1, 16, 33, 100, 100, 250, 600], B)
+    c = Cache(lens, Hq=8, H=2, D=64, seed=B, room=16)
+    c.upload()
+    plan = c.plan(force_mode="direct")
+    assert plan.info()["grid_ctas"] == 2 * B
+    c.decode(plan)
+    c.check()
+    c.lens = (lens + rng.integers(0, 17, B)).astype(np.int32)   # the direct route follows the device's lengths
+    c.d["lens"].copy_(torch.from_numpy(c.lens))
+    c.d["out"].fill_(7.0)
+    c.decode(plan)
+    c.check()
+    c.lens = c.lens.copy()
+    c.d["lens"][3] = -5   # and flags one that cannot be
+    c.decode(plan)
+    torch.cuda.synchronize()
+    assert plan.status() == pkv.DEV_PLAN_MISMATCH and torch.isnan(c.d["out"][3]).all()
+    c.check(rows=[b for b in range(B) if b != 3])
+
+
 def test_decode_reads_nothing_behind_the_last_token():
     c = Cache([5, 16, 31, 100], Hq=16, H=2, D=128, ps=32, seed=6)
     for b, n in enumerate(c.lens):
@@ -214,6 +239,32 @@ def test_decode_one_token_holds_the_weight_in_a_small_block():
     v = cache8.E4M3[c.vc.reshape(-1, 1, 64)[rows[37], 0]] * 2.0 ** -12
     got = c.d["out"].cpu().numpy()[0]
     assert np.max(np.abs(got - v)) <= 2.0 ** -20 * np.abs(v).max() + 448 * 2.0 ** -31
+
+
+@pytest.mark.parametrize("D, G", [(64, 1), (64, 8), (128, 2), (128, 4)])
+def test_decode_many_light_tokens_beside_a_heavy_one(D, G):
+    """One key 2^31 times heavier than each of 200 thousand others: together the light ones carry 2^-13 of the sum, and
+    their values, 2^10 times larger, an eighth of the output."""
+    n = 200_000
+    c = Cache([n], Hq=G, H=1, D=D, ps=256, seed=17)
+    c.q = bf16(np.full((1, G, D), 0.5))
+    c.kc[:], c.ks[:] = 0, 1.0
+    first = int(c.table[0, 0]) * 256
+    score = 31 * np.log(2.0) * np.sqrt(D)
+    c.kc.reshape(-1, 1, D)[first] = cache8.e4m3_encode(1.0)
+    c.ks.reshape(-1)[first // 16] = score / (0.5 * D)
+    c.vs[:] = 2.0 ** -9 * 1024
+    c.vs.reshape(-1)[first // 16] = 2.0 ** -9
+    c.vc &= 0x7F   # no signs: the light tokens' values do not cancel
+    c.upload()
+    for route in ("direct", "split_queue"):
+        c.decode(c.plan(force_mode=route))
+        torch.cuda.synchronize()
+        ref, _ = cache8.decode_q8(cache8.bf16_to_f64(c.q), c.kc, c.vc, c.ks, c.vs, c.table, c.lens)
+        got = c.d["out"].cpu().numpy()
+        # every term is positive: sums, weights and values are each off by a few 2^-20 relative at most
+        # (200000 tokens over 8 warps and 8 lanes: 2^12 additions of 2^-24 each in a lane)
+        assert np.max(np.abs(got / ref - 1)) <= 2.0 ** -11, (route, np.max(np.abs(got / ref - 1)))
 
 
 @pytest.mark.parametrize("size", [2.0 ** -60, 2.0 ** -20, 1.0, 2.0 ** 40])
