@@ -2,6 +2,8 @@
 against torch's float8 and float64 arithmetic, pkv_rotary_init, and every
 refusal that needs no device."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -109,6 +111,27 @@ def test_rotary_shape_check():
         pkv.Rotary(32, inv_freq=np.ones(8))
     with pytest.raises(pkv.PkvError):
         pkv.Rotary(24)
+
+
+def test_struct_layouts_match_the_header(tmp_path):
+    """pkv_rotary and pkv_tokens as the C compiler lays them out, against the binding's."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    lines = []
+    for name, cls in (("pkv_rotary", pkv.RotaryParams), ("pkv_tokens", pkv.Tokens)):
+        lines.append(f'printf("%zu\\n", sizeof({name}));')
+        lines += [f'printf("%zu\\n", offsetof({name}, {f[0]}));' for f in cls._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "pkv.h"\nint main(void) {\n' + "\n".join(lines) +
+                   "\nreturn 0;\n}\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-std=c11", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    want = []
+    for cls in (pkv.RotaryParams, pkv.Tokens):
+        want.append(ctypes.sizeof(cls))
+        want += [getattr(cls, f[0]).offset for f in cls._fields_]
+    assert got == want
+    assert pkv.ROTARY_MAX_DIM == 128 and pkv.Q8_BLOCK == cache8.BLOCK
 
 
 def test_calls_without_a_plan_are_refused():

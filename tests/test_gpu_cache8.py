@@ -593,6 +593,47 @@ def test_append_in_place_queries_and_many_rows():
     assert n.after.tolist() == (lens + counts).tolist()
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_turns_the_queries_inside_a_fused_projection(interleaved):
+    """q_out is q's own slice of the projection's output: the queries turn in place, keys and values beside them stay."""
+    c = Cache([3, 40, 0], Hq=16, H=2, D=128, seed=33, room=80)   # G = 8: two passes over the queries
+    c.upload()
+    n = New(c, [60, 1, 17], fused=True)
+    k, v = n.kd.clone(), n.vd.clone()
+    r, turn = rotary_of(dim=64, interleaved=interleaved)
+    plan = c.plan()
+    pkv.append_q8(n.kd, n.vd, *(c.d[x] for x in ("kp", "vp", "ks", "vs", "table", "lens")), n.after, plan, r, q=n.qd,
+                  q_out=n.qd, cu_tokens=n.cu)
+    torch.cuda.synchronize()
+    near_bf16(bits(n.qd), turn(cache8.bf16_to_f64(n.q), n.pos), cache8.bf16_to_f64(n.q))
+    check_q8(c, n, turn, (c.kc, c.ks, c.vc, c.vs))
+    assert torch.equal(n.kd, k) and torch.equal(n.vd, v) and plan.status() == 0
+
+
+@pytest.mark.parametrize("H, G", [(8, 4), (3, 1), (2, 8)])
+@pytest.mark.parametrize("q8", [False, True])
+def test_append_long_prompts(H, G, q8):
+    """Prompts long enough that a CTA takes two KV heads, and an odd number of heads, which it takes one by one."""
+    c = Cache([5, 0, 700], Hq=G * H, H=H, D=64, seed=34, room=6000, ps=16)
+    c.upload()
+    n = New(c, [5000, 1111, 600], fused=True)
+    r, turn = rotary_of(dim=64)
+    plan = c.plan()
+    if q8:
+        pkv.append_q8(n.kd, n.vd, *(c.d[x] for x in ("kp", "vp", "ks", "vs", "table", "lens")), n.after, plan, r, q=n.qd,
+                      q_out=n.q_out, cu_tokens=n.cu)
+        check_q8(c, n, turn, (c.kc, c.ks, c.vc, c.vs))
+    else:
+        kd, vd = (torch.zeros((c.pages, 16, H, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        pkv.append_rotary(n.kd, n.vd, kd, vd, c.d["table"], c.d["lens"], n.after, plan, r, q=n.qd, q_out=n.q_out,
+                          cu_tokens=n.cu)
+        rows = np.concatenate([cache8.places(c.table, b, c.lens[b], c.lens[b] + k, 16) for b, k in enumerate(n.counts)])
+        near_bf16(bits(kd).reshape(-1, H, 64)[rows], turn(cache8.bf16_to_f64(n.k), n.pos), cache8.bf16_to_f64(n.k))
+        assert np.array_equal(bits(vd).reshape(-1, H, 64)[rows], n.v)
+    near_bf16(bits(n.q_out), turn(cache8.bf16_to_f64(n.q), n.pos), cache8.bf16_to_f64(n.q))
+    assert n.after.tolist() == [5005, 1111, 1300] and plan.status() == 0
+
+
 def test_append_far_positions():
     """Positions up to 2^31: the angles stay exact (an fp32 product would be off by whole turns)."""
     ps, D = 256, 64
