@@ -20,8 +20,15 @@
 // move to a new reference that puts the block's maximum at 2^6, so what a token 2^42
 // times lighter than the heaviest adds is still there.
 //
-// What bounds it: HBM, 2 * D + 8 / 16 bytes per token and KV head against 4 * G * D
-// flops (G flop per byte).  Layout of the work:
+// What bounds it: HBM, 2 * D + 1/2 bytes per token and KV head against 4 * G * D
+// flops (2 G flop per byte).  Measured at 32 / 8 heads, D = 128, back to back: 64 x 4096
+// tokens 84-89 us by box (6.0-6.4 TB/s), 38 x 8192 96-100 us (6.4-6.7 TB/s), one row of
+// 32768 15.0-15.3 us (4.4 TB/s: ramp, merge and launch gap are a third).  Next to
+// HBM a warp's own time counts: about 300 instructions a block, 64 of them widening
+// codes, and a loop that does not quite fit the instruction cache.  tcgen05 is not
+// used: it would want the widened codes back in shared memory, for products of 8
+// columns.  Staging with TMA boxes and mbarriers measured slower than cp.async
+// (64 x 4096 90 against 86 us, D = 64 106 against 88 us).  Layout of the work:
 //   * one CTA per tile, eight warps; warp w owns blocks w, w + 8, ... of the tile
 //     with a private softmax state, so the loop has no barrier and no shared state;
 //   * a warp copies its blocks by whole rows (cp.async, 16 bytes a lane) into a ring
@@ -698,17 +705,6 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q8_kernel(const __grid_
 template <int D, int G>
 cudaError_t launch_q8_t(const AttnQ8Params& p, int grid, cudaStream_t stream, bool cooperative) {
     constexpr size_t smem = sizeof(Q8Smem<D, G>);
-    static std::atomic<uint64_t> configured{0};   // devices whose copy of the kernel may use that much
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (!(configured.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(attention_q8_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-        configured.fetch_or(bit, std::memory_order_relaxed);
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
@@ -726,6 +722,22 @@ cudaError_t launch_q8_t(const AttnQ8Params& p, int grid, cudaStream_t stream, bo
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
+    // Devices on which the kernel has been allowed that much shared memory; a device
+    // that was reset since forgets it, and the launch is refused.
+    static std::atomic<uint64_t> configured{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (configured.load(std::memory_order_relaxed) & bit) {
+        e = cudaLaunchKernelEx(&cfg, attention_q8_kernel<D, G>, p);
+        if (e != cudaErrorInvalidValue) return e;
+        (void)cudaGetLastError();
+    }
+    e = cudaFuncSetAttribute(attention_q8_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_relaxed);
     return cudaLaunchKernelEx(&cfg, attention_q8_kernel<D, G>, p);
 }
 
