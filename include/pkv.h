@@ -327,7 +327,8 @@ typedef struct {
  * (PKV_DEV_ROW_FULL: past the table's end, or a negative entry; also a negative
  * length), lies outside the pool (PKV_DEV_PAGE_OOB), or its offsets do not lie
  * ascending in [0, total_tokens] (PKV_DEV_PLAN_MISMATCH; where offsets descend,
- * the rows around may be written in part).  Two rows must not append to one page.  One kernel on `stream`; needs no memory of its own.
+ * the rows around may be written in part).  Two rows must not append to one page.
+ * One kernel on `stream`; needs no memory of its own.
  * Errors: PKV_EINVAL (null or misaligned pointer, bad stride or count, a rotary
  * dim above D, another current device than the plan's), PKV_ECUDA.
  */
@@ -353,10 +354,13 @@ int pkv_append_rotary(const pkv_tokens *tokens, const pkv_rotary *rotary, void *
  *
  * pkv_decode_q8 is pkv_decode over such a cache (any scales, also ones not made
  * by pkv_append_q8): the same plan with every route and merge of it, outputs,
- * flags and errors.  The softmax and all sums are fp32; codes and queries enter
- * the products exactly.  A slot behind the row's last token may hold anything.
- * PKV_EUNSUPPORTED for a plan with math = PKV_MATH_FMA; the plan's copy option
- * has no effect.
+ * flags and errors, and the same rule for calls that overlap on the GPU: decodes
+ * with one plan share its workspace and counters, so they have to be ordered.  The
+ * softmax and all sums are fp32; codes enter the products exactly, queries to
+ * 2^-25 of their head's largest element.  A slot behind the row's last token may
+ * hold anything.  pkv_trace_enable and pkv_profile_enable cover its launches;
+ * pkv_plan_info.kv_bytes goes on counting bf16.  PKV_EUNSUPPORTED for a plan with
+ * math = PKV_MATH_FMA; the plan's copy option has no effect.
  */
 #define PKV_Q8_BLOCK 16
 int pkv_append_q8(const pkv_tokens *tokens, const pkv_rotary *rotary, void *k_pages, void *v_pages, float *k_scales,
@@ -393,7 +397,7 @@ int pkv_selftest_wait(int64_t limit_ns, uint32_t *status_h, int32_t *result_h);
 /*
  * Per-CTA timeline of the attention launch, a diagnostic (the debug per-CTA
  * tile counter and phase stamps).  While enabled, every attention launch of
- * pkv_decode / pkv_decode_host writes one row of PKV_TRACE_WORDS uint64 per CTA
+ * pkv_decode / pkv_decode_host / pkv_decode_q8 writes one row of PKV_TRACE_WORDS uint64 per CTA
  * into a device buffer owned by the plan (grown, synchronously, when a launch
  * has more CTAs than it holds); pkv_trace_read synchronises the device and
  * copies the last traced launch's rows out (row = blockIdx.x; *count = its
@@ -412,8 +416,8 @@ int pkv_selftest_wait(int64_t limit_ns, uint32_t *status_h, int32_t *result_h);
 int pkv_trace_enable(pkv_plan_t plan, int32_t enable);
 int pkv_trace_read(pkv_plan_t plan, uint64_t *rows_h, int32_t capacity, int32_t *count);
 
-/* Per-launch timing.  While enabled, pkv_decode brackets each kernel it
- * launches with CUDA events; pkv_profile_read waits for them and returns the
+/* Per-launch timing.  While enabled, pkv_decode / pkv_decode_q8 bracket each kernel they
+ * launch with CUDA events; pkv_profile_read waits for them and returns the
  * durations in milliseconds of the last pkv_decode's launches, in launch order. */
 int pkv_profile_enable(pkv_plan_t plan, int32_t enable);
 int pkv_profile_read(pkv_plan_t plan, float *ms, int32_t capacity, int32_t *count);

@@ -190,10 +190,6 @@ __device__ __forceinline__ Slice load_slice(const uint16_t* head, int e0, int e1
     return s;
 }
 
-// Turn a slice by the thread's eight angles (cos and sin already scaled).
-// Half pairs: x runs through a, y through b.  Neighbouring pairs: (x, y) are
-// (0, 1), (2, 3), ... of a, then of b.  A slice past the rotated elements is
-// only widened.
 __device__ __forceinline__ void widen(const Slice& s, float (&x)[16]) {
     float a[8], b[8];
     unpack_bf16x8(s.a, a);
@@ -205,6 +201,10 @@ __device__ __forceinline__ void widen(const Slice& s, float (&x)[16]) {
     }
 }
 
+// Turn a slice by the thread's eight angles (cos and sin already scaled).
+// Half pairs: x runs through a, y through b.  Neighbouring pairs: (x, y) are
+// (0, 1), (2, 3), ... of a, then of b.  A slice past the rotated elements is
+// only widened.
 template <bool kPairs>
 __device__ __forceinline__ void turn(const Slice& s, bool rotate, const float (&c)[8], const float (&sn)[8],
                                      float (&x)[16]) {

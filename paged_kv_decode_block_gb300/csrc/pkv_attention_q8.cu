@@ -576,6 +576,8 @@ __device__ int row_by_length(Q8Smem<D, G>& sm, const AttnParams& p, int rank) {
 
 template <int D, int G>
 __global__ void __launch_bounds__(kThreads, 2) attention_q8_kernel(const __grid_constant__ AttnQ8Params qp) {
+    // (aligned by its declaration: through an address rounded up at run time the
+    // compiler would lose sight of the memory being shared)
     extern __shared__ __align__(1024) uint8_t smem_q8[];
     Q8Smem<D, G>& sm = *reinterpret_cast<Q8Smem<D, G>*>(smem_q8);
     const AttnParams& p = qp.attn;
