@@ -1000,6 +1000,7 @@ int append_tokens(const pkv_tokens* t, const pkv_rotary* rotary, void* k_pages, 
     a.page_size = p->page_size;
     a.max_pages = g.max_pages_per_seq;
     a.num_pages = g.num_pages;
+    a.num_sms = p->num_sms;
     if (rotary) a.rot = *rotary;
     PKV_CUDA(pkv::launch_append_tokens(a, s));
     return PKV_OK;

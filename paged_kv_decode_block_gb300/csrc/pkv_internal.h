@@ -166,9 +166,11 @@ struct AppendTokensParams {
     uint32_t* status;
     int32_t B, Hq, Hkv, D, page_size, max_pages, num_pages;
     pkv_rotary rot;             // dim 0: no rotation
+    int32_t num_sms;            // SMs of the device
     // set by launch_append_tokens
     uint32_t page_magic;        // as AttnQ8Params::page_magic
     int32_t heads;              // KV heads per CTA
+    int32_t early;              // the next kernel may start before this one has ended
 };
 cudaError_t launch_append_tokens(const AppendTokensParams& p, cudaStream_t stream);
 
