@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import sys
 
 import numpy as np
@@ -85,6 +86,9 @@ class Tokens(ctypes.Structure):
                 ("v_stride", ctypes.c_int64), ("cu_tokens_d", ctypes.c_void_p), ("total_tokens", ctypes.c_int32)]
 
 
+_pack_tokens = struct.Struct("PPPPqqqqPi4x").pack   # a Tokens as bytes, which takes a fifth of the time to make
+
+
 # symbol -> (restype, argtypes); the full C ABI of include/pkv.h
 _P, _I32, _I64, _U32P = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(ctypes.c_uint32)
 _I32P = ctypes.POINTER(ctypes.c_int32)
@@ -102,10 +106,8 @@ SIGNATURES = {
     "pkv_append": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P]),
     "pkv_rotary_init": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), _I32, _I32, ctypes.c_float,
                                        ctypes.POINTER(RotaryParams)]),
-    "pkv_append_rotary": (ctypes.c_int, [ctypes.POINTER(Tokens), ctypes.POINTER(RotaryParams), _P, _P, _P, _P, _P, _P,
-                                         _P]),
-    "pkv_append_q8": (ctypes.c_int, [ctypes.POINTER(Tokens), ctypes.POINTER(RotaryParams), _P, _P, _P, _P, _P, _P, _P,
-                                     _P, _P]),
+    "pkv_append_rotary": (ctypes.c_int, [_P, ctypes.POINTER(RotaryParams), _P, _P, _P, _P, _P, _P, _P]),
+    "pkv_append_q8": (ctypes.c_int, [_P, ctypes.POINTER(RotaryParams), _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "pkv_decode_q8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "pkv_status": (ctypes.c_int, [_P, _P, _U32P]),
     "pkv_read_workspace": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I32P]),
@@ -472,7 +474,7 @@ def _tokens_arg(t, name, shape, dev):
     if t.shape == shape and t.dtype in _BF16 and t.get_device() == dev:
         T, heads, D = shape
         if T == 0:
-            return None, 0
+            return 0, 0
         between, head, one = t.stride()
         if one == 1 and (head == D or heads == 1):
             return t.data_ptr(), (between if T > 1 else 0)
@@ -503,22 +505,22 @@ def _append_tokens(what, fn, k_new, v_new, k_pages, v_pages, scales, block_table
         kv = (T, plan.Hkv, plan.D)
         k, k_stride = _tokens_arg(k_new, "k_new", kv, dev)
         v, v_stride = _tokens_arg(v_new, "v_new", kv, dev)
-        qp = qo = None
-        q_stride = qo_stride = 0
+        qp = qo = q_stride = qo_stride = cu = 0
         if q is not None and q_out is not None:
             heads = (T, plan.Hq, plan.D)
             qp, q_stride = _tokens_arg(q, "q", heads, dev)
             qo, qo_stride = _tokens_arg(q_out, "q_out", heads, dev)
         elif q is not None or q_out is not None:
             raise ValueError("q and q_out: give both or neither")
-        cu = _arg(cu_tokens, "cu_tokens", _I32T, (g.batch + 1,), dev) if cu_tokens is not None else None
+        if cu_tokens is not None:
+            cu = _arg(cu_tokens, "cu_tokens", _I32T, (g.batch + 1,), dev)
         types = bf if scales is None else _F8 or _f8_types()
         pages = (_arg(k_pages, "k_pages", types, plan.pool_shape, dev), _arg(v_pages, "v_pages", types, plan.pool_shape, dev))
         if scales is not None:
             pages += (_arg(scales[0], "k_scales", _F32T, plan.scales_shape, dev),
                       _arg(scales[1], "v_scales", _F32T, plan.scales_shape, dev))
         rows = plan.rows_shape
-        rc = fn(ctypes.byref(Tokens(qp, qo, k, v, q_stride, qo_stride, k_stride, v_stride, cu, T)),
+        rc = fn(_pack_tokens(qp, qo, k, v, q_stride, qo_stride, k_stride, v_stride, cu, T),
                 rotary.params if rotary is not None else None, *pages,
                 _arg(block_table, "block_table", _I32T, plan.table_shape, dev), _arg(seq_lens, "seq_lens", _I32T, rows, dev),
                 _arg(new_lens, "new_lens", _I32T, rows, dev), plan.handle,
