@@ -27,10 +27,10 @@
 // scale needs no other CTA, a thread owns 16 elements of one token of every head
 // of the group, so its eight sines and cosines serve the K head and the G query
 // heads, and every access is 16 bytes (8 for e4m3 codes of half pairs).  8 x 128
-// and 32 query heads, prompts of 12.5 thousand tokens in bf16: 49 us, 6.3 TB/s; of
-// 8.8 thousand in e4m3: 35.6 us, 5.5 TB/s, where the arithmetic (about 1000
+// and 32 query heads, prompts of 12.5 thousand tokens in bf16: 48.5 us, 6.3 TB/s; of
+// 8.8 thousand in e4m3: 34.7 us, 5.7 TB/s, where the arithmetic (about 1000
 // instructions a warp and head, half of the issue slots) bounds it too; one token
-// for each of 64 rows: 4.4 us in a graph, a chain of round trips (length, table
+// for each of 64 rows: 4.2 us in a graph, a chain of round trips (length, table
 // entry, scales, then the stores).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
