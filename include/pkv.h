@@ -296,8 +296,8 @@ int pkv_rotary_init(const double *inv_freq_h, int32_t dim, int32_t interleaved, 
  *   q, q_out     device bf16 [Hq][D] per token, or both NULL: the rotated queries
  *                go to q_out, which may be q itself (with the same stride)
  *   *_stride     elements from one token to the next, a multiple of 8 and at
- *                least the token's own size; 0: dense.  A slice of a fused
- *                projection's output needs no copy
+ *                least the token's own size; 0: dense (never one token for all).
+ *                A slice of a fused projection's output needs no copy
  *   cu_tokens_d  device int32 [B + 1], ascending from 0 to total_tokens, or NULL
  *   total_tokens tokens in k / v / q; B without offsets
  */

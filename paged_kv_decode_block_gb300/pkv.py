@@ -477,7 +477,11 @@ def _tokens_arg(t, name, shape, dev):
             return 0, 0
         between, head, one = t.stride()
         if one == 1 and (head == D or heads == 1):
-            return t.data_ptr(), (between if T > 1 else 0)
+            if T == 1:
+                return t.data_ptr(), 0
+            if between > 0:   # (0 would mean dense to the call, and a broadcast holds one token only)
+                return t.data_ptr(), between
+            raise ValueError(f"{name}: tokens must not share memory (a broadcast, strides {t.stride()})")
         raise ValueError(f"{name}: a token's heads must be dense (strides {t.stride()})")
     if not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -535,7 +539,7 @@ def append_rotary(k_new, v_new, k_pages, v_pages, block_table, seq_lens, new_len
                   q=None, q_out=None, cu_tokens=None, stream=None):
     """pkv_append_rotary: row b's tokens cu_tokens[b]..cu_tokens[b + 1] (without cu_tokens: its one
     token) go to positions seq_lens[b] on, keys and queries rotated; new_lens = the lengths after.
-    k_new / v_new / q: bf16 [T][heads][D], also slices of one projection's output."""
+    k_new / v_new / q: bf16 [T][heads][D], also slices of one projection's output, but no broadcast."""
     _append_tokens("pkv_append_rotary", (_lib or load()).pkv_append_rotary, k_new, v_new, k_pages, v_pages, None,
                    block_table, seq_lens, new_lens, plan, rotary, q, q_out, cu_tokens, stream)
 
