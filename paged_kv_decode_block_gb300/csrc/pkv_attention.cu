@@ -182,7 +182,7 @@ __device__ __forceinline__ void fma_init(FmaState<D, G>& st, const AttnParams& p
     const uint16_t* qrow = p.q + (static_cast<size_t>(tw.b) * p.Hq + tw.kvh * G) * D + sub * 8;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        const uint4 raw = __ldg(reinterpret_cast<const uint4*>(qrow + g * D));
+        const uint4 raw = *reinterpret_cast<const uint4*>(qrow + g * D);
         unpack_bf16x8(raw, st.qf[g]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -326,8 +326,8 @@ __device__ __forceinline__ void mma_init(MmaState<D, G>& st, const AttnParams& p
     const uint16_t* qh = p.q + (static_cast<size_t>(tw.b) * p.Hq + tw.kvh * G + (gid < G ? gid : 0)) * D;
 #pragma unroll
     for (int kt = 0; kt < D / 16; ++kt) {
-        st.qb[kt][0] = gid < G ? __ldg(reinterpret_cast<const uint32_t*>(qh + kt * 16 + 2 * tig)) : 0u;
-        st.qb[kt][1] = gid < G ? __ldg(reinterpret_cast<const uint32_t*>(qh + kt * 16 + 8 + 2 * tig)) : 0u;
+        st.qb[kt][0] = gid < G ? *reinterpret_cast<const uint32_t*>(qh + kt * 16 + 2 * tig) : 0u;
+        st.qb[kt][1] = gid < G ? *reinterpret_cast<const uint32_t*>(qh + kt * 16 + 8 + 2 * tig) : 0u;
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -531,11 +531,11 @@ __device__ void run_tile(Smem<D, G>& sm, const AttnParams& p, TileWork tw, uint3
         const int32_t* bt_row = p.block_table + static_cast<size_t>(tw.b) * p.max_pages;
         const uint64_t policy = l2_evict_first_policy();
         const int bpp = ps / kBlockRows;   // blocks per page (page sizes are multiples of 16)
-        int next_id = first_page + lane < last_page ? __ldg(bt_row + first_page + lane) : 0;
+        int next_id = first_page + lane < last_page ? bt_row[first_page + lane] : 0;
         for (int pg0 = first_page; pg0 < last_page; pg0 += 32) {
             const int ids = next_id;   // lane l: the table entry of page pg0 + l
             const int pg_next = pg0 + 32 + lane;
-            next_id = pg_next < last_page ? __ldg(bt_row + pg_next) : 0;
+            next_id = pg_next < last_page ? bt_row[pg_next] : 0;
             const int n_here = min(32, last_page - pg0);
             // Every lane checks its own entry once, and a batch with an entry outside
             // the pool is reported once; a block of such a page is not copied.

@@ -196,7 +196,7 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         return qp.page_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(blk), qp.page_magic)) : blk;
     };
     auto read_entry = [&](int i0) {
-        if (i0 + lane < mine) entry = __ldg(bt_row + page_of(row_block(i0 + lane)));
+        if (i0 + lane < mine) entry = bt_row[page_of(row_block(i0 + lane))];
     };
     auto fetch_batch = [&](int i0) {
         if (i0 + lane < mine) {
@@ -209,8 +209,8 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
             const int blk = row_block(i0 + lane);
             row_i = page * p.page_size + blk * kBlockRows - page_of(blk) * p.page_size;
             const size_t s = static_cast<size_t>(row_i / kBlockRows) * p.Hkv + tw.kvh;
-            k_next = __ldg(qp.k_scales + s);
-            v_next = __ldg(qp.v_scales + s);
+            k_next = qp.k_scales[s];
+            v_next = qp.v_scales[s];
         }
         read_entry(i0 + 32);
     };
@@ -236,7 +236,7 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
     {
         const uint16_t* qh = p.q + (static_cast<size_t>(tw.b) * p.Hq + tw.kvh * G + g % G) * D + t * 4;
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) q_raw[j] = __ldg(reinterpret_cast<const uint2*>(qh + 16 * j));
+        for (int j = 0; j < D / 16; ++j) q_raw[j] = *reinterpret_cast<const uint2*>(qh + 16 * j);
     }
     if (tw.lazy) tile_finish(p, tw);
     // the ring's first blocks

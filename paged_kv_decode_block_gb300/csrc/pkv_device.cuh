@@ -137,6 +137,11 @@ __device__ __forceinline__ void cp_async_commit_wait_all() {
 // Programmatic dependent launch: wait until the grids this launch depends on
 // have completed and their memory is visible (a no-op for an ordinary launch),
 // and let the next grid in the stream start launching its CTAs.
+// A grid that starts early lives while the one before it still writes (an append
+// its scales and rotated queries, say), so whatever a kernel may have written is
+// read by ordinary loads behind the wait, not by read-only ones (ld.global.nc):
+// those are defined only for data that nobody writes while the grid lives, and
+// nothing keeps the compiler from moving them above the wait.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
