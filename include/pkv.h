@@ -357,8 +357,10 @@ int pkv_append_rotary(const pkv_tokens *tokens, const pkv_rotary *rotary, void *
  * flags and errors, and the same rule for calls that overlap on the GPU: decodes
  * with one plan share its workspace and counters, so they have to be ordered.  The
  * softmax and all sums are fp32; codes enter the products exactly, queries to
- * 2^-25 of their head's largest element.  A slot behind the row's last token may
- * hold anything.  pkv_trace_enable and pkv_profile_enable cover its launches;
+ * 2^-25 of their head's largest element, weights times V scales to 2^-22 of
+ * themselves and at least to 2^-42 of their head's largest such product in the row,
+ * however far the scales of its blocks lie apart.  A slot behind the row's last
+ * token may hold anything.  pkv_trace_enable and pkv_profile_enable cover its launches;
  * pkv_plan_info.kv_bytes goes on counting bf16.  PKV_EUNSUPPORTED for a plan with
  * math = PKV_MATH_FMA; the plan's copy option has no effect.
  */

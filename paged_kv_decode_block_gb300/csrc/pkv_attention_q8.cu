@@ -11,14 +11,15 @@
 // e4m3 codes are exact in f16, so both products run on f16 tensor cores
 // (mma.m16n8k16, fp32 accumulation).  q (bf16) is scaled per head by the power
 // of two that brings its largest element to [1, 2), so it is exact in f16 down to
-// 2^-14 of that element and rounded by at most 2^-25 of it below.  A weight
-// 2^(s - m) * vs_B / r (r: the largest block scale so far, rounded up to a power of
-// two) is split into f16 hi + 2^-11 lo, 22 bits, and 2^-36 is the least that is not
-// rounded to zero; the parts are columns of the products' right operand (with G =
-// 8, of a second one).  Statistics and sums are fp32.  m follows the running
-// maximum lazily: weights may grow to 2^14 (within f16) before the accumulators
-// move to a new reference that puts the block's maximum at 2^6, so what a token 2^42
-// times lighter than the heaviest adds is still there.
+// 2^-14 of that element and rounded by at most 2^-25 of it below.  A query head has
+// two references: m for its weights 2^(s - m), fp32, and m - lift for what goes into
+// O, because a light token may lie in a block of large scale and the heaviest in one
+// of small scale.  w = 2^(s - m + lift) * vs_B is split into f16 hi + 2^-11 lo, 22
+// bits, and 2^-36 is the least that is not rounded to zero; the parts are columns of
+// the products' right operand (with G = 8, of a second one).  Statistics and sums are
+// fp32.  The references follow their running maxima lazily: w may grow to 2^14 (within
+// f16) before O moves to a reference that puts the block's largest w at 2^6 or more,
+// so what a token adds whose w is 2^42 times smaller than the largest is still there.
 //
 // What bounds it: HBM, 2 * D + 1/2 bytes per token and KV head against 4 * G * D
 // flops (2 G flop per byte).  Measured at 32 / 8 heads, D = 128, back to back: 64 x 4096
@@ -43,6 +44,7 @@
 // of such a page.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 #include <stdint.h>
@@ -58,8 +60,11 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = kThreads / 32;
-constexpr float kHeadroom = 6.f;     // a new reference puts the block's largest weight at 2^6
-constexpr float kGrowth = 14.f;      // and holds until a weight would pass 2^14
+// m, the reference of the weights, puts the largest weight of the block that moves it at 2^5 to 2^6 and
+// holds until one would pass 2^13; O's reference does the same with weights times V scales, 2^6 to 2^8
+// and 2^14.
+constexpr float kHeadroom = 6.f, kGrowth = 13.f, kHeadroomV = 8.f, kGrowthV = 14.f;
+constexpr float kMaxLift = 112.f;    // most that O's reference lies below m, in powers of two (2^13 * 2^112 is finite)
 constexpr float kLoUp = 2048.f, kLoDown = 1.f / 2048.f;   // P's lo parts are held times 2^11
 
 template <int D, int G>
@@ -148,12 +153,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// The least power of two not below x > 0 (x a finite fp32; the exponent saturates at 2^126).
-__device__ __forceinline__ float power_of_two_above(float x) {
-    const uint32_t u = __float_as_uint(x);
-    int e = static_cast<int>(u >> 23) + ((u & 0x7fffffu) ? 1 : 0);
-    e = max(1, min(253, e));
-    return __uint_as_float(static_cast<uint32_t>(e) << 23);
+// 2^e for a whole e from -126 to 127.
+__device__ __forceinline__ float exp2i(float e) {
+    return __uint_as_float(static_cast<uint32_t>(static_cast<int>(e) + 127) << 23);
+}
+
+// The least whole number e with |x| < 2^e (-126 for zero and subnormals).
+__device__ __forceinline__ float exponent_above(float x) {
+    const uint32_t biased = (__float_as_uint(x) >> 23) & 0xffu;
+    return __uint_as_float(0x4b000000u | biased) - (8388608.f + 126.f);   // 2^23 + biased, exactly
 }
 
 // One tile: every warp reduces its blocks, then the eight states are combined
@@ -272,23 +280,24 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         big = max(big, __shfl_xor_sync(kFull, big, 2));
         const int e = max(-126, min(126, static_cast<int>(big >> 23) - 127));
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        const float up = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        qs[0] = __shfl_sync(kFull, up, 8 * t);       // column 2t: the lanes of g = 2t hold its head
-        qs[1] = __shfl_sync(kFull, up, 8 * t + 4);
+        const float back = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        qs[0] = __shfl_sync(kFull, back, 8 * t);     // column 2t: the lanes of g = 2t hold its head
+        qs[1] = __shfl_sync(kFull, back, 8 * t + 4);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
             qb[j][0] = pack_half(__uint_as_float(q_raw[j].x << 16) * down, __uint_as_float(q_raw[j].x & 0xffff0000u) * down);
             qb[j][1] = pack_half(__uint_as_float(q_raw[j].y << 16) * down, __uint_as_float(q_raw[j].y & 0xffff0000u) * down);
         }
     }
-    // Where the parts share a column tile, columns 2t and 2t + 1 carry up * w - part * f16(w):
-    // P's hi parts (up 1, part 0) or its lo parts (both 2^11)
-    const float up0 = 2 * t < G ? 1.f : kLoUp, up1 = 2 * t + 1 < G ? 1.f : kLoUp;
+    // Where the parts share a column tile, columns 2t and 2t + 1 carry whole * w - part * f16(w):
+    // P's hi parts (whole 1, part 0) or its lo parts (both 2^11)
+    const float whole0 = 2 * t < G ? 1.f : kLoUp, whole1 = 2 * t + 1 < G ? 1.f : kLoUp;
     const float part0 = 2 * t < G ? 0.f : kLoUp, part1 = 2 * t + 1 < G ? 0.f : kLoUp;
 
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // columns 2t, 2t + 1: reference, this lane's share of the sum
-    float vref = 1.1754944e-38f;       // power of two not below any block's V scale so far
-    float vinv = 8.5070592e37f;
+    // columns 2t, 2t + 1: the reference m (a whole number; before the first block less than any), this
+    // lane's share of the sum of the weights 2^(s - m), and up = 2^lift, by which a weight is multiplied
+    // on its way into O: O's reference is m - lift
+    float m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f}, up[2] = {1.f, 1.f}, lift[2] = {0.f, 0.f};
     float o[C::kParts][D / 16][4];     // O^T accumulators
 #pragma unroll
     for (int x = 0; x < C::kParts; ++x)
@@ -363,56 +372,58 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
             }
             if constexpr (U == 1) take_v(0);
 
-            // a reference moves when one of its weights would pass 2^14 (m = -inf: at
-            // once), or a block's V scale passes r; neither happens often, so the exact
-            // maximum is found only then
-            float bm0 = fmaxf(z[0][0], z[0][2]), bm1 = fmaxf(z[0][1], z[0][3]), va = fabsf(vs[0]);
-            if constexpr (U == 2) {
-                bm0 = fmaxf(bm0, fmaxf(z[1][0], z[1][2]));
-                bm1 = fmaxf(bm1, fmaxf(z[1][1], z[1][3]));
-                va = fmaxf(va, fabsf(vs[1]));
+            // A reference moves when a weight would pass 2^13, or a weight times V scale 2^14 in O's
+            // units; neither happens often, so the exact maxima are found only then
+            float t0 = -INFINITY, t1 = -INFINITY, y0 = -INFINITY, y1 = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float ev = exponent_above(vs[u]);
+                const float a0 = fmaxf(z[u][0], z[u][2]) - m[0], a1 = fmaxf(z[u][1], z[u][3]) - m[1];
+                t0 = fmaxf(t0, a0);
+                t1 = fmaxf(t1, a1);
+                y0 = fmaxf(y0, a0 + ev);
+                y1 = fmaxf(y1, a1 + ev);
             }
-            if (__any_sync(kFull, bm0 > m[0] + kGrowth || bm1 > m[1] + kGrowth) || va > vref) {
+            if (__any_sync(kFull, t0 > kGrowth || t1 > kGrowth || y0 + lift[0] > kGrowthV || y1 + lift[1] > kGrowthV)) {
 #pragma unroll
-                for (int x = 4; x < 32; x <<= 1) {
-                    bm0 = fmaxf(bm0, __shfl_xor_sync(kFull, bm0, x));
-                    bm1 = fmaxf(bm1, __shfl_xor_sync(kFull, bm1, x));
+                for (int c = 0; c < 2; ++c) {
+                    float top = fmaxf(z[0][c], z[0][2 + c]);
+                    if constexpr (U == 2) top = fmaxf(top, fmaxf(z[1][c], z[1][2 + c]));
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+                    const float mn = top - m[c] > kGrowth ? ceilf(top) - kHeadroom : m[c];
+                    float most = fmaxf(z[0][c], z[0][2 + c]) - mn + exponent_above(vs[0]);
+                    if constexpr (U == 2) most = fmaxf(most, fmaxf(z[1][c], z[1][2 + c]) - mn + exponent_above(vs[1]));
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, x));
+                    const float moved = m[c] == mn ? 0.f : mn - m[c];
+                    float ln = fminf(lift[c] + moved, kMaxLift);   // O's reference stays where it is ...
+                    if (most + ln > kGrowthV) ln = fmaxf(kHeadroomV - ceilf(most), -126.f);   // ... or moves up too
+                    l[c] *= exp2f(-moved);
+                    const float f = exp2f(ln - lift[c] - moved);
+                    m[c] = mn;
+                    lift[c] = ln;
+                    up[c] = exp2i(ln);
+#pragma unroll
+                    for (int x = 0; x < C::kParts; ++x)
+#pragma unroll
+                        for (int n = 0; n < D / 16; ++n) {
+                            o[x][n][c] *= f;
+                            o[x][n][2 + c] *= f;
+                        }
                 }
-                const float mn0 = bm0 > m[0] + kGrowth ? bm0 - kHeadroom : m[0];
-                const float mn1 = bm1 > m[1] + kGrowth ? bm1 - kHeadroom : m[1];
-                float f0 = m[0] == mn0 ? 1.f : exp2f(m[0] - mn0);   // from m = -inf: 0
-                float f1 = m[1] == mn1 ? 1.f : exp2f(m[1] - mn1);
-                m[0] = mn0;
-                m[1] = mn1;
-                l[0] *= f0;
-                l[1] *= f1;
-                if (va > vref) {
-                    const float vn = power_of_two_above(va);
-                    f0 *= vref / vn;
-                    f1 *= vref / vn;
-                    vref = vn;
-                    vinv = 1.f / vn;
-                }
-#pragma unroll
-                for (int x = 0; x < C::kParts; ++x)
-#pragma unroll
-                    for (int n = 0; n < D / 16; ++n) {
-                        o[x][n][0] *= f0;
-                        o[x][n][1] *= f1;
-                        o[x][n][2] *= f0;
-                        o[x][n][3] *= f1;
-                    }
             }
             // B fragments of P^T: the 8 x 8 transposes of the token-major tiles
             uint32_t pb[U][C::kParts][2];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float vw = vs[u] * vinv;
                 const float p0 = ex2(z[u][0] - m[0]), p1 = ex2(z[u][1] - m[1]);   // token g (masked: 0)
                 const float p2 = ex2(z[u][2] - m[0]), p3 = ex2(z[u][3] - m[1]);   // token g + 8
                 l[0] += p0 + p2;
                 l[1] += p1 + p3;
-                const float w0 = p0 * vw, w1 = p1 * vw, w2 = p2 * vw, w3 = p3 * vw;
+                // (in this order no product overflows, whatever the scale of a block that weighs nothing)
+                const float w0 = p0 * up[0] * vs[u], w1 = p1 * up[1] * vs[u];
+                const float w2 = p2 * up[0] * vs[u], w3 = p3 * up[1] * vs[u];
                 const uint32_t ha = pack_half(w0, w1), hb = pack_half(w2, w3);
                 const float2 ua = unpack_half(ha), ub = unpack_half(hb);
                 if constexpr (C::kParts == 2) {
@@ -421,8 +432,8 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
                     pb[u][1][0] = transpose8(pack_half((w0 - ua.x) * kLoUp, (w1 - ua.y) * kLoUp));
                     pb[u][1][1] = transpose8(pack_half((w2 - ub.x) * kLoUp, (w3 - ub.y) * kLoUp));
                 } else {
-                    pb[u][0][0] = transpose8(pack_half(fmaf(-part0, ua.x, w0 * up0), fmaf(-part1, ua.y, w1 * up1)));
-                    pb[u][0][1] = transpose8(pack_half(fmaf(-part0, ub.x, w2 * up0), fmaf(-part1, ub.y, w3 * up1)));
+                    pb[u][0][0] = transpose8(pack_half(fmaf(-part0, ua.x, w0 * whole0), fmaf(-part1, ua.y, w1 * whole1)));
+                    pb[u][0][1] = transpose8(pack_half(fmaf(-part0, ub.x, w2 * whole0), fmaf(-part1, ub.y, w3 * whole1)));
                 }
             }
 
@@ -471,6 +482,7 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         l[0] += __shfl_xor_sync(kFull, l[0], x);
         l[1] += __shfl_xor_sync(kFull, l[1], x);
     }
+    const float down[2] = {exp2i(-lift[0]), exp2i(-lift[1])};   // from O's reference to m
     poisoned = __any_sync(kFull, poisoned) ? 1 : 0;
     cp_async_wait<0>();   // (planned blocks past the row's end may still be on their way)
     __syncwarp();         // every lane has read its slots: the ring takes the partial
@@ -492,7 +504,7 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         for (int c = 0; c < 2; ++c)
             if (2 * t + c < G)
                 *reinterpret_cast<float2*>(acc + (2 * t + c) * Q8Smem<D, G>::kAccRow + 16 * n) =
-                    make_float2(f[2 * c] * vref, f[2 * c + 1] * vref);
+                    make_float2(f[2 * c] * down[c], f[2 * c + 1] * down[c]);
     }
     if (g == 0) {
 #pragma unroll
@@ -521,7 +533,7 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float mw = sm.m[w][h];
-                const float f = mw == -INFINITY && sm.l[w][h] == 0.f ? 0.f : exp2f(mw - M);   // idle warp: 0
+                const float f = exp2f(mw - M);   // idle warp: 0
                 lsum = fmaf(sm.l[w][h], f, lsum);
                 const float4 a = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w]) +
                                                                   h * Q8Smem<D, G>::kAccRow + d);

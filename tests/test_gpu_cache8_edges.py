@@ -1,7 +1,7 @@
 """pkv_append_q8 and pkv_decode_q8 on the GPU where test_gpu_cache8.py does not look: calls that follow one another with
-nothing between them.
+nothing between them, weights and V scales far apart.
 
-Tolerances: as in test_gpu_cache8.py.
+Tolerances: as in test_gpu_cache8.py, or derived at the test.
 """
 import numpy as np
 import pytest
@@ -9,7 +9,7 @@ import torch
 
 from oracle import cache8
 from paged_kv_decode_block_gb300 import pkv
-from test_gpu_cache8 import Cache, New, bits
+from test_gpu_cache8 import Cache, New, bf16, bits
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +72,103 @@ def test_append_and_decode_back_to_back(B, H, G, D, route):
         c.lens, c.q = (lens + i + 1).astype(np.int32), turned[i]
         d["out"], d["lse"] = outs[i], lses[i]
         c.check(what=f"step {i}")
+
+
+# ------------------------------------------------------------------ weights and V scales far apart
+
+def check_by_terms(c, what=""):
+    """out against the oracle, each element by the sum of its own terms: |error| <= F sum_t p_t |v_t| with the factor F
+    of Cache.bounds (scores of the tokens that weigh anything, weights, sums; once for the numerator and once for the
+    denominator), and for each token at most half a step of the least weight kept, 2^-42 of the row's largest weight times V scale, times a code of 448."""
+    torch.cuda.synchronize()
+    q = cache8.bf16_to_f64(c.q)
+    out, lse = c.d["out"].cpu().numpy().astype(np.float64), c.d["lse"].cpu().numpy()
+    G = c.Hq // c.H
+    for b in range(c.B):
+        n = int(c.lens[b])
+        rows = cache8.places(c.table, b, 0, n, c.ps)
+        for h in range(c.H):
+            ks, vs = (s.reshape(-1, c.H).astype(np.float64)[rows // 16, h][:, None] for s in (c.ks, c.vs))
+            k, v = (cache8.E4M3[x.reshape(-1, c.H, c.D)[rows, h]] * s for x, s in ((c.kc, ks), (c.vc, vs)))
+            s = q[b, h * G:(h + 1) * G] @ k.T / np.sqrt(c.D)
+            m = s.max(1, keepdims=True)
+            p = np.exp(s - m)
+            total = p.sum(1, keepdims=True)
+            dot = (np.abs(q[b, h * G:(h + 1) * G]) @ np.abs(k).T)[p >= 2.0 ** -126].max() / np.sqrt(c.D)
+            f = 2 * (c.D + 16) * 2.0 ** -23 * dot + (n + 64) * 2.0 ** -23 + 2.0 ** -20
+            want, size = p @ v / total, p @ np.abs(v) / total
+            least = n * 448 * 2.0 ** -42 * (p * np.abs(vs).T).max(1, keepdims=True) / total
+            off = np.abs(out[b, h * G:(h + 1) * G] - want)
+            limit = 2 * f * size + least
+            assert np.all(off <= limit), (what, b, h, np.max(off / np.maximum(limit, 1e-300)))
+            ref = (m + np.log(total))[:, 0]
+            assert np.all(np.abs(lse[b, h * G:(h + 1) * G] - ref) <= f * np.maximum(1, np.abs(ref))), (what, b, h)
+
+
+@pytest.mark.parametrize("D, G", [(64, 1), (64, 8), (128, 2), (128, 4), (128, 8)])
+@pytest.mark.parametrize("k", [12, 20, 30, 36, 44, 80, 120])
+@pytest.mark.parametrize("first", [True, False])
+def test_decode_heavy_token_in_a_block_of_small_scale(D, G, k, first):
+    """One key far above the others, in a block whose V scale is 2^-k of the others', before or behind them in the same
+    warp's blocks (0 and 8): the others weigh nothing (e^-1000), and out is that token's V: its weight times scale split
+    to 22 bits, one rounding where the parts meet, the division by its weight and its rounding, 2^-21 in all."""
+    c = Cache([144], Hq=G, H=1, D=D, seed=200 + k)
+    rows = cache8.places(c.table, 0, 0, 144, 16)
+    c.kc[:] = 0
+    q = cache8.bf16_to_f64(c.q)[0]
+    c.q = bf16(np.broadcast_to(q[:1], (1, G, D)))
+    heavy = rows[3] if first else rows[8 * 16 + 3]
+    c.kc.reshape(-1, 1, D)[heavy, 0] = cache8.e4m3_encode(np.sign(q[0]) * 448)
+    c.ks[:] = 1.0   # the heavy token's score: 448 sum |q| / sqrt(D), over 1000
+    c.vs[:] = 1.0
+    c.vs.reshape(-1)[heavy // 16] = 2.0 ** -k
+    c.upload()
+    for route in ("direct", "persistent"):
+        c.d["out"].fill_(7.0)
+        c.decode(c.plan(force_mode=route))
+        torch.cuda.synchronize()
+        want = cache8.E4M3[c.vc.reshape(-1, D)[heavy]] * 2.0 ** -k
+        got = c.d["out"].cpu().numpy().astype(np.float64)[0]
+        assert np.all(np.abs(got - want) <= 2.0 ** -20 * np.abs(want)), (route, np.max(np.abs(got - want)) * 2.0 ** k)
+
+
+@pytest.mark.parametrize("D, G, n", [(64, 4, 700), (128, 4, 700), (128, 8, 300), (64, 1, 3000), (128, 2, 6000)])
+@pytest.mark.parametrize("seed", [1, 2])
+def test_decode_scales_against_weights(D, G, n, seed):
+    """Blocks whose V scales, from 2^-55 to 2^55, undo their tokens' weights up to a factor of 2^12, in a random order:
+    every block adds to the output, the heavy ones to the sum, and both references move again and again.  6000 tokens
+    of D = 128 and 3000 of D = 64 (one tile) take the loop that reduces two blocks a turn."""
+    rng = np.random.default_rng(300 + seed)
+    c = Cache([n], Hq=G, H=1, D=D, seed=310 + seed)
+    rows = cache8.places(c.table, 0, 0, n, 16)
+    blk = rows[::16] // 16
+    c.q = bf16(np.full((1, G, D), 0.5))
+    power = rng.uniform(-55, 55, len(blk))
+    c.kc[:] = 0
+    c.kc.reshape(-1, 1, D)[rows, 0, 0] = cache8.e4m3_encode(rng.uniform(240, 272, n))
+    # a score of -power ln 2 at a code of 256 (and up to 1/16 of it more or less)
+    c.ks.reshape(-1)[blk] = -power * np.log(2.0) * np.sqrt(D) / 128
+    c.vs.reshape(-1)[blk] = 2.0 ** np.round(power + rng.uniform(-6, 6, len(blk)))
+    c.upload()
+    for route, splits in (("direct", 0), ("split_queue", 3)):
+        c.d["out"].fill_(7.0)
+        c.decode(c.plan(force_mode=route, num_splits=splits))
+        check_by_terms(c, route)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -120, 2.0 ** -149, 2.0 ** 110, -2.0 ** 100])
+def test_decode_blocks_of_extreme_scale_that_weigh_nothing(scale):
+    """Blocks of extreme V scale before (every warp's first), between and behind ordinary ones, with scores so low that
+    their weights are zero: the output is the ordinary ones'."""
+    c = Cache([800], Hq=8, H=2, D=128, seed=320)
+    rows = cache8.places(c.table, 0, 0, 800, 16)
+    q = cache8.bf16_to_f64(c.q)[0]
+    c.q = bf16(np.broadcast_to(q[:1], (1, 8, 128)))
+    for i in np.r_[0:9, 20:24, 45:50]:
+        at = rows[16 * i:16 * i + 16]
+        c.kc.reshape(-1, 2, 128)[at] = cache8.e4m3_encode(np.sign(q[0]) * -448)
+        c.ks.reshape(-1, 2)[at[0] // 16] = 1.0
+        c.vs.reshape(-1, 2)[at[0] // 16] = scale
+    c.upload()
+    c.decode(c.plan(force_mode="direct"))
+    check_by_terms(c)
