@@ -64,7 +64,9 @@ constexpr int kWarps = kThreads / 32;
 // holds until one would pass 2^13; O's reference does the same with weights times V scales, 2^6 to 2^8
 // and 2^14.
 constexpr float kHeadroom = 6.f, kGrowth = 13.f, kHeadroomV = 8.f, kGrowthV = 14.f;
-constexpr float kMaxLift = 112.f;    // most that O's reference lies below m, in powers of two (2^13 * 2^112 is finite)
+// Most that O's reference lies below m, in powers of two: 2^13 * 2^104 is finite, and a sum of 2^28
+// weights brings m another 2^41 above, 2^145 in all, whose reciprocal fp32 just holds.
+constexpr float kMaxLift = 104.f;
 constexpr float kLoUp = 2048.f, kLoDown = 1.f / 2048.f;   // P's lo parts are held times 2^11
 
 template <int D, int G>
@@ -475,14 +477,23 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         reduce(std::integral_constant<int, 1>{});
     trace_stamp(sm, p, kTrStreamEnd);
 
-    // publish the warp's state: fold the lo parts into the hi parts; a lane then
-    // holds D / 8 neighbouring dimensions of its columns' heads
+    // publish the warp's state, divided by the power of two that brings the sum of its
+    // weights to [1, 2), or to [1/16, 1/8) where large scales are about, so that the
+    // eight partials together are no larger than the output: fold the lo parts into the
+    // hi parts; a lane then holds D / 8 neighbouring dimensions of its columns' heads
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1) {
         l[0] += __shfl_xor_sync(kFull, l[0], x);
         l[1] += __shfl_xor_sync(kFull, l[1], x);
     }
-    const float down[2] = {exp2i(-lift[0]), exp2i(-lift[1])};   // from O's reference to m
+    float down[2];   // from O's reference to m, and the division
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const float e = l[c] > 0.f ? fminf(exponent_above(l[c]) + (lift[c] > 0.f ? -1.f : 3.f), 126.f) : 0.f;
+        down[c] = exp2f(-lift[c] - e);
+        l[c] *= exp2i(-e);
+        m[c] += e;
+    }
     poisoned = __any_sync(kFull, poisoned) ? 1 : 0;
     cp_async_wait<0>();   // (planned blocks past the row's end may still be on their way)
     __syncwarp();         // every lane has read its slots: the ring takes the partial

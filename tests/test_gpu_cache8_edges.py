@@ -172,3 +172,14 @@ def test_decode_blocks_of_extreme_scale_that_weigh_nothing(scale):
     c.upload()
     c.decode(c.plan(force_mode="direct"))
     check_by_terms(c)
+
+
+@pytest.mark.parametrize("route, splits", [("direct", 0), ("split_queue", 3), ("persistent", 0)])
+def test_decode_values_near_the_largest_float(route, splits):
+    """V values up to 448 * 2^118, which is 2^126.8: sums of weights times values pass the largest float where the
+    output does not."""
+    c = Cache([500, 3, 33], Hq=8, H=2, D=64, seed=330)
+    c.vs[:] = 2.0 ** 118
+    c.upload()
+    c.decode(c.plan(force_mode=route, num_splits=splits))
+    check_by_terms(c)
