@@ -553,7 +553,7 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
                 r.z = fmaf(a.z, f, r.z);
                 r.w = fmaf(a.w, f, r.w);
             }
-            const float inv = 1.f / lsum;
+            const float inv = lsum == 0.f ? 0.f : 1.f / lsum;   // (every score -inf: as no token at all)
             r = make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv);
             lse2 = M + log2f(lsum);
         }

@@ -183,3 +183,27 @@ def test_decode_values_near_the_largest_float(route, splits):
     c.upload()
     c.decode(c.plan(force_mode=route, num_splits=splits))
     check_by_terms(c)
+
+
+@pytest.mark.parametrize("route, splits", [("direct", 0), ("split_queue", 3), ("persistent", 0)])
+def test_decode_scores_of_minus_infinity(route, splits):
+    """Scores past the least float, in every warp's first blocks: those tokens weigh nothing; a row of nothing else has
+    no weight at all, as an empty row."""
+    c = Cache([500, 500, 40, 40], Hq=4, H=1, D=64, seed=331)
+    q = cache8.bf16_to_f64(c.q)
+    c.q = bf16(np.broadcast_to(np.sign(q[:, :1]) * 2.0 ** 60, q.shape))
+    kc, ks = c.kc.reshape(-1, 1, 64), c.ks.reshape(-1)
+    c.ks *= np.float32(2.0 ** -60)
+    for b, blocks in ((0, range(8)), (1, range(3, 32)), (2, range(1)), (3, range(3))):
+        for i in blocks:
+            at = cache8.places(c.table, b, 16 * i, 16 * i + 16, 16)
+            kc[at] = cache8.e4m3_encode(np.sign(q[b, 0]) * -448)
+            ks[at[0] // 16] = 2.0 ** 100   # scores of -2^60 448 64 2^100 / 8
+    c.upload()
+    c.decode(c.plan(force_mode=route, num_splits=splits))
+    torch.cuda.synchronize()
+    assert (c.d["out"][3] == 0).all() and torch.isneginf(c.d["lse"][3]).all()
+    c.lens[3] = 0   # (in 64 bits its scores are finite)
+    live = c.d["out"].clone(), c.d["lse"].clone()
+    c.B, c.d["out"], c.d["lse"] = 3, live[0][:3], live[1][:3]
+    check_by_terms(c)
