@@ -270,7 +270,7 @@ int pkv_append(const void *k_new, const void *v_new, void *k_pages, void *v_page
  *     (x, y) -> scale * (x cos - y sin, y cos + x sin)
  * with (x, y) = elements (m, m + dim / 2), or (2m, 2m + 1) if interleaved; the
  * elements from `dim` on pass unchanged.  The angle is exact to about 2^-32 of a
- * turn at any position.
+ * turn at any position, for |inv_freq| up to 2^40.
  *   pkv_rotary_init   fills *rotary (a plain value: copy it freely, nothing is
  *                     owned).  inv_freq_h host double [dim / 2], radians per
  *                     token, finite; dim a multiple of 16 up to

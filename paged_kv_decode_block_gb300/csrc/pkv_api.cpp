@@ -918,6 +918,33 @@ int pkv_append(const void* k_new, const void* v_new, void* k_pages, void* v_page
     return PKV_OK;
 }
 
+}  // extern "C"
+
+namespace {
+
+// freq / 2 pi modulo 1, in units of 2^-64 (off by at most one of them for |freq| up
+// to 2^40).  1 / 2 pi is held in two doubles; the product's rounding error comes from
+// a fused multiply-add; whole turns are dropped from both parts before they are put
+// together as an integer.  In one double the quotient is off by up to 2^-56 turns a
+// token, 2^-25 at the farthest position.
+uint64_t turn_step(double freq) {
+    constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;   // 1 / 2 pi
+    const double a = std::fabs(freq);
+    double hi = a * kHi;
+    double lo = std::fma(a, kLo, std::fma(a, kHi, -hi));
+    hi = std::ldexp(hi - std::floor(hi), 64);      // in [0, 2^64)
+    lo = std::ldexp(lo - std::nearbyint(lo), 64);  // in [-2^63, 2^63]
+    const double whole = std::floor(hi);
+    double rest = std::nearbyint((hi - whole) + lo);
+    if (rest >= 0x1p63) rest -= 0x1p64;
+    const uint64_t step = static_cast<uint64_t>(whole) + static_cast<uint64_t>(static_cast<int64_t>(rest));
+    return freq < 0 ? 0 - step : step;   // modulo 2^64
+}
+
+}  // namespace
+
+extern "C" {
+
 int pkv_rotary_init(const double* inv_freq_h, int32_t dim, int32_t interleaved, float scale, pkv_rotary* rotary) {
     if (!inv_freq_h || !rotary || dim <= 0 || dim > PKV_ROTARY_MAX_DIM || dim % 16 || (interleaved & ~1) ||
         !std::isfinite(scale))
@@ -929,9 +956,7 @@ int pkv_rotary_init(const double* inv_freq_h, int32_t dim, int32_t interleaved, 
     r.interleaved = interleaved;
     r.scale = scale;
     for (int m = 0; m < dim / 2; ++m) {
-        const double turns = inv_freq_h[m] / 6.283185307179586476925;
-        const double part = ldexp(turns - floor(turns), 64);   // in [0, 2^64]; a whole turn is none
-        r.step[m] = part < 18446744073709551616.0 ? static_cast<uint64_t>(part) : 0;
+        r.step[m] = turn_step(inv_freq_h[m]);
     }
     *rotary = r;
     return PKV_OK;

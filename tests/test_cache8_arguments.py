@@ -1,4 +1,7 @@
 """What the calls of the rotated append and the 8-bit cache refuse or derive on the host, without a GPU."""
+from fractions import Fraction
+
+import numpy as np
 import pytest
 import torch
 
@@ -33,3 +36,48 @@ def test_token_strides():
                       (x[:1].expand(1, 10, 64), 0)):
         assert tokens_arg(t, tuple(t.shape)) == (t.data_ptr(), stride)
     assert tokens_arg(x[:0], (0, 10, 64)) == (0, 0)
+
+
+# ------------------------------------------------------------------ angles
+
+def turns_of(freq):
+    """freq / 2 pi modulo 1 as a fraction, 1 / 2 pi to 400 bits by Machin's formula in integers."""
+    bits = 420
+    one = 1 << bits
+
+    def arctan_inverse(x):
+        term = total = one // x
+        n, sign = 3, -1
+        while term:
+            term //= x * x
+            total += sign * (term // n)
+            n, sign = n + 2, -sign
+        return total
+
+    pi = 4 * (4 * arctan_inverse(5) - arctan_inverse(239))
+    return Fraction(freq) * Fraction(one, 2 * pi) % 1
+
+
+@pytest.mark.parametrize("base, dim", [(10000.0, 128), (500000.0, 64), (1e6, 16)])
+def test_rotary_steps_to_a_unit_of_the_last_place(base, dim):
+    """The angle of a step off by one unit, 2^-64 turns, is off by 2^-33 turns at position 2^31."""
+    got = pkv.Rotary(dim, base=base).params
+    for m, f in enumerate(base ** (-np.arange(0, dim, 2, dtype=np.float64) / dim)):
+        off = (got.step[m] - turns_of(float(f)) * 2 ** 64) % 2 ** 64
+        assert min(off, 2 ** 64 - off) <= 1, m
+
+
+def test_rotary_steps_of_any_frequency():
+    rng = np.random.default_rng(1)
+    freq = np.concatenate([rng.uniform(-10, 10, 100), 2.0 ** rng.uniform(-70, 40, 100), -2.0 ** rng.uniform(-70, 40, 100),
+                           [0.0, -0.0, 2.0 ** -1074, -2.0 ** -64, 2 * np.pi, 2.0 ** 40, 1e300, -1e300, 1.7e308, 2.0 ** 62]])
+    for i in range(0, len(freq) - 8, 8):
+        got = pkv.Rotary(16, inv_freq=freq[i:i + 8]).params
+        for m in range(8):
+            if abs(freq[i + m]) > 2.0 ** 40:   # finite: taken, its angle says nothing
+                continue
+            off = (got.step[m] - turns_of(float(freq[i + m])) * 2 ** 64) % 2 ** 64
+            assert min(off, 2 ** 64 - off) <= 1, freq[i + m]
+    for f in freq[-10:]:
+        up, down = (pkv.Rotary(16, inv_freq=np.full(8, x)).params.step[0] for x in (f, -f))
+        assert (up + down) % 2 ** 64 == 0   # the other way round
