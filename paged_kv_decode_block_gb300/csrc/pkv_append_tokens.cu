@@ -234,13 +234,35 @@ __device__ __forceinline__ void store_bf16(uint16_t* head, int e0, int e1, const
         make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]), pack_bf16(x[12], x[13]), pack_bf16(x[14], x[15]));
 }
 
-// Eight values to eight codes.  NaN stays NaN; an infinite value becomes NaN too,
-// not the largest code, where the block is known to hold one (x * 0 is NaN for
-// it and +-0 otherwise).
-__device__ __forceinline__ uint2 codes8(const float* x, float inv, bool infinite) {
+// x / s and x * s rounded so that a second rounding, to fewer bits, gives what one
+// rounding would: towards zero, with the last bit set where something was cut off.
+__device__ __forceinline__ float sticky(float toward_zero, float rest) {
+    return __uint_as_float(__float_as_uint(toward_zero) | (rest != 0.f ? 1u : 0u));
+}
+
+__device__ __forceinline__ float divide_odd(float x, float s) {
+    const float q = __fdiv_rz(x, s);
+    return sticky(q, fmaf(-q, s, x));
+}
+
+__device__ __forceinline__ float multiply_odd(float x, float s) {
+    const float q = __fmul_rz(x, s);
+    return sticky(q, fmaf(x, s, -q));
+}
+
+__device__ __forceinline__ bool power_of_two(float s) { return (__float_as_uint(s) & 0x7fffffu) == 0; }
+
+// Eight values to eight codes.  Scales that the append makes are powers of two, and x
+// times their reciprocal is exact; a block filled by somebody else may hold its tokens
+// at another scale.  NaN stays NaN; an infinite value becomes NaN too, not the largest
+// code, where the block is known to hold one (x * 0 is NaN for it and +-0 otherwise).
+__device__ __forceinline__ uint2 codes8(const float* x, float s, float inv, bool infinite) {
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = x[i] * inv;
+    if (!power_of_two(s))
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = divide_odd(x[i], s);
     if (infinite)
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], 0.f, y[i]);
@@ -251,7 +273,8 @@ __device__ __forceinline__ uint2 codes8(const float* x, float inv, bool infinite
 // Move 16 codes from one scale to a larger one.
 __device__ __forceinline__ uint32_t requantise4(uint32_t w, float ratio) {
     const float2 lo = unpack_e4m3(w & 0xffffu), hi = unpack_e4m3(w >> 16);
-    return pack_e4m3(lo.x * ratio, lo.y * ratio) | pack_e4m3(hi.x * ratio, hi.y * ratio) << 16;
+    return pack_e4m3(multiply_odd(lo.x, ratio), multiply_odd(lo.y, ratio)) |
+           pack_e4m3(multiply_odd(hi.x, ratio), multiply_odd(hi.y, ratio)) << 16;
 }
 
 __device__ __forceinline__ uint4 requantise16(const uint4& w, float ratio) {
@@ -425,10 +448,10 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
             uint8_t* vp = static_cast<uint8_t*>(p.v_pages) + head_off;
             if (live) {
                 const float ki = 1.f / k_new, vi = 1.f / v_new;
-                *reinterpret_cast<uint2*>(kp + e0) = codes8(x, ki, infinite);
-                *reinterpret_cast<uint2*>(kp + e1) = codes8(x + 8, ki, infinite);
-                *reinterpret_cast<uint2*>(vp + e0) = codes8(y, vi, infinite);
-                *reinterpret_cast<uint2*>(vp + e1) = codes8(y + 8, vi, infinite);
+                *reinterpret_cast<uint2*>(kp + e0) = codes8(x, k_new, ki, infinite);
+                *reinterpret_cast<uint2*>(kp + e1) = codes8(x + 8, k_new, ki, infinite);
+                *reinterpret_cast<uint2*>(vp + e0) = codes8(y, v_new, vi, infinite);
+                *reinterpret_cast<uint2*>(vp + e1) = codes8(y + 8, v_new, vi, infinite);
             } else if (pos < lo) {   // an older token of the block
                 if (k_new != k_old) *reinterpret_cast<uint4*>(kp + 16 * j) = requantise16(k_held, k_old / k_new);
                 if (v_new != v_old) *reinterpret_cast<uint4*>(vp + 16 * j) = requantise16(v_held, v_old / v_new);

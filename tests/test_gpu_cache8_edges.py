@@ -1,5 +1,6 @@
 """pkv_append_q8 and pkv_decode_q8 on the GPU where test_gpu_cache8.py does not look: calls that follow one another with
-nothing between them, weights and V scales far apart.
+nothing between them, weights and V scales far apart,
+values next to the middles between two codes.
 
 Tolerances: as in test_gpu_cache8.py, or derived at the test.
 """
@@ -9,7 +10,7 @@ import torch
 
 from oracle import cache8
 from paged_kv_decode_block_gb300 import pkv
-from test_gpu_cache8 import Cache, New, bf16, bits
+from test_gpu_cache8 import Cache, New, bf16, bits, on_gpu, rotary_of
 
 pytestmark = pytest.mark.gpu
 
@@ -207,3 +208,68 @@ def test_decode_scores_of_minus_infinity(route, splits):
     live = c.d["out"].clone(), c.d["lse"].clone()
     c.B, c.d["out"], c.d["lse"] = 3, live[0][:3], live[1][:3]
     check_by_terms(c)
+
+
+# ------------------------------------------------------------------ codes at scales that are no powers of two
+
+def nearest_codes(c, n, turn, before):
+    """Every code of the written slots is a nearest one: of exact values (V, and K without rotation) the oracle's own,
+    ties included; of a rotated key at most the rotation's error (see test_gpu_cache8.py) further off than it."""
+    d = c.d
+    for x, codes, scales, pages, sc, exact in (
+            (turn(cache8.bf16_to_f64(n.k), n.pos), before[0], before[1], "kp", "ks", turn is not_turned),
+            (cache8.bf16_to_f64(n.v), before[2], before[3], "vp", "vs", True)):
+        wc, ws, want = cache8.append_q8(x, codes, scales, c.table, c.lens, n.counts, c.ps)
+        assert np.array_equal(d[sc].cpu().numpy().astype(np.float64), ws)
+        got, wc = d[pages].view(torch.uint8).cpu().numpy().reshape(want.shape), wc.reshape(want.shape)
+        written = ~np.isnan(want)
+        assert np.array_equal(got[~written], codes.reshape(want.shape)[~written])
+        if exact:
+            assert np.array_equal(got[written], wc[written]), np.mean(got[written] != wc[written])
+        else:
+            slop = 2.0 ** -20 * 2 * np.abs(cache8.bf16_to_f64(n.k)).max() / np.repeat(ws.reshape(-1, c.H), 16, 0)[..., None]
+            off, least = np.abs(cache8.E4M3[got] - want), np.abs(cache8.E4M3[wc] - want)
+            assert np.all(off[written] <= (least + 2 * slop)[written])
+
+
+def not_turned(x, pos):
+    return cache8.rotate(x, pos, [])
+
+
+@pytest.mark.parametrize("scale", [7.0, 0.3, 1 / 448, 100 / 3])
+def test_append_rounds_ties_at_any_held_scale(scale):
+    """Values at and next to the middles between two codes, in units of a scale that the block's tokens hold (e4m3's
+    middles have five significant bits; times 7 they are bf16 values)."""
+    c = Cache([3, 20, 9], Hq=2, H=1, D=64, seed=400, room=16)
+    c.ks[:] = c.vs[:] = np.float32(scale)
+    c.upload()
+    n = New(c, [12, 5, 7], seed=401)
+    rng = np.random.default_rng(402)
+    middles = np.arange(17, 32, 2) * 2.0 ** rng.integers(-8, 4, (24, 1, 8))   # 17/256 .. 31 * 8 of the scale
+    near = (middles[..., None] * scale * 2.0 ** (np.arange(8) / 512 - 4 / 512)).reshape(24, 1, 64)
+    near[..., ::8] = (middles * np.float64(np.float32(scale)))   # as near to the middle as bf16 comes
+    n.k = n.v = bf16(near * np.where(rng.random((24, 1, 64)) < 0.5, -1, 1))
+    n.kd = n.vd = on_gpu(n.k)
+    plan = c.plan()
+    pkv.append_q8(n.kd, n.vd, *(c.d[x] for x in ("kp", "vp", "ks", "vs", "table", "lens")), n.after, plan, None,
+                  cu_tokens=n.cu)
+    torch.cuda.synchronize()
+    assert plan.status() == 0
+    nearest_codes(c, n, not_turned, (c.kc, c.ks, c.vc, c.vs))
+
+
+@pytest.mark.parametrize("dim, interleaved", [(0, False), (64, False), (128, True)])
+@pytest.mark.parametrize("size", [0.01, 1.0, 300.0])
+def test_append_into_blocks_of_any_scale(dim, interleaved, size):
+    """Rows that go on inside blocks quantised by somebody else: the held scale stays (small values), or rises to a
+    power of two and the held codes move to it (large ones)."""
+    c = Cache([5, 16, 31, 100, 7, 48], Hq=8, H=4, D=128, ps=48, seed=410, room=40, scales="amax")
+    c.upload()
+    n = New(c, [1, 11, 16, 33, 0, 3], fused=True, seed=411, size=size)
+    r, turn = (None, not_turned) if not dim else rotary_of(dim=dim, interleaved=interleaved)
+    plan = c.plan()
+    pkv.append_q8(n.kd, n.vd, *(c.d[x] for x in ("kp", "vp", "ks", "vs", "table", "lens")), n.after, plan, r,
+                  q=n.qd, q_out=n.q_out, cu_tokens=n.cu)
+    torch.cuda.synchronize()
+    assert plan.status() == 0
+    nearest_codes(c, n, turn, (c.kc, c.ks, c.vc, c.vs))
