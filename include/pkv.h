@@ -212,6 +212,10 @@ void pkv_plan_destroy(pkv_plan_t plan);
 
 int pkv_plan_get_info(pkv_plan_t plan, pkv_plan_info *info);
 
+/* The CUDA device that the plan is bound to: the one that was current when it
+ * was made. */
+int pkv_plan_device(pkv_plan_t plan, int32_t *device);
+
 /* Copy the plan's tiles to host memory: the compact queue (SPLIT_QUEUE,
  * PERSISTENT), the padded grid with its empty slots (SPLIT_PADDED), or one tile
  * per (row, KV head) (DIRECT).  *count receives the total; at most `capacity`

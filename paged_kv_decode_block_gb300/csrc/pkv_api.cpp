@@ -632,6 +632,12 @@ int pkv_plan_get_info(pkv_plan_t p, pkv_plan_info* info) {
     return PKV_OK;
 }
 
+int pkv_plan_device(pkv_plan_t p, int32_t* device) {
+    if (!p || !device) return PKV_EINVAL;
+    *device = p->device;
+    return PKV_OK;
+}
+
 int pkv_plan_queue(pkv_plan_t p, pkv_work_item* items, int32_t capacity, int32_t* count) {
     if (!p || !count) return PKV_EINVAL;
     const int32_t n = static_cast<int32_t>(p->plan.items.size());

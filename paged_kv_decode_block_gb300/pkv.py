@@ -10,7 +10,6 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
-import sys
 
 import numpy as np
 
@@ -99,6 +98,7 @@ SIGNATURES = {
                                         ctypes.POINTER(PlanInfo), ctypes.POINTER(WorkItem), _I32, _I32P]),
     "pkv_plan_update": (ctypes.c_int, [_P, _P, _P]),
     "pkv_plan_destroy": (None, [_P]),
+    "pkv_plan_device": (ctypes.c_int, [_P, _I32P]),
     "pkv_plan_get_info": (ctypes.c_int, [_P, ctypes.POINTER(PlanInfo)]),
     "pkv_plan_queue": (ctypes.c_int, [_P, ctypes.POINTER(WorkItem), _I32, _I32P]),
     "pkv_decode": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P]),
@@ -265,9 +265,9 @@ class Plan:
         _check(lib.pkv_plan(_ptr_i32(lens), _ptr_i32(table), self.page_size, ctypes.byref(self.geom),
                             ctypes.byref(o), ctypes.byref(h)), "pkv_plan")
         self._h = h
-        torch = sys.modules.get("torch")
-        # the device the plan is bound to
-        self.device = torch.cuda.current_device() if torch is not None and torch.cuda.is_available() else 0
+        dev = ctypes.c_int32(0)
+        _check(lib.pkv_plan_device(h, ctypes.byref(dev)), "pkv_plan_device")
+        self.device = dev.value   # the device the plan is bound to
         # the shapes of the tensors that go with the plan
         self.Hq, self.Hkv = int(Hq), int(Hkv)
         self.pool_shape = (int(num_pages), self.page_size, self.Hkv, self.D)

@@ -1,4 +1,5 @@
 """What the calls of the rotated append and the 8-bit cache refuse or derive on the host, without a GPU."""
+import ctypes
 from fractions import Fraction
 
 import numpy as np
@@ -81,3 +82,31 @@ def test_rotary_steps_of_any_frequency():
     for f in freq[-10:]:
         up, down = (pkv.Rotary(16, inv_freq=np.full(8, x)).params.step[0] for x in (f, -f))
         assert (up + down) % 2 ** 64 == 0   # the other way round
+
+
+# ------------------------------------------------------------------ devices
+
+def test_a_plan_names_its_own_device(monkeypatch):
+    """The device that tensors are checked against is the one the library bound the plan to, whatever torch, which may
+    not even be imported when the plan is made, holds for current."""
+    class Library:
+        def pkv_plan(self, lens, table, page_size, geom, opts, handle):
+            handle._obj.value = 1
+            return pkv.OK
+
+        def pkv_plan_device(self, handle, device):
+            device._obj.value = 3
+            return pkv.OK
+
+        def pkv_plan_destroy(self, handle):
+            pass
+    monkeypatch.setattr(pkv, "_lib", Library())
+    plan = pkv.Plan([1], None, 16, B=1, Hq=4, Hkv=1, D=64, max_pages=1, num_pages=1)
+    device = plan.device
+    plan.close()
+    assert device == 3
+
+
+def test_plan_device_refuses_null():
+    device = ctypes.c_int32(7)
+    assert pkv.load().pkv_plan_device(None, ctypes.byref(device)) == pkv.EINVAL and device.value == 7
