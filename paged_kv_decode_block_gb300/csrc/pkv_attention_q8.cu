@@ -75,7 +75,7 @@ struct Q8Cfg {
     static constexpr int kStages = D == 128 ? 3 : 5;         // 12 or 10 KB in flight per warp, 80-96 KB per CTA
     static constexpr int kMatBytes = kBlockRows * D;         // one K or V block: 16 rows of D bytes
     static constexpr int kChunks = D / 16;                   // 16-byte chunks of a row
-    static constexpr int kPairFrom = D == 128 ? 40 : 16;     // blocks a warp from which two are reduced at a time
+    static constexpr int kPairFrom = D == 128 ? 40 : 4;     // blocks a warp from which two are reduced at a time
     static constexpr int kParts = G == 8 ? 2 : 1;            // P^T column tiles: the lo parts share one while 2G <= 8
     static_assert(D == 64 || D == 128, "head_dim");
 };
@@ -467,10 +467,12 @@ __device__ void run_tile_q8(Q8Smem<D, G>& sm, const AttnQ8Params& qp, TileWork t
         }
     };
     // Two blocks at a time share a turn's bookkeeping and overlap their latencies; one
-    // at a time starts earlier and has its loads out earlier.  Measured (one / two at
-    // a time): D = 128, 7 blocks a warp 15.3 / 16.5 us (1 x 32768 tokens), 14 on
-    // average 23.0 / 23.7 us, 32 blocks 84.4 / 86.3 us (64 x 4096), 64 blocks 101.8 /
-    // 95.8 us (38 x 8192); D = 64, 32 blocks 91.1 / 87.7 us (128 x 4096).
+    // at a time starts earlier and has its loads out earlier.  Measured, one / two at a
+    // time, by blocks a warp (G = 4; the other G differ alike, by up to 2 % from these):
+    // D = 128, 4 blocks (200 x 500 tokens) 46.1 / 50.0 us, 7 (1 x 32768) 16.7 / 17.5, 8 (128
+    // x 1024) 52.1 / 55.3, 14 on average (8 rows of 512-32768) 25.4 / 24.9, 32 (64 x 4096)
+    // 85.7 / 86.5, 64 (38 x 8192) 109.4 / 100.0; D = 64, 2 blocks (64 x 300) 11.1 / 11.4, 4
+    // 32.8 / 31.9, 7 14.6 / 14.5, 8 32.6 / 31.4, 14 18.4 / 17.5, 32 51.3 / 48.5.
     if (nblk >= C::kPairFrom * kWarps)
         reduce(std::integral_constant<int, 2>{});
     else
