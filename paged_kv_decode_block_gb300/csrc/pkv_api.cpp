@@ -798,10 +798,13 @@ int enqueue_decode(pkv_plan_t p, const void* q, const void* k_pages, const void*
         if (q8) {
             const uint32_t bpp = static_cast<uint32_t>(p->page_size / pkv::kBlockRows);
             const uint32_t magic = bpp > 1 ? static_cast<uint32_t>((1ull << 32) / bpp + 1) : 0u;
-            // More than one wave of rows of unequal lengths: a long row that starts in a
-            // later wave sets the tail, so the long ones start first (56 rows of 1024 to
-            // 8192 tokens: 90 us in row order, 81 us by length; equal rows keep row order,
-            // which saves the ranking).
+            // More than one wave (this kernel too holds two CTAs an SM, as resident_ctas
+            // counts) of rows of unequal lengths: a long row that starts in a later wave
+            // sets the tail, so the long ones start first.  In row order / by length: 56 rows
+            // of 1024 to 8192 tokens 94.7 / 84.7 us, 100 such 162 / 150, 64 of 512 to 16384
+            // 131 / 117; D = 64, 64 rows of 2000 to 4000 39.7 / 40.1.  Rows within an eighth
+            // of each other keep row order, which saves the ranking (56 of 5000 to 6000
+            // 110.4 either way).
             const Plan& pl = p->plan;
             const bool longest_first = a.route == pkv::kRouteDirect && a.B <= kRankedRows && grid > p->resident_ctas &&
                                        pl.p_max * a.B > pl.p_total + pl.p_total / 8;

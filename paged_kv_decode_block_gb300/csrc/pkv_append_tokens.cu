@@ -28,7 +28,7 @@
 // of the group, so its eight sines and cosines serve the K head and the G query
 // heads, and every access is 16 bytes (8 for e4m3 codes of half pairs).  8 x 128
 // and 32 query heads, prompts of 12.5 thousand tokens in bf16: 48.5 us, 6.3 TB/s; of
-// 8.8 thousand in e4m3: 34.7 us, 5.7 TB/s, where the arithmetic (about 1000
+// 8.8 thousand in e4m3: 35.1-35.5 us, 5.6 TB/s, where the arithmetic (about 930
 // instructions a warp and head, half of the issue slots) bounds it too; one token
 // for each of 64 rows: 4.2 us in a graph, a chain of round trips (length, table
 // entry, scales, then the stores).
@@ -158,6 +158,10 @@ __device__ __forceinline__ int page_of(const AppendTokensParams& p, int blk) {
 
 // The rest of the check, over the table entries of all of the row's new tokens,
 // by the whole CTA (a barrier): a row is refused before any byte of it is written.
+// One coalesced read up to D pages, then a loop, and every CTA of the row makes it:
+// at 16-token pages and 8 KV heads n^2 / 16 bytes for n tokens, which shows from some
+// 100 thousand on (e4m3, 32 query heads: 1.21 times the bytes' time at 65 thousand,
+// 1.42 at 131 thousand).
 __device__ __forceinline__ uint32_t row_pages_bad(const AppendTokensParams& p, int b, const RowWork& w) {
     uint32_t bad = w.bad;
     if (!bad && w.n > 0) {
@@ -487,9 +491,9 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
 // From this many (block, KV head) units on a CTA takes two KV heads one after the
 // other, which share its row look-up and its sines and cosines.  Below, one: the
 // call is a chain of round trips.  Measured, one / two heads, one row, 8 KV heads,
-// e4m3: 512 tokens 4.29 / 4.92 us, 1024 (528 units) 5.64 / 5.85, 2048 (1040) 12.8 /
-// 11.7, 16384 68.7 / 64.9 us; bf16: 3.90 / 4.05, 5.35 / 5.49, 12.2 / 11.1, 68.3 /
-// 67.7 us.  (Loading the second head's inputs during the first's arithmetic costs
+// e4m3: 512 tokens 4.41 / 5.06 us, 1024 (528 units) 5.62 / 6.13, 2048 (1040) 12.6 /
+// 12.2, 16384 69.1 / 64.6 us; bf16: 3.81 / 4.03, 5.19 / 5.65, 12.0 / 11.3, 66.9 /
+// 66.1 us.  (Loading the second head's inputs during the first's arithmetic costs
 // a fourth CTA per SM its registers: slower.)
 constexpr int64_t kTwoHeadUnits = 1024;
 

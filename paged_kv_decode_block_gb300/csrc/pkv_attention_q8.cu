@@ -23,9 +23,10 @@
 //
 // What bounds it: HBM, 2 * D + 1/2 bytes per token and KV head against 4 * G * D
 // flops (2 G flop per byte).  Measured at 32 / 8 heads, D = 128, back to back: 64 x 4096
-// tokens 84-89 us by box (6.0-6.4 TB/s), 38 x 8192 96-100 us (6.4-6.7 TB/s), one row of
-// 32768 15.0-15.3 us (4.4 TB/s: ramp, merge and launch gap are a third).  Next to
-// HBM a warp's own time counts: about 300 instructions a block, 64 of them widening
+// tokens 84-90 us by box (6.0-6.4 TB/s), 38 x 8192 96-100 us (6.4-6.7 TB/s), one row of
+// 32768 17.3 us from twelve caches in turn (3.9 TB/s: ramp, merge and launch gap are two
+// fifths) and 14.6-15.0 us from three, whose 201 MB L2 holds in part.  Next to
+// HBM a warp's own time counts: about 310 instructions a block, 64 of them widening
 // codes, and a loop that does not quite fit the instruction cache.  tcgen05 is not
 // used: it would want the widened codes back in shared memory, for products of 8
 // columns.  Staging with TMA boxes and mbarriers measured slower than cp.async

@@ -2,7 +2,13 @@
 nothing between them, weights and V scales far apart,
 values next to the middles between two codes.
 
-Tolerances: as in test_gpu_cache8.py, or derived at the test.
+Tolerances are derived at the tests; two come from test_gpu_cache8.py:
+* Rotation: the angle is cut to 2^-32 turns (2^-29 rad) and rounded to fp32 twice, by 2^-25 of at most pi / 4 each; the
+  first terms that the series of sin and cos leave out are below 2^-28 and their evaluation rounds a few times by 2^-25;
+  factor, products and sum add three roundings of 2^-24: |error| <= 2^-20 (|x| + |y|) scale covers it.
+* Attention: exact inputs, fp32 dot products and sums.  A score is off by at most
+  d = (D + 16) 2^-23 max_t sum_d |q_d k_td| / sqrt(D); a weight by a factor of 2 d and about 2^-20 (exp2, the f16 split,
+  the reference's product), the sum of n weights by n 2^-23.
 """
 import numpy as np
 import pytest
