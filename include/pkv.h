@@ -348,9 +348,9 @@ int pkv_append_rotary(const pkv_tokens *tokens, const pkv_rotary *rotary, void *
  *
  * pkv_append_q8 is pkv_append_rotary into such a cache.  A block's scale becomes
  * the least power of two s (2^-120 to 2^120) with |x| / s <= 448 for every finite
- * new value x of the block, but not less than the scale of the tokens of the row
- * that the block already holds; if it rises, the codes of those tokens are
- * requantised to it.  A block that the new tokens begin starts afresh, whatever
+ * new value x of the block, but not less than the magnitude of the scale of the
+ * tokens of the row that the block already holds; if it changes, the codes of those
+ * tokens are requantised to it.  A block that the new tokens begin starts afresh, whatever
  * its page held.  New values are rotated in fp32 and rounded once, to nearest
  * even, to e4m3; a value that is not finite is stored as NaN.  The slots behind
  * the row's last token are left as they were.  Rows, flags and errors as in

@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(D) append_tokens_kernel(const __grid_constant_
                 __syncthreads();   // s_max is read
                 cta_max(km, vm, s_max[h & 1]);
             }
-            const float k_new = fmaxf(block_scale(km), k_old), v_new = fmaxf(block_scale(vm), v_old);
+            const float k_new = fmaxf(block_scale(km), fabsf(k_old)), v_new = fmaxf(block_scale(vm), fabsf(v_old));
             uint8_t* kp = static_cast<uint8_t*>(p.k_pages) + head_off;
             uint8_t* vp = static_cast<uint8_t*>(p.v_pages) + head_off;
             if (live) {

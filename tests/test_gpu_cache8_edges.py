@@ -81,6 +81,52 @@ def test_append_and_decode_back_to_back(B, H, G, D, route):
         c.check(what=f"step {i}")
 
 
+@pytest.mark.parametrize("route", ["direct", "split_padded"])
+@pytest.mark.parametrize("copy", ["tma", "lsu"])
+@pytest.mark.parametrize("B, H, G, D", [(1, 8, 4, 128), (16, 4, 8, 64)])
+def test_rotated_append_and_bf16_decode_back_to_back(B, H, G, D, copy, route):
+    """The same into bf16 pages, read by pkv_decode with either copy engine: the bits of a run that waits after each
+    call, and the oracle's values at the last step."""
+    rng = np.random.default_rng(B)
+    steps = 40
+    lens = rng.integers(1, 200, B)
+    c = Cache(lens, Hq=G * H, H=H, D=D, seed=140 + B, room=steps)
+    d = c.upload()
+    kv = [bf16(rng.standard_normal((c.pages, 16, H, D))) for _ in range(2)]
+    r = pkv.Rotary(64)
+    news = [New(c, [1] * B, offsets=False, seed=150 + i) for i in range(steps)]
+
+    def run(wait):
+        kp, vp = (on_gpu(x) for x in kv)
+        buf = [torch.from_numpy(c.lens.copy()).cuda(), torch.empty(B, dtype=torch.int32, device="cuda")]
+        plan = pkv.Plan(lens + steps, None, 16, B=B, Hq=G * H, Hkv=H, D=D, max_pages=c.table.shape[1], copy=copy,
+                        num_pages=c.pages, force_mode=route, num_splits=0 if route == "direct" else 3)
+        outs = torch.full((steps, B, G * H, D), 7.0, device="cuda")
+        lses = torch.full((steps, B, G * H), 7.0, device="cuda")
+        pkv.decode(d["q"], kp, vp, d["table"], buf[0], plan, outs[0], lses[0])   # the plan goes to the device now
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        for i, x in enumerate(news):
+            pkv.append_rotary(x.kd, x.vd, kp, vp, d["table"], buf[i % 2], buf[1 - i % 2], plan, r, q=x.qd, q_out=x.q_out)
+            if wait:
+                torch.cuda.synchronize()
+            pkv.decode(x.q_out, kp, vp, d["table"], buf[1 - i % 2], plan, outs[i], lses[i])
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert plan.status() == 0
+        return outs, lses, kp, vp
+
+    apart, at_once = run(True), run(False)
+    for a, b in zip(apart, at_once):
+        assert torch.equal(a, b)
+    import oracle
+    outs, lses, kp, vp = at_once
+    ref = oracle.decode(bits(news[-1].q_out), bits(kp), bits(vp), c.table, (lens + steps).astype(np.int32))
+    assert np.max(np.abs(outs[-1].cpu().numpy() - ref[0])) <= 2e-3   # pkv_decode's own tolerances
+    assert np.max(np.abs(lses[-1].cpu().numpy() - ref[1])) <= 1e-4
+
+
 # ------------------------------------------------------------------ weights and V scales far apart
 
 def check_by_terms(c, what=""):
@@ -279,3 +325,27 @@ def test_append_into_blocks_of_any_scale(dim, interleaved, size):
     torch.cuda.synchronize()
     assert plan.status() == 0
     nearest_codes(c, n, turn, (c.kc, c.ks, c.vc, c.vs))
+
+
+def test_append_into_blocks_of_negative_scale():
+    """A code stands for code * scale whatever the scale's sign: the held tokens keep their values at the new scale."""
+    c = Cache([5, 9], Hq=2, H=1, D=64, seed=420, room=16)
+    n = New(c, [3, 4], seed=421, size=4.0)
+    c.ks[:], c.vs[:] = -np.float32(2.0) ** -3, -np.float32(2.0) ** 4   # lower and higher than the new values ask for
+    c.upload()
+    plan = c.plan()
+    pkv.append_q8(n.kd, n.vd, *(c.d[x] for x in ("kp", "vp", "ks", "vs", "table", "lens")), n.after, plan, None,
+                  cu_tokens=n.cu)
+    torch.cuda.synchronize()
+    # the same cache with positive scales
+    c.kc, c.vc, c.ks, c.vs = c.kc ^ 0x80, c.vc ^ 0x80, -c.ks, -c.vs
+    for b in range(2):   # (blocks without new tokens are left as they are)
+        rows = cache8.places(c.table, b, c.lens[b], c.lens[b] + n.counts[b], 16)
+        blk = np.unique(rows // 16)
+        for x, codes, scales, pages, sc in ((n.k, c.kc, c.ks, "kp", "ks"), (n.v, c.vc, c.vs, "vp", "vs")):
+            wc, ws, want = cache8.append_q8(cache8.bf16_to_f64(x), codes, scales, c.table, c.lens, n.counts, 16)
+            got = c.d[pages].view(torch.uint8).cpu().numpy().reshape(want.shape)
+            assert np.array_equal(c.d[sc].cpu().numpy().reshape(-1)[blk], ws.reshape(-1)[blk])
+            here = np.arange(blk[0] * 16, blk[-1] * 16 + 16)
+            here = here[~np.isnan(want[here, 0, 0])]
+            assert np.array_equal(cache8.E4M3[got[here]], cache8.E4M3[wc.reshape(want.shape)[here]])
