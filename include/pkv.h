@@ -363,7 +363,8 @@ int pkv_append_rotary(const pkv_tokens *tokens, const pkv_rotary *rotary, void *
  * softmax and all sums are fp32; codes enter the products exactly, queries to
  * 2^-25 of their head's largest element, weights times V scales to 2^-22 of
  * themselves and at least to 2^-42 of their head's largest such product in the row,
- * however far the scales of its blocks lie apart.  A slot behind the row's last
+ * however far the scales of its blocks lie apart.  A query head whose scores are all
+ * -inf has output 0 and lse -inf, as in an empty row.  A slot behind the row's last
  * token may hold anything.  pkv_trace_enable and pkv_profile_enable cover its launches;
  * pkv_plan_info.kv_bytes goes on counting bf16.  PKV_EUNSUPPORTED for a plan with
  * math = PKV_MATH_FMA; the plan's copy option has no effect.
