@@ -76,7 +76,8 @@ enum pkv_status_code {
 /* Bits of the device status word. */
 enum pkv_device_status_bits {
     PKV_DEV_PAGE_OOB = 1u,       /* a block-table entry outside [0, num_pages) */
-    PKV_DEV_PLAN_MISMATCH = 2u,  /* the device seq_lens disagree with the plan */
+    PKV_DEV_PLAN_MISMATCH = 2u,  /* the device seq_lens disagree with the plan (or with the call's
+                                    token offsets) */
     PKV_DEV_TIMEOUT = 4u,        /* a bounded wait inside a kernel ran out */
     PKV_DEV_ROW_FULL = 8u        /* an append found no page for a row's new token: the row's
                                     table is full, or its entry for that position is unassigned
@@ -376,6 +377,75 @@ int pkv_append_q8(const pkv_tokens *tokens, const pkv_rotary *rotary, void *k_pa
 int pkv_decode_q8(const void *q, const void *k_pages, const void *v_pages, const float *k_scales,
                   const float *v_scales, const int32_t *block_table_d, const int32_t *seq_lens_d, pkv_plan_t plan,
                   float *out, float *lse, pkv_stream_t stream);
+
+/*
+ * Attention of the rows' new tokens, whose keys and values the cache holds
+ * already (pkv_append_rotary / pkv_append_q8): a prompt, a chunk of one, drafted
+ * tokens to be verified.  Row b has n_b new tokens, the last n_b of its
+ * seq_lens_d[b] (what the append wrote to new_lens_d); its new token i is token
+ * cu_tokens_d[b] + i of q and sees the row's tokens up to its own:
+ *     s_t = (1/sqrt(D)) * <q[.][h], K[kvh] of token t>   for t <= seq_lens_d[b] - n_b + i
+ *     out[.][h] = sum_t softmax(s)_t * V[kvh] of token t
+ *     lse[.][h] = ln sum_t exp(s_t)
+ *   q            device bf16 [Hq][D] per token, total_tokens of them
+ *   out          device bf16, the same; it may be q itself (with the same stride),
+ *                but must not overlap it otherwise
+ *   lse          device fp32 [total_tokens][Hq], or NULL
+ *   *_stride     elements from one token to the next, as in pkv_tokens
+ *   cu_tokens_d  device int32 [B + 1], ascending in [0, total_tokens], or NULL:
+ *                token b is row b's one new token (total_tokens = B)
+ *   total_tokens tokens in q / out
+ */
+typedef struct {
+    const void *q;
+    void *out;
+    float *lse;
+    int64_t q_stride, out_stride;
+    const int32_t *cu_tokens_d;
+    int32_t total_tokens;
+} pkv_queries;
+
+/*
+ * Memory that pkv_extend / pkv_extend_q8 need in the plan: partial states of 256
+ * rows for two tiles per SM, 40 MB at D = 128 and 20 MB at D = 64, independent
+ * of the problem.  Allocates it once (a repeated call does nothing) and
+ * synchronises the device the first time.  The first pkv_extend does it too, but
+ * not on a stream that is being captured.  Errors: PKV_ENOMEM, PKV_EINVAL
+ * (another current device than the plan's), PKV_ECUDA.
+ */
+int pkv_extend_reserve(pkv_plan_t plan);
+
+/*
+ * pkv_extend attends over a bf16 cache, pkv_extend_q8 over an 8-bit one (any
+ * scales).  Needs no host knowledge of the lengths: the plan gives the geometry,
+ * the page size, the status word and the reserved memory only, and may be stale;
+ * a captured call may be replayed with other lengths and offsets.  Calls with
+ * one plan share its memory and have to be ordered on the GPU, as decodes have;
+ * they may overlap its decodes and appends.  Two kernels on `stream`.
+ *
+ * Products take bf16 factors (8-bit codes are exact in it) and fp32 sums; the
+ * softmax is fp32 with the weights rounded once to bf16 for the product with V
+ * (after their V scale in the 8-bit cache) and summed before that rounding; the
+ * output is rounded once to bf16.  The order of all sums is fixed by the lengths,
+ * so a repeated call gives the same bits.  A query whose scores are all -inf has
+ * output 0 and lse -inf.  Slots behind a row's last token may hold anything.  An
+ * infinity or NaN in a token's V reaches the queries that see the token and no
+ * others.  Tokens of q that belong to no row, and their outputs, are left as they are.
+ *
+ * A row whose n_b exceeds seq_lens_d[b], or whose length exceeds its table, sets
+ * PKV_DEV_PLAN_MISMATCH and its outputs are NaN; offsets outside [0, total_tokens]
+ * or descending set the same flag and leave their row out.  A page outside the
+ * pool sets PKV_DEV_PAGE_OOB; the queries that see it are NaN, and so may be
+ * others of the row's.
+ * Errors: PKV_EINVAL (null or misaligned pointer, bad stride or count, another
+ * current device than the plan's, no reserved memory during a capture),
+ * PKV_ENOMEM, PKV_ECUDA.
+ */
+int pkv_extend(const pkv_queries *queries, const void *k_pages, const void *v_pages, const int32_t *block_table_d,
+               const int32_t *seq_lens_d, pkv_plan_t plan, pkv_stream_t stream);
+int pkv_extend_q8(const pkv_queries *queries, const void *k_pages, const void *v_pages, const float *k_scales,
+                  const float *v_scales, const int32_t *block_table_d, const int32_t *seq_lens_d, pkv_plan_t plan,
+                  pkv_stream_t stream);
 
 /* Read and clear the plan's device status word (synchronises `stream`). */
 int pkv_status(pkv_plan_t plan, pkv_stream_t stream, uint32_t *status);

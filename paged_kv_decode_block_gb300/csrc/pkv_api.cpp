@@ -345,24 +345,36 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
+// [tokens][heads][D] of bf16 (rows of a box swizzled by 128 bytes) or bytes (not swizzled), heads
+// dense, `stride` elements from token to token, as a 3-D tensor {D, heads, tokens}.
+int encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType type, int32_t D, int32_t heads, int64_t tokens,
+               int64_t stride, int32_t box_d, int32_t box_heads, int32_t box_tokens) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return cuda_fail(cudaErrorNotSupported);
+    const bool bytes = type == CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const cuuint64_t size = bytes ? 1 : 2;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * size, static_cast<cuuint64_t>(stride) * size};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_d), static_cast<cuuint32_t>(box_heads),
+                               static_cast<cuuint32_t>(box_tokens)};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    CUresult r = fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
+    return PKV_OK;
+}
+
 // The pool [num_pages][page_size][Hkv][D] bf16 as a 3-D tensor
 // {D, Hkv, num_pages * page_size} (innermost first); one box is 64 elements
 // (128 B) of kBlockRows consecutive tokens of one KV head, stored with the
 // 128-byte swizzle the kernels' shared-memory addressing expects.
-int encode_pool_map(CUtensorMap* map, const void* pool, const pkv_geom& g, int32_t page_size) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return cuda_fail(cudaErrorNotSupported);
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(g.head_dim), static_cast<cuuint64_t>(g.num_kv_heads),
-                                static_cast<cuuint64_t>(g.num_pages) * page_size};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(g.head_dim) * 2,
-                                   static_cast<cuuint64_t>(g.num_kv_heads) * g.head_dim * 2};
-    const cuuint32_t box[3] = {64u, 1u, static_cast<cuuint32_t>(pkv::kBlockRows)};   // 128 B x 16 tokens
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
-    return PKV_OK;
+int encode_pool_map(CUtensorMap* map, const void* pool, const pkv_geom& g, int32_t page_size,
+                    int32_t box_tokens = pkv::kBlockRows) {
+    return encode_map(map, pool, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.head_dim, g.num_kv_heads,
+                      static_cast<int64_t>(g.num_pages) * page_size, static_cast<int64_t>(g.num_kv_heads) * g.head_dim,
+                      64, 1, box_tokens);   // 128 B x box_tokens
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -432,6 +444,12 @@ struct pkv_plan_s {
     // address space), so pkv_decode_host can read a fresh plan in place.
     const int32_t* host_buf_dev = nullptr;
 
+    // pkv_extend: partial states of shared tiles (pkv_extend_reserve)
+    float* ext_o = nullptr;
+    float2* ext_ml = nullptr;
+    pkv::ExtSplit* ext_splits = nullptr;
+    int ext_ctas = 0;   // CTAs they are made for: the device's SMs
+
     // pkv_decode_host: pinned, device-mapped staging [q][out][lse] for host
     // buffers the GPU cannot address itself (allocated on first need)
     uint8_t* host_stage = nullptr;
@@ -450,6 +468,9 @@ void release(pkv_plan_s* p) {
     cudaFree(p->arrive);
     cudaFree(p->ctr);
     cudaFree(p->trace);
+    cudaFree(p->ext_o);
+    cudaFree(p->ext_ml);
+    cudaFree(p->ext_splits);
     cudaFreeHost(p->host_stage);
     if (p->upload_done) cudaEventDestroy(p->upload_done);
     for (auto& e : p->ev)
@@ -1074,6 +1095,130 @@ int pkv_decode_q8(const void* q, const void* k_pages, const void* v_pages, const
     const Q8Scales scales{k_scales, v_scales};
     return enqueue_decode(p, q, k_pages, v_pages, block_table_d, seq_lens_d, out, lse,
                           reinterpret_cast<cudaStream_t>(stream), nullptr, PlanSource::kUpload, &scales);
+}
+
+}  // extern "C"
+
+namespace {
+
+int extend_reserve(pkv_plan_t p) {
+    if (p->ext_ctas) return PKV_OK;
+    int sms = 0;
+    PKV_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, p->device));
+    const size_t rows = static_cast<size_t>(sms) * 2 * pkv::kExtTileRows;
+    if ((!p->ext_o && cudaMalloc(&p->ext_o, rows * p->g.head_dim * sizeof(float)) != cudaSuccess) ||
+        (!p->ext_ml && cudaMalloc(&p->ext_ml, rows * sizeof(float2)) != cudaSuccess) ||
+        (!p->ext_splits && cudaMalloc(&p->ext_splits, sms * sizeof(pkv::ExtSplit)) != cudaSuccess)) {
+        (void)cudaGetLastError();
+        return PKV_ENOMEM;
+    }
+    p->ext_ctas = sms;
+    return PKV_OK;
+}
+
+int extend(const pkv_queries* t, const void* k_pages, const void* v_pages, const Q8Scales* scales,
+           const int32_t* block_table_d, const int32_t* seq_lens_d, pkv_plan_t p, cudaStream_t s) {
+    if (!p || !t) return PKV_EINVAL;
+    const pkv_geom& g = p->g;
+    const int64_t row = static_cast<int64_t>(g.num_q_heads) * g.head_dim;
+    if (t->total_tokens < 0 || (!t->cu_tokens_d && t->total_tokens != g.batch)) return PKV_EINVAL;
+    if (g.batch == 0 && t->total_tokens > 0) return PKV_EINVAL;
+    if (t->total_tokens == 0) return PKV_OK;
+    if (!t->q || !t->out || !k_pages || !v_pages || !block_table_d || !seq_lens_d) return PKV_EINVAL;
+    if (!aligned16(t->q) || !aligned16(t->out) || !aligned16(k_pages) || !aligned16(v_pages)) return PKV_EINVAL;
+    uintptr_t words = reinterpret_cast<uintptr_t>(t->cu_tokens_d) | reinterpret_cast<uintptr_t>(t->lse) |
+                      reinterpret_cast<uintptr_t>(block_table_d) | reinterpret_cast<uintptr_t>(seq_lens_d);
+    if (scales) {
+        if (!scales->k || !scales->v) return PKV_EINVAL;
+        words |= reinterpret_cast<uintptr_t>(scales->k) | reinterpret_cast<uintptr_t>(scales->v);
+    }
+    if (words & 3u) return PKV_EINVAL;
+    for (const int64_t stride : {t->q_stride, t->out_stride})
+        if (stride != 0 && (stride % 8 || stride < row || stride >= int64_t{1} << 38)) return PKV_EINVAL;
+    const int64_t q_stride = t->q_stride ? t->q_stride : row, out_stride = t->out_stride ? t->out_stride : row;
+    if (t->q == t->out && q_stride != out_stride) return PKV_EINVAL;
+    int dev = -1;
+    PKV_CUDA(cudaGetDevice(&dev));
+    if (dev != p->device) return PKV_EINVAL;
+    if (!p->ext_ctas) {
+        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+        PKV_CUDA(cudaStreamIsCapturing(s, &capture));
+        if (capture != cudaStreamCaptureStatusNone) return PKV_EINVAL;
+        const int rc = extend_reserve(p);
+        if (rc) return rc;
+    }
+    const int G = g.num_q_heads / g.num_kv_heads;
+    int box = 128;   // the largest that divides the block of 128 tokens and the page
+    while (p->page_size % box) box /= 2;
+    const int64_t pool_tokens = static_cast<int64_t>(g.num_pages) * p->page_size;
+    const int64_t kv_row = static_cast<int64_t>(g.num_kv_heads) * g.head_dim;
+    CUtensorMap qmap{}, kmap{}, vmap{};
+    int rc = encode_map(&qmap, t->q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.head_dim, g.num_q_heads, t->total_tokens,
+                        q_stride, 64, G, 128 / G);
+    for (const auto& m : {std::make_pair(&kmap, k_pages), std::make_pair(&vmap, v_pages)}) {
+        if (rc) return rc;
+        rc = scales ? encode_map(m.first, m.second, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.head_dim, g.num_kv_heads,
+                                 pool_tokens, kv_row, g.head_dim, 1, box)
+                    : encode_pool_map(m.first, m.second, g, p->page_size, box);
+    }
+    if (rc) return rc;
+    pkv::ExtendParams a{};
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.k_scales = scales ? scales->k : nullptr;
+    a.v_scales = scales ? scales->v : nullptr;
+    a.block_table = block_table_d;
+    a.seq_lens = seq_lens_d;
+    a.cu = t->cu_tokens_d;
+    a.out = static_cast<uint16_t*>(t->out);
+    a.lse = t->lse;
+    a.out_stride = out_stride;
+    a.ws_o = p->ext_o;
+    a.ws_ml = p->ext_ml;
+    a.splits = p->ext_splits;
+    a.status = &p->ctr->status;
+    a.T = t->total_tokens;
+    a.B = g.batch;
+    a.Hq = g.num_q_heads;
+    a.Hkv = g.num_kv_heads;
+    a.G = G;
+    a.D = g.head_dim;
+    a.page_size = p->page_size;
+    a.max_pages = g.max_pages_per_seq;
+    a.num_pages = g.num_pages;
+    a.box_tokens = box;
+    a.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(g.head_dim)));
+    PKV_CUDA(pkv::launch_extend(a, qmap, kmap, vmap, p->ext_ctas, s));
+    return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkv_extend_reserve(pkv_plan_t p) {
+    NvtxRange range("pkv_extend_reserve");
+    if (!p) return PKV_EINVAL;
+    int dev = -1;
+    PKV_CUDA(cudaGetDevice(&dev));
+    if (dev != p->device) return PKV_EINVAL;
+    return extend_reserve(p);
+}
+
+int pkv_extend(const pkv_queries* queries, const void* k_pages, const void* v_pages, const int32_t* block_table_d,
+               const int32_t* seq_lens_d, pkv_plan_t p, pkv_stream_t stream) {
+    NvtxRange range("pkv_extend");
+    return extend(queries, k_pages, v_pages, nullptr, block_table_d, seq_lens_d, p,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+int pkv_extend_q8(const pkv_queries* queries, const void* k_pages, const void* v_pages, const float* k_scales,
+                  const float* v_scales, const int32_t* block_table_d, const int32_t* seq_lens_d, pkv_plan_t p,
+                  pkv_stream_t stream) {
+    NvtxRange range("pkv_extend_q8");
+    const Q8Scales scales{k_scales, v_scales};
+    return extend(queries, k_pages, v_pages, &scales, block_table_d, seq_lens_d, p,
+                  reinterpret_cast<cudaStream_t>(stream));
 }
 
 int pkv_status(pkv_plan_t p, pkv_stream_t stream, uint32_t* status) {

@@ -1,0 +1,928 @@
+// pkv_extend.cu -- causal attention of each row's new tokens over its pages
+// (pkv_extend), also over the 8-bit cache (pkv_extend_q8).
+//
+// For new token i of row b (position ctx + i, ctx = len - n) and query head h:
+//     s_t = <q, k_t> / sqrt(D), t <= ctx + i;   out = sum_t softmax(s)_t v_t
+// computed block by block with a running reference m and sum l:
+//     p_t = 2^(c s_t - m),  l += sum p_t,  O += P V;  out = O / l,  lse = ln2 (m + log2 l)
+// with c = log2(e) / sqrt(D).  m follows the running maximum only when that has
+// grown by more than 8 (p stays below 2^8, which fp32 sums and bf16 weights hold
+// as well as 1): most blocks then leave O where it is, in tensor memory.
+//
+// Shape: the G query heads of a KV head are packed with the tokens into rows, so
+// that K and V are read once for all of them.  A tile is 256 rows in two groups
+// of 128; one KV block of 128 tokens serves both.  One CTA per SM, specialised
+// warps: a producer (TMA), a warp that issues tcgen05.mma, two warpgroups of
+// softmax with a row per thread, and a warp that cleans V where masks end (bf16)
+// or four that widen e4m3 to bf16 (8-bit).  Scores and outputs stay in tensor
+// memory: S0, S1, O0, O1 of 128 columns each; P replaces S, in place, as the
+// second product's first operand.  While one group is at its softmax the tensor
+// core works for the other.
+//
+// Bound: the tensor core (4 * 256 * 128 * D operations a block) when a KV head
+// has more than about 300 rows of scores to a byte of cache, HBM below.
+#include "pkv_extend_schedule.h"
+#include "pkv_tcgen05.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kPieceRing = 4;
+constexpr int kScaleRing = 8;      // blocks whose scales are in shared memory
+constexpr float kMoveAt = 8.0f;    // log2 by which the maximum outgrows the reference
+
+template <int D, bool Q8>
+struct Cfg {
+    static constexpr int kHalves = D / 64;                    // 128-byte rows per head
+    static constexpr int kTile = kExtBlock * D * 2;           // bytes of a K or V block in bf16
+    static constexpr int kCode = kExtBlock * D;               // ... in e4m3
+    static constexpr int kQ = kExtRows * D * 2;
+    static constexpr int kStages = Q8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
+    static constexpr int kCodes = Q8 ? (D == 128 ? 4 : 8) : 0;
+    static constexpr int kThreads = Q8 ? 512 : 384;
+    // producer's warpgroup last: [0, 8) softmax; then bf16: 8 producer, 9 mma, 10 fixer;
+    // 8-bit: [8, 12) widening, 12 producer, 13 mma
+    static constexpr int kProducer = Q8 ? 12 : 8;
+    static constexpr int kMma = kProducer + 1;
+    static constexpr int kFixer = Q8 ? -1 : 10;
+    static constexpr int kReaders = Q8 ? 13 : 10;             // warps that read the piece ring
+    static constexpr size_t kBytes = static_cast<size_t>(kQ) + kStages * kTile + kCodes * kCode;
+};
+
+struct Piece {
+    int32_t tok0, ntok;     // the tile's tokens in q / out (ntok 0: no more pieces)
+    int32_t kvh, b;
+    int32_t limit0;         // tokens that the first one sees
+    int32_t lo, hi;         // KV blocks
+    int32_t slot;           // workspace slot, or -1: the whole tile
+    int32_t bad;            // no products: NaN
+    volatile int32_t poison;      // a page of it does not exist
+    volatile int32_t nonfinite;   // V held infinities or NaN in a block with masked places
+    int32_t pad[5];
+};
+
+struct Ctl {
+    uint64_t full[10], empty[10], fixed[10];       // blocks in bf16, and V blocks cleaned
+    uint64_t code_full[8], code_empty[8];          // blocks in e4m3
+    uint64_t scale_full[kScaleRing];
+    uint64_t q_full, q_empty, drain;
+    uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t piece_full[kPieceRing], piece_empty[kPieceRing];
+    Piece piece[kPieceRing];
+    float scales[kScaleRing][16];                  // 8 of K, 8 of V
+    int64_t scan[17];
+    int64_t row_unit;
+    int32_t row0;
+    volatile int abort;
+    uint32_t tmem;
+    int32_t issued;                                // blocks that the producer has begun to load
+    int32_t q_loads;
+};
+
+// As mbar_wait, without a call (the register split below leaves none), for all lanes of a warp alike.
+__device__ __forceinline__ bool wait_until(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort,
+                                           uint64_t limit_ns = kWaitLimitNs) {
+    uint64_t start = 0;
+    for (uint32_t spin = 1; !mbar_try_wait(bar, parity); ++spin) {
+        if (spin % 64) continue;
+        if (abort && *abort) return false;
+        const uint64_t now = globaltimer_ns();
+        if (start == 0) start = now;
+        if (now - start > limit_ns) {
+            atomicOr(status, static_cast<uint32_t>(PKV_DEV_TIMEOUT));
+            if (abort) *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
+    return __all_sync(kFull, wait_until(bar, parity, status, abort));
+}
+
+struct Rows {
+    const ExtendParams& p;
+    int tt;
+    __device__ __forceinline__ ExtRow operator()(int b) const {
+        const int32_t lo = p.cu ? p.cu[b] : b, hi = p.cu ? p.cu[b + 1] : b + 1;
+        return ext_row(lo, hi, p.seq_lens[b], p.T, static_cast<int64_t>(p.max_pages) * p.page_size, tt);
+    }
+};
+
+// Exclusive prefix of v over the block's threads; the total in ctl->scan[16].
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(Ctl* c, int64_t v, int64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int64_t y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) c->scan[warp] = x;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) {
+        const int64_t s = c->scan[i];
+        before += i < warp ? s : 0;
+        all += s;
+    }
+    *total = all;
+    return before + x - v;
+}
+
+// ------------------------------------------------------------------ producer
+
+template <int D, bool Q8>
+__device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* smem, const CUtensorMap* qmap,
+                                        const CUtensorMap* kmap, const CUtensorMap* vmap, ExtWalk& w, const Rows& rows,
+                                        uint64_t policy) {
+    using C = Cfg<D, Q8>;
+    const int lane = threadIdx.x & 31;
+    uint8_t* q_smem = smem;
+    uint8_t* ring = Q8 ? smem + C::kQ + C::kStages * C::kTile : smem + C::kQ;
+    constexpr int kRing = Q8 ? C::kCodes : C::kStages;
+    constexpr int kBox = Q8 ? C::kCode : C::kTile;
+    uint64_t* full = Q8 ? c->code_full : c->full;
+    uint64_t* empty = Q8 ? c->code_empty : c->empty;
+    const int bt = p.box_tokens, nbox = kExtBlock / bt;
+    const int half = lane / nbox, x = lane % nbox;                  // this lane's box
+    const bool mine = half < (Q8 ? 1 : C::kHalves);
+    const int from = x * (bt / 16);                                 // the lane that knows its page
+    const int per = kExtRows / 2 / p.G;                             // tokens of a group
+    uint32_t n = 0, blocks = 0, q_loads = 0;
+    for (uint32_t pc = 0;; ++pc) {
+        ExtPiece e{};
+        const bool more = w.next(e, rows);
+        const int slot = pc % kPieceRing;
+        if (pc >= kPieceRing && !wait_warp(&c->piece_empty[slot], (pc / kPieceRing - 1) & 1, p.status, &c->abort)) return;
+        Piece& pi = c->piece[slot];
+        ExtRow r{};
+        if (more) r = rows(e.b);
+        const int ntok = more ? min(w.tt, r.n - e.tile * w.tt) : 0;
+        if (lane == 0) {
+            pi.tok0 = r.tok0 + e.tile * w.tt;
+            pi.ntok = ntok;
+            pi.kvh = e.kvh;
+            pi.b = e.b;
+            pi.limit0 = r.len - r.n + e.tile * w.tt + 1;
+            pi.lo = more ? e.lo : 0;
+            pi.hi = more ? e.hi : 0;
+            pi.slot = !more || (e.lo == 0 && e.hi == e.blocks) ? -1 : 2 * w.cta + (e.lo == 0 ? 1 : 0);
+            pi.bad = r.bad;
+            pi.poison = 0;
+            pi.nonfinite = 0;
+            if (more && r.bad) atomicOr(p.status, static_cast<uint32_t>(PKV_DEV_PLAN_MISMATCH));
+            if (more && e.parts) p.splits[w.cta] = ExtSplit{pi.tok0, ntok, e.kvh, e.parts};
+            mbar_arrive(&c->piece_full[slot]);
+        }
+        __syncwarp();
+        if (!more) return;
+        if (r.bad) continue;
+
+        if (q_loads > 0 && !wait_warp(&c->q_empty, (q_loads - 1) & 1, p.status, &c->abort)) return;
+        const int groups = ntok > per ? 2 : 1;
+        if (lane == 0) {
+            c->q_loads = q_loads + 1;
+            mbar_arrive_expect_tx(&c->q_full, groups * (C::kQ / 2));
+            for (int g = 0; g < groups; ++g)
+                for (int h = 0; h < C::kHalves; ++h)
+                    tma_load_3d(q_smem + g * (C::kQ / 2) + h * 16384, qmap, h * 64, e.kvh * p.G,
+                                r.tok0 + e.tile * w.tt + g * per, &c->q_full, policy);
+        }
+        ++q_loads;
+
+        const int32_t* row = p.block_table + static_cast<size_t>(e.b) * p.max_pages;
+        auto entry = [&](int j) {   // the page of this lane's 16 tokens of block j, or -1 past the row's end
+            const int t = j * kExtBlock + (lane & 7) * 16;
+            return j < e.hi && t < r.len ? row[t / p.page_size] : -2;
+        };
+        auto page_ok = [&](int page) { return page >= 0 && page < p.num_pages; };
+        auto scale = [&](int j, int page) {   // lanes 0..7: K's, 8..15: V's
+            if (!Q8 || lane >= 16 || !page_ok(page)) return 0.0f;
+            const int blk = (j * kExtBlock + (lane & 7) * 16) % p.page_size / kBlockRows;
+            return (lane < 8 ? p.k_scales : p.v_scales)[(static_cast<size_t>(page) * (p.page_size / kBlockRows) + blk) * p.Hkv + e.kvh];
+        };
+        int next = entry(e.lo);
+        float next_scale = scale(e.lo, next);
+        for (int j = e.lo; j < e.hi; ++j, ++blocks) {
+            const int page = next;
+            const float sc = next_scale;
+            next = entry(j + 1);
+            if (__any_sync(kFull, page != -2 && !page_ok(page)) && lane == 0) {
+                atomicOr(p.status, static_cast<uint32_t>(PKV_DEV_PAGE_OOB));
+                pi.poison = 1;
+            }
+            const int box_page = __shfl_sync(kFull, page, from);
+            const int t = j * kExtBlock + x * bt;
+            const int tok = page_ok(box_page) ? box_page * p.page_size + t % p.page_size : -1;
+            const uint32_t bytes = __popc(__ballot_sync(kFull, mine && tok >= 0)) * (kBox / (Q8 ? 1 : C::kHalves) / nbox);
+            for (int kv = 0; kv < 2; ++kv, ++n) {
+                const int st = n % kRing;
+                if (n >= kRing && !wait_warp(&empty[st], (n / kRing - 1) & 1, p.status, &c->abort)) return;
+                if (Q8 && kv == 0) {
+                    if (lane < 16) c->scales[blocks % kScaleRing][lane] = sc;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&c->scale_full[blocks % kScaleRing]);
+                }
+                if (lane == 0) {
+                    c->issued = n + 1;
+                    mbar_arrive_expect_tx(&full[st], bytes);
+                }
+                __syncwarp();
+                if (mine && tok >= 0)
+                    tma_load_3d(ring + st * kBox + half * 16384 + x * bt * (Q8 ? D : 128), kv ? vmap : kmap,
+                                half * 64, e.kvh, tok, &full[st], policy);
+            }
+            next_scale = scale(j + 1, next);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ matrix products
+
+// Blocks [lo, hi) that group g of the piece works on: those up to its last token.
+__device__ __forceinline__ int group_blocks(const Piece& pi, int g, int per) {
+    const int last = min(pi.ntok, (g + 1) * per) - 1;
+    if (last < g * per || pi.bad) return 0;
+    return max(0, min(pi.hi, (pi.limit0 + last + kExtBlock - 1) / kExtBlock) - pi.lo);
+}
+// The first block with places that some row of the tile does not see.
+__device__ __forceinline__ int first_masked(const Piece& pi) { return pi.limit0 / kExtBlock; }
+
+template <int D, bool Q8>
+__device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t* smem) {
+    using C = Cfg<D, Q8>;
+    const bool lead = (threadIdx.x & 31) == 0;
+    const uint32_t q_smem = smem_addr(smem), kv_smem = q_smem + C::kQ, tmem = c->tmem;
+    const int per = kExtRows / 2 / p.G;
+    constexpr uint32_t kIdQk = umma_idesc(kExtBlock, false), kIdPv = umma_idesc(D, true);
+    uint32_t n = 0, fixed_phase = 0, q_loads = 0, done[2] = {0, 0}, outs[2] = {0, 0};
+
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, p.status, &c->abort); };
+    auto qk = [&](int g, int st) {   // S_g = Q_g K^T
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
+            umma_ss(tmem + g * 128, umma_desc(q_smem + g * (C::kQ / 2) + off, 16), umma_desc(kv_smem + st * C::kTile + off, 16),
+                    kIdQk, k > 0);
+        }
+        umma_commit(&c->s_full[g]);
+    };
+    auto pv = [&](int g, int st, bool add) {   // O_g (+)= P_g V
+#pragma unroll
+        for (int k = 0; k < kExtBlock / 16; ++k)
+            umma_ts(tmem + 256 + g * 128, tmem + g * 128 + k * 8, umma_desc(kv_smem + st * C::kTile + k * 2048, 16384), kIdPv,
+                    add || k > 0);
+    };
+    for (uint32_t pc = 0;; ++pc) {
+        const int slot = pc % kPieceRing;
+        if (!wait(&c->piece_full[slot], (pc / kPieceRing) & 1)) return;
+        const Piece& pi = c->piece[slot];
+        const int nb = pi.bad ? 0 : pi.hi - pi.lo, ntok = pi.ntok, lo = pi.lo;
+        const int e[2] = {group_blocks(pi, 0, per), group_blocks(pi, 1, per)};
+        const int masked = Q8 ? 1 << 30 : first_masked(pi);
+        __syncwarp();
+        if (lead) mbar_arrive(&c->piece_empty[slot]);
+        if (ntok == 0) return;
+        if (nb == 0) continue;
+
+        if (!wait(&c->q_full, q_loads++ & 1)) return;
+        if (!wait(&c->full[n % C::kStages], (n / C::kStages) & 1)) return;
+        tc_fence_after();
+        if (lead) {
+            for (int g = 0; g < 2; ++g)
+                if (e[g] > 0) qk(g, n % C::kStages);
+            umma_commit(&c->empty[n % C::kStages]);
+            if (nb == 1) umma_commit(&c->q_empty);
+        }
+        __syncwarp();
+        for (int j = 0; j < nb; ++j, n += 2) {
+            const uint32_t vs = (n + 1) % C::kStages, ks = (n + 2) % C::kStages;
+            if (lo + j >= masked) {
+                if (!wait(&c->fixed[vs], (fixed_phase >> vs) & 1)) return;
+                fixed_phase ^= 1u << vs;
+            } else if (!wait(&c->full[vs], ((n + 1) / C::kStages) & 1)) {
+                return;
+            }
+            for (int g = 0; g < 2; ++g) {
+                if (j < e[g]) {
+                    if (j == 0 && outs[g] > 0 && !wait(&c->o_empty[g], (outs[g] - 1) & 1)) return;
+                    if (!wait(&c->p_full[g], done[g] & 1)) return;
+                    ++done[g];
+                    tc_fence_after();
+                    if (lead) {
+                        pv(g, vs, j > 0);
+                        if (j + 1 == e[g]) umma_commit(&c->o_full[g]);
+                    }
+                    if (j + 1 == e[g]) ++outs[g];
+                    __syncwarp();
+                }
+                if (g == 1 && lead) umma_commit(&c->empty[vs]);
+                if (g == 0 && j + 1 < nb && !wait(&c->full[ks], ((n + 2) / C::kStages) & 1)) return;
+                if (j + 1 < e[g]) {
+                    tc_fence_after();
+                    if (lead) qk(g, ks);
+                }
+                __syncwarp();
+            }
+            if (j + 1 < nb && lead) {
+                umma_commit(&c->empty[ks]);
+                if (j + 2 == nb) umma_commit(&c->q_empty);
+            }
+            __syncwarp();
+        }
+    }
+}
+
+// ------------------------------------------------------------------ V where masks end (bf16)
+
+// A weight of 0 does not hide an infinity or NaN in a product, so in blocks with
+// masked places V is cleaned before it is used: slots behind the row's end (which
+// may hold anything) become 0; so do infinities and NaN of tokens that some rows
+// see and others don't, which the rows that see them get back at the end.
+template <int D>
+__device__ __forceinline__ void fix_values(const ExtendParams& p, Ctl* c, uint8_t* smem) {
+    using C = Cfg<D, false>;
+    const int lane = threadIdx.x & 31;
+    uint32_t n = 0;
+    for (uint32_t pc = 0;; ++pc) {
+        const int slot = pc % kPieceRing;
+        if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, p.status, &c->abort)) return;
+        Piece& pi = c->piece[slot];
+        const int ntok = pi.ntok, lo = pi.lo, hi = pi.bad || ntok == 0 ? pi.lo : pi.hi, masked = first_masked(pi);
+        const int len = ntok ? p.seq_lens[pi.b] : 0;
+        for (int j = lo; j < hi; ++j, n += 2) {
+            // (every block is waited for, in order: a parity tells a phase from the next one only)
+            if (!wait_warp(&c->full[n % C::kStages], (n / C::kStages) & 1, p.status, &c->abort)) return;
+            const uint32_t vn = n + 1, st = vn % C::kStages;
+            if (!wait_warp(&c->full[st], (vn / C::kStages) & 1, p.status, &c->abort)) return;
+            if (j < masked) continue;
+            const int valid = len - j * kExtBlock;
+            const uint32_t tile = smem_addr(smem) + C::kQ + st * C::kTile;
+            uint32_t odd = 0;
+#pragma unroll 4
+            for (int i = lane; i < C::kTile / 16; i += 32) {
+                const uint32_t at = tile + i * 16;
+                uint32_t v[4];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+                bool put = (i >> 3) % kExtBlock >= valid;
+                if (put) {
+                    v[0] = v[1] = v[2] = v[3] = 0;
+                } else {
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) any |= (v[k] & 0x7f807f80u) + 0x00800080u;
+                    if (any & 0x80008000u) {
+                        put = true;
+                        odd = 1;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if ((v[k] & 0x7f80u) == 0x7f80u) v[k] &= 0xffff0000u;
+                            if ((v[k] & 0x7f800000u) == 0x7f800000u) v[k] &= 0x0000ffffu;
+                        }
+                    }
+                }
+                if (put) asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+            }
+            if (__any_sync(kFull, odd != 0) && lane == 0) pi.nonfinite = 1;
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->fixed[st]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->piece_empty[slot]);
+        if (ntok == 0) return;
+    }
+}
+
+// ------------------------------------------------------------------ e4m3 to bf16
+
+// Codes become bf16 exactly (4 bits of significand into 8); their scales join the
+// scores and the weights in fp32.  In blocks with masked places NaN codes become 0
+// as infinities and NaN do in fix_values.
+template <int D>
+__device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* smem) {
+    using C = Cfg<D, true>;
+    const int tid = threadIdx.x & 127, lane = tid & 31;
+    constexpr int kPerRow = D / 16;                       // threads of a token
+    const int chunk = tid % kPerRow, half = chunk / 4;
+    const uint32_t swap = half & 1;                       // the two halves' stores take other banks
+    const uint32_t q = smem_addr(smem), codes = q + C::kQ + C::kStages * C::kTile;
+    uint32_t n = 0;
+    for (uint32_t pc = 0;; ++pc) {
+        const int slot = pc % kPieceRing;
+        if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, p.status, &c->abort)) return;
+        Piece& pi = c->piece[slot];
+        const int ntok = pi.ntok, lo = pi.lo, hi = pi.bad || ntok == 0 ? pi.lo : pi.hi, masked = first_masked(pi);
+        const int len = ntok ? p.seq_lens[pi.b] : 0;
+        for (int j = lo; j < hi; ++j) {
+            for (int kv = 0; kv < 2; ++kv, ++n) {
+                const uint32_t cs = n % C::kCodes, st = n % C::kStages;
+                if (!wait_warp(&c->code_full[cs], (n / C::kCodes) & 1, p.status, &c->abort)) return;
+                if (n >= C::kStages && !wait_warp(&c->empty[st], (n / C::kStages - 1) & 1, p.status, &c->abort)) return;
+                const int valid = len - j * kExtBlock;
+                const bool clean = kv == 1 && j >= masked;
+                uint32_t odd = 0;
+                const uint32_t src = codes + cs * C::kCode, dst = q + C::kQ + st * C::kTile + half * 16384;
+#pragma unroll 2
+                for (int row = tid / kPerRow; row < kExtBlock; row += 128 / kPerRow) {
+                    uint32_t v[4], o[8];
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(src + row * D + chunk * 16) : "memory");
+                    if (clean) {
+                        if (row >= valid) v[0] = v[1] = v[2] = v[3] = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int b = 0; b < 32; b += 8)
+                                if ((v[k] >> b & 0x7fu) == 0x7fu) {
+                                    v[k] &= ~(0xffu << b);
+                                    odd = 1;
+                                }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint16_t two = static_cast<uint16_t>(v[k / 2] >> (16 * (k & 1)));
+                        uint32_t h;
+                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+                        float lo_f, hi_f;
+                        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(lo_f), "=f"(hi_f) : "r"(h));
+                        o[k] = bf16x2(lo_f, hi_f);
+                    }
+                    const uint32_t first = (chunk % 4) * 2 + swap, at = dst + row * 128;
+                    const uint32_t a0 = at + ((first ^ (row & 7)) << 4), a1 = at + (((first ^ 1) ^ (row & 7)) << 4);
+                    if (swap) {
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+                    } else {
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+                    }
+                }
+                if (clean && __any_sync(kFull, odd != 0) && lane == 0) pi.nonfinite = 1;
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&c->full[st]);
+                    mbar_arrive(&c->code_empty[cs]);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->piece_empty[slot]);
+        if (ntok == 0) return;
+    }
+}
+
+// ------------------------------------------------------------------ softmax and outputs
+
+// What fix_values took out of V and this row sees, added to 32 columns of its
+// output: an infinity or NaN of its own value.  Rare, so read from the pages again.
+template <int D, bool Q8>
+__device__ __noinline__ void add_nonfinite(const ExtendParams& p, const int32_t* row, int kvh, int t0, int t1, int col,
+                                           uint32_t* o) {
+    for (int t = t0; t < t1; ++t) {
+        const int page = row[t / p.page_size];
+        if (page < 0 || page >= p.num_pages) continue;
+        const size_t at = ((static_cast<size_t>(page) * p.page_size + t % p.page_size) * p.Hkv + kvh) * D + col;
+        for (int d = 0; d < 32; ++d) {
+            float v;
+            if (Q8) {
+                const uint8_t code = static_cast<const uint8_t*>(p.v_pages)[at + d];
+                v = (code & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.0f;
+            } else {
+                v = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p.v_pages)[at + d]) << 16);
+            }
+            if (!(fabsf(v) <= 3.4e38f)) o[d] = __float_as_uint(__uint_as_float(o[d]) + v);
+        }
+    }
+}
+
+// Where a row's results go: out / lse, or the state in a workspace slot.
+struct RowOut {
+    uint16_t* out;     // null: a workspace slot
+    float* lse;
+    float4* ws;
+    float2* ml;
+};
+__device__ __forceinline__ RowOut row_out(const ExtendParams& p, const Piece& pi, int row, int shift, int D) {
+    RowOut o{};
+    if (pi.slot < 0) {
+        const int64_t tok = pi.tok0 + (row >> shift);
+        const int head = pi.kvh * p.G + (row & (p.G - 1));
+        o.out = p.out + tok * p.out_stride + static_cast<int64_t>(head) * D;
+        o.lse = p.lse ? p.lse + tok * p.Hq + head : nullptr;
+    } else {
+        o.ws = reinterpret_cast<float4*>(p.ws_o) + static_cast<size_t>(pi.slot) * (D / 4) * kExtRows + row;
+        o.ml = p.ws_ml + static_cast<size_t>(pi.slot) * kExtRows + row;
+    }
+    return o;
+}
+__device__ __forceinline__ void write_nan(const RowOut& o, int D) {
+    if (o.out) {
+        for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(o.out + d) = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+        if (o.lse) *o.lse = __uint_as_float(0x7fffffffu);
+    } else {
+        *o.ml = make_float2(__uint_as_float(0x7fffffffu), __uint_as_float(0x7fffffffu));
+    }
+}
+
+// One block of scores: maximum, weights, sum.  `s` holds the row's 128 scores.
+template <int D, bool Q8>
+__device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
+    using C = Cfg<D, Q8>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = warp >> 2, row = threadIdx.x & 127;
+    const int shift = 31 - __clz(p.G), per = kExtRows / 2 >> shift;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
+    const uint32_t tS = c->tmem + lanes + g * 128, tO = c->tmem + lanes + 256 + g * 128;
+    const float cs = p.scale_log2;
+    uint32_t done = 0, outs = 0, blocks = 0;
+    for (uint32_t pc = 0;; ++pc) {
+        const int slot = pc % kPieceRing;
+        if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, p.status, &c->abort)) return false;
+        const Piece& pi = c->piece[slot];
+        if (pi.ntok == 0) {
+            return true;
+        }
+        const int nb = group_blocks(pi, g, per), lo = pi.lo;
+        const int base_row = g * 128;
+        const bool live = base_row + row < pi.ntok << shift;                // this thread's row exists
+        const bool warp_live = base_row + (row & ~31) < pi.ntok << shift;   // some row of the warp does
+        const int limit = pi.limit0 + ((base_row + row) >> shift);          // tokens that the row sees
+        const int masked = first_masked(pi);
+        float m = -INFINITY, l = 0.0f;
+        for (int j = 0; j < nb; ++j) {
+            if (!wait_warp(&c->s_full[g], done & 1, p.status, &c->abort)) return false;
+            ++done;
+            tc_fence_after();
+            if (warp_live) {
+                uint32_t s[128];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tmem_ld32(s + 32 * k, tS + 32 * k);
+                float vs[8];
+                if (Q8) {
+                    const uint32_t b = blocks + j;
+                    if (!wait_warp(&c->scale_full[b % kScaleRing], (b / kScaleRing) & 1, p.status, &c->abort)) return false;
+                    float ks[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        ks[k] = c->scales[b % kScaleRing][k] * cs;
+                        vs[k] = c->scales[b % kScaleRing][8 + k];
+                    }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tmem_loaded32(s + 32 * k);
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * ks[k / 16]);
+                } else {
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tmem_loaded32(s + 32 * k);
+                }
+                const int seen = limit - (lo + j) * kExtBlock;   // columns of the block that the row sees
+                const bool cut = lo + j >= masked;
+                if (cut) {
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) s[k] = k < seen ? s[k] : 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 4]));
+#pragma unroll
+                for (int k = 8; k < 128; k += 8)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(s[k + i])), __uint_as_float(s[k + 4 + i]));
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (!Q8) top *= cs;
+                if (j == 0) {
+                    m = top;
+                } else if (__any_sync(kFull, top > m + kMoveAt)) {
+                    // the block's product has not begun, the one before is done (its S came after it)
+                    const float to = fmaxf(m, top);
+                    const float f = to == -INFINITY ? 1.0f : ex2(m - to);
+                    l *= f;
+                    m = to;
+#pragma unroll
+                    for (int k = 0; k < D; k += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o, tO + k);
+                        tmem_wait_ld();
+                        tmem_loaded32(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st32(tO + k, o);
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.0f : -m;
+                const uint64_t ref2 = pack2(ref, ref), cs2 = pack2(cs, cs);
+                uint64_t sum[2] = {0, 0};
+#pragma unroll
+                for (int k = 0; k < 128; k += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const uint64_t x = pack2(__uint_as_float(s[k + i]), __uint_as_float(s[k + i + 1]));
+                        const F2 e = unpack2(Q8 ? add2(x, ref2) : fma2(x, cs2, ref2));
+                        const float a = ex2(e.x), b = ex2(e.y);
+                        sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(a, b));
+                        if (Q8) {
+                            const float v = vs[(k + i) / 16];
+                            // (a masked weight stays 0 whatever its scale)
+                            w[i / 2] = bf16x2(cut && k + i >= seen ? 0.0f : a * v, cut && k + i + 1 >= seen ? 0.0f : b * v);
+                        } else {
+                            w[i / 2] = bf16x2(a, b);
+                        }
+                    }
+                    tmem_st16(tS + k / 2, w);
+                }
+                const F2 a = unpack2(add2(sum[0], sum[1]));
+                l += a.x + a.y;
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->p_full[g]);
+        }
+        blocks += pi.bad ? 0 : pi.hi - pi.lo;
+
+        // outputs
+        if (nb > 0) {
+            if (!wait_warp(&c->o_full[g], outs & 1, p.status, &c->abort)) return false;
+            ++outs;
+            tc_fence_after();
+        }
+        const bool poison = pi.bad || pi.poison;
+        if (warp_live) {
+            const RowOut o = row_out(p, pi, base_row + row, shift, D);
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // (all scores -inf: out 0, lse -inf)
+            if (poison) {
+                if (live) write_nan(o, D);
+            } else if (nb == 0) {
+                if (live) *o.ml = make_float2(-INFINITY, 0.0f);   // (only a part of a tile can have nothing to see)
+            } else {
+                const bool odd = pi.nonfinite && live;
+#pragma unroll 1
+                for (int k = 0; k < D; k += 32) {
+                    uint32_t x[32];
+                    tmem_ld32(x, tO + k);
+                    tmem_wait_ld();
+                    tmem_loaded32(x);
+                    if (odd)
+                        add_nonfinite<D, Q8>(p, p.block_table + static_cast<size_t>(pi.b) * p.max_pages, pi.kvh,
+                                             max(lo, masked) * kExtBlock, min(limit, pi.hi * kExtBlock), k, x);
+                    __syncwarp();
+                    if (live && o.out) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int h = 0; h < 4; ++h)
+                                w[h] = bf16x2(__uint_as_float(x[i + 2 * h]) * inv, __uint_as_float(x[i + 2 * h + 1]) * inv);
+                            *reinterpret_cast<uint4*>(o.out + k + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else if (live) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            o.ws[static_cast<size_t>((k + i) / 4) * kExtRows] =
+                                make_float4(__uint_as_float(x[i]), __uint_as_float(x[i + 1]), __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+                    }
+                    __syncwarp();
+                }
+                if (live && o.out && o.lse) *o.lse = kLn2 * (m + log2f(l));
+                if (live && !o.out) *o.ml = make_float2(m, l);
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            if (nb > 0) mbar_arrive(&c->o_empty[g]);
+            mbar_arrive(&c->piece_empty[slot]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
+extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CUtensorMap qmap,
+              const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using C = Cfg<D, Q8>;
+    extern __shared__ uint8_t dyn[];
+    uint8_t* smem = dyn + ((1024 - (smem_addr(dyn) & 1023)) & 1023);
+    Ctl* c = reinterpret_cast<Ctl*>(smem + C::kBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&c->full[i], Q8 ? 4 : 1);
+            mbar_init(&c->empty[i], 1);
+            mbar_init(&c->fixed[i], 1);
+        }
+        for (int i = 0; i < C::kCodes; ++i) {
+            mbar_init(&c->code_full[i], 1);
+            mbar_init(&c->code_empty[i], 4);
+        }
+        for (int i = 0; i < kScaleRing; ++i) mbar_init(&c->scale_full[i], 1);
+        mbar_init(&c->q_full, 1);
+        mbar_init(&c->q_empty, 1);
+        mbar_init(&c->drain, 1);
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(&c->s_full[g], 1);
+            mbar_init(&c->p_full[g], 4);
+            mbar_init(&c->o_full[g], 1);
+            mbar_init(&c->o_empty[g], 4);
+        }
+        for (int i = 0; i < kPieceRing; ++i) {
+            mbar_init(&c->piece_full[i], 1);
+            mbar_init(&c->piece_empty[i], C::kReaders);
+        }
+        c->abort = 0;
+        c->issued = 0;
+        c->q_loads = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::kMma) tmem_alloc(&c->tmem, 512);
+    grid_dependency_wait();
+    launch_dependents();
+
+    // the CTA's part of the work
+    const Rows rows{p, kExtRows / p.G};
+    int64_t local = 0, W = 0;
+    for (int b = tid; b < p.B; b += C::kThreads) {
+        local += rows(b).units * p.Hkv;
+        if (blockIdx.x == 0 && p.cu && (p.cu[b] < 0 || p.cu[b + 1] < p.cu[b] || p.cu[b + 1] > p.T))
+            atomicOr(p.status, static_cast<uint32_t>(PKV_DEV_PLAN_MISMATCH));
+    }
+    int64_t before = block_scan<C::kThreads>(c, local, &W);
+    const int parts = ext_parts(W, gridDim.x), cta = blockIdx.x;
+    const bool work = W > 0 && cta < parts;
+    if (work) {
+        const int64_t first = ext_part_begin(W, parts, cta);
+        if (p.B <= C::kThreads) {
+            if (first >= before && first < before + local) c->row0 = tid, c->row_unit = before;
+        } else {
+            int64_t run = 0, total = 0;
+            for (int base = 0; base < p.B && run <= first; base += C::kThreads) {
+                const int b = base + tid;
+                local = b < p.B ? rows(b).units * p.Hkv : 0;
+                before = run + block_scan<C::kThreads>(c, local, &total);
+                if (first >= before && first < before + local) c->row0 = b, c->row_unit = before;
+                run += total;
+            }
+        }
+    }
+    if (tid == 0) p.splits[cta] = ExtSplit{0, 0, 0, 0};
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    if (work) {
+        if (warp < 8) {
+            if constexpr (Q8)
+                asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+            else
+                asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+            if (!attend<D, Q8>(p, c)) {
+                // a wait ran out: everything that this CTA was to write is NaN
+                ExtWalk w;
+                w.begin(W, parts, cta, p.B, p.Hkv, rows.tt, c->row0, c->row_unit, rows);
+                ExtPiece e;
+                while (w.next(e, rows)) {
+                    const ExtRow r = rows(e.b);
+                    Piece pi{};
+                    pi.tok0 = r.tok0 + e.tile * w.tt;
+                    pi.kvh = e.kvh;
+                    pi.slot = e.lo == 0 && e.hi == e.blocks ? -1 : 2 * cta + (e.lo == 0 ? 1 : 0);
+                    const int ntok = min(w.tt, r.n - e.tile * w.tt);
+                    if (tid < ntok * p.G) write_nan(row_out(p, pi, tid, 31 - __clz(p.G), D), D);
+                    if (tid == 0 && e.parts) p.splits[cta] = ExtSplit{pi.tok0, ntok, e.kvh, e.parts};
+                }
+            }
+        } else if (Q8 && warp < 12) {
+            if constexpr (Q8) {
+                asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+                widen<D>(p, c, smem);
+            }
+        } else {
+            if constexpr (Q8)
+                asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+            else
+                asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+            if (warp == C::kProducer) {
+                ExtWalk w;
+                w.begin(W, parts, cta, p.B, p.Hkv, rows.tt, c->row0, c->row_unit, rows);
+                uint64_t policy;
+                asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+                produce<D, Q8>(p, c, smem, &qmap, &kmap, &vmap, w, rows, policy);
+            } else if (warp == C::kMma) {
+                multiply<D, Q8>(p, c, smem);
+            } else if (warp == C::kFixer) {
+                if constexpr (!Q8) fix_values<D>(p, c, smem);
+            }
+        }
+    }
+    __syncthreads();
+    if (c->abort && warp == C::kMma) {   // products and copies in flight land before the memory goes
+        if (lane == 0) {
+            umma_commit(&c->drain);
+            wait_until(&c->drain, 0, p.status, nullptr);
+            constexpr uint32_t kRing = Q8 ? C::kCodes : C::kStages;
+            uint64_t* full = Q8 ? c->code_full : c->full;
+            const uint32_t n = c->issued;
+            for (uint32_t i = n > kRing ? n - kRing : 0; i < n; ++i)
+                wait_until(&full[i % kRing], (i / kRing) & 1, p.status, nullptr, 200000000ull);
+            if (c->q_loads) wait_until(&c->q_full, (c->q_loads - 1) & 1, p.status, nullptr, 200000000ull);
+        }
+        __syncwarp();
+    }
+    if (warp == C::kMma) tmem_free(c->tmem, 512);
+}
+
+// ------------------------------------------------------------------ shared tiles joined
+
+// The parts of a tile that several CTAs shared, weighted by 2^(m - max m).  One
+// block per CTA that began such a tile and 32 of its rows; lanes are rows (the
+// layout in which the states were left), warps take columns.
+template <int D>
+__global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant__ ExtendParams p) {
+    grid_dependency_wait();
+    const ExtSplit sp = p.splits[blockIdx.x];
+    const int row = blockIdx.y * 32 + (threadIdx.x & 31);
+    if (row >= sp.ntok * p.G) return;
+    const int first = 2 * blockIdx.x + 1;
+    auto slot = [&](int i) { return i == 0 ? first : 2 * (static_cast<int>(blockIdx.x) + i); };
+    float m = -INFINITY, l = 0.0f;
+    bool nan = false;
+    for (int i = 0; i < sp.parts; ++i) {
+        const float2 s = p.ws_ml[static_cast<size_t>(slot(i)) * kExtRows + row];
+        nan |= s.x != s.x;
+        m = fmaxf(m, s.x);
+    }
+    const float ref = m == -INFINITY ? 0.0f : m;
+    constexpr int kCols = D / 4 / 8;   // columns (of four) of a warp
+    const int warp = threadIdx.x >> 5;
+    float4 o[kCols];
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) o[k] = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int i = 0; i < sp.parts; ++i) {
+        const float2 s = p.ws_ml[static_cast<size_t>(slot(i)) * kExtRows + row];
+        if (s.y == 0.0f) continue;   // saw nothing; its state was not written
+        const float f = ex2(s.x - ref);
+        l += s.y * f;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) {
+            const float4 x = reinterpret_cast<const float4*>(p.ws_o)[(static_cast<size_t>(slot(i)) * (D / 4) + warp * kCols + k) * kExtRows + row];
+            o[k].x += x.x * f, o[k].y += x.y * f, o[k].z += x.z * f, o[k].w += x.w * f;
+        }
+    }
+    float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if (nan) inv = l = __uint_as_float(0x7fffffffu);
+    const int shift = 31 - __clz(p.G);
+    const int64_t tok = sp.tok0 + (row >> shift);
+    const int head = sp.kvh * p.G + (row & (p.G - 1));
+    uint16_t* out = p.out + tok * p.out_stride + static_cast<int64_t>(head) * D + warp * kCols * 4;
+#pragma unroll
+    for (int k = 0; k < kCols; ++k)
+        *reinterpret_cast<uint2*>(out + 4 * k) = make_uint2(bf16x2(o[k].x * inv, o[k].y * inv), bf16x2(o[k].z * inv, o[k].w * inv));
+    if (warp == 0 && p.lse) p.lse[tok * p.Hq + head] = kLn2 * (m + log2f(l));
+}
+
+template <int D, bool Q8>
+cudaError_t launch(const ExtendParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                   int ctas, cudaStream_t stream) {
+    constexpr size_t kSmem = Cfg<D, Q8>::kBytes + 1024 + sizeof(Ctl);
+    static_assert(kSmem <= 232448, "shared memory of a CTA");
+    // (on every call, as a device reset drops it)
+    cudaError_t e = cudaFuncSetAttribute(extend_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(Cfg<D, Q8>::kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, extend_kernel<D, Q8>, p, qmap, kmap, vmap);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(ctas, kExtRows / 32);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, extend_merge_kernel<D>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_extend(const ExtendParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                          const CUtensorMap& vmap, int ctas, cudaStream_t stream) {
+    const bool q8 = p.k_scales != nullptr;
+    if (p.D == 128) return q8 ? launch<128, true>(p, qmap, kmap, vmap, ctas, stream) : launch<128, false>(p, qmap, kmap, vmap, ctas, stream);
+    return q8 ? launch<64, true>(p, qmap, kmap, vmap, ctas, stream) : launch<64, false>(p, qmap, kmap, vmap, ctas, stream);
+}
+
+}  // namespace pkv

@@ -1,0 +1,167 @@
+// pkv_extend_schedule.h -- how the work of pkv_extend is shared out among CTAs.
+//
+// Plain arithmetic, compiled for the device and, by the CPU tests, for the host.
+//
+// Row b has n new tokens, the last n of its len.  Its G query heads of one KV
+// head lie next to each other in a token, so a tile packs tile_tokens = 256 / G
+// tokens x G heads into 256 rows of scores, and reads the KV blocks (128 tokens
+// each) up to its last token.  Work is counted in units: one per KV block, and
+// kTileUnits more per tile for what a tile costs besides (loading its queries,
+// filling and draining the pipeline).  Row by row, KV head by KV head, tile by
+// tile the units form one line of W, of which each of P CTAs takes an equal
+// part: nothing has to be known on the host, short and long rows balance, and
+// few tiles over a long cache are split.  A part begins and ends anywhere, so a
+// CTA has at most two tiles that it shares with others (its first and its last):
+// it leaves their partial states in its two workspace slots.
+#pragma once
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define PKV_HD __host__ __device__ __forceinline__
+#else
+#define PKV_HD inline
+#endif
+
+namespace pkv {
+
+constexpr int kExtBlock = 128;      // tokens of a KV block
+constexpr int kExtRows = 256;       // rows of scores of a tile: two groups of 128
+constexpr int kTileUnits = 1;       // units of a tile besides its blocks
+constexpr int kMinShareUnits = 2;   // a CTA takes at least this much (fewer CTAs work otherwise)
+
+struct ExtRow {
+    int32_t tok0;    // the row's first new token in q / out
+    int32_t n;       // its new tokens
+    int32_t len;     // its tokens, the new ones among them
+    int32_t tiles;   // tiles of one KV head
+    int32_t bad;     // lengths that cannot be: the tiles only write NaN
+    int64_t units;   // units of one KV head
+};
+
+// Blocks of the first i tiles of a row whose new tokens begin at position ctx,
+// none of them its last: sum over k = 1..i of ceil((ctx + k * tt) / 128).
+PKV_HD int64_t ext_blocks_before(int64_t ctx, int tt, int64_t i) {
+    if (tt >= kExtBlock) {
+        const int64_t s = tt / kExtBlock;
+        return i * ((ctx + kExtBlock - 1) / kExtBlock) + s * (i * (i + 1) / 2);
+    }
+    const int m = kExtBlock / tt;   // tiles of a block: k = m * a + r adds a to the r-th
+    int64_t sum = 0;
+    for (int r = 1; r <= m; ++r) {
+        const int64_t cnt = i >= r ? (i - r) / m + 1 : 0;
+        sum += cnt * ((ctx + r * tt + kExtBlock - 1) / kExtBlock) + cnt * (cnt - 1) / 2;
+    }
+    return sum;
+}
+
+PKV_HD int32_t ext_tile_blocks(const ExtRow& r, int tt, int32_t i) {
+    if (r.bad) return 1;
+    const int64_t upto = static_cast<int64_t>(r.len - r.n) + static_cast<int64_t>(i + 1) * tt;
+    return static_cast<int32_t>(((upto < r.len ? upto : r.len) + kExtBlock - 1) / kExtBlock);
+}
+
+// Units of the tiles before tile i of one KV head.
+PKV_HD int64_t ext_units_before(const ExtRow& r, int tt, int32_t i) {
+    if (r.bad) return static_cast<int64_t>(i) * (1 + kTileUnits);
+    return ext_blocks_before(r.len - r.n, tt, i) + static_cast<int64_t>(i) * kTileUnits;
+}
+
+// Row of tokens [lo, hi) with `len` tokens in all, of T tokens and at most
+// `cap` in a table.  Offsets that do not lie ascending in [0, T] leave no tiles.
+PKV_HD ExtRow ext_row(int32_t lo, int32_t hi, int32_t len, int32_t T, int64_t cap, int tt) {
+    ExtRow r;
+    r.tok0 = lo;
+    r.len = len;
+    r.n = lo >= 0 && hi <= T && hi > lo ? hi - lo : 0;
+    r.bad = (r.n > 0 && (len < r.n || len > cap)) ? 1 : 0;
+    r.tiles = static_cast<int32_t>((static_cast<int64_t>(r.n) + tt - 1) / tt);
+    r.units = r.tiles == 0 ? 0
+                           : ext_units_before(r, tt, r.tiles - 1) + ext_tile_blocks(r, tt, r.tiles - 1) + kTileUnits;
+    return r;
+}
+
+// The tile of one KV head that holds unit `off` (0 <= off < units).
+PKV_HD int32_t ext_tile_at(const ExtRow& r, int tt, int64_t off) {
+    int32_t lo = 0, hi = r.tiles - 1;
+    while (lo < hi) {
+        const int32_t mid = lo + (hi - lo + 1) / 2;
+        if (ext_units_before(r, tt, mid) <= off)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// CTAs that work on W units, and the first unit of part c of `parts`.
+PKV_HD int32_t ext_parts(int64_t W, int32_t ctas) {
+    const int64_t most = W / kMinShareUnits;
+    return static_cast<int32_t>(most < 1 ? 1 : (most < ctas ? most : ctas));
+}
+PKV_HD int64_t ext_part_begin(int64_t W, int32_t parts, int32_t c) {
+    const int64_t q = W / parts, rest = W % parts;
+    return c * q + (c < rest ? c : rest);
+}
+PKV_HD int32_t ext_part_of(int64_t W, int32_t parts, int64_t unit) {
+    const int64_t q = W / parts, rest = W % parts;
+    return static_cast<int32_t>(unit < rest * (q + 1) ? unit / (q + 1) : rest + (unit - rest * (q + 1)) / q);
+}
+
+// One CTA's stretch of one tile.
+struct ExtPiece {
+    int32_t b, kvh, tile;
+    int32_t lo, hi;    // its KV blocks
+    int32_t blocks;    // the tile's
+    int32_t parts;     // lo == 0 and hi < blocks: CTAs (from this one on) that share the tile; else 0
+};
+
+// Walks one CTA's part of the line.  `rows` gives ExtRow by index.
+struct ExtWalk {
+    int64_t W, unit, end;   // unit: the current tile's first
+    int32_t parts, cta, B, Hkv, tt;
+    int32_t b, kvh, tile;
+    ExtRow r;
+
+    // The part of `cta`, which begins in row b0, whose first unit is row_unit.
+    template <class Rows>
+    PKV_HD void begin(int64_t W_, int32_t parts_, int32_t cta_, int32_t B_, int32_t Hkv_, int tt_, int32_t b0,
+                      int64_t row_unit, const Rows& rows) {
+        W = W_, parts = parts_, cta = cta_, B = B_, Hkv = Hkv_, tt = tt_;
+        const int64_t first = ext_part_begin(W, parts, cta);
+        end = ext_part_begin(W, parts, cta + 1);
+        b = b0;
+        r = rows(b);
+        const int64_t off = first - row_unit;
+        kvh = static_cast<int32_t>(off / r.units);
+        const int64_t in_head = off - kvh * r.units;
+        tile = ext_tile_at(r, tt, in_head);
+        unit = row_unit + kvh * r.units + ext_units_before(r, tt, tile);
+    }
+
+    // The next stretch with blocks in it; false at the end of the part.
+    template <class Rows>
+    PKV_HD bool next(ExtPiece& p, const Rows& rows) {
+        const int64_t first = ext_part_begin(W, parts, cta);
+        while (unit < end) {
+            const int32_t nb = ext_tile_blocks(r, tt, tile);
+            const int64_t b0 = unit + kTileUnits;   // the unit of block 0
+            p.b = b, p.kvh = kvh, p.tile = tile, p.blocks = nb, p.parts = 0;
+            p.lo = first > b0 ? static_cast<int32_t>(first - b0) : 0;
+            p.hi = end < b0 + nb ? static_cast<int32_t>(end - b0) : nb;
+            if (p.lo == 0 && p.hi > 0 && p.hi < nb) p.parts = ext_part_of(W, parts, b0 + nb - 1) - cta + 1;
+            unit = b0 + nb;
+            if (++tile == r.tiles) {
+                tile = 0;
+                if (++kvh == Hkv) {
+                    kvh = 0;
+                    do ++b;
+                    while (unit < end && b < B && (r = rows(b)).tiles == 0);
+                }
+            }
+            if (p.hi > p.lo) return true;
+        }
+        return false;
+    }
+};
+
+}  // namespace pkv

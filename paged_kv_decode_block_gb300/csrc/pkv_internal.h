@@ -185,6 +185,37 @@ struct AttnQ8Params {
 };
 cudaError_t launch_attention_q8(const AttnQ8Params& p, int grid, cudaStream_t stream, bool cooperative);
 
+// Attention of the rows' new tokens (pkv_extend / pkv_extend_q8).
+constexpr int kExtTileRows = 256;   // (token, query head) rows of a tile: one workspace slot holds their states
+struct ExtSplit {               // a tile that `parts` CTAs share, the one with this entry first (0: none)
+    int32_t tok0, ntok, kvh, parts;
+};
+struct ExtendParams {
+    const void* k_pages;        // bf16 or e4m3 [num_pages][page_size][Hkv][D]
+    const void* v_pages;
+    const float* k_scales;      // e4m3 pages: [num_pages][page_size / kBlockRows][Hkv]; null: bf16 pages
+    const float* v_scales;
+    const int32_t* block_table; // [B][max_pages]
+    const int32_t* seq_lens;    // [B] lengths, the new tokens among them
+    const int32_t* cu;          // [B + 1] first token of each row, or null: one token per row
+    uint16_t* out;              // bf16 [T][Hq][D] at out_stride
+    float* lse;                 // [T][Hq], or null
+    int64_t out_stride;         // elements between tokens
+    float* ws_o;                // [CTAs][2][D / 4][256][4] unnormalised partial outputs
+    float2* ws_ml;              // [CTAs][2][256] their reference (log2) and sum
+    ExtSplit* splits;           // [CTAs]
+    uint32_t* status;
+    int32_t T;                  // tokens in q / out
+    int32_t B, Hq, Hkv, G, D, page_size, max_pages, num_pages;
+    int32_t box_tokens;         // tokens of a TMA box: divides the page and the block of 128
+    float scale_log2;           // log2(e) / sqrt(D)
+};
+// qmap: q as [T][Hq][D], box {64, G, 128 / G}, swizzled by 128 bytes.  kmap / vmap: the
+// pools as [num_pages * page_size][Hkv][D], box {64, 1, box_tokens} swizzled (bf16) or
+// {D, 1, box_tokens} (e4m3).
+cudaError_t launch_extend(const ExtendParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                          const CUtensorMap& vmap, int ctas, cudaStream_t stream);
+
 // Slot admit / evict (pkv_session_evict / pkv_session_admit / pkv_resident_*).
 // One request per row; evictions are applied before admissions, each in the
 // order listed.  32 bytes.

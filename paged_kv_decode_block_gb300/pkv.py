@@ -88,6 +88,14 @@ class Tokens(ctypes.Structure):
 _pack_tokens = struct.Struct("PPPPqqqqPi4x").pack   # a Tokens as bytes, which takes a fifth of the time to make
 
 
+class Queries(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("cu_tokens_d", ctypes.c_void_p), ("total_tokens", ctypes.c_int32)]
+
+
+_pack_queries = struct.Struct("PPPqqPi4x").pack   # a Queries as bytes
+
+
 # symbol -> (restype, argtypes); the full C ABI of include/pkv.h
 _P, _I32, _I64, _U32P = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(ctypes.c_uint32)
 _I32P = ctypes.POINTER(ctypes.c_int32)
@@ -109,6 +117,9 @@ SIGNATURES = {
     "pkv_append_rotary": (ctypes.c_int, [_P, ctypes.POINTER(RotaryParams), _P, _P, _P, _P, _P, _P, _P]),
     "pkv_append_q8": (ctypes.c_int, [_P, ctypes.POINTER(RotaryParams), _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "pkv_decode_q8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "pkv_extend_reserve": (ctypes.c_int, [_P]),
+    "pkv_extend": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P]),
+    "pkv_extend_q8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "pkv_status": (ctypes.c_int, [_P, _P, _U32P]),
     "pkv_read_workspace": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I32P]),
     "pkv_profile_enable": (ctypes.c_int, [_P, _I32]),
@@ -339,6 +350,10 @@ class Plan:
             _check(load().pkv_trace_read(self.handle, rows.ctypes.data, n.value, ctypes.byref(n)), "pkv_trace_read")
         return rows
 
+    def reserve_extend(self):
+        """Allocates what extend and extend_q8 keep in the plan (pkv_extend_reserve); their first call does it too."""
+        _check(load().pkv_extend_reserve(self.handle), "pkv_extend_reserve")
+
     def close(self):
         if getattr(self, "_h", None) is not None and _lib is not None:
             _lib.pkv_plan_destroy(self._h)
@@ -568,6 +583,45 @@ def decode_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, pl
         raise TypeError(f"pkv_decode_q8: arguments must be CUDA tensors ({e})") from None
     if rc:
         _check(rc, "pkv_decode_q8")
+
+
+def _extend(what, fn, q, k_pages, v_pages, scales, block_table, seq_lens, plan, out, lse, cu_tokens, stream):
+    bf, g, dev = _BF16 or _bf16_types(), plan.geom, plan.device
+    try:
+        T = q.shape[0]
+        heads = (T, plan.Hq, plan.D)
+        qp, q_stride = _tokens_arg(q, "q", heads, dev)
+        op, out_stride = _tokens_arg(out, "out", heads, dev)
+        lp = _arg(lse, "lse", _F32T, (T, plan.Hq), dev) if lse is not None else 0
+        cu = _arg(cu_tokens, "cu_tokens", _I32T, (g.batch + 1,), dev) if cu_tokens is not None else 0
+        types = bf if scales is None else _F8 or _f8_types()
+        pages = (_arg(k_pages, "k_pages", types, plan.pool_shape, dev), _arg(v_pages, "v_pages", types, plan.pool_shape, dev))
+        if scales is not None:
+            pages += (_arg(scales[0], "k_scales", _F32T, plan.scales_shape, dev),
+                      _arg(scales[1], "v_scales", _F32T, plan.scales_shape, dev))
+        rc = fn(_pack_queries(qp, op, lp, q_stride, out_stride, cu, T), *pages,
+                _arg(block_table, "block_table", _I32T, plan.table_shape, dev),
+                _arg(seq_lens, "seq_lens", _I32T, plan.rows_shape, dev), plan.handle,
+                _raw_stream(dev) if stream is None else _stream_handle(stream))
+    except AttributeError as e:
+        raise TypeError(f"{what}: arguments must be CUDA tensors ({e})") from None
+    if rc:
+        _check(rc, what)
+
+
+def extend(q, k_pages, v_pages, block_table, seq_lens, plan: Plan, out, lse=None, cu_tokens=None, stream=None):
+    """pkv_extend: causal attention of each row's new tokens cu_tokens[b]..cu_tokens[b + 1] (without cu_tokens: its
+    one token), which the cache holds already as the last of its seq_lens[b] tokens.  q / out: bf16 [T][Hq][D], also
+    slices of wider tensors; lse: fp32 [T][Hq] or None."""
+    _extend("pkv_extend", (_lib or load()).pkv_extend, q, k_pages, v_pages, None, block_table, seq_lens, plan, out, lse,
+            cu_tokens, stream)
+
+
+def extend_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, plan: Plan, out, lse=None, cu_tokens=None,
+              stream=None):
+    """pkv_extend_q8: extend over an 8-bit cache (see append_q8)."""
+    _extend("pkv_extend_q8", (_lib or load()).pkv_extend_q8, q, k_pages, v_pages, (k_scales, v_scales), block_table,
+            seq_lens, plan, out, lse, cu_tokens, stream)
 
 
 class Pool:
