@@ -447,6 +447,35 @@ int pkv_extend_q8(const pkv_queries *queries, const void *k_pages, const void *v
                   const float *v_scales, const int32_t *block_table_d, const int32_t *seq_lens_d, pkv_plan_t plan,
                   pkv_stream_t stream);
 
+/*
+ * Copies between pages, in all pools of a cache at once: what pkv_pool_fork and
+ * pkv_pool_compact ask for.  Copy i writes the first tokens_i tokens of page
+ * dst_i from page src_i, in every pool; the rest of dst_i is left as it was.
+ *   pools_h   host [n_pools]: the K and V pages of each layer, and their scales
+ *   copies_h  host [n_copies]; read before the call returns.  A page may be the
+ *             source of several copies, but a target only once and not a source
+ *             too (so the copies may run in any order)
+ * Enqueues one kernel per 2048 copies and 192 pools on `stream` and needs no
+ * memory of its own; in a CUDA graph the copies are those of the capture.  Pools
+ * are on the current device, and no two of them overlap.
+ * Errors: PKV_EINVAL (a page outside [0, num_pages), tokens outside [0,
+ * page_size], a target twice or also a source, a null pointer, a pool whose sizes
+ * or address are no multiples of 4 bytes or whose units do not divide the page),
+ * PKV_ENOMEM, PKV_ECUDA.  Nothing is enqueued on PKV_EINVAL.
+ */
+typedef struct {
+    int32_t src, dst;      /* pages */
+    int32_t tokens;        /* the first tokens of the page; 0: nothing */
+} pkv_page_copy;
+typedef struct {
+    void *data;            /* device [num_pages][page_bytes] */
+    int64_t page_bytes;
+    int64_t unit_tokens;   /* tokens that an entry of the page stands for: 1 for keys and values,
+                              PKV_Q8_BLOCK for the scales; at most 256 */
+} pkv_page_pool;
+int pkv_copy_pages(const pkv_page_pool *pools_h, int32_t n_pools, const pkv_page_copy *copies_h, int32_t n_copies,
+                   int32_t num_pages, int32_t page_size, pkv_stream_t stream);
+
 /* Read and clear the plan's device status word (synchronises `stream`). */
 int pkv_status(pkv_plan_t plan, pkv_stream_t stream, uint32_t *status);
 
@@ -511,14 +540,47 @@ int pkv_profile_read(pkv_plan_t plan, float *ms, int32_t capacity, int32_t *coun
  *                       rows it touched to rows_out (nullable, capacity B) and
  *                       their number to *n_rows.  PKV_ENOSPACE when the pool or
  *                       a row's table runs out (no row is changed then).
- *   pkv_pool_release    returns pages to the back of the free list; PKV_EINVAL
- *                       (and no change) for a page that is already free
+ *   pkv_pool_release    gives up one use of each page listed; a page without further
+ *                       ones goes to the back of the free list.  PKV_EINVAL (and no
+ *                       change) for a page that is already free, or listed more
+ *                       often than it is used
+ *   pkv_pool_fork       row i of dst_table_h [n][max_pages_per_seq] becomes a second
+ *                       user of the first lens_h[i] tokens of row parents_h[i] of
+ *                       src_table_h [src_rows][max_pages_per_seq]: it shares the full
+ *                       pages (no append changes them, as long as no row that shares
+ *                       them is cut back into them), and of a page that it needs in part
+ *                       it gets a fresh one, which one of the *n_copies copies written
+ *                       to copies (capacity n) fills (pkv_copy_pages, before the row is
+ *                       read or appended to).  The
+ *                       row's other entries become -1.  A parent may be listed any
+ *                       number of times.  The tables must not overlap.  PKV_ENOSPACE
+ *                       when the pool runs out; PKV_EINVAL for a parent or length out
+ *                       of range or a page that is free or outside the pool; nothing
+ *                       changes then
+ *   pkv_pool_compact    moves the pages in use to the front: page ids >= their number
+ *                       are replaced throughout block_table_h [batch][max_pages_per_seq]
+ *                       by free ones below it, *n_copies copies of whole pages written
+ *                       to copies fill those, and the free list becomes the ids behind,
+ *                       ascending.  The table has to hold every use of every page in
+ *                       use (each entry >= 0 is one), else PKV_EINVAL; PKV_ENOSPACE
+ *                       when `capacity` is too small (*n_copies is then what it takes;
+ *                       half of the pool always suffices).  Nothing changes then.  The
+ *                       device table has to follow before it is used again
+ * A pool that a session is bound to is not compacted (its tables are the session's),
+ * and once a session has taken the pages to the device (pkv_session_device_plan)
+ * none of its pages is shared any more: both PKV_EINVAL.  That session refuses a
+ * pool with shared pages too.
  */
 int pkv_pool_create(const int32_t *free_pages, int32_t count, int32_t num_pages, pkv_pool_t *pool);
 int pkv_pool_reserve(pkv_pool_t pool, const int32_t *seq_lens_h, int32_t *block_table_h,
                      int32_t batch, int32_t max_pages_per_seq, int32_t page_size,
                      int32_t *rows_out, int32_t *n_rows);
 int pkv_pool_release(pkv_pool_t pool, const int32_t *pages, int32_t count);
+int pkv_pool_fork(pkv_pool_t pool, const int32_t *src_table_h, int32_t src_rows, const int32_t *parents_h,
+                  const int32_t *lens_h, int32_t n, int32_t max_pages_per_seq, int32_t page_size,
+                  int32_t *dst_table_h, pkv_page_copy *copies, int32_t *n_copies);
+int pkv_pool_compact(pkv_pool_t pool, int32_t *block_table_h, int32_t batch, int32_t max_pages_per_seq,
+                     int32_t page_size, pkv_page_copy *copies, int32_t capacity, int32_t *n_copies);
 int32_t pkv_pool_free_count(pkv_pool_t pool);
 void pkv_pool_destroy(pkv_pool_t pool);
 

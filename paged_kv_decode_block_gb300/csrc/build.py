@@ -23,7 +23,7 @@ LIB = os.path.join(BUILD, "libpkv.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 CUDA_SOURCES = ["pkv_attention.cu", "pkv_append.cu", "pkv_static.cu", "pkv_devplan.cu",
-                "pkv_append_tokens.cu", "pkv_attention_q8.cu", "pkv_extend.cu"]
+                "pkv_append_tokens.cu", "pkv_attention_q8.cu", "pkv_extend.cu", "pkv_copy.cu"]
 CXX_SOURCES = ["pkv_api.cpp"]
 HEADERS = ["pkv_internal.h", "pkv_device.cuh", "pkv_merge.cuh", "pkv_devplan.cuh", "pkv_slots.cuh",
            "pkv_tcgen05.cuh", "pkv_extend_schedule.h"]

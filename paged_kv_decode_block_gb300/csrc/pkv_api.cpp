@@ -29,6 +29,7 @@
 #include <chrono>
 #include <cmath>
 #include <deque>
+#include <exception>
 #include <mutex>
 #include <new>
 #include <utility>
@@ -1305,7 +1306,10 @@ int pkv_profile_read(pkv_plan_t p, float* ms, int32_t capacity, int32_t* count) 
 struct pkv_pool_s {
     std::deque<int32_t> free_list;
     std::vector<uint8_t> is_free;   // [num_pages]: the page is in free_list
+    std::vector<int32_t> shared;    // [num_pages]: uses of the page besides the first (pkv_pool_fork)
     int32_t num_pages = 0;
+    bool bound = false;             // a session keeps a table of this pool's pages
+    bool on_device = false;         // ... and hands them out on the device
 };
 
 extern "C" {
@@ -1318,6 +1322,7 @@ int pkv_pool_create(const int32_t* free_pages, int32_t count, int32_t num_pages,
     pkv_pool_s* p = new (std::nothrow) pkv_pool_s;
     if (!p) return PKV_ENOMEM;
     p->is_free.assign(num_pages, 0);
+    p->shared.assign(num_pages, 0);
     for (int32_t i = 0; i < count; ++i) {
         if (p->is_free[free_pages[i]]) {   // listed twice
             delete p;
@@ -1383,15 +1388,180 @@ int pkv_pool_release(pkv_pool_t pool, const int32_t* pages, int32_t count) {
     if (!pool || count < 0 || (count > 0 && !pages)) return PKV_EINVAL;
     for (int32_t i = 0; i < count; ++i)
         if (pages[i] < 0 || pages[i] >= pool->num_pages) return PKV_EINVAL;
-    // a page that is free already (or listed twice) is refused, and nothing changes
-    for (int32_t i = 0; i < count; ++i) {
-        if (pool->is_free[pages[i]]) {
-            for (int32_t j = 0; j < i; ++j) pool->is_free[pages[j]] = 0;
-            return PKV_EINVAL;
+    // a page that is free already (or listed more often than it is used) is refused, and nothing changes
+    const size_t before = pool->free_list.size();
+    int32_t i = 0;
+    int rc = PKV_OK;
+    try {
+        for (; i < count; ++i) {
+            if (pool->is_free[pages[i]]) {
+                rc = PKV_EINVAL;
+                break;
+            }
+            if (pool->shared[pages[i]] > 0) {
+                --pool->shared[pages[i]];
+            } else {
+                pool->free_list.push_back(pages[i]);
+                pool->is_free[pages[i]] = 1;
+            }
         }
-        pool->is_free[pages[i]] = 1;
+    } catch (const std::exception&) {
+        rc = PKV_ENOMEM;
     }
-    pool->free_list.insert(pool->free_list.end(), pages, pages + count);
+    if (rc) {
+        while (--i >= 0) {   // backwards: a page's last use went last
+            if (pool->is_free[pages[i]])
+                pool->is_free[pages[i]] = 0;
+            else
+                ++pool->shared[pages[i]];
+        }
+        while (pool->free_list.size() > before) pool->free_list.pop_back();
+    }
+    return rc;
+}
+
+int pkv_pool_fork(pkv_pool_t pool, const int32_t* src_table_h, int32_t src_rows, const int32_t* parents_h,
+                  const int32_t* lens_h, int32_t n, int32_t max_pages_per_seq, int32_t page_size,
+                  int32_t* dst_table_h, pkv_page_copy* copies, int32_t* n_copies) {
+    if (!pool || !n_copies || n < 0 || src_rows < 0 || max_pages_per_seq <= 0 || page_size <= 0 || pool->on_device)
+        return PKV_EINVAL;
+    *n_copies = 0;
+    if (n == 0) return PKV_OK;
+    if (!src_table_h || !parents_h || !lens_h || !dst_table_h || !copies) return PKV_EINVAL;
+    const size_t mp = static_cast<size_t>(max_pages_per_seq);
+    if (src_table_h < dst_table_h + n * mp && dst_table_h < src_table_h + src_rows * mp) return PKV_EINVAL;
+    size_t need = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        if (parents_h[i] < 0 || parents_h[i] >= src_rows || lens_h[i] < 0 ||
+            lens_h[i] > static_cast<int64_t>(max_pages_per_seq) * page_size)
+            return PKV_EINVAL;
+        const int32_t* src = src_table_h + parents_h[i] * mp;
+        for (int64_t j = 0; j < ceil_div(lens_h[i], page_size); ++j)
+            if (src[j] < 0 || src[j] >= pool->num_pages || pool->is_free[src[j]]) return PKV_EINVAL;
+        need += lens_h[i] % page_size != 0;
+    }
+    if (need > pool->free_list.size()) return PKV_ENOSPACE;
+    int32_t k = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        const int32_t* src = src_table_h + parents_h[i] * mp;
+        int32_t* dst = dst_table_h + i * mp;
+        const int32_t whole = lens_h[i] / page_size, tail = lens_h[i] % page_size;
+        std::fill(dst, dst + mp, -1);
+        for (int32_t j = 0; j < whole; ++j) {
+            dst[j] = src[j];
+            ++pool->shared[src[j]];
+        }
+        if (tail) {
+            const int32_t page = pool->free_list.front();
+            pool->free_list.pop_front();
+            pool->is_free[page] = 0;
+            dst[whole] = page;
+            copies[k++] = pkv_page_copy{src[whole], page, tail};
+        }
+    }
+    *n_copies = k;
+    return PKV_OK;
+}
+
+int pkv_pool_compact(pkv_pool_t pool, int32_t* block_table_h, int32_t batch, int32_t max_pages_per_seq,
+                     int32_t page_size, pkv_page_copy* copies, int32_t capacity, int32_t* n_copies) {
+    if (!pool || !n_copies || batch < 0 || (batch > 0 && !block_table_h) || max_pages_per_seq <= 0 || page_size <= 0 ||
+        capacity < 0 || (capacity > 0 && !copies) || pool->bound || pool->on_device)
+        return PKV_EINVAL;
+    *n_copies = 0;
+    const size_t entries = static_cast<size_t>(batch) * max_pages_per_seq;
+    try {
+        std::vector<int64_t> uses(pool->num_pages, 0);
+        for (size_t i = 0; i < entries; ++i) {
+            if (block_table_h[i] < 0) continue;
+            if (block_table_h[i] >= pool->num_pages) return PKV_EINVAL;
+            ++uses[block_table_h[i]];
+        }
+        int32_t used = 0;
+        for (int32_t i = 0; i < pool->num_pages; ++i) {
+            if (uses[i] != (pool->is_free[i] ? 0 : int64_t{1} + pool->shared[i])) return PKV_EINVAL;
+            used += uses[i] > 0;
+        }
+        int32_t moves = 0;
+        for (int32_t i = used; i < pool->num_pages; ++i) moves += uses[i] > 0;
+        if (moves > capacity) {
+            *n_copies = moves;
+            return PKV_ENOSPACE;
+        }
+        std::vector<int32_t> to(pool->num_pages);
+        std::deque<int32_t> free_list;
+        for (int32_t i = used; i < pool->num_pages; ++i) free_list.push_back(i);
+        int32_t gap = 0, k = 0;
+        for (int32_t i = 0; i < pool->num_pages; ++i) {
+            to[i] = i;
+            if (i < used || uses[i] == 0) continue;
+            while (uses[gap] > 0) ++gap;   // (as many below `used` are free as are used from there on)
+            to[i] = gap;
+            copies[k++] = pkv_page_copy{i, gap++, page_size};
+        }
+        for (int32_t c = 0; c < k; ++c) {
+            pool->is_free[copies[c].src] = 1;
+            pool->is_free[copies[c].dst] = 0;
+            std::swap(pool->shared[copies[c].src], pool->shared[copies[c].dst]);
+        }
+        pool->free_list.swap(free_list);
+        for (size_t i = 0; i < entries; ++i)
+            if (block_table_h[i] >= 0) block_table_h[i] = to[block_table_h[i]];
+        *n_copies = k;
+    } catch (const std::exception&) {
+        return PKV_ENOMEM;
+    }
+    return PKV_OK;
+}
+
+int pkv_copy_pages(const pkv_page_pool* pools_h, int32_t n_pools, const pkv_page_copy* copies_h, int32_t n_copies,
+                   int32_t num_pages, int32_t page_size, pkv_stream_t stream) {
+    NvtxRange range("pkv_copy_pages");
+    if (n_pools < 0 || n_copies < 0 || (n_pools > 0 && !pools_h) || (n_copies > 0 && !copies_h) || num_pages <= 0 ||
+        page_size <= 0)
+        return PKV_EINVAL;
+    try {
+        std::vector<pkv::CopyPool> pools(n_pools);
+        for (int32_t i = 0; i < n_pools; ++i) {
+            const pkv_page_pool& x = pools_h[i];
+            if (!x.data || x.page_bytes <= 0 || x.unit_tokens <= 0 || x.unit_tokens > 256 || page_size % x.unit_tokens)
+                return PKV_EINVAL;
+            const int64_t units = page_size / x.unit_tokens;
+            const uintptr_t at = reinterpret_cast<uintptr_t>(x.data);
+            if (x.page_bytes % units || (x.page_bytes / units) % 4 || at % 4 || x.page_bytes > (int64_t{1} << 24))
+                return PKV_EINVAL;
+            const bool wide = (x.page_bytes / units) % 16 == 0 && at % 16 == 0;
+            const int64_t vec = wide ? 16 : 4;
+            pools[i] = pkv::CopyPool{x.data, static_cast<uint32_t>(x.page_bytes / vec),
+                                     static_cast<uint32_t>(x.page_bytes / units / vec), 0,
+                                     static_cast<uint16_t>(x.unit_tokens), static_cast<uint16_t>(wide)};
+        }
+        // few copies are compared in pairs, many through a mark on each page: 1 a source, 2 a target
+        const bool pairs = n_copies <= 32;
+        std::vector<uint8_t> role(pairs ? 0 : num_pages, 0);
+        for (int32_t i = 0; i < n_copies; ++i) {
+            const pkv_page_copy& c = copies_h[i];
+            if (c.src < 0 || c.src >= num_pages || c.dst < 0 || c.dst >= num_pages || c.src == c.dst || c.tokens < 0 ||
+                c.tokens > page_size)
+                return PKV_EINVAL;
+            if (pairs) {
+                for (int32_t j = 0; j < i; ++j)
+                    if (copies_h[j].dst == c.dst || copies_h[j].dst == c.src || copies_h[j].src == c.dst) return PKV_EINVAL;
+                continue;
+            }
+            if (role[c.dst] || role[c.src] == 2) return PKV_EINVAL;
+            role[c.dst] = 2;
+            role[c.src] = 1;
+        }
+        if (n_pools == 0 || n_copies == 0) return PKV_OK;
+        int dev = -1, sms = 0;
+        PKV_CUDA(cudaGetDevice(&dev));
+        PKV_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+        PKV_CUDA(pkv::launch_copy_pages(pools.data(), n_pools, copies_h, n_copies, sms,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+    } catch (const std::exception&) {
+        return PKV_ENOMEM;
+    }
     return PKV_OK;
 }
 
@@ -1543,6 +1713,7 @@ int pkv_session_create(pkv_plan_t plan, pkv_pool_t pool, const int32_t* seq_lens
         return cuda_fail(e);
     }
     s->req_d = static_cast<const pkv::SlotRequest*>(mapped);
+    pool->bound = true;
     *session = s;
     return PKV_OK;
 }
@@ -1551,6 +1722,8 @@ int pkv_session_device_plan(pkv_session_t s, pkv_stream_t stream) {
     NvtxRange range("pkv_session_device_plan");
     if (!s) return PKV_EINVAL;
     if (s->device_mode) return PKV_OK;
+    for (const int32_t uses : s->pool->shared)   // (the device free list knows of one user a page)
+        if (uses > 0) return PKV_EINVAL;
     pkv_plan_s* p = s->plan;
     const pkv_geom& g = p->g;
     const int B = g.batch, Hkv = g.num_kv_heads, G = g.num_q_heads / g.num_kv_heads;
@@ -1596,6 +1769,7 @@ int pkv_session_device_plan(pkv_session_t s, pkv_stream_t stream) {
     PKV_CUDA(cudaMemcpyAsync(s->dev_free, pages.data(), pages.size() * sizeof(int32_t), cudaMemcpyHostToDevice, st));
     PKV_CUDA(cudaMemcpyAsync(s->dev_free_state, state, sizeof(state), cudaMemcpyHostToDevice, st));
     PKV_CUDA(cudaStreamSynchronize(st));   // the host vectors above go out of scope
+    s->pool->on_device = true;
     s->pool->free_list.clear();            // those pages now belong to the device allocator
     std::fill(s->pool->is_free.begin(), s->pool->is_free.end(), uint8_t{0});
     s->free_cap = static_cast<int32_t>(ring);

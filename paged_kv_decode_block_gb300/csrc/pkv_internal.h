@@ -216,6 +216,19 @@ struct ExtendParams {
 cudaError_t launch_extend(const ExtendParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
                           const CUtensorMap& vmap, int ctas, cudaStream_t stream);
 
+// Page copies in all pools of a cache (pkv_copy_pages), on the current device.
+constexpr int kCopyMaxPools = 192;     // of one launch: what its parameters hold
+constexpr int kCopyMaxCopies = 2048;
+struct CopyPool {
+    void* data;
+    uint32_t page_vecs;         // vectors (16 bytes if `wide`, else 4) of a page
+    uint32_t unit_vecs;         // ... of unit_tokens tokens
+    uint32_t first_item;        // set by launch_copy_pages
+    uint16_t unit_tokens, wide;
+};
+cudaError_t launch_copy_pages(const CopyPool* pools, int num_pools, const pkv_page_copy* copies, int num_copies,
+                              int num_sms, cudaStream_t stream);
+
 // Slot admit / evict (pkv_session_evict / pkv_session_admit / pkv_resident_*).
 // One request per row; evictions are applied before admissions, each in the
 // order listed.  32 bytes.

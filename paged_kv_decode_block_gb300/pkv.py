@@ -96,6 +96,14 @@ class Queries(ctypes.Structure):
 _pack_queries = struct.Struct("PPPqqPi4x").pack   # a Queries as bytes
 
 
+class PageCopy(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_int32), ("dst", ctypes.c_int32), ("tokens", ctypes.c_int32)]
+
+
+class PagePool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("unit_tokens", ctypes.c_int64)]
+
+
 # symbol -> (restype, argtypes); the full C ABI of include/pkv.h
 _P, _I32, _I64, _U32P = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(ctypes.c_uint32)
 _I32P = ctypes.POINTER(ctypes.c_int32)
@@ -129,6 +137,9 @@ SIGNATURES = {
     "pkv_pool_create": (ctypes.c_int, [_I32P, _I32, _I32, ctypes.POINTER(ctypes.c_void_p)]),
     "pkv_pool_reserve": (ctypes.c_int, [_P, _I32P, _I32P, _I32, _I32, _I32, _I32P, _I32P]),
     "pkv_pool_release": (ctypes.c_int, [_P, _I32P, _I32]),
+    "pkv_pool_fork": (ctypes.c_int, [_P, _I32P, _I32, _I32P, _I32P, _I32, _I32, _I32, _I32P, _P, _I32P]),
+    "pkv_pool_compact": (ctypes.c_int, [_P, _I32P, _I32, _I32, _I32, _P, _I32, _I32P]),
+    "pkv_copy_pages": (ctypes.c_int, [_P, _I32, _P, _I32, _I32, _I32, _P]),
     "pkv_pool_free_count": (ctypes.c_int32, [_P]),
     "pkv_pool_destroy": (None, [_P]),
     "pkv_decode_static": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, ctypes.POINTER(Geom), _I32, _I32, _P, _P, _P]),
@@ -624,6 +635,51 @@ def extend_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, pl
             seq_lens, plan, out, lse, cu_tokens, stream)
 
 
+def copy_pages(pools, copies, page_size: int, stream=None):
+    """pkv_copy_pages: for every (source page, target page, tokens) of `copies` (int32 [n][3], as Pool.fork and
+    Pool.compact return it) the first tokens of the target become the source's, in every pool: contiguous tensors
+    [num_pages][page_size // u][...] on the current device, one entry for u tokens (1 for keys and values, Q8_BLOCK for
+    scales)."""
+    import torch
+    if isinstance(copies, np.ndarray) and copies.dtype == np.int32 and copies.flags.c_contiguous:
+        list_ = copies
+    else:
+        list_ = np.asarray(copies)
+        if list_.size and (list_.dtype.kind not in "iu" or list_.min() < -2 ** 31 or list_.max() >= 2 ** 31):
+            raise TypeError("copies: 32-bit integers")
+        list_ = _i32(list_)
+    if list_.ndim != 2 or list_.shape[1] != 3:
+        if list_.size:
+            raise ValueError(f"copies: shape {list_.shape}, expected [n][3]")
+        list_ = np.zeros((0, 3), np.int32)
+    page_size = int(page_size)
+    dev, num_pages, known, flat = torch.cuda.current_device(), None, {}, []
+    for t in pools:
+        try:
+            if t.get_device() != dev or not t.is_contiguous():
+                raise TypeError("pools must be contiguous tensors on the current CUDA device")
+            kind = (t.shape, t.dtype)
+            sizes = known.get(kind)
+        except AttributeError:
+            raise TypeError("pools must be contiguous tensors on the current CUDA device") from None
+        if sizes is None:
+            n, entries = (t.shape + (0, 0))[:2]
+            if num_pages is None:
+                num_pages = n
+            if n != num_pages or n == 0 or entries == 0 or t.numel() == 0 or page_size <= 0 or page_size % entries:
+                raise ValueError(f"pools: shape {tuple(t.shape)}, expected [{num_pages}][{page_size} / tokens an entry][...]")
+            sizes = known[kind] = (t.numel() // n * t.element_size(), page_size // entries)
+        flat.append(t.data_ptr())
+        flat += sizes
+    if not flat:
+        return
+    rc = (_lib or load()).pkv_copy_pages(struct.pack("%dq" % len(flat), *flat), len(flat) // 3, list_.ctypes.data, len(list_),
+                                         num_pages, page_size,
+                                         _raw_stream(dev) if stream is None else _stream_handle(stream))
+    if rc:
+        _check(rc, "pkv_copy_pages")
+
+
 class Pool:
     """Host FIFO page pool (pkv_pool_*)."""
 
@@ -633,6 +689,7 @@ class Pool:
         _check(load().pkv_pool_create(_ptr_i32(pages), len(pages), int(num_pages), ctypes.byref(h)),
                "pkv_pool_create")
         self._h = h
+        self.num_pages = int(num_pages)
 
     def reserve(self, seq_lens, block_table: np.ndarray, page_size: int) -> np.ndarray:
         """Assigns pages in place in `block_table` (int32, C-contiguous); returns touched rows."""
@@ -649,6 +706,32 @@ class Pool:
     def release(self, pages):
         p = _i32(pages)
         _check(load().pkv_pool_release(self._h, _ptr_i32(p), len(p)), "pkv_pool_release")
+
+    def fork(self, src_table: np.ndarray, parents, lens, page_size: int):
+        """pkv_pool_fork: (table [n][max_pages] of the new rows, copies [n'][3] for copy_pages)."""
+        src = np.ascontiguousarray(src_table, dtype=np.int32)
+        rows, n = _i32(parents), _i32(lens)
+        if src.ndim != 2 or rows.shape != n.shape or rows.ndim != 1:
+            raise ValueError("src_table: [rows][max_pages]; parents and lens: one entry for each new row")
+        dst = np.full((len(rows), src.shape[1]), -1, np.int32)
+        copies = np.zeros((max(len(rows), 1), 3), np.int32)
+        count = ctypes.c_int32(0)
+        _check(load().pkv_pool_fork(self._h, _ptr_i32(src), src.shape[0], _ptr_i32(rows), _ptr_i32(n), len(rows),
+                                    src.shape[1], int(page_size), _ptr_i32(dst), copies.ctypes.data,
+                                    ctypes.byref(count)), "pkv_pool_fork")
+        return dst, copies[: count.value].copy()
+
+    def compact(self, block_table: np.ndarray, page_size: int) -> np.ndarray:
+        """pkv_pool_compact: rewrites `block_table` (int32, C-contiguous) in place; returns copies [n][3] for
+        copy_pages."""
+        if block_table.dtype != np.int32 or not block_table.flags.c_contiguous or block_table.ndim != 2:
+            raise TypeError("block_table must be a C-contiguous int32 array of rows")
+        copies = np.zeros((max(self.num_pages // 2, 1), 3), np.int32)
+        count = ctypes.c_int32(0)
+        _check(load().pkv_pool_compact(self._h, _ptr_i32(block_table), block_table.shape[0], block_table.shape[1],
+                                       int(page_size), copies.ctypes.data, len(copies), ctypes.byref(count)),
+               "pkv_pool_compact")
+        return copies[: count.value].copy()
 
     def free_count(self) -> int:
         return int(load().pkv_pool_free_count(self._h))
