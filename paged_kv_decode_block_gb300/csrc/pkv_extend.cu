@@ -40,12 +40,12 @@ struct Cfg {
     static constexpr int kStages = Q8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
     static constexpr int kCodes = Q8 ? (D == 128 ? 4 : 8) : 0;
     static constexpr int kThreads = Q8 ? 512 : 384;
-    // producer's warpgroup last: [0, 8) softmax; then bf16: 8 producer, 9 mma, 10 fixer;
-    // 8-bit: [8, 12) widening, 12 producer, 13 mma
+    // producer's warpgroup last: [0, 8) softmax; then bf16: 8 producer, 9 and 10 products, 11
+    // fixer; 8-bit: [8, 12) widening, 12 producer, 13 and 14 products
     static constexpr int kProducer = Q8 ? 12 : 8;
     static constexpr int kMma = kProducer + 1;
-    static constexpr int kFixer = Q8 ? -1 : 10;
-    static constexpr int kReaders = Q8 ? 13 : 10;             // warps that read the piece ring
+    static constexpr int kFixer = Q8 ? -1 : 11;
+    static constexpr int kReaders = Q8 ? 14 : 11;             // warps that read the piece ring
     static constexpr size_t kBytes = static_cast<size_t>(kQ) + kStages * kTile + kCodes * kCode;
 };
 
@@ -66,7 +66,8 @@ struct Ctl {
     uint64_t code_full[8], code_empty[8];          // blocks in e4m3
     uint64_t scale_full[kScaleRing];
     uint64_t q_full, q_empty, drain;
-    uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], pair_full, turn[2];
+    float2 pair_ml[128];                           // the second group's reference and sum, of shared rows
     uint64_t piece_full[kPieceRing], piece_empty[kPieceRing];
     Piece piece[kPieceRing];
     float scales[kScaleRing][16];                  // 8 of K, 8 of V
@@ -243,96 +244,136 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
 
 // ------------------------------------------------------------------ matrix products
 
-// Blocks [lo, hi) that group g of the piece works on: those up to its last token.
-__device__ __forceinline__ int group_blocks(const Piece& pi, int g, int per) {
+// How group g shares in a piece of nb blocks.  Two groups of rows take every block
+// up to the last that their own tokens see.  A tile whose rows all fit the first
+// group is shared by blocks instead: the first group takes the even ones, the second
+// the odd ones of the same rows, and their states are joined at the end, so that a
+// short chunk's chain of product, softmax, product runs twice side by side.
+struct Share {
+    int nb;      // the piece's blocks
+    int count;   // this group's
+    bool pair;
+    int g;
+    __device__ __forceinline__ int block(int i) const { return pair ? 2 * i + g : i; }
+    __device__ __forceinline__ bool mine(int j) const { return pair ? (j & 1) == g : j < count; }
+    __device__ __forceinline__ bool last(int j) const { return pair ? j + 2 >= nb : j + 1 == count; }
+};
+__device__ __forceinline__ Share share_of(const Piece& pi, int g, int per) {
+    Share s;
+    s.g = g;
+    s.nb = pi.bad || pi.ntok == 0 ? 0 : pi.hi - pi.lo;
+    s.pair = s.nb > 1 && pi.ntok <= per;
     const int last = min(pi.ntok, (g + 1) * per) - 1;
-    if (last < g * per || pi.bad) return 0;
-    return max(0, min(pi.hi, (pi.limit0 + last + kExtBlock - 1) / kExtBlock) - pi.lo);
+    if (s.pair)
+        s.count = (s.nb + 1 - g) / 2;
+    else
+        s.count = s.nb == 0 || last < g * per ? 0 : max(0, min(pi.hi, (pi.limit0 + last + kExtBlock - 1) / kExtBlock) - pi.lo);
+    return s;
 }
 // The first block with places that some row of the tile does not see.
 __device__ __forceinline__ int first_masked(const Piece& pi) { return pi.limit0 / kExtBlock; }
 
+// One thread for each group: the products are asynchronous, and a thread's waits
+// hide behind the other's products.  PV(j) goes before QK(j + 1), which overwrites
+// its weights.  Where both groups have rows the threads take turns, a block each:
+// left alone their products mix, both groups' scores come at the same time, and the
+// tensor core rests while both are at their softmax.  Both threads give every block
+// back, used or not.
 template <int D, bool Q8>
-__device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t* smem) {
+__device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t* smem, const int g) {
     using C = Cfg<D, Q8>;
-    const bool lead = (threadIdx.x & 31) == 0;
-    const uint32_t q_smem = smem_addr(smem), kv_smem = q_smem + C::kQ, tmem = c->tmem;
     const int per = kExtRows / 2 / p.G;
     constexpr uint32_t kIdQk = umma_idesc(kExtBlock, false), kIdPv = umma_idesc(D, true);
-    uint32_t n = 0, fixed_phase = 0, q_loads = 0, done[2] = {0, 0}, outs[2] = {0, 0};
+    const uint32_t tS = c->tmem + g * 128, tO = tS + 256;
+    // descriptors count in 16 bytes: what is added to them never carries out of the address
+    const uint64_t q_first = umma_desc(smem_addr(smem), 16), k_desc = umma_desc(smem_addr(smem) + C::kQ, 16),
+                   v_desc = umma_desc(smem_addr(smem) + C::kQ, 16384);
+    uint32_t fixed_phase = 0, q_loads = 0, done = 0, outs = 0, turns = 0;
+    uint32_t st = 0, phase = 0;   // the ring's next block and its parity
 
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, p.status, &c->abort); };
-    auto qk = [&](int g, int st) {   // S_g = Q_g K^T
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_until(bar, parity, p.status, &c->abort); };
+    auto advance = [&]() {
+        if (++st == C::kStages) st = 0, phase ^= 1;
+    };
+    auto qk = [&](uint64_t q_desc, uint32_t at) {   // S = Q K^T
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-            umma_ss(tmem + g * 128, umma_desc(q_smem + g * (C::kQ / 2) + off, 16), umma_desc(kv_smem + st * C::kTile + off, 16),
-                    kIdQk, k > 0);
+            const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) / 16;
+            umma_ss(tS, q_desc + off, k_desc + at * (C::kTile / 16) + off, kIdQk, k > 0);
         }
         umma_commit(&c->s_full[g]);
     };
-    auto pv = [&](int g, int st, bool add) {   // O_g (+)= P_g V
+    auto pv = [&](uint32_t at, bool add) {   // O (+)= P V
 #pragma unroll
         for (int k = 0; k < kExtBlock / 16; ++k)
-            umma_ts(tmem + 256 + g * 128, tmem + g * 128 + k * 8, umma_desc(kv_smem + st * C::kTile + k * 2048, 16384), kIdPv,
-                    add || k > 0);
+            umma_ts(tO, tS + k * 8, v_desc + at * (C::kTile / 16) + k * (2048 / 16), kIdPv, add || k > 0);
     };
     for (uint32_t pc = 0;; ++pc) {
         const int slot = pc % kPieceRing;
         if (!wait(&c->piece_full[slot], (pc / kPieceRing) & 1)) return;
         const Piece& pi = c->piece[slot];
-        const int nb = pi.bad ? 0 : pi.hi - pi.lo, ntok = pi.ntok, lo = pi.lo;
-        const int e[2] = {group_blocks(pi, 0, per), group_blocks(pi, 1, per)};
-        const int masked = Q8 ? 1 << 30 : first_masked(pi);
-        __syncwarp();
-        if (lead) mbar_arrive(&c->piece_empty[slot]);
+        const Share sh = share_of(pi, g, per);
+        const int nb = sh.nb, ntok = pi.ntok;
+        const int masked = Q8 ? 1 << 30 : first_masked(pi) - pi.lo;
+        mbar_arrive(&c->piece_empty[slot]);
         if (ntok == 0) return;
         if (nb == 0) continue;
+        const uint64_t q_desc = q_first + (sh.pair ? 0 : g * (C::kQ / 2 / 16));
 
         if (!wait(&c->q_full, q_loads++ & 1)) return;
-        if (!wait(&c->full[n % C::kStages], (n / C::kStages) & 1)) return;
-        tc_fence_after();
-        if (lead) {
-            for (int g = 0; g < 2; ++g)
-                if (e[g] > 0) qk(g, n % C::kStages);
-            umma_commit(&c->empty[n % C::kStages]);
-            if (nb == 1) umma_commit(&c->q_empty);
+        if (!wait(&c->full[st], phase)) return;
+        const bool turn = !sh.pair && ntok > per;   // (both threads find the same)
+        if (turn && (g == 1 || turns > 0) && !wait(&c->turn[g], (g == 1 ? turns : turns - 1) & 1)) return;
+        if (sh.count > 0 && sh.mine(0)) {
+            tc_fence_after();
+            qk(q_desc, st);
         }
-        __syncwarp();
-        for (int j = 0; j < nb; ++j, n += 2) {
-            const uint32_t vs = (n + 1) % C::kStages, ks = (n + 2) % C::kStages;
-            if (lo + j >= masked) {
+        if (turn) {
+            mbar_arrive(&c->turn[1 - g]);
+            ++turns;
+        }
+        umma_commit(&c->empty[st]);
+        if (nb == 1) umma_commit(&c->q_empty);
+        advance();
+        bool add = false;
+        for (int j = 0; j < nb; ++j) {
+            const uint32_t vs = st;
+            if (j >= masked) {
                 if (!wait(&c->fixed[vs], (fixed_phase >> vs) & 1)) return;
                 fixed_phase ^= 1u << vs;
-            } else if (!wait(&c->full[vs], ((n + 1) / C::kStages) & 1)) {
+            } else if (!wait(&c->full[vs], phase)) {
                 return;
             }
-            for (int g = 0; g < 2; ++g) {
-                if (j < e[g]) {
-                    if (j == 0 && outs[g] > 0 && !wait(&c->o_empty[g], (outs[g] - 1) & 1)) return;
-                    if (!wait(&c->p_full[g], done[g] & 1)) return;
-                    ++done[g];
-                    tc_fence_after();
-                    if (lead) {
-                        pv(g, vs, j > 0);
-                        if (j + 1 == e[g]) umma_commit(&c->o_full[g]);
-                    }
-                    if (j + 1 == e[g]) ++outs[g];
-                    __syncwarp();
-                }
-                if (g == 1 && lead) umma_commit(&c->empty[vs]);
-                if (g == 0 && j + 1 < nb && !wait(&c->full[ks], ((n + 2) / C::kStages) & 1)) return;
-                if (j + 1 < e[g]) {
-                    tc_fence_after();
-                    if (lead) qk(g, ks);
-                }
-                __syncwarp();
+            advance();
+            if (j + 1 < nb && !wait(&c->full[st], phase)) return;
+            if (sh.mine(j)) {
+                if (!add && outs > 0 && !wait(&c->o_empty[g], (outs - 1) & 1)) return;
+                if (!wait(&c->p_full[g], done++ & 1)) return;
             }
-            if (j + 1 < nb && lead) {
-                umma_commit(&c->empty[ks]);
+            if (turn && !wait(&c->turn[g], (g == 1 ? turns : turns - 1) & 1)) return;
+            if (sh.mine(j)) {
+                tc_fence_after();
+                pv(vs, add);
+                add = true;
+                if (sh.last(j)) {
+                    umma_commit(&c->o_full[g]);
+                    ++outs;
+                }
+            }
+            if (j + 1 < nb && sh.mine(j + 1)) {
+                tc_fence_after();
+                qk(q_desc, st);
+            }
+            if (turn) {
+                mbar_arrive(&c->turn[1 - g]);
+                ++turns;
+            }
+            umma_commit(&c->empty[vs]);
+            if (j + 1 < nb) {
+                umma_commit(&c->empty[st]);
                 if (j + 2 == nb) umma_commit(&c->q_empty);
+                advance();
             }
-            __syncwarp();
         }
     }
 }
@@ -401,7 +442,8 @@ __device__ __forceinline__ void fix_values(const ExtendParams& p, Ctl* c, uint8_
 // ------------------------------------------------------------------ e4m3 to bf16
 
 // Codes become bf16 exactly (4 bits of significand into 8); their scales join the
-// scores and the weights in fp32.  In blocks with masked places NaN codes become 0
+// scores and the weights in fp32.  In integers and one product for two codes: the
+// conversion instruction is slow and shares its unit with ex2.  In blocks with masked places NaN codes become 0
 // as infinities and NaN do in fix_values.
 template <int D>
 __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* smem) {
@@ -431,25 +473,28 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
                 for (int row = tid / kPerRow; row < kExtBlock; row += 128 / kPerRow) {
                     uint32_t v[4], o[8];
                     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(src + row * D + chunk * 16) : "memory");
-                    if (clean) {
-                        if (row >= valid) v[0] = v[1] = v[2] = v[3] = 0;
+                    if (clean && row >= valid) v[0] = v[1] = v[2] = v[3] = 0;
+                    // (s eeee mmm) to the bits of a bf16 2^120 times smaller, times 2^120; a NaN code (all ones) would
+                    // come out as 480
+                    uint32_t nan = 0;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 4; ++k) nan |= (v[k] & 0x7f7f7f7fu) + 0x01010101u;
+                    nan &= 0x80808080u;
+                    if (nan && clean) {
+                        odd = 1;
 #pragma unroll
-                            for (int b = 0; b < 32; b += 8)
-                                if ((v[k] >> b & 0x7fu) == 0x7fu) {
-                                    v[k] &= ~(0xffu << b);
-                                    odd = 1;
-                                }
+                        for (int k = 0; k < 4; ++k) v[k] &= ~((((v[k] & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u) * 0xffu);
                     }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint16_t two = static_cast<uint16_t>(v[k / 2] >> (16 * (k & 1)));
-                        uint32_t h;
-                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-                        float lo_f, hi_f;
-                        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(lo_f), "=f"(hi_f) : "r"(h));
-                        o[k] = bf16x2(lo_f, hi_f);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t high = (v[k] & 0x80808080u) | (v[k] >> 4 & 0x07070707u), low = v[k] << 4 & 0xf0f0f0f0u;
+                        o[2 * k] = bf16x2_mul(__byte_perm(low, high, 0x5140), 0x7b807b80u);
+                        o[2 * k + 1] = bf16x2_mul(__byte_perm(low, high, 0x7362), 0x7b807b80u);
+                    }
+                    if (nan && !clean) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if ((v[k / 4] >> (k % 4 * 8) & 0x7fu) == 0x7fu) o[k / 2] |= 0x7fffu << (k % 2 * 16);
                     }
                     const uint32_t first = (chunk % 4) * 2 + swap, at = dst + row * 128;
                     const uint32_t a0 = at + ((first ^ (row & 7)) << 4), a1 = at + (((first ^ 1) ^ (row & 7)) << 4);
@@ -478,28 +523,6 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
 
 // ------------------------------------------------------------------ softmax and outputs
 
-// What fix_values took out of V and this row sees, added to 32 columns of its
-// output: an infinity or NaN of its own value.  Rare, so read from the pages again.
-template <int D, bool Q8>
-__device__ __noinline__ void add_nonfinite(const ExtendParams& p, const int32_t* row, int kvh, int t0, int t1, int col,
-                                           uint32_t* o) {
-    for (int t = t0; t < t1; ++t) {
-        const int page = row[t / p.page_size];
-        if (page < 0 || page >= p.num_pages) continue;
-        const size_t at = ((static_cast<size_t>(page) * p.page_size + t % p.page_size) * p.Hkv + kvh) * D + col;
-        for (int d = 0; d < 32; ++d) {
-            float v;
-            if (Q8) {
-                const uint8_t code = static_cast<const uint8_t*>(p.v_pages)[at + d];
-                v = (code & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.0f;
-            } else {
-                v = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p.v_pages)[at + d]) << 16);
-            }
-            if (!(fabsf(v) <= 3.4e38f)) o[d] = __float_as_uint(__uint_as_float(o[d]) + v);
-        }
-    }
-}
-
 // Where a row's results go: out / lse, or the state in a workspace slot.
 struct RowOut {
     uint16_t* out;     // null: a workspace slot
@@ -520,6 +543,33 @@ __device__ __forceinline__ RowOut row_out(const ExtendParams& p, const Piece& pi
     }
     return o;
 }
+// What fix_values took out of V and this row sees, tokens [t0, t1), is added to what
+// the row has written: an infinity or NaN of its own value.  Rare, so V is read from
+// the pages again.
+template <int D, bool Q8>
+__device__ __noinline__ void add_nonfinite(const ExtendParams& p, const int32_t* row, int kvh, int t0, int t1, RowOut o) {
+    for (int t = t0; t < t1; ++t) {
+        const int page = row[t / p.page_size];
+        if (page < 0 || page >= p.num_pages) continue;
+        const size_t at = ((static_cast<size_t>(page) * p.page_size + t % p.page_size) * p.Hkv + kvh) * D;
+        for (int d = 0; d < D; ++d) {
+            float v;
+            if (Q8) {
+                const uint8_t code = static_cast<const uint8_t*>(p.v_pages)[at + d];
+                v = (code & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.0f;
+            } else {
+                v = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p.v_pages)[at + d]) << 16);
+            }
+            if (fabsf(v) <= 3.4e38f) continue;
+            if (o.out) {
+                const float x = __uint_as_float(static_cast<uint32_t>(o.out[d]) << 16) + v;
+                o.out[d] = static_cast<uint16_t>(bf16x2(x, 0.0f));
+            } else {
+                reinterpret_cast<float*>(o.ws + static_cast<size_t>(d / 4) * kExtRows)[d % 4] += v;
+            }
+        }
+    }
+}
 __device__ __forceinline__ void write_nan(const RowOut& o, int D) {
     if (o.out) {
         for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(o.out + d) = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
@@ -529,7 +579,141 @@ __device__ __forceinline__ void write_nan(const RowOut& o, int D) {
     }
 }
 
-// One block of scores: maximum, weights, sum.  `s` holds the row's 128 scores.
+// Scores above the running reference m by more than 2^8 move it: the sum and the
+// output follow (the block's product has not begun, and the one before is done, as
+// this block's scores came after it).
+template <int D>
+__device__ __forceinline__ void follow_maximum(float top, bool first, uint32_t tO, float& m, float& l) {
+    if (first) {
+        m = top;
+    } else if (__any_sync(kFull, top > m + kMoveAt)) {
+        const float to = fmaxf(m, top);
+        const float f = to == -INFINITY ? 1.0f : ex2(m - to);
+        l *= f;
+        m = to;
+#pragma unroll
+        for (int k = 0; k < D; k += 32) {
+            uint32_t o[32];
+            tmem_ld32(o, tO + k);
+            tmem_wait_ld();
+            tmem_loaded32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(tO + k, o);
+        }
+    }
+}
+
+// One block of a row's scores to weights: maximum, 2^(c s - m), sum; weights in
+// bf16 over the scores.  Scores stay in registers between the two passes (bf16
+// cache), or are read again where their scales and the widening warps leave fewer
+// registers to a thread (8-bit cache).
+template <int D, bool Q8>
+__device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float cs, const float* scales, bool cut, int seen,
+                                              bool first, float& m, float& l) {
+    uint64_t sum[2] = {0, 0};
+    if constexpr (!Q8) {
+        uint32_t s[128];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld32(s + 32 * k, tS + 32 * k);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_loaded32(s + 32 * k);
+        if (cut) {
+            const int all = __shfl_sync(kFull, seen, 0);   // columns that every row of the warp sees
+#pragma unroll
+            for (int k = 0; k < 128; k += 16) {
+                if (k + 16 <= all) continue;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[k + i] = k + i < seen ? s[k + i] : 0xff800000u;
+            }
+        }
+        float mx[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 4]));
+#pragma unroll
+        for (int k = 8; k < 128; k += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(s[k + i]), __uint_as_float(s[k + 4 + i]));
+        follow_maximum<D>(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs, first, tO, m, l);
+        const float ref = m == -INFINITY ? 0.0f : -m;
+        const uint64_t ref2 = pack2(ref, ref), cs2 = pack2(cs, cs);
+#pragma unroll
+        for (int k = 0; k < 128; k += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const F2 e = unpack2(fma2(pack2(__uint_as_float(s[k + i]), __uint_as_float(s[k + i + 1])), cs2, ref2));
+                const float a = ex2(e.x), b = ex2(e.y);
+                sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(a, b));
+                w[i / 2] = bf16x2(a, b);
+            }
+            tmem_st16(tS + k / 2, w);
+        }
+    } else {
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 128; k += 64) {
+            uint32_t s[64];
+            tmem_ld32(s, tS + k);
+            tmem_ld32(s + 32, tS + k + 32);
+            tmem_wait_ld();
+            tmem_loaded32(s);
+            tmem_loaded32(s + 32);
+            if (cut) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) s[i] = k + i < seen ? s[i] : 0xff800000u;
+            }
+#pragma unroll
+            for (int i = 0; i < 64; i += 16) {   // 16 scores of one scale
+                const float ks = scales[(k + i) / 16] * cs;
+                const float* x = reinterpret_cast<const float*>(s + i);
+                float t = max3(x[0], x[1], x[2]), u = max3(x[3], x[4], x[5]);
+                t = max3(t, x[6], x[7]), u = max3(u, x[8], x[9]);
+                t = max3(t, x[10], x[11]), u = max3(u, x[12], x[13]);
+                t = fmaxf(max3(t, x[14], x[15]), u);
+                if (!(ks >= 0.0f)) {   // a scale below 0 turns them round
+                    t = INFINITY;
+#pragma unroll
+                    for (int h = 0; h < 16; ++h) t = k + i + h < seen || !cut ? fminf(t, x[h]) : t;
+                }
+                t *= ks;
+                if (cut && k + i >= seen) t = -INFINITY;
+                top = fmaxf(top, t);
+            }
+        }
+        follow_maximum<D>(top, first, tO, m, l);
+        const float ref = m == -INFINITY ? 0.0f : -m;
+        const uint64_t ref2 = pack2(ref, ref);
+#pragma unroll
+        for (int k = 0; k < 128; k += 32) {
+            uint32_t s[32], w[16];
+            tmem_ld32(s, tS + k);
+            tmem_wait_ld();
+            tmem_loaded32(s);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const int group = (k + i) / 16;
+                const float ks = scales[group] * cs;
+                // a weight of 0 stays 0 whatever the scale of a block that the row does not see
+                const float vs = cut && 16 * group >= seen ? 0.0f : scales[8 + group];
+                F2 e = unpack2(fma2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), pack2(ks, ks), ref2));
+                if (cut) {
+                    if (k + i >= seen) e.x = -INFINITY;
+                    if (k + i + 1 >= seen) e.y = -INFINITY;
+                }
+                const float a = ex2(e.x), b = ex2(e.y);
+                sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(a, b));
+                const F2 y = unpack2(mul2(pack2(a, b), pack2(vs, vs)));
+                w[i / 2] = bf16x2(y.x, y.y);
+            }
+            tmem_st16(tS + k / 2, w);
+        }
+    }
+    const F2 a = unpack2(add2(sum[0], sum[1]));
+    l += a.x + a.y;
+}
+
 template <int D, bool Q8>
 __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
     using C = Cfg<D, Q8>;
@@ -537,8 +721,7 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
     const int shift = 31 - __clz(p.G), per = kExtRows / 2 >> shift;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
     const uint32_t tS = c->tmem + lanes + g * 128, tO = c->tmem + lanes + 256 + g * 128;
-    const float cs = p.scale_log2;
-    uint32_t done = 0, outs = 0, blocks = 0;
+    uint32_t done = 0, outs = 0, blocks = 0, pairs = 0;
     for (uint32_t pc = 0;; ++pc) {
         const int slot = pc % kPieceRing;
         if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, p.status, &c->abort)) return false;
@@ -546,8 +729,9 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
         if (pi.ntok == 0) {
             return true;
         }
-        const int nb = group_blocks(pi, g, per), lo = pi.lo;
-        const int base_row = g * 128;
+        const Share sh = share_of(pi, g, per);
+        const int nb = sh.count, lo = pi.lo;
+        const int base_row = sh.pair ? 0 : g * 128;
         const bool live = base_row + row < pi.ntok << shift;                // this thread's row exists
         const bool warp_live = base_row + (row & ~31) < pi.ntok << shift;   // some row of the warp does
         const int limit = pi.limit0 + ((base_row + row) >> shift);          // tokens that the row sees
@@ -558,100 +742,51 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
             ++done;
             tc_fence_after();
             if (warp_live) {
-                uint32_t s[128];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_ld32(s + 32 * k, tS + 32 * k);
-                float vs[8];
+                const int at = lo + sh.block(j);
+                const int seen = limit - at * kExtBlock;   // columns of the block that the row sees
+                const bool cut = at >= masked;
+                const float* scales = nullptr;
                 if (Q8) {
-                    const uint32_t b = blocks + j;
+                    const uint32_t b = blocks + sh.block(j);
                     if (!wait_warp(&c->scale_full[b % kScaleRing], (b / kScaleRing) & 1, p.status, &c->abort)) return false;
-                    float ks[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        ks[k] = c->scales[b % kScaleRing][k] * cs;
-                        vs[k] = c->scales[b % kScaleRing][8 + k];
-                    }
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) tmem_loaded32(s + 32 * k);
-#pragma unroll
-                    for (int k = 0; k < 128; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * ks[k / 16]);
-                } else {
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) tmem_loaded32(s + 32 * k);
+                    scales = c->scales[b % kScaleRing];
                 }
-                const int seen = limit - (lo + j) * kExtBlock;   // columns of the block that the row sees
-                const bool cut = lo + j >= masked;
-                if (cut) {
-#pragma unroll
-                    for (int k = 0; k < 128; ++k) s[k] = k < seen ? s[k] : 0xff800000u;
-                }
-                float mx[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 4]));
-#pragma unroll
-                for (int k = 8; k < 128; k += 8)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(s[k + i])), __uint_as_float(s[k + 4 + i]));
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                if (!Q8) top *= cs;
-                if (j == 0) {
-                    m = top;
-                } else if (__any_sync(kFull, top > m + kMoveAt)) {
-                    // the block's product has not begun, the one before is done (its S came after it)
-                    const float to = fmaxf(m, top);
-                    const float f = to == -INFINITY ? 1.0f : ex2(m - to);
-                    l *= f;
-                    m = to;
-#pragma unroll
-                    for (int k = 0; k < D; k += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(o, tO + k);
-                        tmem_wait_ld();
-                        tmem_loaded32(o);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st32(tO + k, o);
-                    }
-                }
-                const float ref = m == -INFINITY ? 0.0f : -m;
-                const uint64_t ref2 = pack2(ref, ref), cs2 = pack2(cs, cs);
-                uint64_t sum[2] = {0, 0};
-#pragma unroll
-                for (int k = 0; k < 128; k += 32) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const uint64_t x = pack2(__uint_as_float(s[k + i]), __uint_as_float(s[k + i + 1]));
-                        const F2 e = unpack2(Q8 ? add2(x, ref2) : fma2(x, cs2, ref2));
-                        const float a = ex2(e.x), b = ex2(e.y);
-                        sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(a, b));
-                        if (Q8) {
-                            const float v = vs[(k + i) / 16];
-                            // (a masked weight stays 0 whatever its scale)
-                            w[i / 2] = bf16x2(cut && k + i >= seen ? 0.0f : a * v, cut && k + i + 1 >= seen ? 0.0f : b * v);
-                        } else {
-                            w[i / 2] = bf16x2(a, b);
-                        }
-                    }
-                    tmem_st16(tS + k / 2, w);
-                }
-                const F2 a = unpack2(add2(sum[0], sum[1]));
-                l += a.x + a.y;
+                softmax_block<D, Q8>(tS, tO, p.scale_log2, scales, cut, seen, j == 0, m, l);
                 tmem_wait_st();
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->p_full[g]);
         }
-        blocks += pi.bad ? 0 : pi.hi - pi.lo;
+        blocks += sh.nb;
 
         // outputs
         if (nb > 0) {
             if (!wait_warp(&c->o_full[g], outs & 1, p.status, &c->abort)) return false;
             ++outs;
             tc_fence_after();
+        }
+        float f0 = 1.0f, f1 = 0.0f;   // the two groups' parts of shared rows
+        if (sh.pair) {
+            if (g == 1) {
+                c->pair_ml[row] = make_float2(m, l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&c->pair_full);
+                    mbar_arrive(&c->piece_empty[slot]);
+                }
+                continue;
+            }
+            if (!wait_warp(&c->pair_full, pairs & 1, p.status, &c->abort)) return false;
+            ++pairs;
+            tc_fence_after();
+            const float2 other = c->pair_ml[row];
+            const float to = fmaxf(m, other.x), ref = to == -INFINITY ? 0.0f : to;
+            f0 = ex2(m - ref);
+            f1 = ex2(other.x - ref);
+            l = l * f0 + other.y * f1;
+            m = to;
         }
         const bool poison = pi.bad || pi.poison;
         if (warp_live) {
@@ -662,17 +797,23 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
             } else if (nb == 0) {
                 if (live) *o.ml = make_float2(-INFINITY, 0.0f);   // (only a part of a tile can have nothing to see)
             } else {
-                const bool odd = pi.nonfinite && live;
-#pragma unroll 1
+#pragma unroll 2
                 for (int k = 0; k < D; k += 32) {
                     uint32_t x[32];
                     tmem_ld32(x, tO + k);
-                    tmem_wait_ld();
-                    tmem_loaded32(x);
-                    if (odd)
-                        add_nonfinite<D, Q8>(p, p.block_table + static_cast<size_t>(pi.b) * p.max_pages, pi.kvh,
-                                             max(lo, masked) * kExtBlock, min(limit, pi.hi * kExtBlock), k, x);
-                    __syncwarp();
+                    if (sh.pair) {
+                        uint32_t y[32];
+                        tmem_ld32(y, tO + 128 + k);
+                        tmem_wait_ld();
+                        tmem_loaded32(x);
+                        tmem_loaded32(y);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            x[i] = __float_as_uint(__uint_as_float(x[i]) * f0 + __uint_as_float(y[i]) * f1);
+                    } else {
+                        tmem_wait_ld();
+                        tmem_loaded32(x);
+                    }
                     if (live && o.out) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 8) {
@@ -690,6 +831,9 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
                     }
                     __syncwarp();
                 }
+                if (pi.nonfinite && live)
+                    add_nonfinite<D, Q8>(p, p.block_table + static_cast<size_t>(pi.b) * p.max_pages, pi.kvh,
+                                         max(lo, masked) * kExtBlock, min(limit, pi.hi * kExtBlock), o);
                 if (live && o.out && o.lse) *o.lse = kLn2 * (m + log2f(l));
                 if (live && !o.out) *o.ml = make_float2(m, l);
             }
@@ -698,6 +842,7 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
         __syncwarp();
         if (lane == 0) {
             if (nb > 0) mbar_arrive(&c->o_empty[g]);
+            if (sh.pair) mbar_arrive(&c->o_empty[1]);
             mbar_arrive(&c->piece_empty[slot]);
         }
     }
@@ -710,14 +855,13 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
 extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CUtensorMap qmap,
               const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using C = Cfg<D, Q8>;
-    extern __shared__ uint8_t dyn[];
-    uint8_t* smem = dyn + ((1024 - (smem_addr(dyn) & 1023)) & 1023);
+    extern __shared__ __align__(1024) uint8_t smem[];   // (the swizzle counts from 1024-byte boundaries)
     Ctl* c = reinterpret_cast<Ctl*>(smem + C::kBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&c->full[i], Q8 ? 4 : 1);
-            mbar_init(&c->empty[i], 1);
+            mbar_init(&c->empty[i], 2);
             mbar_init(&c->fixed[i], 1);
         }
         for (int i = 0; i < C::kCodes; ++i) {
@@ -726,13 +870,15 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
         }
         for (int i = 0; i < kScaleRing; ++i) mbar_init(&c->scale_full[i], 1);
         mbar_init(&c->q_full, 1);
-        mbar_init(&c->q_empty, 1);
-        mbar_init(&c->drain, 1);
+        mbar_init(&c->q_empty, 2);
+        mbar_init(&c->drain, 2);
+        mbar_init(&c->pair_full, 4);
         for (int g = 0; g < 2; ++g) {
             mbar_init(&c->s_full[g], 1);
             mbar_init(&c->p_full[g], 4);
             mbar_init(&c->o_full[g], 1);
             mbar_init(&c->o_empty[g], 4);
+            mbar_init(&c->turn[g], 1);
         }
         for (int i = 0; i < kPieceRing; ++i) {
             mbar_init(&c->piece_full[i], 1);
@@ -756,10 +902,11 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
             atomicOr(p.status, static_cast<uint32_t>(PKV_DEV_PLAN_MISMATCH));
     }
     int64_t before = block_scan<C::kThreads>(c, local, &W);
-    const int parts = ext_parts(W, gridDim.x), cta = blockIdx.x;
-    const bool work = W > 0 && cta < parts;
+    const int cta = blockIdx.x;
+    const ExtParts parts = ext_parts(W, gridDim.x);
+    const bool work = W > 0 && cta < parts.parts;
     if (work) {
-        const int64_t first = ext_part_begin(W, parts, cta);
+        const int64_t first = parts.begin(cta);
         if (p.B <= C::kThreads) {
             if (first >= before && first < before + local) c->row0 = tid, c->row_unit = before;
         } else {
@@ -781,13 +928,13 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
     if (work) {
         if (warp < 8) {
             if constexpr (Q8)
-                asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+                asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
             else
                 asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
             if (!attend<D, Q8>(p, c)) {
                 // a wait ran out: everything that this CTA was to write is NaN
                 ExtWalk w;
-                w.begin(W, parts, cta, p.B, p.Hkv, rows.tt, c->row0, c->row_unit, rows);
+                w.begin(parts, cta, p.B, p.Hkv, rows.tt, c->row0, c->row_unit, rows);
                 ExtPiece e;
                 while (w.next(e, rows)) {
                     const ExtRow r = rows(e.b);
@@ -802,28 +949,30 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
             }
         } else if (Q8 && warp < 12) {
             if constexpr (Q8) {
-                asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+                asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
                 widen<D>(p, c, smem);
             }
         } else {
             if constexpr (Q8)
-                asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+                asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
             else
                 asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
             if (warp == C::kProducer) {
                 ExtWalk w;
-                w.begin(W, parts, cta, p.B, p.Hkv, rows.tt, c->row0, c->row_unit, rows);
+                w.begin(parts, cta, p.B, p.Hkv, rows.tt, c->row0, c->row_unit, rows);
                 uint64_t policy;
                 asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
                 produce<D, Q8>(p, c, smem, &qmap, &kmap, &vmap, w, rows, policy);
-            } else if (warp == C::kMma) {
-                multiply<D, Q8>(p, c, smem);
+            } else if (warp == C::kMma || warp == C::kMma + 1) {
+                if (lane == 0) multiply<D, Q8>(p, c, smem, warp - C::kMma);
+                __syncwarp();
             } else if (warp == C::kFixer) {
                 if constexpr (!Q8) fix_values<D>(p, c, smem);
             }
         }
     }
     __syncthreads();
+    if (c->abort && warp == C::kMma + 1 && lane == 0) umma_commit(&c->drain);
     if (c->abort && warp == C::kMma) {   // products and copies in flight land before the memory goes
         if (lane == 0) {
             umma_commit(&c->drain);
@@ -893,7 +1042,7 @@ __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant
 template <int D, bool Q8>
 cudaError_t launch(const ExtendParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                    int ctas, cudaStream_t stream) {
-    constexpr size_t kSmem = Cfg<D, Q8>::kBytes + 1024 + sizeof(Ctl);
+    constexpr size_t kSmem = Cfg<D, Q8>::kBytes + sizeof(Ctl);
     static_assert(kSmem <= 232448, "shared memory of a CTA");
     // (on every call, as a device reset drops it)
     cudaError_t e = cudaFuncSetAttribute(extend_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);

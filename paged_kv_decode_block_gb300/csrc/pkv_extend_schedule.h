@@ -25,6 +25,7 @@
 namespace pkv {
 
 constexpr int kExtBlock = 128;      // tokens of a KV block
+constexpr int kExtBlockLog2 = 7;
 constexpr int kExtRows = 256;       // rows of scores of a tile: two groups of 128
 constexpr int kTileUnits = 1;       // units of a tile besides its blocks
 constexpr int kMinShareUnits = 2;   // a CTA takes at least this much (fewer CTAs work otherwise)
@@ -38,26 +39,29 @@ struct ExtRow {
     int64_t units;   // units of one KV head
 };
 
+// (tokens are counted without a sign where they are divided: shifts, not divisions)
+PKV_HD uint32_t ext_blocks(uint32_t tokens) { return (tokens + (kExtBlock - 1)) >> kExtBlockLog2; }
+
 // Blocks of the first i tiles of a row whose new tokens begin at position ctx,
 // none of them its last: sum over k = 1..i of ceil((ctx + k * tt) / 128).
-PKV_HD int64_t ext_blocks_before(int64_t ctx, int tt, int64_t i) {
+PKV_HD int64_t ext_blocks_before(uint32_t ctx, int tt, uint32_t i) {
     if (tt >= kExtBlock) {
-        const int64_t s = tt / kExtBlock;
-        return i * ((ctx + kExtBlock - 1) / kExtBlock) + s * (i * (i + 1) / 2);
+        const uint64_t s = static_cast<uint32_t>(tt) >> kExtBlockLog2;
+        return static_cast<int64_t>(static_cast<uint64_t>(i) * ext_blocks(ctx) + s * ((static_cast<uint64_t>(i) * (i + 1)) >> 1));
     }
-    const int m = kExtBlock / tt;   // tiles of a block: k = m * a + r adds a to the r-th
-    int64_t sum = 0;
-    for (int r = 1; r <= m; ++r) {
-        const int64_t cnt = i >= r ? (i - r) / m + 1 : 0;
-        sum += cnt * ((ctx + r * tt + kExtBlock - 1) / kExtBlock) + cnt * (cnt - 1) / 2;
+    const uint32_t log2m = tt == 64 ? 1 : 2;   // 2^log2m tiles of a block: k = 2^log2m * a + r adds a to the r-th
+    uint64_t sum = 0;
+    for (uint32_t r = 1; r <= 1u << log2m; ++r) {
+        const uint64_t cnt = i >= r ? ((i - r) >> log2m) + 1 : 0;
+        sum += cnt * ext_blocks(ctx + r * tt) + ((cnt * (cnt - 1)) >> 1);
     }
-    return sum;
+    return static_cast<int64_t>(sum);
 }
 
 PKV_HD int32_t ext_tile_blocks(const ExtRow& r, int tt, int32_t i) {
     if (r.bad) return 1;
-    const int64_t upto = static_cast<int64_t>(r.len - r.n) + static_cast<int64_t>(i + 1) * tt;
-    return static_cast<int32_t>(((upto < r.len ? upto : r.len) + kExtBlock - 1) / kExtBlock);
+    const uint32_t upto = static_cast<uint32_t>(r.len - r.n) + static_cast<uint32_t>(i + 1) * tt, len = r.len;
+    return static_cast<int32_t>(ext_blocks(upto < len ? upto : len));
 }
 
 // Units of the tiles before tile i of one KV head.
@@ -74,7 +78,9 @@ PKV_HD ExtRow ext_row(int32_t lo, int32_t hi, int32_t len, int32_t T, int64_t ca
     r.len = len;
     r.n = lo >= 0 && hi <= T && hi > lo ? hi - lo : 0;
     r.bad = (r.n > 0 && (len < r.n || len > cap)) ? 1 : 0;
-    r.tiles = static_cast<int32_t>((static_cast<int64_t>(r.n) + tt - 1) / tt);
+    int shift = 8;   // tt = 2^shift, 32 to 256
+    while (1 << shift > tt) --shift;
+    r.tiles = static_cast<int32_t>((static_cast<uint32_t>(r.n) + tt - 1) >> shift);
     r.units = r.tiles == 0 ? 0
                            : ext_units_before(r, tt, r.tiles - 1) + ext_tile_blocks(r, tt, r.tiles - 1) + kTileUnits;
     return r;
@@ -93,18 +99,28 @@ PKV_HD int32_t ext_tile_at(const ExtRow& r, int tt, int64_t off) {
     return lo;
 }
 
-// CTAs that work on W units, and the first unit of part c of `parts`.
-PKV_HD int32_t ext_parts(int64_t W, int32_t ctas) {
+// W units in equal parts for at most `ctas` CTAs: the first `rest` parts have q + 1.
+struct ExtParts {
+    int64_t W, q;
+    int32_t parts, rest;
+    PKV_HD int64_t begin(int32_t c) const { return c * q + (c < rest ? c : rest); }
+    PKV_HD int32_t of(int64_t unit) const {
+        return static_cast<int32_t>(unit < rest * (q + 1) ? unit / (q + 1) : rest + (unit - rest * (q + 1)) / q);
+    }
+};
+PKV_HD ExtParts ext_parts(int64_t W, int32_t ctas) {
+    ExtParts p;
     const int64_t most = W / kMinShareUnits;
-    return static_cast<int32_t>(most < 1 ? 1 : (most < ctas ? most : ctas));
-}
-PKV_HD int64_t ext_part_begin(int64_t W, int32_t parts, int32_t c) {
-    const int64_t q = W / parts, rest = W % parts;
-    return c * q + (c < rest ? c : rest);
-}
-PKV_HD int32_t ext_part_of(int64_t W, int32_t parts, int64_t unit) {
-    const int64_t q = W / parts, rest = W % parts;
-    return static_cast<int32_t>(unit < rest * (q + 1) ? unit / (q + 1) : rest + (unit - rest * (q + 1)) / q);
+    p.W = W;
+    p.parts = static_cast<int32_t>(most < 1 ? 1 : (most < ctas ? most : ctas));
+    if (W <= 0xffffffffll) {
+        p.q = static_cast<uint32_t>(W) / static_cast<uint32_t>(p.parts);
+        p.rest = static_cast<int32_t>(static_cast<uint32_t>(W) % static_cast<uint32_t>(p.parts));
+    } else {
+        p.q = W / p.parts;
+        p.rest = static_cast<int32_t>(W % p.parts);
+    }
+    return p;
 }
 
 // One CTA's stretch of one tile.
@@ -117,38 +133,37 @@ struct ExtPiece {
 
 // Walks one CTA's part of the line.  `rows` gives ExtRow by index.
 struct ExtWalk {
-    int64_t W, unit, end;   // unit: the current tile's first
-    int32_t parts, cta, B, Hkv, tt;
+    ExtParts ps;
+    int64_t unit, first, end;   // unit: the current tile's first
+    int32_t cta, B, Hkv, tt;
     int32_t b, kvh, tile;
     ExtRow r;
 
     // The part of `cta`, which begins in row b0, whose first unit is row_unit.
     template <class Rows>
-    PKV_HD void begin(int64_t W_, int32_t parts_, int32_t cta_, int32_t B_, int32_t Hkv_, int tt_, int32_t b0,
+    PKV_HD void begin(const ExtParts& parts, int32_t cta_, int32_t B_, int32_t Hkv_, int tt_, int32_t b0,
                       int64_t row_unit, const Rows& rows) {
-        W = W_, parts = parts_, cta = cta_, B = B_, Hkv = Hkv_, tt = tt_;
-        const int64_t first = ext_part_begin(W, parts, cta);
-        end = ext_part_begin(W, parts, cta + 1);
+        ps = parts, cta = cta_, B = B_, Hkv = Hkv_, tt = tt_;
+        first = ps.begin(cta);
+        end = ps.begin(cta + 1);
         b = b0;
         r = rows(b);
-        const int64_t off = first - row_unit;
-        kvh = static_cast<int32_t>(off / r.units);
-        const int64_t in_head = off - kvh * r.units;
-        tile = ext_tile_at(r, tt, in_head);
-        unit = row_unit + kvh * r.units + ext_units_before(r, tt, tile);
+        unit = row_unit;
+        for (kvh = 0; first - unit >= r.units; ++kvh) unit += r.units;
+        tile = ext_tile_at(r, tt, first - unit);
+        unit += ext_units_before(r, tt, tile);
     }
 
     // The next stretch with blocks in it; false at the end of the part.
     template <class Rows>
     PKV_HD bool next(ExtPiece& p, const Rows& rows) {
-        const int64_t first = ext_part_begin(W, parts, cta);
         while (unit < end) {
             const int32_t nb = ext_tile_blocks(r, tt, tile);
             const int64_t b0 = unit + kTileUnits;   // the unit of block 0
             p.b = b, p.kvh = kvh, p.tile = tile, p.blocks = nb, p.parts = 0;
             p.lo = first > b0 ? static_cast<int32_t>(first - b0) : 0;
             p.hi = end < b0 + nb ? static_cast<int32_t>(end - b0) : nb;
-            if (p.lo == 0 && p.hi > 0 && p.hi < nb) p.parts = ext_part_of(W, parts, b0 + nb - 1) - cta + 1;
+            if (p.lo == 0 && p.hi > 0 && p.hi < nb) p.parts = ps.of(b0 + nb - 1) - cta + 1;
             unit = b0 + nb;
             if (++tile == r.tiles) {
                 tile = 0;

@@ -52,17 +52,18 @@ int main() {
             W += units * Hkv;
         }
         if (W == 0) continue;
-        const int parts = ext_parts(W, ctas);
-        REQUIRE(parts >= 1 && parts <= ctas);
+        const ExtParts ps = ext_parts(W, ctas);
+        const int parts = ps.parts;
+        REQUIRE(parts >= 1 && parts <= ctas && ps.begin(0) == 0 && ps.begin(parts) == W);
         auto get = [&](int b) { return rows[b]; };
         std::map<std::tuple<int, int, int>, std::vector<std::pair<int, ExtPiece>>> seen;
         for (int c = 0; c < parts; ++c) {
-            const int64_t first = ext_part_begin(W, parts, c);
-            REQUIRE(ext_part_of(W, parts, first) == c && ext_part_of(W, parts, ext_part_begin(W, parts, c + 1) - 1) == c);
+            const int64_t first = ps.begin(c);
+            REQUIRE(ps.of(first) == c && ps.of(ps.begin(c + 1) - 1) == c);
             int b0 = 0;
             while (!(start[b0] <= first && first < start[b0] + rows[b0].units * Hkv)) ++b0;
             ExtWalk w;
-            w.begin(W, parts, c, B, Hkv, tt, b0, start[b0], get);
+            w.begin(ps, c, B, Hkv, tt, b0, start[b0], get);
             ExtPiece p;
             int begun = 0, gone_on = 0;
             while (w.next(p, get)) {
