@@ -101,6 +101,17 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32
     return __all_sync(kFull, wait_until(bar, parity, status, abort));
 }
 
+__device__ __forceinline__ void lds128(uint32_t (&v)[4], uint32_t at) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 struct Rows {
     const ExtendParams& p;
     int tt;
@@ -204,7 +215,8 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
         auto scale = [&](int j, int page) {   // lanes 0..7: K's, 8..15: V's
             if (!Q8 || lane >= 16 || !page_ok(page)) return 0.0f;
             const int blk = (j * kExtBlock + (lane & 7) * 16) % p.page_size / kBlockRows;
-            return (lane < 8 ? p.k_scales : p.v_scales)[(static_cast<size_t>(page) * (p.page_size / kBlockRows) + blk) * p.Hkv + e.kvh];
+            const float x = (lane < 8 ? p.k_scales : p.v_scales)[(static_cast<size_t>(page) * (p.page_size / kBlockRows) + blk) * p.Hkv + e.kvh];
+            return lane < 8 && x == 0.0f ? 0x1p-120f : x;   // (a score of -inf in a place that is not seen stays one)
         };
         int next = entry(e.lo);
         float next_scale = scale(e.lo, next);
@@ -401,34 +413,36 @@ __device__ __forceinline__ void fix_values(const ExtendParams& p, Ctl* c, uint8_
             const uint32_t vn = n + 1, st = vn % C::kStages;
             if (!wait_warp(&c->full[st], (vn / C::kStages) & 1, p.status, &c->abort)) return;
             if (j < masked) continue;
-            const int valid = len - j * kExtBlock;
+            // rows that only some of the tile's rows see, then those behind the row's end
+            const int seen = max(pi.limit0 - j * kExtBlock, 0), valid = min(len - j * kExtBlock, kExtBlock);
             const uint32_t tile = smem_addr(smem) + C::kQ + st * C::kTile;
             uint32_t odd = 0;
-#pragma unroll 4
-            for (int i = lane; i < C::kTile / 16; i += 32) {
-                const uint32_t at = tile + i * 16;
-                uint32_t v[4];
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
-                bool put = (i >> 3) % kExtBlock >= valid;
-                if (put) {
-                    v[0] = v[1] = v[2] = v[3] = 0;
-                } else {
-                    uint32_t any = 0;
+            for (int h = 0; h < C::kHalves; ++h) {
+                const uint32_t half = tile + h * 16384;
+                uint32_t any = 0;
+#pragma unroll 8
+                for (int i = seen * 8 + lane; i < valid * 8; i += 32) {
+                    uint32_t v[4];
+                    lds128(v, half + i * 16);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) any |= (v[k] & 0x7f807f80u) + 0x00800080u;
-                    if (any & 0x80008000u) {
-                        put = true;
-                        odd = 1;
+                }
+                if (__any_sync(kFull, (any & 0x80008000u) != 0)) {
+                    odd = 1;
+                    for (int i = seen * 8 + lane; i < valid * 8; i += 32) {
+                        uint32_t v[4];
+                        lds128(v, half + i * 16);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             if ((v[k] & 0x7f80u) == 0x7f80u) v[k] &= 0xffff0000u;
                             if ((v[k] & 0x7f800000u) == 0x7f800000u) v[k] &= 0x0000ffffu;
                         }
+                        sts128(half + i * 16, v[0], v[1], v[2], v[3]);
                     }
                 }
-                if (put) asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+                for (int i = valid * 8 + lane; i < kExtBlock * 8; i += 32) sts128(half + i * 16, 0, 0, 0, 0);
             }
-            if (__any_sync(kFull, odd != 0) && lane == 0) pi.nonfinite = 1;
+            if (odd && lane == 0) pi.nonfinite = 1;
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->fixed[st]);
@@ -442,8 +456,10 @@ __device__ __forceinline__ void fix_values(const ExtendParams& p, Ctl* c, uint8_
 // ------------------------------------------------------------------ e4m3 to bf16
 
 // Codes become bf16 exactly (4 bits of significand into 8); their scales join the
-// scores and the weights in fp32.  In integers and one product for two codes: the
-// conversion instruction is slow and shares its unit with ex2.  In blocks with masked places NaN codes become 0
+// scores and the weights in fp32.  In integers and one product for two codes (the
+// conversion instruction is slow and shares its unit with ex2): the bits s eeee mmm
+// of a code, moved to those of a bf16, are its value times 2^-120.  A NaN code, all
+// ones, comes out as 480: tiles that hold one are gone over again.  In blocks with masked places NaN codes become 0
 // as infinities and NaN do in fix_values.
 template <int D>
 __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* smem) {
@@ -461,52 +477,65 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
         const int ntok = pi.ntok, lo = pi.lo, hi = pi.bad || ntok == 0 ? pi.lo : pi.hi, masked = first_masked(pi);
         const int len = ntok ? p.seq_lens[pi.b] : 0;
         for (int j = lo; j < hi; ++j) {
+            const uint32_t blk = n / 2;
+            if (!wait_warp(&c->scale_full[blk % kScaleRing], (blk / kScaleRing) & 1, p.status, &c->abort)) return;
+            const float* scales = c->scales[blk % kScaleRing];
             for (int kv = 0; kv < 2; ++kv, ++n) {
                 const uint32_t cs = n % C::kCodes, st = n % C::kStages;
                 if (!wait_warp(&c->code_full[cs], (n / C::kCodes) & 1, p.status, &c->abort)) return;
                 if (n >= C::kStages && !wait_warp(&c->empty[st], (n / C::kStages - 1) & 1, p.status, &c->abort)) return;
-                const int valid = len - j * kExtBlock;
-                const bool clean = kv == 1 && j >= masked;
-                uint32_t odd = 0;
-                const uint32_t src = codes + cs * C::kCode, dst = q + C::kQ + st * C::kTile + half * 16384;
-#pragma unroll 2
-                for (int row = tid / kPerRow; row < kExtBlock; row += 128 / kPerRow) {
+                const uint32_t src = codes + cs * C::kCode + tid * 16;
+                const uint32_t dst = q + C::kQ + st * C::kTile + half * 16384;
+                uint32_t most = 0;
+#pragma unroll 4
+                for (int i = 0; i < kExtBlock * kPerRow / 128; ++i) {
+                    const int row = tid / kPerRow + i * (128 / kPerRow);
                     uint32_t v[4], o[8];
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(src + row * D + chunk * 16) : "memory");
-                    if (clean && row >= valid) v[0] = v[1] = v[2] = v[3] = 0;
-                    // (s eeee mmm) to the bits of a bf16 2^120 times smaller, times 2^120; a NaN code (all ones) would
-                    // come out as 480
-                    uint32_t nan = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) nan |= (v[k] & 0x7f7f7f7fu) + 0x01010101u;
-                    nan &= 0x80808080u;
-                    if (nan && clean) {
-                        odd = 1;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) v[k] &= ~((((v[k] & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u) * 0xffu);
-                    }
+                    lds128(v, src + i * 2048);
+                    // 2^120, in K's with its scale's sign
+                    const uint32_t to = kv ? 0x7b807b80u : 0x7b807b80u ^ (__float_as_uint(scales[row / 16]) >> 31) * 0x80008000u;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const uint32_t high = (v[k] & 0x80808080u) | (v[k] >> 4 & 0x07070707u), low = v[k] << 4 & 0xf0f0f0f0u;
-                        o[2 * k] = bf16x2_mul(__byte_perm(low, high, 0x5140), 0x7b807b80u);
-                        o[2 * k + 1] = bf16x2_mul(__byte_perm(low, high, 0x7362), 0x7b807b80u);
-                    }
-                    if (nan && !clean) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if ((v[k / 4] >> (k % 4 * 8) & 0x7fu) == 0x7fu) o[k / 2] |= 0x7fffu << (k % 2 * 16);
+                        o[2 * k] = bf16x2_mul(__byte_perm(low, high, 0x5140), to);
+                        o[2 * k + 1] = bf16x2_mul(__byte_perm(low, high, 0x7362), to);
+                        most = bf16x2_max_abs(bf16x2_max_abs(most, o[2 * k]), o[2 * k + 1]);
                     }
                     const uint32_t first = (chunk % 4) * 2 + swap, at = dst + row * 128;
-                    const uint32_t a0 = at + ((first ^ (row & 7)) << 4), a1 = at + (((first ^ 1) ^ (row & 7)) << 4);
+                    const uint32_t a0 = at + ((first ^ (row & 7)) << 4), a1 = a0 ^ 16;
                     if (swap) {
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+                        sts128(a0, o[4], o[5], o[6], o[7]);
+                        sts128(a1, o[0], o[1], o[2], o[3]);
                     } else {
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+                        sts128(a0, o[0], o[1], o[2], o[3]);
+                        sts128(a1, o[4], o[5], o[6], o[7]);
                     }
                 }
-                if (clean && __any_sync(kFull, odd != 0) && lane == 0) pi.nonfinite = 1;
+                const bool clean = kv == 1 && j >= masked;
+                const bool nan = (most & 0x7fffu) >= 0x43f0u || (most >> 16 & 0x7fffu) >= 0x43f0u;   // 480
+                if (clean || __any_sync(kFull, nan)) {
+                    // rows that not all of the tile's rows see, and what lies behind the row's end
+                    const int seen = clean ? max(pi.limit0 - j * kExtBlock, 0) : kExtBlock, valid = len - j * kExtBlock;
+                    bool odd = false;
+                    for (int i = 0; i < kExtBlock * kPerRow / 128; ++i) {
+                        const int row = tid / kPerRow + i * (128 / kPerRow);
+                        uint32_t v[4];
+                        lds128(v, src + i * 2048);
+                        for (int k = 0; k < 16; ++k) {
+                            uint32_t w = v[0];   // (no index into registers)
+                            w = k / 4 == 1 ? v[1] : k / 4 == 2 ? v[2] : k / 4 == 3 ? v[3] : w;
+                            const bool is_nan = (w >> (k % 4 * 8) & 0x7fu) == 0x7fu, behind = kv == 1 && row >= valid;
+                            if (!is_nan && !behind) continue;
+                            const bool hide = behind || row >= seen;
+                            odd |= is_nan && hide && !behind;
+                            const uint32_t x = (chunk % 4) * 2 + k / 8;
+                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + row * 128 + ((x ^ (row & 7)) << 4) + k % 8 * 2),
+                                         "h"(static_cast<uint16_t>(hide ? 0 : 0x7fff))
+                                         : "memory");
+                        }
+                    }
+                    if (__any_sync(kFull, odd) && lane == 0) pi.nonfinite = 1;
+                }
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) {
@@ -604,111 +633,115 @@ __device__ __forceinline__ void follow_maximum(float top, bool first, uint32_t t
     }
 }
 
-// One block of a row's scores to weights: maximum, 2^(c s - m), sum; weights in
-// bf16 over the scores.  Scores stay in registers between the two passes (bf16
-// cache), or are read again where their scales and the widening warps leave fewer
-// registers to a thread (8-bit cache).
-template <int D, bool Q8>
-__device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float cs, const float* scales, bool cut, int seen,
-                                              bool first, float& m, float& l) {
-    uint64_t sum[2] = {0, 0};
-    if constexpr (!Q8) {
-        uint32_t s[128];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld32(s + 32 * k, tS + 32 * k);
+// Scores of a block that the row does not see become -inf, where they lie.
+__device__ __forceinline__ void mask_scores(uint32_t tS, int seen) {
+    const int all = __shfl_sync(kFull, seen, 0);   // what every row of the warp sees: the first row sees least
+#pragma unroll 1
+    for (int k = 0; k < kExtBlock; k += 32) {
+        if (k + 32 <= all) continue;
+        uint32_t s[32];
+        tmem_ld32(s, tS + k);
         tmem_wait_ld();
+        tmem_loaded32(s);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_loaded32(s + 32 * k);
-        if (cut) {
-            const int all = __shfl_sync(kFull, seen, 0);   // columns that every row of the warp sees
+        for (int i = 0; i < 32; ++i) s[i] = i < seen - k ? s[i] : 0xff800000u;
+        tmem_st32(tS + k, s);
+    }
+    tmem_wait_st();
+}
+
+// One block of a row's scores to weights: maximum, 2^(c s - m), sum; weights in
+// bf16 over the scores.  All 128 scores stay in registers between the two passes.
+template <int D>
+__device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float cs, bool first, float& m, float& l) {
+    uint32_t s[128];
 #pragma unroll
-            for (int k = 0; k < 128; k += 16) {
-                if (k + 16 <= all) continue;
+    for (int k = 0; k < 4; ++k) tmem_ld32(s + 32 * k, tS + 32 * k);
+    tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[k + i] = k + i < seen ? s[k + i] : 0xff800000u;
-            }
+    for (int k = 0; k < 4; ++k) tmem_loaded32(s + 32 * k);
+    float mx[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 4]));
+#pragma unroll
+    for (int k = 8; k < 128; k += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(s[k + i]), __uint_as_float(s[k + 4 + i]));
+    follow_maximum<D>(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs, first, tO, m, l);
+    const float ref = m == -INFINITY ? 0.0f : -m;
+    const uint64_t ref2 = pack2(ref, ref), cs2 = pack2(cs, cs);
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 128; k += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const F2 e = unpack2(fma2(pack2(__uint_as_float(s[k + i]), __uint_as_float(s[k + i + 1])), cs2, ref2));
+            const float a = ex2(e.x), b = ex2(e.y);
+            sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(a, b));
+            w[i / 2] = bf16x2(a, b);
         }
-        float mx[4];
+        tmem_st16(tS + k / 2, w);
+    }
+    const F2 a = unpack2(add2(sum[0], sum[1]));
+    l += a.x + a.y;
+}
+
+// The same over the 8-bit cache: 16 scores share a scale of K, their weights one of
+// V.  `scales` has K's 8 (whose signs have gone into the codes) and V's 8; those of
+// blocks that the row does not see at all may be anything.  The scores are read
+// twice, as the widening warps leave too few registers to hold them.
+template <int D>
+__device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float cs, const float* scales, int seen, bool first,
+                                                 float& m, float& l) {
+    float top = -INFINITY;
+    uint32_t s[2][32];
+    tmem_ld32(s[0], tS);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 4]));
+    for (int k = 0; k < 128; k += 32) {
+        uint32_t* x = s[k / 32 & 1];
+        tmem_wait_ld();
+        tmem_loaded32(x);
+        tmem_ld32(s[k / 32 & 1 ^ 1], tS + (k + 32) % 128);   // (at last the second pass's first)
 #pragma unroll
-        for (int k = 8; k < 128; k += 8)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(s[k + i]), __uint_as_float(s[k + 4 + i]));
-        follow_maximum<D>(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs, first, tO, m, l);
-        const float ref = m == -INFINITY ? 0.0f : -m;
-        const uint64_t ref2 = pack2(ref, ref), cs2 = pack2(cs, cs);
-#pragma unroll
-        for (int k = 0; k < 128; k += 32) {
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                const F2 e = unpack2(fma2(pack2(__uint_as_float(s[k + i]), __uint_as_float(s[k + i + 1])), cs2, ref2));
-                const float a = ex2(e.x), b = ex2(e.y);
-                sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(a, b));
-                w[i / 2] = bf16x2(a, b);
-            }
-            tmem_st16(tS + k / 2, w);
+        for (int i = 0; i < 32; i += 16) {
+            const float* y = reinterpret_cast<const float*>(x + i);
+            float t = max3(y[0], y[1], y[2]), u = max3(y[3], y[4], y[5]);
+            t = max3(t, y[6], y[7]), u = max3(u, y[8], y[9]);
+            t = max3(t, y[10], y[11]), u = max3(u, y[12], y[13]);
+            t = max3(max3(t, y[14], y[15]), u, u);
+            top = fmaxf(top, t * (k + i < seen ? fabsf(scales[(k + i) / 16]) : 1.0f));
         }
-    } else {
-        float top = -INFINITY;
+    }
+    tmem_wait_ld();
+    tmem_loaded32(s[0]);
+    follow_maximum<D>(top * cs, first, tO, m, l);
+    const float ref = m == -INFINITY ? 0.0f : -m;
+    const uint64_t ref2 = pack2(ref, ref);
+    uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int k = 0; k < 128; k += 64) {
-            uint32_t s[64];
-            tmem_ld32(s, tS + k);
-            tmem_ld32(s + 32, tS + k + 32);
+    for (int k = 0; k < 128; k += 32) {
+        uint32_t* x = s[k / 32 & 1];
+        if (k > 0) {
             tmem_wait_ld();
-            tmem_loaded32(s);
-            tmem_loaded32(s + 32);
-            if (cut) {
+            tmem_loaded32(x);
+        }
+        if (k + 32 < 128) tmem_ld32(s[k / 32 & 1 ^ 1], tS + k + 32);
+        uint32_t w[16];
 #pragma unroll
-                for (int i = 0; i < 64; ++i) s[i] = k + i < seen ? s[i] : 0xff800000u;
-            }
+        for (int h = 0; h < 32; h += 16) {
+            const float ks = k + h < seen ? fabsf(scales[(k + h) / 16]) * cs : 1.0f, vs = k + h < seen ? scales[8 + (k + h) / 16] : 0.0f;
+            const uint64_t ks2 = pack2(ks, ks), vs2 = pack2(vs, vs);
 #pragma unroll
-            for (int i = 0; i < 64; i += 16) {   // 16 scores of one scale
-                const float ks = scales[(k + i) / 16] * cs;
-                const float* x = reinterpret_cast<const float*>(s + i);
-                float t = max3(x[0], x[1], x[2]), u = max3(x[3], x[4], x[5]);
-                t = max3(t, x[6], x[7]), u = max3(u, x[8], x[9]);
-                t = max3(t, x[10], x[11]), u = max3(u, x[12], x[13]);
-                t = fmaxf(max3(t, x[14], x[15]), u);
-                if (!(ks >= 0.0f)) {   // a scale below 0 turns them round
-                    t = INFINITY;
-#pragma unroll
-                    for (int h = 0; h < 16; ++h) t = k + i + h < seen || !cut ? fminf(t, x[h]) : t;
-                }
-                t *= ks;
-                if (cut && k + i >= seen) t = -INFINITY;
-                top = fmaxf(top, t);
+            for (int i = h; i < h + 16; i += 2) {
+                const F2 e = unpack2(fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), ks2, ref2));
+                const uint64_t y = pack2(ex2(e.x), ex2(e.y));
+                sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], y);
+                const F2 z = unpack2(mul2(y, vs2));
+                w[i / 2] = bf16x2(z.x, z.y);
             }
         }
-        follow_maximum<D>(top, first, tO, m, l);
-        const float ref = m == -INFINITY ? 0.0f : -m;
-        const uint64_t ref2 = pack2(ref, ref);
-#pragma unroll
-        for (int k = 0; k < 128; k += 32) {
-            uint32_t s[32], w[16];
-            tmem_ld32(s, tS + k);
-            tmem_wait_ld();
-            tmem_loaded32(s);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                const int group = (k + i) / 16;
-                const float ks = scales[group] * cs;
-                // a weight of 0 stays 0 whatever the scale of a block that the row does not see
-                const float vs = cut && 16 * group >= seen ? 0.0f : scales[8 + group];
-                F2 e = unpack2(fma2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), pack2(ks, ks), ref2));
-                if (cut) {
-                    if (k + i >= seen) e.x = -INFINITY;
-                    if (k + i + 1 >= seen) e.y = -INFINITY;
-                }
-                const float a = ex2(e.x), b = ex2(e.y);
-                sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(a, b));
-                const F2 y = unpack2(mul2(pack2(a, b), pack2(vs, vs)));
-                w[i / 2] = bf16x2(y.x, y.y);
-            }
-            tmem_st16(tS + k / 2, w);
-        }
+        tmem_st16(tS + k / 2, w);
     }
     const F2 a = unpack2(add2(sum[0], sum[1]));
     l += a.x + a.y;
@@ -751,7 +784,11 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
                     if (!wait_warp(&c->scale_full[b % kScaleRing], (b / kScaleRing) & 1, p.status, &c->abort)) return false;
                     scales = c->scales[b % kScaleRing];
                 }
-                softmax_block<D, Q8>(tS, tO, p.scale_log2, scales, cut, seen, j == 0, m, l);
+                if (cut) mask_scores(tS, seen);
+                if constexpr (Q8)
+                    softmax_block_q8<D>(tS, tO, p.scale_log2, scales, cut ? seen : kExtBlock, j == 0, m, l);
+                else
+                    softmax_block<D>(tS, tO, p.scale_log2, j == 0, m, l);
                 tmem_wait_st();
             }
             tc_fence_before();
@@ -890,6 +927,7 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
         fence_mbar_init();
     }
     if (warp == C::kMma) tmem_alloc(&c->tmem, 512);
+    if (warp == C::kProducer && lane < 3) prefetch_map(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap);
     grid_dependency_wait();
     launch_dependents();
 

@@ -180,6 +180,28 @@ def test_one_token_a_row_without_offsets(q8):
     Problem([5, 0, 300], [1, 1, 1], q8=q8).run(cu_tokens=None).check()
 
 
+def test_scales_of_any_kind():
+    """Negative scales, zeros, and far apart ones; a scale that is not a number reaches who sees its block."""
+    p = Problem([200, 0], [90, 300], q8=True, scales="amax")
+    g = torch.Generator("cuda").manual_seed(9)
+    for s in (p.ks, p.vs):
+        s *= torch.where(torch.rand(s.shape, generator=g, device="cuda") < 0.3, -1.0, 1.0)
+        s *= torch.exp2(torch.randint(-20, 3, s.shape, generator=g, device="cuda"))
+        s[torch.rand(s.shape, generator=g, device="cuda") < 0.2] = 0
+    p.run().check()
+    was = p.out.clone(), p.lse.clone()
+    p.ks[int(p.table[0, 256 // 16])] = math.nan      # tokens 256 to 271 of the first row: new ones from 56 on
+    p.run()
+    assert p.out[56:90].isnan().all() and p.lse[56:90].isnan().all()
+    fine = torch.ones(p.T, dtype=torch.bool, device="cuda")
+    fine[56:90] = False
+    assert torch.equal(p.out[fine], was[0][fine]) and torch.equal(p.lse[fine], was[1][fine])
+    p.ks[int(p.table[0, 256 // 16])] = 0.5
+    p.vs[int(p.table[0, 256 // 16])] = math.inf
+    p.run()
+    assert not p.out[56:90].isfinite().any() and p.lse.isfinite().all() and torch.equal(p.out[fine], was[0][fine])
+
+
 def test_one_token_a_row_is_the_decode():
     p = Problem([4096, 77, 0], [1, 1, 1], Hq=8, Hkv=2).run()
     out, lse = torch.empty(3, 8, 128, device="cuda"), torch.empty(3, 8, device="cuda")
