@@ -1174,6 +1174,7 @@ int extend(const pkv_queries* t, const void* k_pages, const void* v_pages, const
     a.out = static_cast<uint16_t*>(t->out);
     a.lse = t->lse;
     a.out_stride = out_stride;
+    a.out_wide = out_stride % 16 == 0 && reinterpret_cast<uintptr_t>(t->out) % 32 == 0;
     a.ws_o = p->ext_o;
     a.ws_ml = p->ext_ml;
     a.splits = p->ext_splits;

@@ -112,6 +112,12 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+__device__ __forceinline__ void stg256(void* to, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 struct Rows {
     const ExtendParams& p;
     int tt;
@@ -194,18 +200,6 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
         if (!more) return;
         if (r.bad) continue;
 
-        if (q_loads > 0 && !wait_warp(&c->q_empty, (q_loads - 1) & 1, p.status, &c->abort)) return;
-        const int groups = ntok > per ? 2 : 1;
-        if (lane == 0) {
-            c->q_loads = q_loads + 1;
-            mbar_arrive_expect_tx(&c->q_full, groups * (C::kQ / 2));
-            for (int g = 0; g < groups; ++g)
-                for (int h = 0; h < C::kHalves; ++h)
-                    tma_load_3d(q_smem + g * (C::kQ / 2) + h * 16384, qmap, h * 64, e.kvh * p.G,
-                                r.tok0 + e.tile * w.tt + g * per, &c->q_full, policy);
-        }
-        ++q_loads;
-
         const int32_t* row = p.block_table + static_cast<size_t>(e.b) * p.max_pages;
         auto entry = [&](int j) {   // the page of this lane's 16 tokens of block j, or -1 past the row's end
             const int t = j * kExtBlock + (lane & 7) * 16;
@@ -233,6 +227,19 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
             const int tok = page_ok(box_page) ? box_page * p.page_size + t % p.page_size : -1;
             const uint32_t bytes = __popc(__ballot_sync(kFull, mine && tok >= 0)) * (kBox / (Q8 ? 1 : C::kHalves) / nbox);
             for (int kv = 0; kv < 2; ++kv, ++n) {
+                if (j == e.lo && kv == 1) {   // the queries, behind the first keys: their place is free later
+                    if (q_loads > 0 && !wait_warp(&c->q_empty, (q_loads - 1) & 1, p.status, &c->abort)) return;
+                    const int groups = ntok > per ? 2 : 1;
+                    if (lane == 0) {
+                        c->q_loads = q_loads + 1;
+                        mbar_arrive_expect_tx(&c->q_full, groups * (C::kQ / 2));
+                        for (int g = 0; g < groups; ++g)
+                            for (int h = 0; h < C::kHalves; ++h)
+                                tma_load_3d(q_smem + g * (C::kQ / 2) + h * 16384, qmap, h * 64, e.kvh * p.G,
+                                            r.tok0 + e.tile * w.tt + g * per, &c->q_full, policy);
+                    }
+                    ++q_loads;
+                }
                 const int st = n % kRing;
                 if (n >= kRing && !wait_warp(&empty[st], (n / kRing - 1) & 1, p.status, &c->abort)) return;
                 if (Q8 && kv == 0) {
@@ -487,11 +494,16 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
                 const uint32_t src = codes + cs * C::kCode + tid * 16;
                 const uint32_t dst = q + C::kQ + st * C::kTile + half * 16384;
                 uint32_t most = 0;
-#pragma unroll 4
-                for (int i = 0; i < kExtBlock * kPerRow / 128; ++i) {
-                    const int row = tid / kPerRow + i * (128 / kPerRow);
-                    uint32_t v[4], o[8];
-                    lds128(v, src + i * 2048);
+#pragma unroll 1
+                for (int i2 = 0; i2 < kPerRow; i2 += 2) {
+                uint32_t two[2][4];   // (both loads first: the stores would hold the second up)
+                lds128(two[0], src + i2 * 2048);
+                lds128(two[1], src + i2 * 2048 + 2048);
+#pragma unroll
+                for (int i1 = 0; i1 < 2; ++i1) {
+                    const int row = tid / kPerRow + (i2 + i1) * (128 / kPerRow);
+                    const uint32_t(&v)[4] = two[i1];
+                    uint32_t o[8];
                     // 2^120, in K's with its scale's sign
                     const uint32_t to = kv ? 0x7b807b80u : 0x7b807b80u ^ (__float_as_uint(scales[row / 16]) >> 31) * 0x80008000u;
 #pragma unroll
@@ -511,13 +523,14 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
                         sts128(a1, o[4], o[5], o[6], o[7]);
                     }
                 }
+                }
                 const bool clean = kv == 1 && j >= masked;
                 const bool nan = (most & 0x7fffu) >= 0x43f0u || (most >> 16 & 0x7fffu) >= 0x43f0u;   // 480
                 if (clean || __any_sync(kFull, nan)) {
                     // rows that not all of the tile's rows see, and what lies behind the row's end
                     const int seen = clean ? max(pi.limit0 - j * kExtBlock, 0) : kExtBlock, valid = len - j * kExtBlock;
                     bool odd = false;
-                    for (int i = 0; i < kExtBlock * kPerRow / 128; ++i) {
+                    for (int i = 0; i < kPerRow; ++i) {
                         const int row = tid / kPerRow + i * (128 / kPerRow);
                         uint32_t v[4];
                         lds128(v, src + i * 2048);
@@ -695,17 +708,18 @@ template <int D>
 __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float cs, const float* scales, int seen, bool first,
                                                  float& m, float& l) {
     float top = -INFINITY;
-    uint32_t s[2][32];
-    tmem_ld32(s[0], tS);
-#pragma unroll
-    for (int k = 0; k < 128; k += 32) {
-        uint32_t* x = s[k / 32 & 1];
+    uint32_t s[64];
+    // (loops, not straight code: three warps of a scheduler run three pieces of code, and instructions have to be near)
+#pragma unroll 1
+    for (int k = 0; k < 128; k += 64) {
+        tmem_ld32(s, tS + k);
+        tmem_ld32(s + 32, tS + k + 32);
         tmem_wait_ld();
-        tmem_loaded32(x);
-        tmem_ld32(s[k / 32 & 1 ^ 1], tS + (k + 32) % 128);   // (at last the second pass's first)
+        tmem_loaded32(s);
+        tmem_loaded32(s + 32);
 #pragma unroll
-        for (int i = 0; i < 32; i += 16) {
-            const float* y = reinterpret_cast<const float*>(x + i);
+        for (int i = 0; i < 64; i += 16) {
+            const float* y = reinterpret_cast<const float*>(s + i);
             float t = max3(y[0], y[1], y[2]), u = max3(y[3], y[4], y[5]);
             t = max3(t, y[6], y[7]), u = max3(u, y[8], y[9]);
             t = max3(t, y[10], y[11]), u = max3(u, y[12], y[13]);
@@ -713,35 +727,31 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
             top = fmaxf(top, t * (k + i < seen ? fabsf(scales[(k + i) / 16]) : 1.0f));
         }
     }
-    tmem_wait_ld();
-    tmem_loaded32(s[0]);
     follow_maximum<D>(top * cs, first, tO, m, l);
     const float ref = m == -INFINITY ? 0.0f : -m;
     const uint64_t ref2 = pack2(ref, ref);
     uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+    for (int k = 0; k < 128; k += 64) {
+        tmem_ld32(s, tS + k);
+        tmem_ld32(s + 32, tS + k + 32);
+        tmem_wait_ld();
+        tmem_loaded32(s);
+        tmem_loaded32(s + 32);
 #pragma unroll
-    for (int k = 0; k < 128; k += 32) {
-        uint32_t* x = s[k / 32 & 1];
-        if (k > 0) {
-            tmem_wait_ld();
-            tmem_loaded32(x);
-        }
-        if (k + 32 < 128) tmem_ld32(s[k / 32 & 1 ^ 1], tS + k + 32);
-        uint32_t w[16];
-#pragma unroll
-        for (int h = 0; h < 32; h += 16) {
+        for (int h = 0; h < 64; h += 16) {
             const float ks = k + h < seen ? fabsf(scales[(k + h) / 16]) * cs : 1.0f, vs = k + h < seen ? scales[8 + (k + h) / 16] : 0.0f;
             const uint64_t ks2 = pack2(ks, ks), vs2 = pack2(vs, vs);
 #pragma unroll
             for (int i = h; i < h + 16; i += 2) {
-                const F2 e = unpack2(fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), ks2, ref2));
+                const F2 e = unpack2(fma2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), ks2, ref2));
                 const uint64_t y = pack2(ex2(e.x), ex2(e.y));
                 sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], y);
                 const F2 z = unpack2(mul2(y, vs2));
-                w[i / 2] = bf16x2(z.x, z.y);
+                s[i / 2] = bf16x2(z.x, z.y);
             }
         }
-        tmem_st16(tS + k / 2, w);
+        tmem_st32(tS + k / 2, s);
     }
     const F2 a = unpack2(add2(sum[0], sum[1]));
     l += a.x + a.y;
@@ -852,13 +862,16 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
                         tmem_loaded32(x);
                     }
                     if (live && o.out) {
+                        uint32_t w[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint32_t w[4];
+                        for (int i = 0; i < 16; ++i) w[i] = bf16x2(__uint_as_float(x[2 * i]) * inv, __uint_as_float(x[2 * i + 1]) * inv);
+                        if (p.out_wide) {   // whole sectors
+                            stg256(o.out + k, w);
+                            stg256(o.out + k + 16, w + 8);
+                        } else {
 #pragma unroll
-                            for (int h = 0; h < 4; ++h)
-                                w[h] = bf16x2(__uint_as_float(x[i + 2 * h]) * inv, __uint_as_float(x[i + 2 * h + 1]) * inv);
-                            *reinterpret_cast<uint4*>(o.out + k + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int i = 0; i < 16; i += 4)
+                                *reinterpret_cast<uint4*>(o.out + k + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
                         }
                     } else if (live) {
 #pragma unroll

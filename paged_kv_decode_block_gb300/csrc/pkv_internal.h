@@ -201,6 +201,7 @@ struct ExtendParams {
     uint16_t* out;              // bf16 [T][Hq][D] at out_stride
     float* lse;                 // [T][Hq], or null
     int64_t out_stride;         // elements between tokens
+    int32_t out_wide;           // every head of out begins on 32 bytes
     float* ws_o;                // [CTAs][2][D / 4][256][4] unnormalised partial outputs
     float2* ws_ml;              // [CTAs][2][256] their reference (log2) and sum
     ExtSplit* splits;           // [CTAs]
