@@ -37,8 +37,8 @@ struct Cfg {
     static constexpr int kTile = kExtBlock * D * 2;           // bytes of a K or V block in bf16
     static constexpr int kCode = kExtBlock * D;               // ... in e4m3
     static constexpr int kQ = kExtRows * D * 2;
-    static constexpr int kStages = Q8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
-    static constexpr int kCodes = Q8 ? (D == 128 ? 4 : 8) : 0;
+    static constexpr int kStages = Q8 ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 10);
+    static constexpr int kCodes = Q8 ? (D == 128 ? 2 : 6) : 0;
     static constexpr int kThreads = Q8 ? 512 : 384;
     // producer's warpgroup last: [0, 8) softmax; then bf16: 8 producer, 9 and 10 products, 11
     // fixer; 8-bit: [8, 12) widening, 12 producer, 13 and 14 products
@@ -364,7 +364,6 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
                 return;
             }
             advance();
-            if (j + 1 < nb && !wait(&c->full[st], phase)) return;
             if (sh.mine(j)) {
                 if (!add && outs > 0 && !wait(&c->o_empty[g], (outs - 1) & 1)) return;
                 if (!wait(&c->p_full[g], done++ & 1)) return;
@@ -379,6 +378,7 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
                     ++outs;
                 }
             }
+            if (j + 1 < nb && !wait(&c->full[st], phase)) return;
             if (j + 1 < nb && sh.mine(j + 1)) {
                 tc_fence_after();
                 qk(q_desc, st);
@@ -463,11 +463,8 @@ __device__ __forceinline__ void fix_values(const ExtendParams& p, Ctl* c, uint8_
 // ------------------------------------------------------------------ e4m3 to bf16
 
 // Codes become bf16 exactly (4 bits of significand into 8); their scales join the
-// scores and the weights in fp32.  In integers and one product for two codes (the
-// conversion instruction is slow and shares its unit with ex2): the bits s eeee mmm
-// of a code, moved to those of a bf16, are its value times 2^-120.  A NaN code, all
-// ones, comes out as 480: tiles that hold one are gone over again.  In blocks with masked places NaN codes become 0
-// as infinities and NaN do in fix_values.
+// scores and the weights in fp32.  In blocks with masked places NaN codes of V become
+// 0, as infinities and NaN do in fix_values.
 template <int D>
 __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* smem) {
     using C = Cfg<D, true>;
@@ -493,42 +490,38 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
                 if (n >= C::kStages && !wait_warp(&c->empty[st], (n / C::kStages - 1) & 1, p.status, &c->abort)) return;
                 const uint32_t src = codes + cs * C::kCode + tid * 16;
                 const uint32_t dst = q + C::kQ + st * C::kTile + half * 16384;
-                uint32_t most = 0;
 #pragma unroll 1
-                for (int i2 = 0; i2 < kPerRow; i2 += 2) {
-                uint32_t two[2][4];   // (both loads first: the stores would hold the second up)
-                lds128(two[0], src + i2 * 2048);
-                lds128(two[1], src + i2 * 2048 + 2048);
+                for (int i = 0; i < kPerRow; i += 2) {
+                    uint32_t v[2][4];   // (both loads first: the stores would hold the second up)
+                    lds128(v[0], src + i * 2048);
+                    lds128(v[1], src + i * 2048 + 2048);
 #pragma unroll
-                for (int i1 = 0; i1 < 2; ++i1) {
-                    const int row = tid / kPerRow + (i2 + i1) * (128 / kPerRow);
-                    const uint32_t(&v)[4] = two[i1];
-                    uint32_t o[8];
-                    // 2^120, in K's with its scale's sign
-                    const uint32_t to = kv ? 0x7b807b80u : 0x7b807b80u ^ (__float_as_uint(scales[row / 16]) >> 31) * 0x80008000u;
+                    for (int h = 0; h < 2; ++h) {
+                        const int row = tid / kPerRow + (i + h) * (128 / kPerRow);
+                        // K's codes take their scale's sign
+                        const uint32_t sign = kv ? 0 : (__float_as_uint(scales[row / 16]) >> 31) * 0x80808080u;
+                        uint32_t o[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t high = (v[k] & 0x80808080u) | (v[k] >> 4 & 0x07070707u), low = v[k] << 4 & 0xf0f0f0f0u;
-                        o[2 * k] = bf16x2_mul(__byte_perm(low, high, 0x5140), to);
-                        o[2 * k + 1] = bf16x2_mul(__byte_perm(low, high, 0x7362), to);
-                        most = bf16x2_max_abs(bf16x2_max_abs(most, o[2 * k]), o[2 * k + 1]);
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t w = v[h][k] ^ sign;
+                            o[2 * k] = e4m3x2_bf16x2(static_cast<uint16_t>(w));
+                            o[2 * k + 1] = e4m3x2_bf16x2(static_cast<uint16_t>(w >> 16));
+                        }
+                        const uint32_t first = (chunk % 4) * 2 + swap, at = dst + row * 128;
+                        const uint32_t a0 = at + ((first ^ (row & 7)) << 4), a1 = a0 ^ 16;
+                        if (swap) {
+                            sts128(a0, o[4], o[5], o[6], o[7]);
+                            sts128(a1, o[0], o[1], o[2], o[3]);
+                        } else {
+                            sts128(a0, o[0], o[1], o[2], o[3]);
+                            sts128(a1, o[4], o[5], o[6], o[7]);
+                        }
                     }
-                    const uint32_t first = (chunk % 4) * 2 + swap, at = dst + row * 128;
-                    const uint32_t a0 = at + ((first ^ (row & 7)) << 4), a1 = a0 ^ 16;
-                    if (swap) {
-                        sts128(a0, o[4], o[5], o[6], o[7]);
-                        sts128(a1, o[0], o[1], o[2], o[3]);
-                    } else {
-                        sts128(a0, o[0], o[1], o[2], o[3]);
-                        sts128(a1, o[4], o[5], o[6], o[7]);
-                    }
-                }
                 }
                 const bool clean = kv == 1 && j >= masked;
-                const bool nan = (most & 0x7fffu) >= 0x43f0u || (most >> 16 & 0x7fffu) >= 0x43f0u;   // 480
-                if (clean || __any_sync(kFull, nan)) {
+                if (clean) {
                     // rows that not all of the tile's rows see, and what lies behind the row's end
-                    const int seen = clean ? max(pi.limit0 - j * kExtBlock, 0) : kExtBlock, valid = len - j * kExtBlock;
+                    const int seen = max(pi.limit0 - j * kExtBlock, 0), valid = len - j * kExtBlock;
                     bool odd = false;
                     for (int i = 0; i < kPerRow; ++i) {
                         const int row = tid / kPerRow + i * (128 / kPerRow);
@@ -537,13 +530,12 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
                         for (int k = 0; k < 16; ++k) {
                             uint32_t w = v[0];   // (no index into registers)
                             w = k / 4 == 1 ? v[1] : k / 4 == 2 ? v[2] : k / 4 == 3 ? v[3] : w;
-                            const bool is_nan = (w >> (k % 4 * 8) & 0x7fu) == 0x7fu, behind = kv == 1 && row >= valid;
-                            if (!is_nan && !behind) continue;
-                            const bool hide = behind || row >= seen;
-                            odd |= is_nan && hide && !behind;
+                            const bool is_nan = (w >> (k % 4 * 8) & 0x7fu) == 0x7fu, behind = row >= valid;
+                            if (row < seen || (!is_nan && !behind)) continue;
+                            odd |= !behind;
                             const uint32_t x = (chunk % 4) * 2 + k / 8;
                             asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + row * 128 + ((x ^ (row & 7)) << 4) + k % 8 * 2),
-                                         "h"(static_cast<uint16_t>(hide ? 0 : 0x7fff))
+                                         "h"(static_cast<uint16_t>(0))
                                          : "memory");
                         }
                     }
