@@ -72,33 +72,36 @@ struct Ctl {
     Piece piece[kPieceRing];
     float scales[kScaleRing][16];                  // 8 of K, 8 of V
     int64_t scan[17];
+    ExtRow row;                                    // the row that the CTA's part begins in, its first unit, its index
     int64_t row_unit;
     int32_t row0;
-    volatile int abort;
+    volatile int abort, late;                      // a wait ran out; one at the end did too
     uint32_t tmem;
     int32_t issued;                                // blocks that the producer has begun to load
     int32_t q_loads;
 };
 
-// As mbar_wait, without a call (the register split below leaves none), for all lanes of a warp alike.
-__device__ __forceinline__ bool wait_until(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort,
-                                           uint64_t limit_ns = kWaitLimitNs) {
-    uint64_t start = 0;
-    for (uint32_t spin = 1; !mbar_try_wait(bar, parity); ++spin) {
-        if (spin % 64) continue;
-        if (abort && *abort) return false;
-        const uint64_t now = globaltimer_ns();
+// Waits for a phase, for at most kWaitLimitNs: then every wait of the CTA gives up, and the kernel's end sets the
+// status.  Without a call, which a register split does not allow, and short, as there are many.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    uint32_t start = 0;
+    for (uint32_t tries = 1; !mbar_try_wait(bar, parity); ++tries) {
+        if (tries % 64) continue;   // (reading the clock would make the wait late)
+        if (*abort) return false;
+        uint32_t now;
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+        now |= 1;
         if (start == 0) start = now;
-        if (now - start > limit_ns) {
-            atomicOr(status, static_cast<uint32_t>(PKV_DEV_TIMEOUT));
-            if (abort) *abort = 1;
+        if (now - start > static_cast<uint32_t>(kWaitLimitNs)) {
+            *abort = 1;
             return false;
         }
     }
     return true;
 }
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
-    return __all_sync(kFull, wait_until(bar, parity, status, abort));
+// (for all lanes of a warp alike)
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(kFull, wait_for(bar, parity, abort));
 }
 
 __device__ __forceinline__ void lds128(uint32_t (&v)[4], uint32_t at) {
@@ -107,7 +110,6 @@ __device__ __forceinline__ void lds128(uint32_t (&v)[4], uint32_t at) {
 __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -175,10 +177,9 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
         ExtPiece e{};
         const bool more = w.next(e, rows);
         const int slot = pc % kPieceRing;
-        if (pc >= kPieceRing && !wait_warp(&c->piece_empty[slot], (pc / kPieceRing - 1) & 1, p.status, &c->abort)) return;
+        if (pc >= kPieceRing && !wait_warp(&c->piece_empty[slot], (pc / kPieceRing - 1) & 1, &c->abort)) return;
         Piece& pi = c->piece[slot];
-        ExtRow r{};
-        if (more) r = rows(e.b);
+        const ExtRow& r = e.r;
         const int ntok = more ? min(w.tt, r.n - e.tile * w.tt) : 0;
         if (lane == 0) {
             pi.tok0 = r.tok0 + e.tile * w.tt;
@@ -189,7 +190,7 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
             pi.lo = more ? e.lo : 0;
             pi.hi = more ? e.hi : 0;
             pi.slot = !more || (e.lo == 0 && e.hi == e.blocks) ? -1 : 2 * w.cta + (e.lo == 0 ? 1 : 0);
-            pi.bad = r.bad;
+            pi.bad = more ? r.bad : 0;
             pi.poison = 0;
             pi.nonfinite = 0;
             if (more && r.bad) atomicOr(p.status, static_cast<uint32_t>(PKV_DEV_PLAN_MISMATCH));
@@ -228,7 +229,7 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
             const uint32_t bytes = __popc(__ballot_sync(kFull, mine && tok >= 0)) * (kBox / (Q8 ? 1 : C::kHalves) / nbox);
             for (int kv = 0; kv < 2; ++kv, ++n) {
                 if (j == e.lo && kv == 1) {   // the queries, behind the first keys: their place is free later
-                    if (q_loads > 0 && !wait_warp(&c->q_empty, (q_loads - 1) & 1, p.status, &c->abort)) return;
+                    if (q_loads > 0 && !wait_warp(&c->q_empty, (q_loads - 1) & 1, &c->abort)) return;
                     const int groups = ntok > per ? 2 : 1;
                     if (lane == 0) {
                         c->q_loads = q_loads + 1;
@@ -241,7 +242,7 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
                     ++q_loads;
                 }
                 const int st = n % kRing;
-                if (n >= kRing && !wait_warp(&empty[st], (n / kRing - 1) & 1, p.status, &c->abort)) return;
+                if (n >= kRing && !wait_warp(&empty[st], (n / kRing - 1) & 1, &c->abort)) return;
                 if (Q8 && kv == 0) {
                     if (lane < 16) c->scales[blocks % kScaleRing][lane] = sc;
                     __syncwarp();
@@ -310,7 +311,7 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
     uint32_t fixed_phase = 0, q_loads = 0, done = 0, outs = 0, turns = 0;
     uint32_t st = 0, phase = 0;   // the ring's next block and its parity
 
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_until(bar, parity, p.status, &c->abort); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_for(bar, parity, &c->abort); };
     auto advance = [&]() {
         if (++st == C::kStages) st = 0, phase ^= 1;
     };
@@ -364,6 +365,8 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
                 return;
             }
             advance();
+            // (bf16: the next keys are there, as a rule, and are asked for while there is time; 8-bit: they are still being widened)
+            if (!Q8 && j + 1 < nb && !wait(&c->full[st], phase)) return;
             if (sh.mine(j)) {
                 if (!add && outs > 0 && !wait(&c->o_empty[g], (outs - 1) & 1)) return;
                 if (!wait(&c->p_full[g], done++ & 1)) return;
@@ -378,7 +381,7 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
                     ++outs;
                 }
             }
-            if (j + 1 < nb && !wait(&c->full[st], phase)) return;
+            if (Q8 && j + 1 < nb && !wait(&c->full[st], phase)) return;
             if (j + 1 < nb && sh.mine(j + 1)) {
                 tc_fence_after();
                 qk(q_desc, st);
@@ -410,15 +413,15 @@ __device__ __forceinline__ void fix_values(const ExtendParams& p, Ctl* c, uint8_
     uint32_t n = 0;
     for (uint32_t pc = 0;; ++pc) {
         const int slot = pc % kPieceRing;
-        if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, p.status, &c->abort)) return;
+        if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, &c->abort)) return;
         Piece& pi = c->piece[slot];
         const int ntok = pi.ntok, lo = pi.lo, hi = pi.bad || ntok == 0 ? pi.lo : pi.hi, masked = first_masked(pi);
         const int len = ntok ? p.seq_lens[pi.b] : 0;
         for (int j = lo; j < hi; ++j, n += 2) {
             // (every block is waited for, in order: a parity tells a phase from the next one only)
-            if (!wait_warp(&c->full[n % C::kStages], (n / C::kStages) & 1, p.status, &c->abort)) return;
+            if (!wait_warp(&c->full[n % C::kStages], (n / C::kStages) & 1, &c->abort)) return;
             const uint32_t vn = n + 1, st = vn % C::kStages;
-            if (!wait_warp(&c->full[st], (vn / C::kStages) & 1, p.status, &c->abort)) return;
+            if (!wait_warp(&c->full[st], (vn / C::kStages) & 1, &c->abort)) return;
             if (j < masked) continue;
             // rows that only some of the tile's rows see, then those behind the row's end
             const int seen = max(pi.limit0 - j * kExtBlock, 0), valid = min(len - j * kExtBlock, kExtBlock);
@@ -476,18 +479,18 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
     uint32_t n = 0;
     for (uint32_t pc = 0;; ++pc) {
         const int slot = pc % kPieceRing;
-        if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, p.status, &c->abort)) return;
+        if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, &c->abort)) return;
         Piece& pi = c->piece[slot];
         const int ntok = pi.ntok, lo = pi.lo, hi = pi.bad || ntok == 0 ? pi.lo : pi.hi, masked = first_masked(pi);
         const int len = ntok ? p.seq_lens[pi.b] : 0;
         for (int j = lo; j < hi; ++j) {
             const uint32_t blk = n / 2;
-            if (!wait_warp(&c->scale_full[blk % kScaleRing], (blk / kScaleRing) & 1, p.status, &c->abort)) return;
+            if (!wait_warp(&c->scale_full[blk % kScaleRing], (blk / kScaleRing) & 1, &c->abort)) return;
             const float* scales = c->scales[blk % kScaleRing];
             for (int kv = 0; kv < 2; ++kv, ++n) {
                 const uint32_t cs = n % C::kCodes, st = n % C::kStages;
-                if (!wait_warp(&c->code_full[cs], (n / C::kCodes) & 1, p.status, &c->abort)) return;
-                if (n >= C::kStages && !wait_warp(&c->empty[st], (n / C::kStages - 1) & 1, p.status, &c->abort)) return;
+                if (!wait_warp(&c->code_full[cs], (n / C::kCodes) & 1, &c->abort)) return;
+                if (n >= C::kStages && !wait_warp(&c->empty[st], (n / C::kStages - 1) & 1, &c->abort)) return;
                 const uint32_t src = codes + cs * C::kCode + tid * 16;
                 const uint32_t dst = q + C::kQ + st * C::kTile + half * 16384;
 #pragma unroll 1
@@ -625,7 +628,7 @@ __device__ __forceinline__ void follow_maximum(float top, bool first, uint32_t t
         const float f = to == -INFINITY ? 1.0f : ex2(m - to);
         l *= f;
         m = to;
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < D; k += 32) {
             uint32_t o[32];
             tmem_ld32(o, tO + k);
@@ -759,7 +762,7 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
     uint32_t done = 0, outs = 0, blocks = 0, pairs = 0;
     for (uint32_t pc = 0;; ++pc) {
         const int slot = pc % kPieceRing;
-        if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, p.status, &c->abort)) return false;
+        if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, &c->abort)) return false;
         const Piece& pi = c->piece[slot];
         if (pi.ntok == 0) {
             return true;
@@ -773,7 +776,7 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
         const int masked = first_masked(pi);
         float m = -INFINITY, l = 0.0f;
         for (int j = 0; j < nb; ++j) {
-            if (!wait_warp(&c->s_full[g], done & 1, p.status, &c->abort)) return false;
+            if (!wait_warp(&c->s_full[g], done & 1, &c->abort)) return false;
             ++done;
             tc_fence_after();
             if (warp_live) {
@@ -783,7 +786,7 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
                 const float* scales = nullptr;
                 if (Q8) {
                     const uint32_t b = blocks + sh.block(j);
-                    if (!wait_warp(&c->scale_full[b % kScaleRing], (b / kScaleRing) & 1, p.status, &c->abort)) return false;
+                    if (!wait_warp(&c->scale_full[b % kScaleRing], (b / kScaleRing) & 1, &c->abort)) return false;
                     scales = c->scales[b % kScaleRing];
                 }
                 if (cut) mask_scores(tS, seen);
@@ -801,7 +804,7 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
 
         // outputs
         if (nb > 0) {
-            if (!wait_warp(&c->o_full[g], outs & 1, p.status, &c->abort)) return false;
+            if (!wait_warp(&c->o_full[g], outs & 1, &c->abort)) return false;
             ++outs;
             tc_fence_after();
         }
@@ -817,7 +820,7 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
                 }
                 continue;
             }
-            if (!wait_warp(&c->pair_full, pairs & 1, p.status, &c->abort)) return false;
+            if (!wait_warp(&c->pair_full, pairs & 1, &c->abort)) return false;
             ++pairs;
             tc_fence_after();
             const float2 other = c->pair_ml[row];
@@ -836,7 +839,8 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
             } else if (nb == 0) {
                 if (live) *o.ml = make_float2(-INFINITY, 0.0f);   // (only a part of a tile can have nothing to see)
             } else {
-#pragma unroll 2
+                // (a loop: this is run once a tile, and its instructions come from afar)
+#pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
                     uint32_t x[32];
                     tmem_ld32(x, tO + k);
@@ -854,16 +858,15 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
                         tmem_loaded32(x);
                     }
                     if (live && o.out) {
-                        uint32_t w[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = bf16x2(__uint_as_float(x[2 * i]) * inv, __uint_as_float(x[2 * i + 1]) * inv);
+                        for (int i = 0; i < 16; ++i) x[i] = bf16x2(__uint_as_float(x[2 * i]) * inv, __uint_as_float(x[2 * i + 1]) * inv);
                         if (p.out_wide) {   // whole sectors
-                            stg256(o.out + k, w);
-                            stg256(o.out + k + 16, w + 8);
+                            stg256(o.out + k, x);
+                            stg256(o.out + k + 16, x + 8);
                         } else {
 #pragma unroll
                             for (int i = 0; i < 16; i += 4)
-                                *reinterpret_cast<uint4*>(o.out + k + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                                *reinterpret_cast<uint4*>(o.out + k + 2 * i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                         }
                     } else if (live) {
 #pragma unroll
@@ -887,6 +890,24 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
             if (sh.pair) mbar_arrive(&c->o_empty[1]);
             mbar_arrive(&c->piece_empty[slot]);
         }
+    }
+}
+
+// A wait has run out: everything that this CTA was to write is NaN.
+template <int D>
+__device__ __noinline__ void poison(const ExtendParams& p, Ctl* c, const ExtParts& parts, const Rows& rows) {
+    const int cta = blockIdx.x, tid = threadIdx.x;
+    ExtWalk w;
+    w.begin(parts, cta, p.B, p.Hkv, rows.tt, c->row0, c->row, c->row_unit);
+    ExtPiece e{};
+    while (w.next(e, rows)) {
+        Piece pi{};
+        pi.tok0 = e.r.tok0 + e.tile * w.tt;
+        pi.kvh = e.kvh;
+        pi.slot = e.lo == 0 && e.hi == e.blocks ? -1 : 2 * cta + (e.lo == 0 ? 1 : 0);
+        const int ntok = min(w.tt, e.r.n - e.tile * w.tt);
+        if (tid < ntok * p.G) write_nan(row_out(p, pi, tid, 31 - __clz(p.G), D), D);
+        if (tid == 0 && e.parts) p.splits[cta] = ExtSplit{pi.tok0, ntok, e.kvh, e.parts};
     }
 }
 
@@ -927,6 +948,7 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
             mbar_init(&c->piece_empty[i], C::kReaders);
         }
         c->abort = 0;
+        c->late = 0;
         c->issued = 0;
         c->q_loads = 0;
         fence_mbar_init();
@@ -938,31 +960,36 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
 
     // the CTA's part of the work
     const Rows rows{p, kExtRows / p.G};
-    int64_t local = 0, W = 0;
-    for (int b = tid; b < p.B; b += C::kThreads) {
-        local += rows(b).units * p.Hkv;
-        if (blockIdx.x == 0 && p.cu && (p.cu[b] < 0 || p.cu[b + 1] < p.cu[b] || p.cu[b + 1] > p.T))
-            atomicOr(p.status, static_cast<uint32_t>(PKV_DEV_PLAN_MISMATCH));
-    }
-    int64_t before = block_scan<C::kThreads>(c, local, &W);
     const int cta = blockIdx.x;
-    const ExtParts parts = ext_parts(W, gridDim.x);
-    const bool work = W > 0 && cta < parts.parts;
-    if (work) {
-        const int64_t first = parts.begin(cta);
-        if (p.B <= C::kThreads) {
-            if (first >= before && first < before + local) c->row0 = tid, c->row_unit = before;
-        } else {
-            int64_t run = 0, total = 0;
-            for (int base = 0; base < p.B && run <= first; base += C::kThreads) {
-                const int b = base + tid;
-                local = b < p.B ? rows(b).units * p.Hkv : 0;
-                before = run + block_scan<C::kThreads>(c, local, &total);
-                if (first >= before && first < before + local) c->row0 = b, c->row_unit = before;
-                run += total;
-            }
+    int64_t W = 0, first = -1, run = 0;
+    ExtParts parts{};
+    // units of all rows, then (with more rows than threads in another pass) the row that holds the part's first
+    const int chunks = (p.B + C::kThreads - 1) / C::kThreads;
+    for (int i = 0; i < 2 * chunks; ++i) {
+        const bool find = i >= chunks;
+        const int b = (find ? i - chunks : i) * C::kThreads + tid;
+        ExtRow r{};
+        if (b < p.B) {
+            r = rows(b);
+            if (cta == 0 && p.cu && !find && (p.cu[b] < 0 || p.cu[b + 1] < p.cu[b] || p.cu[b + 1] > p.T))
+                atomicOr(p.status, static_cast<uint32_t>(PKV_DEV_PLAN_MISMATCH));
         }
+        const int64_t units = r.units * p.Hkv;
+        int64_t total;
+        const int64_t before = run + block_scan<C::kThreads>(c, units, &total);
+        run += total;
+        if (!find && i + 1 == chunks) {
+            W = run;
+            if (W == 0) break;
+            parts = ext_parts(W, gridDim.x);
+            if (cta >= parts.parts) break;
+            first = parts.begin(cta);
+            run = 0;
+        }
+        if ((find || chunks == 1) && first >= before && first < before + units) c->row = r, c->row0 = b, c->row_unit = before;
+        if (chunks == 1) break;
     }
+    const bool work = first >= 0;
     if (tid == 0) p.splits[cta] = ExtSplit{0, 0, 0, 0};
     tc_fence_before();
     __syncthreads();
@@ -975,20 +1002,7 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
             else
                 asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
             if (!attend<D, Q8>(p, c)) {
-                // a wait ran out: everything that this CTA was to write is NaN
-                ExtWalk w;
-                w.begin(parts, cta, p.B, p.Hkv, rows.tt, c->row0, c->row_unit, rows);
-                ExtPiece e;
-                while (w.next(e, rows)) {
-                    const ExtRow r = rows(e.b);
-                    Piece pi{};
-                    pi.tok0 = r.tok0 + e.tile * w.tt;
-                    pi.kvh = e.kvh;
-                    pi.slot = e.lo == 0 && e.hi == e.blocks ? -1 : 2 * cta + (e.lo == 0 ? 1 : 0);
-                    const int ntok = min(w.tt, r.n - e.tile * w.tt);
-                    if (tid < ntok * p.G) write_nan(row_out(p, pi, tid, 31 - __clz(p.G), D), D);
-                    if (tid == 0 && e.parts) p.splits[cta] = ExtSplit{pi.tok0, ntok, e.kvh, e.parts};
-                }
+                poison<D>(p, c, parts, rows);
             }
         } else if (Q8 && warp < 12) {
             if constexpr (Q8) {
@@ -1002,7 +1016,7 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
                 asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
             if (warp == C::kProducer) {
                 ExtWalk w;
-                w.begin(parts, cta, p.B, p.Hkv, rows.tt, c->row0, c->row_unit, rows);
+                w.begin(parts, cta, p.B, p.Hkv, rows.tt, c->row0, c->row, c->row_unit);
                 uint64_t policy;
                 asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
                 produce<D, Q8>(p, c, smem, &qmap, &kmap, &vmap, w, rows, policy);
@@ -1018,14 +1032,15 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
     if (c->abort && warp == C::kMma + 1 && lane == 0) umma_commit(&c->drain);
     if (c->abort && warp == C::kMma) {   // products and copies in flight land before the memory goes
         if (lane == 0) {
+            atomicOr(p.status, static_cast<uint32_t>(PKV_DEV_TIMEOUT));
             umma_commit(&c->drain);
-            wait_until(&c->drain, 0, p.status, nullptr);
+            wait_for(&c->drain, 0, &c->late);
             constexpr uint32_t kRing = Q8 ? C::kCodes : C::kStages;
             uint64_t* full = Q8 ? c->code_full : c->full;
             const uint32_t n = c->issued;
             for (uint32_t i = n > kRing ? n - kRing : 0; i < n; ++i)
-                wait_until(&full[i % kRing], (i / kRing) & 1, p.status, nullptr, 200000000ull);
-            if (c->q_loads) wait_until(&c->q_full, (c->q_loads - 1) & 1, p.status, nullptr, 200000000ull);
+                wait_for(&full[i % kRing], (i / kRing) & 1, &c->late);
+            if (c->q_loads) wait_for(&c->q_full, (c->q_loads - 1) & 1, &c->late);
         }
         __syncwarp();
     }

@@ -129,6 +129,7 @@ struct ExtPiece {
     int32_t lo, hi;    // its KV blocks
     int32_t blocks;    // the tile's
     int32_t parts;     // lo == 0 and hi < blocks: CTAs (from this one on) that share the tile; else 0
+    ExtRow r;          // its row
 };
 
 // Walks one CTA's part of the line.  `rows` gives ExtRow by index.
@@ -139,15 +140,14 @@ struct ExtWalk {
     int32_t b, kvh, tile;
     ExtRow r;
 
-    // The part of `cta`, which begins in row b0, whose first unit is row_unit.
-    template <class Rows>
-    PKV_HD void begin(const ExtParts& parts, int32_t cta_, int32_t B_, int32_t Hkv_, int tt_, int32_t b0,
-                      int64_t row_unit, const Rows& rows) {
+    // The part of `cta`, which begins in row b0 = `row`, whose first unit is row_unit.
+    PKV_HD void begin(const ExtParts& parts, int32_t cta_, int32_t B_, int32_t Hkv_, int tt_, int32_t b0, const ExtRow& row,
+                      int64_t row_unit) {
         ps = parts, cta = cta_, B = B_, Hkv = Hkv_, tt = tt_;
         first = ps.begin(cta);
         end = ps.begin(cta + 1);
         b = b0;
-        r = rows(b);
+        r = row;
         unit = row_unit;
         for (kvh = 0; first - unit >= r.units; ++kvh) unit += r.units;
         tile = ext_tile_at(r, tt, first - unit);
@@ -160,7 +160,7 @@ struct ExtWalk {
         while (unit < end) {
             const int32_t nb = ext_tile_blocks(r, tt, tile);
             const int64_t b0 = unit + kTileUnits;   // the unit of block 0
-            p.b = b, p.kvh = kvh, p.tile = tile, p.blocks = nb, p.parts = 0;
+            p.b = b, p.kvh = kvh, p.tile = tile, p.blocks = nb, p.parts = 0, p.r = r;
             p.lo = first > b0 ? static_cast<int32_t>(first - b0) : 0;
             p.hi = end < b0 + nb ? static_cast<int32_t>(end - b0) : nb;
             if (p.lo == 0 && p.hi > 0 && p.hi < nb) p.parts = ps.of(b0 + nb - 1) - cta + 1;

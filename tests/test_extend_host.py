@@ -63,11 +63,11 @@ int main() {
             int b0 = 0;
             while (!(start[b0] <= first && first < start[b0] + rows[b0].units * Hkv)) ++b0;
             ExtWalk w;
-            w.begin(ps, c, B, Hkv, tt, b0, start[b0], get);
+            w.begin(ps, c, B, Hkv, tt, b0, rows[b0], start[b0]);
             ExtPiece p;
             int begun = 0, gone_on = 0;
             while (w.next(p, get)) {
-                REQUIRE(p.b < B && p.kvh < Hkv && p.tile < rows[p.b].tiles && p.lo < p.hi);
+                REQUIRE(p.r.tok0 == cu[p.b] && p.r.len == len[p.b] && p.b < B && p.kvh < Hkv && p.tile < rows[p.b].tiles && p.lo < p.hi);
                 begun += p.lo == 0 && p.hi < p.blocks;
                 gone_on += p.lo > 0;
                 seen[{p.b, p.kvh, p.tile}].push_back({c, p});
