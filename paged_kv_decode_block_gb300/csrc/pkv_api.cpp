@@ -371,11 +371,30 @@ int encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType type, int
 // {D, Hkv, num_pages * page_size} (innermost first); one box is 64 elements
 // (128 B) of kBlockRows consecutive tokens of one KV head, stored with the
 // 128-byte swizzle the kernels' shared-memory addressing expects.
-int encode_pool_map(CUtensorMap* map, const void* pool, const pkv_geom& g, int32_t page_size,
-                    int32_t box_tokens = pkv::kBlockRows) {
+int encode_pool_map(CUtensorMap* map, const void* pool, const pkv_geom& g, int32_t page_size) {
     return encode_map(map, pool, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.head_dim, g.num_kv_heads,
                       static_cast<int64_t>(g.num_pages) * page_size, static_cast<int64_t>(g.num_kv_heads) * g.head_dim,
-                      64, 1, box_tokens);   // 128 B x box_tokens
+                      64, 1, pkv::kBlockRows);   // 128 B x 16 tokens
+}
+
+// The pool [num_pages][page_size][Hkv][D] bf16 for pkv_extend, {64 elements, 8 tokens, halves of a
+// head, groups of 8 tokens, heads}: one box brings all of a head's elements of box_tokens tokens of a
+// page, 8 tokens by 64 elements together, which is how the matrix products read them.
+int encode_group_map(CUtensorMap* map, const void* pool, const pkv_geom& g, int32_t page_size, int32_t box_tokens) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return cuda_fail(cudaErrorNotSupported);
+    const cuuint64_t row = static_cast<cuuint64_t>(g.num_kv_heads) * g.head_dim * 2;   // bytes of a token
+    const cuuint32_t halves = static_cast<cuuint32_t>(g.head_dim / 64);
+    const cuuint64_t dims[5] = {64, 8, halves, static_cast<cuuint64_t>(g.num_pages) * page_size / 8,
+                                static_cast<cuuint64_t>(g.num_kv_heads)};
+    const cuuint64_t strides[4] = {row, 128, row * 8, static_cast<cuuint64_t>(g.head_dim) * 2};
+    const cuuint32_t box[5] = {64, 8, halves, static_cast<cuuint32_t>(box_tokens / 8), 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(pool), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
+    return PKV_OK;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -1160,7 +1179,7 @@ int extend(const pkv_queries* t, const void* k_pages, const void* v_pages, const
         if (rc) return rc;
         rc = scales ? encode_map(m.first, m.second, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.head_dim, g.num_kv_heads,
                                  pool_tokens, kv_row, g.head_dim, 1, box)
-                    : encode_pool_map(m.first, m.second, g, p->page_size, box);
+                    : encode_group_map(m.first, m.second, g, p->page_size, box);
     }
     if (rc) return rc;
     pkv::ExtendParams a{};

@@ -34,6 +34,7 @@ constexpr float kMoveAt = 8.0f;    // log2 by which the maximum outgrows the ref
 template <int D, bool Q8>
 struct Cfg {
     static constexpr int kHalves = D / 64;                    // 128-byte rows per head
+    static constexpr int kGroup = kHalves * 1024;             // 8 tokens of a block: [half][8 tokens][128 bytes]
     static constexpr int kTile = kExtBlock * D * 2;           // bytes of a K or V block in bf16
     static constexpr int kCode = kExtBlock * D;               // ... in e4m3
     static constexpr int kQ = kExtRows * D * 2;
@@ -110,6 +111,14 @@ __device__ __forceinline__ void lds128(uint32_t (&v)[4], uint32_t at) {
 __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+// 8-token groups from `group` on of one head: [group][half][8 tokens][64 elements]
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int group, int head, uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(head), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -168,8 +177,8 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
     uint64_t* full = Q8 ? c->code_full : c->full;
     uint64_t* empty = Q8 ? c->code_empty : c->empty;
     const int bt = p.box_tokens, nbox = kExtBlock / bt;
-    const int half = lane / nbox, x = lane % nbox;                  // this lane's box
-    const bool mine = half < (Q8 ? 1 : C::kHalves);
+    const int x = lane % nbox;                                      // this lane's box
+    const bool mine = lane < nbox;
     const int from = x * (bt / 16);                                 // the lane that knows its page
     const int per = kExtRows / 2 / p.G;                             // tokens of a group
     uint32_t n = 0, blocks = 0, q_loads = 0;
@@ -226,7 +235,7 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
             const int box_page = __shfl_sync(kFull, page, from);
             const int t = j * kExtBlock + x * bt;
             const int tok = page_ok(box_page) ? box_page * p.page_size + t % p.page_size : -1;
-            const uint32_t bytes = __popc(__ballot_sync(kFull, mine && tok >= 0)) * (kBox / (Q8 ? 1 : C::kHalves) / nbox);
+            const uint32_t bytes = __popc(__ballot_sync(kFull, mine && tok >= 0)) * (kBox / nbox);
             for (int kv = 0; kv < 2; ++kv, ++n) {
                 if (j == e.lo && kv == 1) {   // the queries, behind the first keys: their place is free later
                     if (q_loads > 0 && !wait_warp(&c->q_empty, (q_loads - 1) & 1, &c->abort)) return;
@@ -253,9 +262,13 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
                     mbar_arrive_expect_tx(&full[st], bytes);
                 }
                 __syncwarp();
-                if (mine && tok >= 0)
-                    tma_load_3d(ring + st * kBox + half * 16384 + x * bt * (Q8 ? D : 128), kv ? vmap : kmap,
-                                half * 64, e.kvh, tok, &full[st], policy);
+                if (mine && tok >= 0) {
+                    uint8_t* to = ring + st * kBox + x * (kBox / nbox);
+                    if (Q8)
+                        tma_load_3d(to, kv ? vmap : kmap, 0, e.kvh, tok, &full[st], policy);
+                    else
+                        tma_load_5d(to, kv ? vmap : kmap, tok / 8, e.kvh, &full[st], policy);
+                }
             }
             next_scale = scale(j + 1, next);
         }
@@ -306,8 +319,8 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
     constexpr uint32_t kIdQk = umma_idesc(kExtBlock, false), kIdPv = umma_idesc(D, true);
     const uint32_t tS = c->tmem + g * 128, tO = tS + 256;
     // descriptors count in 16 bytes: what is added to them never carries out of the address
-    const uint64_t q_first = umma_desc(smem_addr(smem), 16), k_desc = umma_desc(smem_addr(smem) + C::kQ, 16),
-                   v_desc = umma_desc(smem_addr(smem) + C::kQ, 16384);
+    const uint64_t q_first = umma_desc(smem_addr(smem), 16, 1024), k_desc = umma_desc(smem_addr(smem) + C::kQ, 16, C::kGroup),
+                   v_desc = umma_desc(smem_addr(smem) + C::kQ, 1024, C::kGroup);
     uint32_t fixed_phase = 0, q_loads = 0, done = 0, outs = 0, turns = 0;
     uint32_t st = 0, phase = 0;   // the ring's next block and its parity
 
@@ -318,15 +331,15 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
     auto qk = [&](uint64_t q_desc, uint32_t at) {   // S = Q K^T
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) / 16;
-            umma_ss(tS, q_desc + off, k_desc + at * (C::kTile / 16) + off, kIdQk, k > 0);
+            umma_ss(tS, q_desc + (k / 4) * (16384 / 16) + (k % 4) * 2, k_desc + at * (C::kTile / 16) + (k / 4) * (1024 / 16) + (k % 4) * 2,
+                    kIdQk, k > 0);
         }
         umma_commit(&c->s_full[g]);
     };
     auto pv = [&](uint32_t at, bool add) {   // O (+)= P V
 #pragma unroll
         for (int k = 0; k < kExtBlock / 16; ++k)
-            umma_ts(tO, tS + k * 8, v_desc + at * (C::kTile / 16) + k * (2048 / 16), kIdPv, add || k > 0);
+            umma_ts(tO, tS + k * 8, v_desc + at * (C::kTile / 16) + k * (2 * C::kGroup / 16), kIdPv, add || k > 0);
     };
     for (uint32_t pc = 0;; ++pc) {
         const int slot = pc % kPieceRing;
@@ -426,32 +439,30 @@ __device__ __forceinline__ void fix_values(const ExtendParams& p, Ctl* c, uint8_
             // rows that only some of the tile's rows see, then those behind the row's end
             const int seen = max(pi.limit0 - j * kExtBlock, 0), valid = min(len - j * kExtBlock, kExtBlock);
             const uint32_t tile = smem_addr(smem) + C::kQ + st * C::kTile;
-            uint32_t odd = 0;
-            for (int h = 0; h < C::kHalves; ++h) {
-                const uint32_t half = tile + h * 16384;
-                uint32_t any = 0;
+            constexpr int kPer = C::kHalves * 8;   // 16-byte pieces of a token
+            auto at = [&](int i) { return tile + i / (8 * kPer) * C::kGroup + i / 8 % C::kHalves * 1024 + i / kPer % 8 * 128 + i % 8 * 16; };
+            uint32_t any = 0;
 #pragma unroll 8
-                for (int i = seen * 8 + lane; i < valid * 8; i += 32) {
-                    uint32_t v[4];
-                    lds128(v, half + i * 16);
+            for (int i = seen * kPer + lane; i < valid * kPer; i += 32) {
+                uint32_t v[4];
+                lds128(v, at(i));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) any |= (v[k] & 0x7f807f80u) + 0x00800080u;
-                }
-                if (__any_sync(kFull, (any & 0x80008000u) != 0)) {
-                    odd = 1;
-                    for (int i = seen * 8 + lane; i < valid * 8; i += 32) {
-                        uint32_t v[4];
-                        lds128(v, half + i * 16);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if ((v[k] & 0x7f80u) == 0x7f80u) v[k] &= 0xffff0000u;
-                            if ((v[k] & 0x7f800000u) == 0x7f800000u) v[k] &= 0x0000ffffu;
-                        }
-                        sts128(half + i * 16, v[0], v[1], v[2], v[3]);
-                    }
-                }
-                for (int i = valid * 8 + lane; i < kExtBlock * 8; i += 32) sts128(half + i * 16, 0, 0, 0, 0);
+                for (int k = 0; k < 4; ++k) any |= (v[k] & 0x7f807f80u) + 0x00800080u;
             }
+            const bool odd = __any_sync(kFull, (any & 0x80008000u) != 0);
+            if (odd) {
+                for (int i = seen * kPer + lane; i < valid * kPer; i += 32) {
+                    uint32_t v[4];
+                    lds128(v, at(i));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if ((v[k] & 0x7f80u) == 0x7f80u) v[k] &= 0xffff0000u;
+                        if ((v[k] & 0x7f800000u) == 0x7f800000u) v[k] &= 0x0000ffffu;
+                    }
+                    sts128(at(i), v[0], v[1], v[2], v[3]);
+                }
+            }
+            for (int i = valid * kPer + lane; i < kExtBlock * kPer; i += 32) sts128(at(i), 0, 0, 0, 0);
             if (odd && lane == 0) pi.nonfinite = 1;
             fence_proxy_async_shared();
             __syncwarp();
@@ -492,7 +503,7 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
                 if (!wait_warp(&c->code_full[cs], (n / C::kCodes) & 1, &c->abort)) return;
                 if (n >= C::kStages && !wait_warp(&c->empty[st], (n / C::kStages - 1) & 1, &c->abort)) return;
                 const uint32_t src = codes + cs * C::kCode + tid * 16;
-                const uint32_t dst = q + C::kQ + st * C::kTile + half * 16384;
+                const uint32_t dst = q + C::kQ + st * C::kTile + half * 1024;
 #pragma unroll 1
                 for (int i = 0; i < kPerRow; i += 2) {
                     uint32_t v[2][4];   // (both loads first: the stores would hold the second up)
@@ -510,7 +521,7 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
                             o[2 * k] = e4m3x2_bf16x2(static_cast<uint16_t>(w));
                             o[2 * k + 1] = e4m3x2_bf16x2(static_cast<uint16_t>(w >> 16));
                         }
-                        const uint32_t first = (chunk % 4) * 2 + swap, at = dst + row * 128;
+                        const uint32_t first = (chunk % 4) * 2 + swap, at = dst + row / 8 * C::kGroup + row % 8 * 128;
                         const uint32_t a0 = at + ((first ^ (row & 7)) << 4), a1 = a0 ^ 16;
                         if (swap) {
                             sts128(a0, o[4], o[5], o[6], o[7]);
@@ -537,7 +548,7 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
                             if (row < seen || (!is_nan && !behind)) continue;
                             odd |= !behind;
                             const uint32_t x = (chunk % 4) * 2 + k / 8;
-                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + row * 128 + ((x ^ (row & 7)) << 4) + k % 8 * 2),
+                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + row / 8 * C::kGroup + row % 8 * 128 + ((x ^ (row & 7)) << 4) + k % 8 * 2),
                                          "h"(static_cast<uint16_t>(0))
                                          : "memory");
                         }

@@ -212,8 +212,9 @@ struct ExtendParams {
     float scale_log2;           // log2(e) / sqrt(D)
 };
 // qmap: q as [T][Hq][D], box {64, G, 128 / G}, swizzled by 128 bytes.  kmap / vmap: the
-// pools as [num_pages * page_size][Hkv][D], box {64, 1, box_tokens} swizzled (bf16) or
-// {D, 1, box_tokens} (e4m3).
+// bf16 pools as {64 elements, 8 tokens, D / 64 halves, groups of 8 tokens, heads}, box
+// {64, 8, D / 64, box_tokens / 8, 1}, swizzled; e4m3 pools as {D, heads, tokens}, box
+// {D, 1, box_tokens}.
 cudaError_t launch_extend(const ExtendParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
                           const CUtensorMap& vmap, int ctas, cudaStream_t stream);
 

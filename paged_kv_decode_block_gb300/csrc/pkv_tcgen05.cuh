@@ -63,12 +63,12 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // ------------------------------------------------------------------ matrix product
 
 // Shared-memory operand in 128-byte swizzled rows of 64 16-bit elements, 8 rows
-// (1024 bytes) after one another.  With the product's inner dimension along the
-// row (K-major) `lead` is not used; with the outer one along it (MN-major) it is
-// the distance in bytes from 64 elements to the next 64.
-__device__ __forceinline__ uint64_t umma_desc(uint32_t smem, uint32_t lead) {
+// (1024 bytes) together, the next 8 `group` bytes on.  With the product's inner
+// dimension along the row (K-major) `lead` is not used; with the outer one along it
+// (MN-major) it is the distance in bytes from 64 elements to the next 64.
+__device__ __forceinline__ uint64_t umma_desc(uint32_t smem, uint32_t lead, uint32_t group) {
     return static_cast<uint64_t>((smem & 0x3ffffu) >> 4) | static_cast<uint64_t>(lead >> 4) << 16 |
-           static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+           static_cast<uint64_t>(group >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 
 // bf16 x bf16 -> fp32, 128 rows, `n` columns; B's rows are its outer dimension
