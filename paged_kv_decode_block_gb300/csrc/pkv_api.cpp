@@ -346,14 +346,13 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// [tokens][heads][D] of bf16 (rows of a box swizzled by 128 bytes) or bytes (not swizzled), heads
-// dense, `stride` elements from token to token, as a 3-D tensor {D, heads, tokens}.
-int encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType type, int32_t D, int32_t heads, int64_t tokens,
-               int64_t stride, int32_t box_d, int32_t box_heads, int32_t box_tokens) {
+// [tokens][heads][D] of bf16 or bytes, heads dense, `stride` elements from token to token, as a 3-D
+// tensor {D, heads, tokens}.
+int encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, int32_t D,
+               int32_t heads, int64_t tokens, int64_t stride, int32_t box_d, int32_t box_heads, int32_t box_tokens) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return cuda_fail(cudaErrorNotSupported);
-    const bool bytes = type == CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    const cuuint64_t size = bytes ? 1 : 2;
+    const cuuint64_t size = type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
                                 static_cast<cuuint64_t>(tokens)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * size, static_cast<cuuint64_t>(stride) * size};
@@ -361,8 +360,7 @@ int encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType type, int
                                static_cast<cuuint32_t>(box_tokens)};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
     CUresult r = fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
     return PKV_OK;
 }
@@ -372,7 +370,7 @@ int encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType type, int
 // (128 B) of kBlockRows consecutive tokens of one KV head, stored with the
 // 128-byte swizzle the kernels' shared-memory addressing expects.
 int encode_pool_map(CUtensorMap* map, const void* pool, const pkv_geom& g, int32_t page_size) {
-    return encode_map(map, pool, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.head_dim, g.num_kv_heads,
+    return encode_map(map, pool, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, g.head_dim, g.num_kv_heads,
                       static_cast<int64_t>(g.num_pages) * page_size, static_cast<int64_t>(g.num_kv_heads) * g.head_dim,
                       64, 1, pkv::kBlockRows);   // 128 B x 16 tokens
 }
@@ -1173,13 +1171,19 @@ int extend(const pkv_queries* t, const void* k_pages, const void* v_pages, const
     const int64_t pool_tokens = static_cast<int64_t>(g.num_pages) * p->page_size;
     const int64_t kv_row = static_cast<int64_t>(g.num_kv_heads) * g.head_dim;
     CUtensorMap qmap{}, kmap{}, vmap{};
-    int rc = encode_map(&qmap, t->q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.head_dim, g.num_q_heads, t->total_tokens,
-                        q_stride, 64, G, 128 / G);
-    for (const auto& m : {std::make_pair(&kmap, k_pages), std::make_pair(&vmap, v_pages)}) {
-        if (rc) return rc;
-        rc = scales ? encode_map(m.first, m.second, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.head_dim, g.num_kv_heads,
-                                 pool_tokens, kv_row, g.head_dim, 1, box)
-                    : encode_group_map(m.first, m.second, g, p->page_size, box);
+    int rc = encode_map(&qmap, t->q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, g.head_dim,
+                        g.num_q_heads, t->total_tokens, q_stride, 64, G, 128 / G);
+    if (rc) return rc;
+    if (scales) {   // keys as the product reads them, values as the widening warps do
+        rc = encode_map(&kmap, k_pages, CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                        g.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, g.head_dim,
+                        g.num_kv_heads, pool_tokens, kv_row, g.head_dim, 1, box);
+        if (!rc)
+            rc = encode_map(&vmap, v_pages, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, g.head_dim,
+                            g.num_kv_heads, pool_tokens, kv_row, g.head_dim, 1, box);
+    } else {
+        rc = encode_group_map(&kmap, k_pages, g, p->page_size, box);
+        if (!rc) rc = encode_group_map(&vmap, v_pages, g, p->page_size, box);
     }
     if (rc) return rc;
     pkv::ExtendParams a{};

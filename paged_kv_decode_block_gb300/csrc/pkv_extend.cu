@@ -38,8 +38,10 @@ struct Cfg {
     static constexpr int kTile = kExtBlock * D * 2;           // bytes of a K or V block in bf16
     static constexpr int kCode = kExtBlock * D;               // ... in e4m3
     static constexpr int kQ = kExtRows * D * 2;
-    static constexpr int kStages = Q8 ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 10);
-    static constexpr int kCodes = Q8 ? (D == 128 ? 2 : 6) : 0;
+    // K and V take turns in one ring (bf16); or K's codes, V's codes and V in bf16 have a ring each (8-bit)
+    static constexpr int kStages = Q8 ? (D == 128 ? 2 : 4) : (D == 128 ? 5 : 10);
+    static constexpr int kKeys = Q8 ? (D == 128 ? 4 : 8) : 0;
+    static constexpr int kCodes = Q8 ? (D == 128 ? 2 : 4) : 0;
     static constexpr int kThreads = Q8 ? 512 : 384;
     // producer's warpgroup last: [0, 8) softmax; then bf16: 8 producer, 9 and 10 products, 11
     // fixer; 8-bit: [8, 12) widening, 12 producer, 13 and 14 products
@@ -47,7 +49,8 @@ struct Cfg {
     static constexpr int kMma = kProducer + 1;
     static constexpr int kFixer = Q8 ? -1 : 11;
     static constexpr int kReaders = Q8 ? 14 : 11;             // warps that read the piece ring
-    static constexpr size_t kBytes = static_cast<size_t>(kQ) + kStages * kTile + kCodes * kCode;
+    static constexpr int kKeysAt = kQ + kStages * kTile, kCodesAt = kKeysAt + kKeys * kCode;
+    static constexpr size_t kBytes = static_cast<size_t>(kCodesAt) + kCodes * kCode;
 };
 
 struct Piece {
@@ -64,11 +67,15 @@ struct Piece {
 
 struct Ctl {
     uint64_t full[10], empty[10], fixed[10];       // blocks in bf16, and V blocks cleaned
-    uint64_t code_full[8], code_empty[8];          // blocks in e4m3
+    uint64_t key_full[8], key_empty[8];            // blocks of K in e4m3
+    uint64_t code_full[4], code_empty[4];          // ... of V
+    uint64_t q_split[2];                           // the groups' queries in two e4m3 parts
     uint64_t scale_full[kScaleRing];
     uint64_t q_full, q_empty, drain;
     uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], pair_full, turn[2];
-    float2 pair_ml[128];                           // the second group's reference and sum, of shared rows
+    // of shared rows: (8-bit, at first) what the first group has scaled the query's parts by; the second group's
+    // reference and sum
+    float2 pair_ml[128];
     uint64_t piece_full[kPieceRing], piece_empty[kPieceRing];
     Piece piece[kPieceRing];
     float scales[kScaleRing][16];                  // 8 of K, 8 of V
@@ -78,7 +85,7 @@ struct Ctl {
     int32_t row0;
     volatile int abort, late;                      // a wait ran out; one at the end did too
     uint32_t tmem;
-    int32_t issued;                                // blocks that the producer has begun to load
+    int32_t issued;                                // K and V blocks that the producer has begun to load
     int32_t q_loads;
 };
 
@@ -171,11 +178,7 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
     using C = Cfg<D, Q8>;
     const int lane = threadIdx.x & 31;
     uint8_t* q_smem = smem;
-    uint8_t* ring = Q8 ? smem + C::kQ + C::kStages * C::kTile : smem + C::kQ;
-    constexpr int kRing = Q8 ? C::kCodes : C::kStages;
     constexpr int kBox = Q8 ? C::kCode : C::kTile;
-    uint64_t* full = Q8 ? c->code_full : c->full;
-    uint64_t* empty = Q8 ? c->code_empty : c->empty;
     const int bt = p.box_tokens, nbox = kExtBlock / bt;
     const int x = lane % nbox;                                      // this lane's box
     const bool mine = lane < nbox;
@@ -250,8 +253,11 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
                     }
                     ++q_loads;
                 }
-                const int st = n % kRing;
-                if (n >= kRing && !wait_warp(&empty[st], (n / kRing - 1) & 1, &c->abort)) return;
+                // the place: K's and V's rings, or the one of both
+                const uint32_t at = Q8 ? blocks : n, ring = Q8 ? (kv ? C::kCodes : C::kKeys) : C::kStages, st = at % ring;
+                uint64_t* full = Q8 ? (kv ? c->code_full : c->key_full) : c->full;
+                uint64_t* empty = Q8 ? (kv ? c->code_empty : c->key_empty) : c->empty;
+                if (at >= ring && !wait_warp(&empty[st], (at / ring - 1) & 1, &c->abort)) return;
                 if (Q8 && kv == 0) {
                     if (lane < 16) c->scales[blocks % kScaleRing][lane] = sc;
                     __syncwarp();
@@ -263,7 +269,7 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
                 }
                 __syncwarp();
                 if (mine && tok >= 0) {
-                    uint8_t* to = ring + st * kBox + x * (kBox / nbox);
+                    uint8_t* to = smem + (Q8 ? (kv ? C::kCodesAt : C::kKeysAt) : C::kQ) + st * kBox + x * (kBox / nbox);
                     if (Q8)
                         tma_load_3d(to, kv ? vmap : kmap, 0, e.kvh, tok, &full[st], policy);
                     else
@@ -316,23 +322,39 @@ template <int D, bool Q8>
 __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t* smem, const int g) {
     using C = Cfg<D, Q8>;
     const int per = kExtRows / 2 / p.G;
-    constexpr uint32_t kIdQk = umma_idesc(kExtBlock, false), kIdPv = umma_idesc(D, true);
-    const uint32_t tS = c->tmem + g * 128, tO = tS + 256;
-    // descriptors count in 16 bytes: what is added to them never carries out of the address
-    const uint64_t q_first = umma_desc(smem_addr(smem), 16, 1024), k_desc = umma_desc(smem_addr(smem) + C::kQ, 16, C::kGroup),
-                   v_desc = umma_desc(smem_addr(smem) + C::kQ, 1024, C::kGroup);
-    uint32_t fixed_phase = 0, q_loads = 0, done = 0, outs = 0, turns = 0;
-    uint32_t st = 0, phase = 0;   // the ring's next block and its parity
+    constexpr uint32_t kIdQk = Q8 ? umma_idesc_e4m3(kExtBlock) : umma_idesc(kExtBlock, false), kIdPv = umma_idesc(D, true);
+    const uint32_t tS = c->tmem + g * 128, tO = tS + 256, base = smem_addr(smem);
+    // descriptors count in 16 bytes: what is added to them never carries out of the address.  The parts of Q and the
+    // codes of K are rows of D bytes.
+    const uint64_t q_first = Q8 ? umma_desc_bytes<D>(base) : umma_desc(base, 16, 1024),
+                   k_desc = Q8 ? umma_desc_bytes<D>(base + C::kKeysAt) : umma_desc(base + C::kQ, 16, C::kGroup),
+                   v_desc = umma_desc(base + C::kQ, 1024, C::kGroup);
+    uint32_t fixed_phase = 0, q_loads = 0, done = 0, outs = 0, turns = 0, splits = 0;
+    struct Place {   // in a ring: the next block's, and its parity
+        uint32_t st = 0, phase = 0;
+        __device__ __forceinline__ void advance(uint32_t ring) {
+            if (++st == ring) st = 0, phase ^= 1;
+        }
+    } both, keys;
+    Place &v = both, &k = Q8 ? keys : both;
+    constexpr uint32_t kKeyRing = Q8 ? C::kKeys : C::kStages;
+    uint64_t* const key_full = Q8 ? c->key_full : c->full;
+    uint64_t* const key_empty = Q8 ? c->key_empty : c->empty;
 
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_for(bar, parity, &c->abort); };
-    auto advance = [&]() {
-        if (++st == C::kStages) st = 0, phase ^= 1;
-    };
-    auto qk = [&](uint64_t q_desc, uint32_t at) {   // S = Q K^T
+    auto qk = [&](uint64_t q_desc, uint32_t at, bool turn) {   // S = Q K^T
+        constexpr int kSteps = D / 16;   // bf16: 16 elements each; e4m3: 32, of both parts of Q
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            umma_ss(tS, q_desc + (k / 4) * (16384 / 16) + (k % 4) * 2, k_desc + at * (C::kTile / 16) + (k / 4) * (1024 / 16) + (k % 4) * 2,
-                    kIdQk, k > 0);
+        for (int k = 0; k < kSteps; ++k) {
+            // (the other thread wakes while the last two products go out)
+            if (k == kSteps - 2 && turn) mbar_arrive(&c->turn[1 - g]);
+            if constexpr (Q8) {
+                const int part = k / (kSteps / 2), step = k % (kSteps / 2);
+                umma_ss_e4m3(tS, q_desc + part * (C::kQ / 4 / 16) + step * 2, k_desc + at * (C::kCode / 16) + step * 2, kIdQk, k > 0);
+            } else {
+                umma_ss(tS, q_desc + (k / 4) * (16384 / 16) + (k % 4) * 2,
+                        k_desc + at * (C::kTile / 16) + (k / 4) * (1024 / 16) + (k % 4) * 2, kIdQk, k > 0);
+            }
         }
         umma_commit(&c->s_full[g]);
     };
@@ -353,33 +375,38 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
         if (nb == 0) continue;
         const uint64_t q_desc = q_first + (sh.pair ? 0 : g * (C::kQ / 2 / 16));
 
-        if (!wait(&c->q_full, q_loads++ & 1)) return;
-        if (!wait(&c->full[st], phase)) return;
+        const uint32_t q_phase = q_loads++ & 1;
+        if (!wait(&c->q_full, q_phase)) return;
+        if (Q8 && (g == 0 || sh.pair)) {   // (the loads of a piece's queries follow the products of the last one's)
+            if (!wait(&c->q_split[0], q_phase)) return;
+        } else if (Q8 && ntok > per) {
+            if (!wait(&c->q_split[1], splits++ & 1)) return;
+        }
+        if (!wait(&key_full[k.st], k.phase)) return;
         const bool turn = !sh.pair && ntok > per;   // (both threads find the same)
         if (turn && (g == 1 || turns > 0) && !wait(&c->turn[g], (g == 1 ? turns : turns - 1) & 1)) return;
         if (sh.count > 0 && sh.mine(0)) {
             tc_fence_after();
-            qk(q_desc, st);
-        }
-        if (turn) {
+            qk(q_desc, k.st, turn);
+        } else if (turn) {
             mbar_arrive(&c->turn[1 - g]);
-            ++turns;
         }
-        umma_commit(&c->empty[st]);
+        turns += turn;
+        umma_commit(&key_empty[k.st]);
         if (nb == 1) umma_commit(&c->q_empty);
-        advance();
+        k.advance(kKeyRing);
         bool add = false;
         for (int j = 0; j < nb; ++j) {
-            const uint32_t vs = st;
+            const uint32_t vs = v.st;
             if (j >= masked) {
                 if (!wait(&c->fixed[vs], (fixed_phase >> vs) & 1)) return;
                 fixed_phase ^= 1u << vs;
-            } else if (!wait(&c->full[vs], phase)) {
+            } else if (!wait(&c->full[vs], v.phase)) {
                 return;
             }
-            advance();
-            // (bf16: the next keys are there, as a rule, and are asked for while there is time; 8-bit: they are still being widened)
-            if (!Q8 && j + 1 < nb && !wait(&c->full[st], phase)) return;
+            v.advance(C::kStages);
+            // (the next keys are there, as a rule, and are asked for while there is time)
+            if (j + 1 < nb && !wait(&key_full[k.st], k.phase)) return;
             if (sh.mine(j)) {
                 if (!add && outs > 0 && !wait(&c->o_empty[g], (outs - 1) & 1)) return;
                 if (!wait(&c->p_full[g], done++ & 1)) return;
@@ -394,20 +421,18 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
                     ++outs;
                 }
             }
-            if (Q8 && j + 1 < nb && !wait(&c->full[st], phase)) return;
             if (j + 1 < nb && sh.mine(j + 1)) {
                 tc_fence_after();
-                qk(q_desc, st);
-            }
-            if (turn) {
+                qk(q_desc, k.st, turn);
+            } else if (turn) {
                 mbar_arrive(&c->turn[1 - g]);
-                ++turns;
             }
+            turns += turn;
             umma_commit(&c->empty[vs]);
             if (j + 1 < nb) {
-                umma_commit(&c->empty[st]);
+                umma_commit(&key_empty[k.st]);
                 if (j + 2 == nb) umma_commit(&c->q_empty);
-                advance();
+                k.advance(kKeyRing);
             }
         }
     }
@@ -476,9 +501,9 @@ __device__ __forceinline__ void fix_values(const ExtendParams& p, Ctl* c, uint8_
 
 // ------------------------------------------------------------------ e4m3 to bf16
 
-// Codes become bf16 exactly (4 bits of significand into 8); their scales join the
-// scores and the weights in fp32.  In blocks with masked places NaN codes of V become
-// 0, as infinities and NaN do in fix_values.
+// V's codes become bf16 exactly (4 bits of significand into 8); their scales join the
+// weights in fp32.  (K's go into the product as they are.)  In blocks with masked
+// places NaN codes become 0, as infinities and NaN do in fix_values.
 template <int D>
 __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* smem) {
     using C = Cfg<D, true>;
@@ -486,7 +511,7 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
     constexpr int kPerRow = D / 16;                       // threads of a token
     const int chunk = tid % kPerRow, half = chunk / 4;
     const uint32_t swap = half & 1;                       // the two halves' stores take other banks
-    const uint32_t q = smem_addr(smem), codes = q + C::kQ + C::kStages * C::kTile;
+    const uint32_t base = smem_addr(smem);
     uint32_t n = 0;
     for (uint32_t pc = 0;; ++pc) {
         const int slot = pc % kPieceRing;
@@ -494,79 +519,127 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
         Piece& pi = c->piece[slot];
         const int ntok = pi.ntok, lo = pi.lo, hi = pi.bad || ntok == 0 ? pi.lo : pi.hi, masked = first_masked(pi);
         const int len = ntok ? p.seq_lens[pi.b] : 0;
-        for (int j = lo; j < hi; ++j) {
-            const uint32_t blk = n / 2;
-            if (!wait_warp(&c->scale_full[blk % kScaleRing], (blk / kScaleRing) & 1, &c->abort)) return;
-            const float* scales = c->scales[blk % kScaleRing];
-            for (int kv = 0; kv < 2; ++kv, ++n) {
-                const uint32_t cs = n % C::kCodes, st = n % C::kStages;
-                if (!wait_warp(&c->code_full[cs], (n / C::kCodes) & 1, &c->abort)) return;
-                if (n >= C::kStages && !wait_warp(&c->empty[st], (n / C::kStages - 1) & 1, &c->abort)) return;
-                const uint32_t src = codes + cs * C::kCode + tid * 16;
-                const uint32_t dst = q + C::kQ + st * C::kTile + half * 1024;
+        for (int j = lo; j < hi; ++j, ++n) {
+            const uint32_t cs = n % C::kCodes, st = n % C::kStages;
+            if (!wait_warp(&c->code_full[cs], (n / C::kCodes) & 1, &c->abort)) return;
+            if (n >= C::kStages && !wait_warp(&c->empty[st], (n / C::kStages - 1) & 1, &c->abort)) return;
+            const uint32_t src = base + C::kCodesAt + cs * C::kCode + tid * 16;
+            const uint32_t dst = base + C::kQ + st * C::kTile + half * 1024;
+            const bool clean = j >= masked;
+            constexpr int kAtOnce = 4;
 #pragma unroll 1
-                for (int i = 0; i < kPerRow; i += 2) {
-                    uint32_t v[2][4];   // (both loads first: the stores would hold the second up)
-                    lds128(v[0], src + i * 2048);
-                    lds128(v[1], src + i * 2048 + 2048);
+            for (int i = 0; i < kPerRow; i += kAtOnce) {
+                uint32_t v[kAtOnce][4];   // (the loads first: the stores would hold them up)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int row = tid / kPerRow + (i + h) * (128 / kPerRow);
-                        // K's codes take their scale's sign
-                        const uint32_t sign = kv ? 0 : (__float_as_uint(scales[row / 16]) >> 31) * 0x80808080u;
-                        uint32_t o[8];
+                for (int h = 0; h < kAtOnce; ++h) lds128(v[h], src + (i + h) * 2048);
+                if (i + kAtOnce == kPerRow && !clean) {   // read: the next codes may come
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&c->code_empty[cs]);
+                }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t w = v[h][k] ^ sign;
-                            o[2 * k] = e4m3x2_bf16x2(static_cast<uint16_t>(w));
-                            o[2 * k + 1] = e4m3x2_bf16x2(static_cast<uint16_t>(w >> 16));
-                        }
-                        const uint32_t first = (chunk % 4) * 2 + swap, at = dst + row / 8 * C::kGroup + row % 8 * 128;
-                        const uint32_t a0 = at + ((first ^ (row & 7)) << 4), a1 = a0 ^ 16;
-                        if (swap) {
-                            sts128(a0, o[4], o[5], o[6], o[7]);
-                            sts128(a1, o[0], o[1], o[2], o[3]);
-                        } else {
-                            sts128(a0, o[0], o[1], o[2], o[3]);
-                            sts128(a1, o[4], o[5], o[6], o[7]);
-                        }
+                for (int h = 0; h < kAtOnce; ++h) {
+                    const int row = tid / kPerRow + (i + h) * (128 / kPerRow);
+                    uint32_t o[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        o[2 * k] = e4m3x2_bf16x2(static_cast<uint16_t>(v[h][k]));
+                        o[2 * k + 1] = e4m3x2_bf16x2(static_cast<uint16_t>(v[h][k] >> 16));
+                    }
+                    const uint32_t first = (chunk % 4) * 2 + swap, at = dst + row / 8 * C::kGroup + row % 8 * 128;
+                    const uint32_t a0 = at + ((first ^ (row & 7)) << 4), a1 = a0 ^ 16;
+                    if (swap) {
+                        sts128(a0, o[4], o[5], o[6], o[7]);
+                        sts128(a1, o[0], o[1], o[2], o[3]);
+                    } else {
+                        sts128(a0, o[0], o[1], o[2], o[3]);
+                        sts128(a1, o[4], o[5], o[6], o[7]);
                     }
                 }
-                const bool clean = kv == 1 && j >= masked;
-                if (clean) {
-                    // rows that not all of the tile's rows see, and what lies behind the row's end
-                    const int seen = max(pi.limit0 - j * kExtBlock, 0), valid = len - j * kExtBlock;
-                    bool odd = false;
-                    for (int i = 0; i < kPerRow; ++i) {
-                        const int row = tid / kPerRow + i * (128 / kPerRow);
-                        uint32_t v[4];
-                        lds128(v, src + i * 2048);
-                        for (int k = 0; k < 16; ++k) {
-                            uint32_t w = v[0];   // (no index into registers)
-                            w = k / 4 == 1 ? v[1] : k / 4 == 2 ? v[2] : k / 4 == 3 ? v[3] : w;
-                            const bool is_nan = (w >> (k % 4 * 8) & 0x7fu) == 0x7fu, behind = row >= valid;
-                            if (row < seen || (!is_nan && !behind)) continue;
-                            odd |= !behind;
-                            const uint32_t x = (chunk % 4) * 2 + k / 8;
-                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + row / 8 * C::kGroup + row % 8 * 128 + ((x ^ (row & 7)) << 4) + k % 8 * 2),
-                                         "h"(static_cast<uint16_t>(0))
-                                         : "memory");
-                        }
+            }
+            if (clean) {
+                // rows that not all of the tile's rows see, and what lies behind the row's end
+                const int seen = max(pi.limit0 - j * kExtBlock, 0), valid = len - j * kExtBlock;
+                bool odd = false;
+                for (int i = 0; i < kPerRow; ++i) {
+                    const int row = tid / kPerRow + i * (128 / kPerRow);
+                    uint32_t v[4];
+                    lds128(v, src + i * 2048);
+                    for (int k = 0; k < 16; ++k) {
+                        uint32_t w = v[0];   // (no index into registers)
+                        w = k / 4 == 1 ? v[1] : k / 4 == 2 ? v[2] : k / 4 == 3 ? v[3] : w;
+                        const bool is_nan = (w >> (k % 4 * 8) & 0x7fu) == 0x7fu, behind = row >= valid;
+                        if (row < seen || (!is_nan && !behind)) continue;
+                        odd |= !behind;
+                        const uint32_t x = (chunk % 4) * 2 + k / 8;
+                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + row / 8 * C::kGroup + row % 8 * 128 + ((x ^ (row & 7)) << 4) + k % 8 * 2),
+                                     "h"(static_cast<uint16_t>(0))
+                                     : "memory");
                     }
-                    if (__any_sync(kFull, odd) && lane == 0) pi.nonfinite = 1;
                 }
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&c->full[st]);
-                    mbar_arrive(&c->code_empty[cs]);
-                }
+                if (__any_sync(kFull, odd) && lane == 0) pi.nonfinite = 1;
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&c->full[st]);
+                if (clean) mbar_arrive(&c->code_empty[cs]);
             }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->piece_empty[slot]);
         if (ntok == 0) return;
     }
+}
+
+// ------------------------------------------------------------------ queries for e4m3 products
+
+// A row's query, bf16, becomes the sum of two e4m3 numbers in place, times a power of
+// two that brings its largest element to [2^7, 2^8): 4 bits of significand and the 4
+// that are left, exact for elements down to 2^-10 of the largest, and off by at most
+// 2^-18 of the largest below that.  Two e4m3 products cost what one of bf16 does, and
+// the cache's keys go into them untouched; widening them too took more of the
+// scheduler's slots than the softmax does (2048 tokens after 6144, 32/8 heads, D 128:
+// 252 us).  Returns what the scores are to be multiplied by; NaN if an element is not
+// finite.
+template <int D>
+__device__ __forceinline__ float split_query(uint32_t at, int row, int barrier) {
+    uint32_t q[D / 2];   // pairs
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+        uint32_t v[4];
+        lds128(v, at + i / 8 * 16384 + row * 128 + ((i % 8 ^ (row & 7)) << 4));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q[4 * i + k] = v[k];
+    }
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < D / 2; ++i) most = max(most, max(q[i] & 0x7fff0000u, q[i] << 16 & 0x7fff0000u));
+    const uint32_t e = max(most >> 23, 8u);   // exponent of the largest
+    const float by = __uint_as_float((261 - e) << 23);
+    if (D == 64) named_barrier_sync(barrier, 128);   // rows of 64 bytes lie in other rows' places
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t h2[2], l2[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint32_t w = q[8 * i + 2 * k + u];
+                const float x = __uint_as_float(w << 16) * by, y = __uint_as_float(w & 0xffff0000u) * by;
+                h2[u] = e4m3x2(x, y);
+                const F2 b = e4m3x2_f32(static_cast<uint16_t>(h2[u]));
+                l2[u] = e4m3x2(x - b.x, y - b.y);
+            }
+            hi[k] = h2[0] | h2[1] << 16;
+            lo[k] = l2[0] | l2[1] << 16;
+        }
+        // (D = 64: a row is 64 bytes, whose four pieces change places with pairs of rows)
+        const uint32_t to = D == 128 ? at + row * 128 + ((i ^ (row & 7)) << 4) : at + row * 64 + ((i ^ (row >> 1 & 3)) << 4);
+        sts128(to, hi[0], hi[1], hi[2], hi[3]);
+        sts128(to + 128 * D, lo[0], lo[1], lo[2], lo[3]);
+    }
+    return most >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __uint_as_float((e - 7) << 23);
 }
 
 // ------------------------------------------------------------------ softmax and outputs
@@ -669,6 +742,22 @@ __device__ __forceinline__ void mask_scores(uint32_t tS, int seen) {
     tmem_wait_st();
 }
 
+// Scores of keys with a scale below 0 change their sign, where they lie (16 columns a scale).
+__device__ __forceinline__ void turn_scores(uint32_t tS, const float* scales) {
+#pragma unroll 1
+    for (int k = 0; k < kExtBlock; k += 32) {
+        uint32_t s[32];
+        tmem_ld32(s, tS + k);
+        tmem_wait_ld();
+        tmem_loaded32(s);
+        const uint32_t a = __float_as_uint(scales[k / 16]) & 0x80000000u, b = __float_as_uint(scales[k / 16 + 1]) & 0x80000000u;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] ^= i < 16 ? a : b;
+        tmem_st32(tS + k, s);
+    }
+    tmem_wait_st();
+}
+
 // One block of a row's scores to weights: maximum, 2^(c s - m), sum; weights in
 // bf16 over the scores.  All 128 scores stay in registers between the two passes.
 template <int D>
@@ -707,7 +796,7 @@ __device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float cs
 }
 
 // The same over the 8-bit cache: 16 scores share a scale of K, their weights one of
-// V.  `scales` has K's 8 (whose signs have gone into the codes) and V's 8; those of
+// V.  `scales` has K's 8 (whose signs have gone into the scores) and V's 8; those of
 // blocks that the row does not see at all may be anything.  The scores are read
 // twice, as the widening warps leave too few registers to hold them.
 template <int D>
@@ -764,13 +853,13 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
 }
 
 template <int D, bool Q8>
-__device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
+__device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* smem) {
     using C = Cfg<D, Q8>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = warp >> 2, row = threadIdx.x & 127;
     const int shift = 31 - __clz(p.G), per = kExtRows / 2 >> shift;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
     const uint32_t tS = c->tmem + lanes + g * 128, tO = c->tmem + lanes + 256 + g * 128;
-    uint32_t done = 0, outs = 0, blocks = 0, pairs = 0;
+    uint32_t done = 0, outs = 0, blocks = 0, pairs = 0, q_loads = 0;
     for (uint32_t pc = 0;; ++pc) {
         const int slot = pc % kPieceRing;
         if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, &c->abort)) return false;
@@ -785,7 +874,24 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
         const bool warp_live = base_row + (row & ~31) < pi.ntok << shift;   // some row of the warp does
         const int limit = pi.limit0 + ((base_row + row) >> shift);          // tokens that the row sees
         const int masked = first_masked(pi);
-        float m = -INFINITY, l = 0.0f;
+        float m = -INFINITY, l = 0.0f, cs = p.scale_log2;
+        if (Q8 && sh.nb > 0) {   // (every piece's load is waited for: a parity tells a phase from the next one only)
+            const uint32_t phase = q_loads++ & 1;
+            if (!wait_warp(&c->q_full, phase, &c->abort)) return false;
+            if (sh.pair && g == 1) {
+                if (!wait_warp(&c->q_split[0], phase, &c->abort)) return false;
+                cs *= c->pair_ml[row].x;
+            } else if (pi.ntok > g * per) {
+                if (D == 64 || warp_live) {
+                    const float scale = split_query<D>(smem_addr(smem) + g * (C::kQ / 2), row, 1 + g);
+                    if (sh.pair) c->pair_ml[row].x = scale;
+                    cs *= scale;
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c->q_split[g]);
+            }
+        }
         for (int j = 0; j < nb; ++j) {
             if (!wait_warp(&c->s_full[g], done & 1, &c->abort)) return false;
             ++done;
@@ -800,9 +906,10 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c) {
                     if (!wait_warp(&c->scale_full[b % kScaleRing], (b / kScaleRing) & 1, &c->abort)) return false;
                     scales = c->scales[b % kScaleRing];
                 }
+                if (Q8 && __any_sync(kFull, scales[lane & 7] < 0.0f)) turn_scores(tS, scales);
                 if (cut) mask_scores(tS, seen);
                 if constexpr (Q8)
-                    softmax_block_q8<D>(tS, tO, p.scale_log2, scales, cut ? seen : kExtBlock, j == 0, m, l);
+                    softmax_block_q8<D>(tS, tO, cs, scales, cut ? seen : kExtBlock, j == 0, m, l);
                 else
                     softmax_block<D>(tS, tO, p.scale_log2, j == 0, m, l);
                 tmem_wait_st();
@@ -938,6 +1045,10 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
             mbar_init(&c->empty[i], 2);
             mbar_init(&c->fixed[i], 1);
         }
+        for (int i = 0; i < C::kKeys; ++i) {
+            mbar_init(&c->key_full[i], 1);
+            mbar_init(&c->key_empty[i], 2);
+        }
         for (int i = 0; i < C::kCodes; ++i) {
             mbar_init(&c->code_full[i], 1);
             mbar_init(&c->code_empty[i], 4);
@@ -953,6 +1064,7 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
             mbar_init(&c->o_full[g], 1);
             mbar_init(&c->o_empty[g], 4);
             mbar_init(&c->turn[g], 1);
+            mbar_init(&c->q_split[g], 4);
         }
         for (int i = 0; i < kPieceRing; ++i) {
             mbar_init(&c->piece_full[i], 1);
@@ -1012,7 +1124,7 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
                 asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
             else
                 asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-            if (!attend<D, Q8>(p, c)) {
+            if (!attend<D, Q8>(p, c, smem)) {
                 poison<D>(p, c, parts, rows);
             }
         } else if (Q8 && warp < 12) {
@@ -1046,11 +1158,12 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
             atomicOr(p.status, static_cast<uint32_t>(PKV_DEV_TIMEOUT));
             umma_commit(&c->drain);
             wait_for(&c->drain, 0, &c->late);
-            constexpr uint32_t kRing = Q8 ? C::kCodes : C::kStages;
-            uint64_t* full = Q8 ? c->code_full : c->full;
             const uint32_t n = c->issued;
-            for (uint32_t i = n > kRing ? n - kRing : 0; i < n; ++i)
-                wait_for(&full[i % kRing], (i / kRing) & 1, &c->late);
+            for (uint32_t i = n > 16 ? n - 16 : 0; i < n; ++i) {   // (more than any ring holds; those before have landed)
+                const uint32_t at = Q8 ? i / 2 : i, ring = Q8 ? (i % 2 ? C::kCodes : C::kKeys) : C::kStages;
+                uint64_t* full = Q8 ? (i % 2 ? c->code_full : c->key_full) : c->full;
+                if (at + ring >= (Q8 ? (n + 1) / 2 : n)) wait_for(&full[at % ring], (at / ring) & 1, &c->late);
+            }
             if (c->q_loads) wait_for(&c->q_full, (c->q_loads - 1) & 1, &c->late);
         }
         __syncwarp();

@@ -77,11 +77,29 @@ __host__ __device__ constexpr uint32_t umma_idesc(int n, bool b_mn) {
     return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
 }
 
+// Operand in rows of D bytes (8-bit elements, K-major), 64 or 128, swizzled by as many.
+template <int D>
+__device__ __forceinline__ uint64_t umma_desc_bytes(uint32_t smem) {
+    return static_cast<uint64_t>((smem & 0x3ffffu) >> 4) | 1ull << 16 | static_cast<uint64_t>(8 * D >> 4) << 32 | 1ull << 46 |
+           (D == 128 ? 2ull : 4ull) << 61;
+}
+// e4m3 x e4m3 -> fp32, 128 rows, `n` columns, both K-major
+__host__ __device__ constexpr uint32_t umma_idesc_e4m3(int n) {
+    return 1u << 4 | static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
+}
+
 // D (tensor memory) = A * B, or += if `add`; one thread issues it.  A in shared memory.
 __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+__device__ __forceinline__ void umma_ss_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
         : "memory");
 }
@@ -146,12 +164,22 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return r;
 }
 // two e4m3 codes, exactly (through f16)
-__device__ __forceinline__ uint32_t e4m3x2_bf16x2(uint16_t codes) {
+__device__ __forceinline__ F2 e4m3x2_f32(uint16_t codes) {
     uint32_t h;
-    float lo, hi;
+    F2 r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(lo), "=f"(hi) : "r"(h));
-    return bf16x2(lo, hi);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(r.x), "=f"(r.y) : "r"(h));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_bf16x2(uint16_t codes) {
+    const F2 r = e4m3x2_f32(codes);
+    return bf16x2(r.x, r.y);
+}
+// {lo, hi} rounded to e4m3, lo in the lower byte
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 }  // namespace
