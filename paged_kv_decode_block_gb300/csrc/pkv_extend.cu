@@ -342,6 +342,8 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
     uint64_t* const key_empty = Q8 ? c->key_empty : c->empty;
 
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_for(bar, parity, &c->abort); };
+    // (unrolled, with the descriptors' steps as constants: a product takes 64 cycles, and a loop no fewer to issue one;
+    // 2048 tokens after 6144 182 us against 230)
     auto qk = [&](uint64_t q_desc, uint32_t at, bool turn) {   // S = Q K^T
         constexpr int kSteps = D / 16;   // bf16: 16 elements each; e4m3: 32, of both parts of Q
 #pragma unroll
@@ -382,38 +384,30 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
         } else if (Q8 && ntok > per) {
             if (!wait(&c->q_split[1], splits++ & 1)) return;
         }
-        if (!wait(&key_full[k.st], k.phase)) return;
         const bool turn = !sh.pair && ntok > per;   // (both threads find the same)
-        if (turn && (g == 1 || turns > 0) && !wait(&c->turn[g], (g == 1 ? turns : turns - 1) & 1)) return;
-        if (sh.count > 0 && sh.mine(0)) {
-            tc_fence_after();
-            qk(q_desc, k.st, turn);
-        } else if (turn) {
-            mbar_arrive(&c->turn[1 - g]);
-        }
-        turns += turn;
-        umma_commit(&key_empty[k.st]);
-        if (nb == 1) umma_commit(&c->q_empty);
-        k.advance(kKeyRing);
         bool add = false;
-        for (int j = 0; j < nb; ++j) {
-            const uint32_t vs = v.st;
-            if (j >= masked) {
-                if (!wait(&c->fixed[vs], (fixed_phase >> vs) & 1)) return;
-                fixed_phase ^= 1u << vs;
-            } else if (!wait(&c->full[vs], v.phase)) {
-                return;
+        for (int j = -1; j < nb; ++j) {   // PV of block j, QK of the next
+            uint32_t vs = 0;
+            if (j >= 0) {
+                vs = v.st;
+                if (j >= masked) {
+                    if (!wait(&c->fixed[vs], (fixed_phase >> vs) & 1)) return;
+                    fixed_phase ^= 1u << vs;
+                } else if (!wait(&c->full[vs], v.phase)) {
+                    return;
+                }
+                v.advance(C::kStages);
             }
-            v.advance(C::kStages);
             // (the next keys are there, as a rule, and are asked for while there is time)
             if (j + 1 < nb && !wait(&key_full[k.st], k.phase)) return;
-            if (sh.mine(j)) {
+            const bool mine = j >= 0 && sh.mine(j);
+            if (mine) {
                 if (!add && outs > 0 && !wait(&c->o_empty[g], (outs - 1) & 1)) return;
                 if (!wait(&c->p_full[g], done++ & 1)) return;
             }
-            if (turn && !wait(&c->turn[g], (g == 1 ? turns : turns - 1) & 1)) return;
-            if (sh.mine(j)) {
-                tc_fence_after();
+            if (turn && (g == 1 || turns > 0) && !wait(&c->turn[g], (g == 1 ? turns : turns - 1) & 1)) return;
+            tc_fence_after();
+            if (mine) {
                 pv(vs, add);
                 add = true;
                 if (sh.last(j)) {
@@ -421,14 +415,12 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
                     ++outs;
                 }
             }
-            if (j + 1 < nb && sh.mine(j + 1)) {
-                tc_fence_after();
+            if (j + 1 < nb && sh.mine(j + 1))
                 qk(q_desc, k.st, turn);
-            } else if (turn) {
+            else if (turn)
                 mbar_arrive(&c->turn[1 - g]);
-            }
             turns += turn;
-            umma_commit(&c->empty[vs]);
+            if (j >= 0) umma_commit(&c->empty[vs]);
             if (j + 1 < nb) {
                 umma_commit(&key_empty[k.st]);
                 if (j + 2 == nb) umma_commit(&c->q_empty);
