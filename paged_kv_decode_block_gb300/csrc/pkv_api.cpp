@@ -1557,8 +1557,8 @@ int pkv_copy_pages(const pkv_page_pool* pools_h, int32_t n_pools, const pkv_page
             const bool wide = (x.page_bytes / units) % 16 == 0 && at % 16 == 0;
             const int64_t vec = wide ? 16 : 4;
             pools[i] = pkv::CopyPool{x.data, static_cast<uint32_t>(x.page_bytes / vec),
-                                     static_cast<uint32_t>(x.page_bytes / units / vec), 0,
-                                     static_cast<uint16_t>(x.unit_tokens), static_cast<uint16_t>(wide)};
+                                     static_cast<uint32_t>(x.page_bytes / units / vec),
+                                     static_cast<uint16_t>(x.unit_tokens), static_cast<uint16_t>(wide), 0, 0};
         }
         // few copies are compared in pairs, many through a mark on each page: 1 a source, 2 a target
         const bool pairs = n_copies <= 32;

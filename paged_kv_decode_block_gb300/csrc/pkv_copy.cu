@@ -5,20 +5,44 @@
 // compaction copies is many short stretches (a tail page of a few KB, a block's
 // scales of 32 bytes) in many pools, so all of them go into one launch: the list of
 // copies and the pools travel as the kernel's parameter (no upload, no memory that a
-// later call could overwrite), and each pool's copies form one line of vectors,
-// (copy, vector of the page), of which a block takes kItem at a time whatever the
-// page's size.  Vectors behind a copy's tokens are passed over.
+// later call could overwrite).  A block takes one work item at a time: 32 KB of one
+// page, of which the vectors behind the copied tokens cost nothing, or, where pages
+// are smaller, that much of the pool's line of (copy, vector of the page).
 #include "pkv_device.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kEach = 4;                  // vectors of a thread in flight
+constexpr int kEach = 8;                  // vectors of a thread in flight
 constexpr int kItem = kThreads * kEach;   // vectors of a work item
 
+__device__ __forceinline__ uint32_t vectors_of(const CopyPool& pool, int32_t tokens) {
+    return (tokens + pool.unit_tokens - 1) / pool.unit_tokens * pool.unit_vecs;
+}
+
+// A stretch of one page.
 template <class V>
-__device__ __forceinline__ void copy_item(const CopyPool& pool, const pkv_page_copy* copies, uint32_t first, uint32_t total) {
+__device__ __forceinline__ void copy_stretch(const CopyPool& pool, const pkv_page_copy& cp, uint32_t first) {
+    const uint32_t n = vectors_of(pool, cp.tokens);
+    const V* from = static_cast<const V*>(pool.data) + static_cast<size_t>(cp.src) * pool.page_vecs;
+    V* to = static_cast<V*>(pool.data) + static_cast<size_t>(cp.dst) * pool.page_vecs;
+    V v[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const uint32_t k = first + i * kThreads + threadIdx.x;
+        if (k < n) v[i] = from[k];
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const uint32_t k = first + i * kThreads + threadIdx.x;
+        if (k < n) to[k] = v[i];
+    }
+}
+
+// A stretch of a pool's line.
+template <class V>
+__device__ __forceinline__ void copy_line(const CopyPool& pool, const pkv_page_copy* copies, uint32_t first, uint32_t total) {
     V v[kEach];
     V* to[kEach];
 #pragma unroll
@@ -28,7 +52,7 @@ __device__ __forceinline__ void copy_item(const CopyPool& pool, const pkv_page_c
         if (at >= total) continue;
         const uint32_t c = at / pool.page_vecs, k = at - c * pool.page_vecs;
         const pkv_page_copy cp = copies[c];
-        if (k >= (cp.tokens + pool.unit_tokens - 1) / pool.unit_tokens * pool.unit_vecs) continue;
+        if (k >= vectors_of(pool, cp.tokens)) continue;
         V* base = static_cast<V*>(pool.data);
         to[i] = base + static_cast<size_t>(cp.dst) * pool.page_vecs + k;
         v[i] = base[static_cast<size_t>(cp.src) * pool.page_vecs + k];
@@ -52,11 +76,18 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ 
                 hi = mid - 1;
         }
         const CopyPool& pool = p.pools[lo];
-        const uint32_t first = (item - pool.first_item) * kItem, total = p.num_copies * pool.page_vecs;
-        if (pool.wide)
-            copy_item<uint4>(pool, p.copies, first, total);
-        else
-            copy_item<uint32_t>(pool, p.copies, first, total);
+        const uint32_t at = item - pool.first_item;
+        if (pool.stretches) {
+            const uint32_t c = at / pool.stretches, first = (at - c * pool.stretches) * kItem;
+            if (pool.wide)
+                copy_stretch<uint4>(pool, p.copies[c], first);
+            else
+                copy_stretch<uint32_t>(pool, p.copies[c], first);
+        } else if (pool.wide) {
+            copy_line<uint4>(pool, p.copies, at * kItem, p.num_copies * pool.page_vecs);
+        } else {
+            copy_line<uint32_t>(pool, p.copies, at * kItem, p.num_copies * pool.page_vecs);
+        }
     }
 }
 
@@ -81,7 +112,10 @@ cudaError_t launch(const CopyPool* pools, int num_pools, const pkv_page_copy* co
     for (int i = 0; i < num_pools; ++i) {
         p.pools[i] = pools[i];
         p.pools[i].first_item = items;
-        items += (static_cast<uint32_t>(num_copies) * pools[i].page_vecs + kItem - 1) / kItem;
+        // pages of at least half an item are taken one by one
+        p.pools[i].stretches = pools[i].page_vecs >= kItem / 2 ? (pools[i].page_vecs + kItem - 1) / kItem : 0;
+        items += p.pools[i].stretches ? num_copies * p.pools[i].stretches
+                                      : (static_cast<uint32_t>(num_copies) * pools[i].page_vecs + kItem - 1) / kItem;
     }
     p.items = items;
     for (int i = 0; i < num_copies; ++i) p.copies[i] = copies[i];

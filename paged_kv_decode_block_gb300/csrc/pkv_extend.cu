@@ -1167,40 +1167,74 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
 
 // The parts of a tile that several CTAs shared, weighted by 2^(m - max m).  One
 // block per CTA that began such a tile and 32 of its rows; lanes are rows (the
-// layout in which the states were left), warps take columns.
+// layout in which the states were left).  What it waits for is memory: the
+// references and sums of all parts come in one round (warps take parts), then the
+// states, of which a warp takes an eighth of the columns and eight parts at once.
 template <int D>
 __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant__ ExtendParams p) {
+    extern __shared__ float weights[];   // [part][32 rows]; -1: saw nothing, its state was not written
+    __shared__ float part_of[2][8][32];
     grid_dependency_wait();
     const ExtSplit sp = p.splits[blockIdx.x];
-    const int row = blockIdx.y * 32 + (threadIdx.x & 31);
-    if (row >= sp.ntok * p.G) return;
-    const int first = 2 * blockIdx.x + 1;
-    auto slot = [&](int i) { return i == 0 ? first : 2 * (static_cast<int>(blockIdx.x) + i); };
-    float m = -INFINITY, l = 0.0f;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y * 32 + lane;
+    if (static_cast<int>(blockIdx.y) * 32 >= sp.ntok * p.G) return;   // (the block as a whole: rows behind the last are done for nothing)
+    auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)); };
+    float m = -INFINITY;
     bool nan = false;
-    for (int i = 0; i < sp.parts; ++i) {
-        const float2 s = p.ws_ml[static_cast<size_t>(slot(i)) * kExtRows + row];
-        nan |= s.x != s.x;
+#pragma unroll 4
+    for (int i = warp; i < sp.parts; i += 8) {
+        const float2 s = p.ws_ml[slot(i) * kExtRows + row];
         m = fmaxf(m, s.x);
+        nan |= s.x != s.x;
+    }
+    part_of[0][warp][lane] = nan ? __uint_as_float(0x7fffffffu) : m;
+    __syncthreads();
+    nan = false;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        const float x = part_of[0][w][lane];
+        m = fmaxf(m, x);
+        nan |= x != x;
     }
     const float ref = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f;
+#pragma unroll 4
+    for (int i = warp; i < sp.parts; i += 8) {
+        const float2 s = p.ws_ml[slot(i) * kExtRows + row];
+        const float f = ex2(s.x - ref);
+        weights[i * 32 + lane] = s.y == 0.0f ? -1.0f : f;
+        l += s.y * f;
+    }
+    part_of[1][warp][lane] = l;
+    __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) l += part_of[1][w][lane];
     constexpr int kCols = D / 4 / 8;   // columns (of four) of a warp
-    const int warp = threadIdx.x >> 5;
     float4 o[kCols];
 #pragma unroll
     for (int k = 0; k < kCols; ++k) o[k] = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-    for (int i = 0; i < sp.parts; ++i) {
-        const float2 s = p.ws_ml[static_cast<size_t>(slot(i)) * kExtRows + row];
-        if (s.y == 0.0f) continue;   // saw nothing; its state was not written
-        const float f = ex2(s.x - ref);
-        l += s.y * f;
+    constexpr int kAtOnce = 16 / kCols;   // (16 loads of a thread in flight; a state that was not written is read too, and left out)
+    for (int i0 = 0; i0 < sp.parts; i0 += kAtOnce) {
+        float4 x[kAtOnce][kCols];
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) {
-            const float4 x = reinterpret_cast<const float4*>(p.ws_o)[(static_cast<size_t>(slot(i)) * (D / 4) + warp * kCols + k) * kExtRows + row];
-            o[k].x += x.x * f, o[k].y += x.y * f, o[k].z += x.z * f, o[k].w += x.w * f;
+        for (int i = 0; i < kAtOnce; ++i) {
+            const float4* from = reinterpret_cast<const float4*>(p.ws_o) +
+                                 (slot(min(i0 + i, sp.parts - 1)) * (D / 4) + warp * kCols) * kExtRows + row;
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) x[i][k] = from[static_cast<size_t>(k) * kExtRows];
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            if (i0 + i >= sp.parts) break;
+            const float f = weights[(i0 + i) * 32 + lane];
+            if (f == -1.0f) continue;
+#pragma unroll
+            for (int k = 0; k < kCols; ++k)
+                o[k].x += x[i][k].x * f, o[k].y += x[i][k].y * f, o[k].z += x[i][k].z * f, o[k].w += x[i][k].w * f;
         }
     }
+    if (row >= sp.ntok * p.G) return;
     float inv = l == 0.0f ? 0.0f : 1.0f / l;
     if (nan) inv = l = __uint_as_float(0x7fffffffu);
     const int shift = 31 - __clz(p.G);
@@ -1208,8 +1242,9 @@ __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant
     const int head = sp.kvh * p.G + (row & (p.G - 1));
     uint16_t* out = p.out + tok * p.out_stride + static_cast<int64_t>(head) * D + warp * kCols * 4;
 #pragma unroll
-    for (int k = 0; k < kCols; ++k)
-        *reinterpret_cast<uint2*>(out + 4 * k) = make_uint2(bf16x2(o[k].x * inv, o[k].y * inv), bf16x2(o[k].z * inv, o[k].w * inv));
+    for (int k = 0; k < kCols; k += 2)
+        *reinterpret_cast<uint4*>(out + 4 * k) = make_uint4(bf16x2(o[k].x * inv, o[k].y * inv), bf16x2(o[k].z * inv, o[k].w * inv),
+                                                            bf16x2(o[k + 1].x * inv, o[k + 1].y * inv), bf16x2(o[k + 1].z * inv, o[k + 1].w * inv));
     if (warp == 0 && p.lse) p.lse[tok * p.Hq + head] = kLn2 * (m + log2f(l));
 }
 
@@ -1235,7 +1270,7 @@ cudaError_t launch(const ExtendParams& p, const CUtensorMap& qmap, const CUtenso
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(ctas, kExtRows / 32);
     cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = 0;
+    cfg.dynamicSmemBytes = static_cast<size_t>(ctas) * 32 * sizeof(float);   // (19 KB: a tile has at most a part on each SM)
     return cudaLaunchKernelEx(&cfg, extend_merge_kernel<D>, p);
 }
 

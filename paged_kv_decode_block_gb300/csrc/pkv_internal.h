@@ -219,14 +219,15 @@ cudaError_t launch_extend(const ExtendParams& p, const CUtensorMap& qmap, const 
                           const CUtensorMap& vmap, int ctas, cudaStream_t stream);
 
 // Page copies in all pools of a cache (pkv_copy_pages), on the current device.
-constexpr int kCopyMaxPools = 192;     // of one launch: what its parameters hold
+constexpr int kCopyMaxPools = 192;     // of one launch: what its parameters hold (32764 bytes)
 constexpr int kCopyMaxCopies = 2048;
 struct CopyPool {
     void* data;
     uint32_t page_vecs;         // vectors (16 bytes if `wide`, else 4) of a page
     uint32_t unit_vecs;         // ... of unit_tokens tokens
-    uint32_t first_item;        // set by launch_copy_pages
     uint16_t unit_tokens, wide;
+    uint32_t first_item;        // set by launch_copy_pages: its first work item,
+    uint32_t stretches;         // items of a page (0: an item takes several pages)
 };
 cudaError_t launch_copy_pages(const CopyPool* pools, int num_pools, const pkv_page_copy* copies, int num_copies,
                               int num_sms, cudaStream_t stream);
