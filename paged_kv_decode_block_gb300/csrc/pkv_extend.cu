@@ -53,16 +53,19 @@ struct Cfg {
     static constexpr size_t kBytes = static_cast<size_t>(kCodesAt) + kCodes * kCode;
 };
 
-struct Piece {
+struct alignas(16) Piece {
     int32_t tok0, ntok;     // the tile's tokens in q / out (ntok 0: no more pieces)
     int32_t kvh, b;
     int32_t limit0;         // tokens that the first one sees
     int32_t lo, hi;         // KV blocks
     int32_t slot;           // workspace slot, or -1: the whole tile
+    int32_t len;            // the row's tokens
     int32_t bad;            // no products: NaN
+    int32_t pad[2];
+};
+struct Found {              // about a piece, while it is worked on
     volatile int32_t poison;      // a page of it does not exist
     volatile int32_t nonfinite;   // V held infinities or NaN in a block with masked places
-    int32_t pad[5];
 };
 
 struct Ctl {
@@ -78,6 +81,7 @@ struct Ctl {
     float2 pair_ml[128];
     uint64_t piece_full[kPieceRing], piece_empty[kPieceRing];
     Piece piece[kPieceRing];
+    Found found[kPieceRing];
     float scales[kScaleRing][16];                  // 8 of K, 8 of V
     int64_t scan[17];
     ExtRow row;                                    // the row that the CTA's part begins in, its first unit, its index
@@ -203,8 +207,9 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
             pi.hi = more ? e.hi : 0;
             pi.slot = !more || (e.lo == 0 && e.hi == e.blocks) ? -1 : 2 * w.cta + (e.lo == 0 ? 1 : 0);
             pi.bad = more ? r.bad : 0;
-            pi.poison = 0;
-            pi.nonfinite = 0;
+            pi.len = more ? r.len : 0;
+            c->found[slot].poison = 0;
+            c->found[slot].nonfinite = 0;
             if (more && r.bad) atomicOr(p.status, static_cast<uint32_t>(PKV_DEV_PLAN_MISMATCH));
             if (more && e.parts) p.splits[w.cta] = ExtSplit{pi.tok0, ntok, e.kvh, e.parts};
             mbar_arrive(&c->piece_full[slot]);
@@ -233,7 +238,7 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
             next = entry(j + 1);
             if (__any_sync(kFull, page != -2 && !page_ok(page)) && lane == 0) {
                 atomicOr(p.status, static_cast<uint32_t>(PKV_DEV_PAGE_OOB));
-                pi.poison = 1;
+                c->found[slot].poison = 1;
             }
             const int box_page = __shfl_sync(kFull, page, from);
             const int t = j * kExtBlock + x * bt;
@@ -368,7 +373,7 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
     for (uint32_t pc = 0;; ++pc) {
         const int slot = pc % kPieceRing;
         if (!wait(&c->piece_full[slot], (pc / kPieceRing) & 1)) return;
-        const Piece& pi = c->piece[slot];
+        const Piece pi = c->piece[slot];
         const Share sh = share_of(pi, g, per);
         const int nb = sh.nb, ntok = pi.ntok;
         const int masked = Q8 ? 1 << 30 : first_masked(pi) - pi.lo;
@@ -444,9 +449,9 @@ __device__ __forceinline__ void fix_values(const ExtendParams& p, Ctl* c, uint8_
     for (uint32_t pc = 0;; ++pc) {
         const int slot = pc % kPieceRing;
         if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, &c->abort)) return;
-        Piece& pi = c->piece[slot];
+        const Piece pi = c->piece[slot];
         const int ntok = pi.ntok, lo = pi.lo, hi = pi.bad || ntok == 0 ? pi.lo : pi.hi, masked = first_masked(pi);
-        const int len = ntok ? p.seq_lens[pi.b] : 0;
+        const int len = pi.len;
         for (int j = lo; j < hi; ++j, n += 2) {
             // (every block is waited for, in order: a parity tells a phase from the next one only)
             if (!wait_warp(&c->full[n % C::kStages], (n / C::kStages) & 1, &c->abort)) return;
@@ -480,7 +485,7 @@ __device__ __forceinline__ void fix_values(const ExtendParams& p, Ctl* c, uint8_
                 }
             }
             for (int i = valid * kPer + lane; i < kExtBlock * kPer; i += 32) sts128(at(i), 0, 0, 0, 0);
-            if (odd && lane == 0) pi.nonfinite = 1;
+            if (odd && lane == 0) c->found[slot].nonfinite = 1;
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->fixed[st]);
@@ -508,9 +513,9 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
     for (uint32_t pc = 0;; ++pc) {
         const int slot = pc % kPieceRing;
         if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, &c->abort)) return;
-        Piece& pi = c->piece[slot];
+        const Piece pi = c->piece[slot];
         const int ntok = pi.ntok, lo = pi.lo, hi = pi.bad || ntok == 0 ? pi.lo : pi.hi, masked = first_masked(pi);
-        const int len = ntok ? p.seq_lens[pi.b] : 0;
+        const int len = pi.len;
         for (int j = lo; j < hi; ++j, ++n) {
             const uint32_t cs = n % C::kCodes, st = n % C::kStages;
             if (!wait_warp(&c->code_full[cs], (n / C::kCodes) & 1, &c->abort)) return;
@@ -568,7 +573,7 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
                                      : "memory");
                     }
                 }
-                if (__any_sync(kFull, odd) && lane == 0) pi.nonfinite = 1;
+                if (__any_sync(kFull, odd) && lane == 0) c->found[slot].nonfinite = 1;
             }
             fence_proxy_async_shared();
             __syncwarp();
@@ -719,16 +724,22 @@ __device__ __forceinline__ void follow_maximum(float top, bool first, uint32_t t
 
 // Scores of a block that the row does not see become -inf, where they lie.
 __device__ __forceinline__ void mask_scores(uint32_t tS, int seen) {
-    const int all = __shfl_sync(kFull, seen, 0);   // what every row of the warp sees: the first row sees least
+    // what every row of the warp sees, and what some row does: a later row sees more
+    const int all = __shfl_sync(kFull, seen, 0), most = __shfl_sync(kFull, seen, 31);
 #pragma unroll 1
     for (int k = 0; k < kExtBlock; k += 32) {
         if (k + 32 <= all) continue;
         uint32_t s[32];
-        tmem_ld32(s, tS + k);
-        tmem_wait_ld();
-        tmem_loaded32(s);
+        if (k >= most) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] = i < seen - k ? s[i] : 0xff800000u;
+            for (int i = 0; i < 32; ++i) s[i] = 0xff800000u;
+        } else {
+            tmem_ld32(s, tS + k);
+            tmem_wait_ld();
+            tmem_loaded32(s);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = i < seen - k ? s[i] : 0xff800000u;
+        }
         tmem_st32(tS + k, s);
     }
     tmem_wait_st();
@@ -852,13 +863,12 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
     const uint32_t tS = c->tmem + lanes + g * 128, tO = c->tmem + lanes + 256 + g * 128;
     uint32_t done = 0, outs = 0, blocks = 0, pairs = 0, q_loads = 0;
+    if (!wait_warp(&c->piece_full[0], 0, &c->abort)) return false;
+    Piece next = c->piece[0];   // (read ahead: shared memory is slow beside the products' operands)
     for (uint32_t pc = 0;; ++pc) {
         const int slot = pc % kPieceRing;
-        if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, &c->abort)) return false;
-        const Piece& pi = c->piece[slot];
-        if (pi.ntok == 0) {
-            return true;
-        }
+        const Piece pi = next;
+        if (pi.ntok == 0) return true;
         const Share sh = share_of(pi, g, per);
         const int nb = sh.count, lo = pi.lo;
         const int base_row = sh.pair ? 0 : g * 128;
@@ -903,7 +913,7 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
                 if constexpr (Q8)
                     softmax_block_q8<D>(tS, tO, cs, scales, cut ? seen : kExtBlock, j == 0, m, l);
                 else
-                    softmax_block<D>(tS, tO, p.scale_log2, j == 0, m, l);
+                    softmax_block<D>(tS, tO, cs, j == 0, m, l);
                 tmem_wait_st();
             }
             tc_fence_before();
@@ -911,6 +921,10 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
             if (lane == 0) mbar_arrive(&c->p_full[g]);
         }
         blocks += sh.nb;
+
+        const int after = (pc + 1) % kPieceRing;
+        if (!wait_warp(&c->piece_full[after], ((pc + 1) / kPieceRing) & 1, &c->abort)) return false;
+        next = c->piece[after];
 
         // outputs
         if (nb > 0) {
@@ -940,7 +954,7 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
             l = l * f0 + other.y * f1;
             m = to;
         }
-        const bool poison = pi.bad || pi.poison;
+        const bool poison = pi.bad || c->found[slot].poison;
         if (warp_live) {
             const RowOut o = row_out(p, pi, base_row + row, shift, D);
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // (all scores -inf: out 0, lse -inf)
@@ -986,7 +1000,7 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
                     }
                     __syncwarp();
                 }
-                if (pi.nonfinite && live)
+                if (c->found[slot].nonfinite && live)
                     add_nonfinite<D, Q8>(p, p.block_table + static_cast<size_t>(pi.b) * p.max_pages, pi.kvh,
                                          max(lo, masked) * kExtBlock, min(limit, pi.hi * kExtBlock), o);
                 if (live && o.out && o.lse) *o.lse = kLn2 * (m + log2f(l));
