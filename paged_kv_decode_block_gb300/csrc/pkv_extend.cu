@@ -40,8 +40,8 @@ struct Cfg {
     static constexpr int kQ = kExtRows * D * 2;
     // K and V take turns in one ring (bf16); or K's codes, V's codes and V in bf16 have a ring each (8-bit)
     static constexpr int kStages = Q8 ? (D == 128 ? 2 : 4) : (D == 128 ? 5 : 10);
-    static constexpr int kKeys = Q8 ? (D == 128 ? 4 : 8) : 0;
-    static constexpr int kCodes = Q8 ? (D == 128 ? 2 : 4) : 0;
+    static constexpr int kKeys = Q8 ? (D == 128 ? 3 : 8) : 0;
+    static constexpr int kCodes = Q8 ? (D == 128 ? 3 : 4) : 0;
     static constexpr int kThreads = Q8 ? 512 : 384;
     // producer's warpgroup last: [0, 8) softmax; then bf16: 8 producer, 9 and 10 products, 11
     // fixer; 8-bit: [8, 12) widening, 12 producer, 13 and 14 products
@@ -230,12 +230,15 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
             const float x = (lane < 8 ? p.k_scales : p.v_scales)[(static_cast<size_t>(page) * (p.page_size / kBlockRows) + blk) * p.Hkv + e.kvh];
             return lane < 8 && x == 0.0f ? 0x1p-120f : x;   // (a score of -inf in a place that is not seen stays one)
         };
-        int next = entry(e.lo);
+        // pages are asked for two blocks ahead and scales one, so that no block waits for one load behind the other
+        int next = entry(e.lo), next2 = entry(e.lo + 1);
         float next_scale = scale(e.lo, next);
         for (int j = e.lo; j < e.hi; ++j, ++blocks) {
             const int page = next;
             const float sc = next_scale;
-            next = entry(j + 1);
+            next = next2;
+            next2 = entry(j + 2);
+            next_scale = scale(j + 1, next);
             if (__any_sync(kFull, page != -2 && !page_ok(page)) && lane == 0) {
                 atomicOr(p.status, static_cast<uint32_t>(PKV_DEV_PAGE_OOB));
                 c->found[slot].poison = 1;
@@ -281,7 +284,6 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
                         tma_load_5d(to, kv ? vmap : kmap, tok / 8, e.kvh, &full[st], policy);
                 }
             }
-            next_scale = scale(j + 1, next);
         }
     }
 }
@@ -523,19 +525,29 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
             const uint32_t src = base + C::kCodesAt + cs * C::kCode + tid * 16;
             const uint32_t dst = base + C::kQ + st * C::kTile + half * 1024;
             const bool clean = j >= masked;
-            constexpr int kAtOnce = 4;
+            const int seen = max(pi.limit0 - j * kExtBlock, 0), valid = len - j * kExtBlock;
+            bool odd = false;
+            constexpr int kAtOnce = 1;
 #pragma unroll 1
             for (int i = 0; i < kPerRow; i += kAtOnce) {
                 uint32_t v[kAtOnce][4];   // (the loads first: the stores would hold them up)
 #pragma unroll
                 for (int h = 0; h < kAtOnce; ++h) lds128(v[h], src + (i + h) * 2048);
-                if (i + kAtOnce == kPerRow && !clean) {   // read: the next codes may come
+                if (i + kAtOnce == kPerRow) {   // read: the next codes may come
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&c->code_empty[cs]);
                 }
 #pragma unroll
                 for (int h = 0; h < kAtOnce; ++h) {
                     const int row = tid / kPerRow + (i + h) * (128 / kPerRow);
+                    if (clean && row >= seen) {   // rows that not all of the tile's rows see, and what lies behind the row's end
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t nan = ((v[h][k] & 0x7f7f7f7fu) + 0x01010101u & 0x80808080u) >> 7;
+                            odd |= nan != 0 && row < valid;
+                            v[h][k] = row < valid ? v[h][k] & ~(nan * 0xffu) : 0;
+                        }
+                    }
                     uint32_t o[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -553,33 +565,11 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
                     }
                 }
             }
-            if (clean) {
-                // rows that not all of the tile's rows see, and what lies behind the row's end
-                const int seen = max(pi.limit0 - j * kExtBlock, 0), valid = len - j * kExtBlock;
-                bool odd = false;
-                for (int i = 0; i < kPerRow; ++i) {
-                    const int row = tid / kPerRow + i * (128 / kPerRow);
-                    uint32_t v[4];
-                    lds128(v, src + i * 2048);
-                    for (int k = 0; k < 16; ++k) {
-                        uint32_t w = v[0];   // (no index into registers)
-                        w = k / 4 == 1 ? v[1] : k / 4 == 2 ? v[2] : k / 4 == 3 ? v[3] : w;
-                        const bool is_nan = (w >> (k % 4 * 8) & 0x7fu) == 0x7fu, behind = row >= valid;
-                        if (row < seen || (!is_nan && !behind)) continue;
-                        odd |= !behind;
-                        const uint32_t x = (chunk % 4) * 2 + k / 8;
-                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + row / 8 * C::kGroup + row % 8 * 128 + ((x ^ (row & 7)) << 4) + k % 8 * 2),
-                                     "h"(static_cast<uint16_t>(0))
-                                     : "memory");
-                    }
-                }
-                if (__any_sync(kFull, odd) && lane == 0) c->found[slot].nonfinite = 1;
-            }
+            if (clean && __any_sync(kFull, odd) && lane == 0) c->found[slot].nonfinite = 1;
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&c->full[st]);
-                if (clean) mbar_arrive(&c->code_empty[cs]);
             }
         }
         __syncwarp();
@@ -806,17 +796,15 @@ template <int D>
 __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float cs, const float* scales, int seen, bool first,
                                                  float& m, float& l) {
     float top = -INFINITY;
-    uint32_t s[64];
+    uint32_t s[32];
     // (loops, not straight code: three warps of a scheduler run three pieces of code, and instructions have to be near)
 #pragma unroll 1
-    for (int k = 0; k < 128; k += 64) {
+    for (int k = 0; k < 128; k += 32) {
         tmem_ld32(s, tS + k);
-        tmem_ld32(s + 32, tS + k + 32);
         tmem_wait_ld();
         tmem_loaded32(s);
-        tmem_loaded32(s + 32);
 #pragma unroll
-        for (int i = 0; i < 64; i += 16) {
+        for (int i = 0; i < 32; i += 16) {
             const float* y = reinterpret_cast<const float*>(s + i);
             float t = max3(y[0], y[1], y[2]), u = max3(y[3], y[4], y[5]);
             t = max3(t, y[6], y[7]), u = max3(u, y[8], y[9]);
@@ -830,14 +818,12 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
     const uint64_t ref2 = pack2(ref, ref);
     uint64_t sum[2] = {0, 0};
 #pragma unroll 1
-    for (int k = 0; k < 128; k += 64) {
+    for (int k = 0; k < 128; k += 32) {
         tmem_ld32(s, tS + k);
-        tmem_ld32(s + 32, tS + k + 32);
         tmem_wait_ld();
         tmem_loaded32(s);
-        tmem_loaded32(s + 32);
 #pragma unroll
-        for (int h = 0; h < 64; h += 16) {
+        for (int h = 0; h < 32; h += 16) {
             const float ks = k + h < seen ? fabsf(scales[(k + h) / 16]) * cs : 1.0f, vs = k + h < seen ? scales[8 + (k + h) / 16] : 0.0f;
             const uint64_t ks2 = pack2(ks, ks), vs2 = pack2(vs, vs);
 #pragma unroll
@@ -849,7 +835,7 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
                 s[i / 2] = bf16x2(z.x, z.y);
             }
         }
-        tmem_st32(tS + k / 2, s);
+        tmem_st16(tS + k / 2, s);
     }
     const F2 a = unpack2(add2(sum[0], sum[1]));
     l += a.x + a.y;

@@ -27,7 +27,7 @@ namespace pkv {
 constexpr int kExtBlock = 128;      // tokens of a KV block
 constexpr int kExtBlockLog2 = 7;
 constexpr int kExtRows = 256;       // rows of scores of a tile: two groups of 128
-constexpr int kTileUnits = 1;       // units of a tile besides its blocks
+constexpr int kTileUnits = 3;       // units of a tile besides its blocks: measured, see below
 constexpr int kMinShareUnits = 2;   // a CTA takes at least this much (fewer CTAs work otherwise)
 
 struct ExtRow {
