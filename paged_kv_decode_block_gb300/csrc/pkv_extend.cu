@@ -12,9 +12,9 @@
 // Shape: the G query heads of a KV head are packed with the tokens into rows, so
 // that K and V are read once for all of them.  A tile is 256 rows in two groups
 // of 128; one KV block of 128 tokens serves both.  One CTA per SM, specialised
-// warps: a producer (TMA), a warp that issues tcgen05.mma, two warpgroups of
-// softmax with a row per thread, and a warp that cleans V where masks end (bf16)
-// or four that widen e4m3 to bf16 (8-bit).  Scores and outputs stay in tensor
+// warps: one loads (TMA), two issue tcgen05.mma, two warpgroups do the softmax with
+// a row per thread, and one cleans V where masks end (bf16), or one loads V's codes
+// and four widen them to bf16 (8-bit).  Scores and outputs stay in tensor
 // memory: S0, S1, O0, O1 of 128 columns each; P replaces S, in place, as the
 // second product's first operand.  While one group is at its softmax the tensor
 // core works for the other.
@@ -43,12 +43,11 @@ struct Cfg {
     static constexpr int kKeys = Q8 ? (D == 128 ? 3 : 8) : 0;
     static constexpr int kCodes = Q8 ? (D == 128 ? 3 : 4) : 0;
     static constexpr int kThreads = Q8 ? 512 : 384;
-    // producer's warpgroup last: [0, 8) softmax; then bf16: 8 producer, 9 and 10 products, 11
-    // fixer; 8-bit: [8, 12) widening, 12 producer, 13 and 14 products
-    static constexpr int kProducer = Q8 ? 12 : 8;
-    static constexpr int kMma = kProducer + 1;
-    static constexpr int kFixer = Q8 ? -1 : 11;
-    static constexpr int kReaders = Q8 ? 14 : 11;             // warps that read the piece ring
+    // [0, 8) softmax; 8-bit: [8, 12) widening; then one warp for loads, two for products, one for values
+    static constexpr int kLoad = Q8 ? 12 : 8;
+    static constexpr int kMma = kLoad + 1;
+    static constexpr int kValues = kLoad + 3;
+    static constexpr int kReaders = Q8 ? 15 : 11;             // warps that read the piece ring
     static constexpr int kKeysAt = kQ + kStages * kTile, kCodesAt = kKeysAt + kKeys * kCode;
     static constexpr size_t kBytes = static_cast<size_t>(kCodesAt) + kCodes * kCode;
 };
@@ -89,7 +88,7 @@ struct Ctl {
     int32_t row0;
     volatile int abort, late;                      // a wait ran out; one at the end did too
     uint32_t tmem;
-    int32_t issued;                                // K and V blocks that the producer has begun to load
+    int32_t keys_issued, values_issued;            // blocks whose loads have begun
     int32_t q_loads;
 };
 
@@ -173,22 +172,69 @@ __device__ __forceinline__ int64_t block_scan(Ctl* c, int64_t v, int64_t* total)
     return before + x - v;
 }
 
-// ------------------------------------------------------------------ producer
+// ------------------------------------------------------------------ loads
+//
+// One warp walks the CTA's part, tells the others its pieces, and loads queries, keys
+// and (bf16) values.  It is busy for 100 cycles with each box of a page (16 tokens at
+// least), 16 boxes a block.  In the 8-bit cache, whose blocks are half the bytes, that
+// was what a block waited for, so a second warp loads the values there (drafts over
+// 56 rows of 1024-8192 246 -> 207 us); in bf16 a second warp makes no more room in the
+// ring and the two hold one another up (2048 tokens after 30720 723 against 775 us).
+
+// Where a lane finds its boxes of a block: the page of 16 tokens, and its own box's tokens.
+struct Boxes {
+    const int32_t* row;   // the row's table
+    int32_t hi, len, page_size, num_pages, tokens, x, from;
+    bool mine;
+    __device__ __forceinline__ Boxes(const ExtendParams& p)
+        : page_size(p.page_size), num_pages(p.num_pages), tokens(p.box_tokens) {
+        const int lane = threadIdx.x & 31, n = kExtBlock / tokens;
+        x = lane % n;
+        from = x * (tokens / 16);   // the lane that knows its page
+        mine = lane < n;
+    }
+    // the page of this lane's 16 tokens of block j, or -2 past the row's end
+    __device__ __forceinline__ int entry(int j) const {
+        const uint32_t t = j * kExtBlock + (threadIdx.x & 7) * 16;
+        return j < hi && t < static_cast<uint32_t>(len) ? row[t / static_cast<uint32_t>(page_size)] : -2;
+    }
+    __device__ __forceinline__ bool ok(int page) const { return page >= 0 && page < num_pages; }
+    // the pool's token that this lane's box begins with, or -1: nothing to load
+    __device__ __forceinline__ int token(int j, int page) const {
+        const int box_page = __shfl_sync(kFull, page, from);
+        const uint32_t t = j * kExtBlock + x * tokens;
+        return mine && ok(box_page) ? box_page * page_size + static_cast<int>(t % static_cast<uint32_t>(page_size)) : -1;
+    }
+};
+
+// Loads this lane's box of a block of K or V (`bytes` a box) into `to`, completing on `bar`.
+template <bool Q8>
+__device__ __forceinline__ void load_block(uint8_t* to, const Boxes& bx, int tok, int bytes, const CUtensorMap* map, int head,
+                                           uint64_t* bar, uint64_t policy) {
+    const int n = __popc(__ballot_sync(kFull, tok >= 0));
+    if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(bar, n * bytes);
+    __syncwarp();
+    if (tok >= 0) {
+        if (Q8)
+            tma_load_3d(to + bx.x * bytes, map, 0, head, tok, bar, policy);
+        else
+            tma_load_5d(to + bx.x * bytes, map, tok / 8, head, bar, policy);
+    }
+}
 
 template <int D, bool Q8>
-__device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* smem, const CUtensorMap* qmap,
-                                        const CUtensorMap* kmap, const CUtensorMap* vmap, ExtWalk& w, const Rows& rows,
-                                        uint64_t policy) {
+__device__ __forceinline__ void load(const ExtendParams& p, Ctl* c, uint8_t* smem, const CUtensorMap* qmap,
+                                     const CUtensorMap* kmap, const CUtensorMap* vmap, ExtWalk& w, const Rows& rows, uint64_t policy) {
     using C = Cfg<D, Q8>;
     const int lane = threadIdx.x & 31;
-    uint8_t* q_smem = smem;
-    constexpr int kBox = Q8 ? C::kCode : C::kTile;
-    const int bt = p.box_tokens, nbox = kExtBlock / bt;
-    const int x = lane % nbox;                                      // this lane's box
-    const bool mine = lane < nbox;
-    const int from = x * (bt / 16);                                 // the lane that knows its page
+    constexpr int kBlock = Q8 ? C::kCode : C::kTile;
+    constexpr uint32_t kRing = Q8 ? C::kKeys : C::kStages;
+    uint64_t* const full = Q8 ? c->key_full : c->full;
+    uint64_t* const empty = Q8 ? c->key_empty : c->empty;
+    Boxes bx(p);
+    const int bytes = kBlock / (kExtBlock / bx.tokens);
     const int per = kExtRows / 2 / p.G;                             // tokens of a group
-    uint32_t n = 0, blocks = 0, q_loads = 0;
+    uint32_t blocks = 0, q_loads = 0;
     for (uint32_t pc = 0;; ++pc) {
         ExtPiece e{};
         const bool more = w.next(e, rows);
@@ -218,73 +264,161 @@ __device__ __forceinline__ void produce(const ExtendParams& p, Ctl* c, uint8_t* 
         if (!more) return;
         if (r.bad) continue;
 
-        const int32_t* row = p.block_table + static_cast<size_t>(e.b) * p.max_pages;
-        auto entry = [&](int j) {   // the page of this lane's 16 tokens of block j, or -1 past the row's end
-            const int t = j * kExtBlock + (lane & 7) * 16;
-            return j < e.hi && t < r.len ? row[t / p.page_size] : -2;
-        };
-        auto page_ok = [&](int page) { return page >= 0 && page < p.num_pages; };
+        bx.row = p.block_table + static_cast<size_t>(e.b) * p.max_pages;
+        bx.hi = e.hi;
+        bx.len = r.len;
         auto scale = [&](int j, int page) {   // lanes 0..7: K's, 8..15: V's
-            if (!Q8 || lane >= 16 || !page_ok(page)) return 0.0f;
-            const int blk = (j * kExtBlock + (lane & 7) * 16) % p.page_size / kBlockRows;
+            if (!Q8 || lane >= 16 || !bx.ok(page)) return 0.0f;
+            const uint32_t blk = (j * kExtBlock + (lane & 7) * 16) % static_cast<uint32_t>(p.page_size) / kBlockRows;
             const float x = (lane < 8 ? p.k_scales : p.v_scales)[(static_cast<size_t>(page) * (p.page_size / kBlockRows) + blk) * p.Hkv + e.kvh];
             return lane < 8 && x == 0.0f ? 0x1p-120f : x;   // (a score of -inf in a place that is not seen stays one)
         };
         // pages are asked for two blocks ahead and scales one, so that no block waits for one load behind the other
-        int next = entry(e.lo), next2 = entry(e.lo + 1);
+        int next = bx.entry(e.lo), next2 = bx.entry(e.lo + 1);
         float next_scale = scale(e.lo, next);
         for (int j = e.lo; j < e.hi; ++j, ++blocks) {
             const int page = next;
             const float sc = next_scale;
             next = next2;
-            next2 = entry(j + 2);
+            next2 = bx.entry(j + 2);
             next_scale = scale(j + 1, next);
-            if (__any_sync(kFull, page != -2 && !page_ok(page)) && lane == 0) {
+            if (__any_sync(kFull, page != -2 && !bx.ok(page)) && lane == 0) {
                 atomicOr(p.status, static_cast<uint32_t>(PKV_DEV_PAGE_OOB));
                 c->found[slot].poison = 1;
             }
-            const int box_page = __shfl_sync(kFull, page, from);
-            const int t = j * kExtBlock + x * bt;
-            const int tok = page_ok(box_page) ? box_page * p.page_size + t % p.page_size : -1;
-            const uint32_t bytes = __popc(__ballot_sync(kFull, mine && tok >= 0)) * (kBox / nbox);
-            for (int kv = 0; kv < 2; ++kv, ++n) {
-                if (j == e.lo && kv == 1) {   // the queries, behind the first keys: their place is free later
-                    if (q_loads > 0 && !wait_warp(&c->q_empty, (q_loads - 1) & 1, &c->abort)) return;
-                    const int groups = ntok > per ? 2 : 1;
-                    if (lane == 0) {
-                        c->q_loads = q_loads + 1;
-                        mbar_arrive_expect_tx(&c->q_full, groups * (C::kQ / 2));
-                        for (int g = 0; g < groups; ++g)
-                            for (int h = 0; h < C::kHalves; ++h)
-                                tma_load_3d(q_smem + g * (C::kQ / 2) + h * 16384, qmap, h * 64, e.kvh * p.G,
-                                            r.tok0 + e.tile * w.tt + g * per, &c->q_full, policy);
-                    }
-                    ++q_loads;
-                }
-                // the place: K's and V's rings, or the one of both
-                const uint32_t at = Q8 ? blocks : n, ring = Q8 ? (kv ? C::kCodes : C::kKeys) : C::kStages, st = at % ring;
-                uint64_t* full = Q8 ? (kv ? c->code_full : c->key_full) : c->full;
-                uint64_t* empty = Q8 ? (kv ? c->code_empty : c->key_empty) : c->empty;
-                if (at >= ring && !wait_warp(&empty[st], (at / ring - 1) & 1, &c->abort)) return;
-                if (Q8 && kv == 0) {
-                    if (lane < 16) c->scales[blocks % kScaleRing][lane] = sc;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&c->scale_full[blocks % kScaleRing]);
-                }
+            const int tok = bx.token(j, page);
+            const uint32_t at = Q8 ? blocks : 2 * blocks, st = at % kRing;
+            if (at >= kRing && !wait_warp(&empty[st], (at / kRing - 1) & 1, &c->abort)) return;
+            if (Q8) {
+                if (lane < 16) c->scales[blocks % kScaleRing][lane] = sc;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c->scale_full[blocks % kScaleRing]);
+            }
+            if (lane == 0) c->keys_issued = blocks + 1;
+            load_block<Q8>(smem + (Q8 ? C::kKeysAt : C::kQ) + st * kBlock, bx, tok, bytes, kmap, e.kvh, &full[st], policy);
+            if (j == e.lo) {   // the queries, behind the first keys: their place is free later
+                if (q_loads > 0 && !wait_warp(&c->q_empty, (q_loads - 1) & 1, &c->abort)) return;
+                const int groups = ntok > per ? 2 : 1;
                 if (lane == 0) {
-                    c->issued = n + 1;
-                    mbar_arrive_expect_tx(&full[st], bytes);
+                    c->q_loads = q_loads + 1;
+                    mbar_arrive_expect_tx(&c->q_full, groups * (C::kQ / 2));
+                    for (int g = 0; g < groups; ++g)
+                        for (int h = 0; h < C::kHalves; ++h)
+                            tma_load_3d(smem + g * (C::kQ / 2) + h * 16384, qmap, h * 64, e.kvh * p.G,
+                                        r.tok0 + e.tile * w.tt + g * per, &c->q_full, policy);
                 }
                 __syncwarp();
-                if (mine && tok >= 0) {
-                    uint8_t* to = smem + (Q8 ? (kv ? C::kCodesAt : C::kKeysAt) : C::kQ) + st * kBox + x * (kBox / nbox);
-                    if (Q8)
-                        tma_load_3d(to, kv ? vmap : kmap, 0, e.kvh, tok, &full[st], policy);
-                    else
-                        tma_load_5d(to, kv ? vmap : kmap, tok / 8, e.kvh, &full[st], policy);
-                }
+                ++q_loads;
+            }
+            if (!Q8) {
+                const uint32_t vt = (at + 1) % kRing;
+                if (at + 1 >= kRing && !wait_warp(&empty[vt], ((at + 1) / kRing - 1) & 1, &c->abort)) return;
+                if (lane == 0) c->values_issued = blocks + 1;
+                load_block<Q8>(smem + C::kQ + vt * kBlock, bx, tok, bytes, vmap, e.kvh, &full[vt], policy);
             }
         }
+    }
+}
+
+// The first block with places that some row of the tile does not see.
+__device__ __forceinline__ int first_masked(const Piece& pi) { return pi.limit0 / kExtBlock; }
+
+// V of a block with masked places (bf16).  A weight of 0 does not hide an infinity or
+// NaN in a product, so V is cleaned before it is used: slots behind the row's end
+// (which may hold anything) become 0; so do infinities and NaN of tokens that some
+// rows see and others don't, which the rows that see them get back at the end (true
+// is returned if there are any).  Rows of the block from `seen` on are not seen by
+// all, those from `valid` on lie behind the end.
+template <int D>
+__device__ __forceinline__ bool clean_values(uint32_t tile, int seen, int valid) {
+    using C = Cfg<D, false>;
+    const int lane = threadIdx.x & 31;
+    constexpr int kPer = C::kHalves * 8;   // 16-byte pieces of a token
+    auto at = [&](int i) { return tile + i / (8 * kPer) * C::kGroup + i / 8 % C::kHalves * 1024 + i / kPer % 8 * 128 + i % 8 * 16; };
+    uint32_t any = 0;
+#pragma unroll 8
+    for (int i = seen * kPer + lane; i < valid * kPer; i += 32) {
+        uint32_t v[4];
+        lds128(v, at(i));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) any |= (v[k] & 0x7f807f80u) + 0x00800080u;
+    }
+    const bool odd = __any_sync(kFull, (any & 0x80008000u) != 0);
+    if (odd) {
+        for (int i = seen * kPer + lane; i < valid * kPer; i += 32) {
+            uint32_t v[4];
+            lds128(v, at(i));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if ((v[k] & 0x7f80u) == 0x7f80u) v[k] &= 0xffff0000u;
+                if ((v[k] & 0x7f800000u) == 0x7f800000u) v[k] &= 0x0000ffffu;
+            }
+            sts128(at(i), v[0], v[1], v[2], v[3]);
+        }
+    }
+    for (int i = valid * kPer + lane; i < kExtBlock * kPer; i += 32) sts128(at(i), 0, 0, 0, 0);
+    return odd;
+}
+
+// bf16: the warp that cleans V in blocks with masked places.
+template <int D>
+__device__ __forceinline__ void clean(const ExtendParams& p, Ctl* c, uint8_t* smem) {
+    using C = Cfg<D, false>;
+    uint32_t n = 0;
+    for (uint32_t pc = 0;; ++pc) {
+        const int slot = pc % kPieceRing;
+        if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, &c->abort)) return;
+        const Piece pi = c->piece[slot];
+        const int hi = pi.bad || pi.ntok == 0 ? pi.lo : pi.hi, masked = first_masked(pi);
+        for (int j = pi.lo; j < hi; ++j, n += 2) {
+            // (every block is waited for, in order: a parity tells a phase from the next one only)
+            if (!wait_warp(&c->full[n % C::kStages], (n / C::kStages) & 1, &c->abort)) return;
+            const uint32_t vn = n + 1, st = vn % C::kStages;
+            if (!wait_warp(&c->full[st], (vn / C::kStages) & 1, &c->abort)) return;
+            if (j < masked) continue;
+            const int first = j * kExtBlock;
+            const bool odd = clean_values<D>(smem_addr(smem) + C::kQ + st * C::kTile, max(pi.limit0 - first, 0), min(pi.len - first, kExtBlock));
+            fence_proxy_async_shared();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) {
+                if (odd) c->found[slot].nonfinite = 1;
+                mbar_arrive(&c->fixed[st]);
+            }
+        }
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&c->piece_empty[slot]);
+        if (pi.ntok == 0) return;
+    }
+}
+
+// 8-bit: the warp that loads V's codes.
+template <int D>
+__device__ __forceinline__ void load_values(const ExtendParams& p, Ctl* c, uint8_t* smem, const CUtensorMap* vmap, uint64_t policy) {
+    using C = Cfg<D, true>;
+    const int lane = threadIdx.x & 31;
+    Boxes bx(p);
+    const int bytes = C::kCode / (kExtBlock / bx.tokens);
+    uint32_t n = 0;
+    for (uint32_t pc = 0;; ++pc) {
+        const int slot = pc % kPieceRing;
+        if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, &c->abort)) return;
+        const Piece pi = c->piece[slot];
+        bx.row = p.block_table + static_cast<size_t>(pi.b) * p.max_pages;
+        bx.hi = pi.bad || pi.ntok == 0 ? pi.lo : pi.hi;
+        bx.len = pi.len;
+        int next = bx.entry(pi.lo), next2 = bx.entry(pi.lo + 1);
+        for (int j = pi.lo; j < bx.hi; ++j, ++n) {
+            const int tok = bx.token(j, next);
+            next = next2;
+            next2 = bx.entry(j + 2);
+            const uint32_t st = n % C::kCodes;
+            if (n >= C::kCodes && !wait_warp(&c->code_empty[st], (n / C::kCodes - 1) & 1, &c->abort)) return;
+            if (lane == 0) c->values_issued = n + 1;
+            load_block<true>(smem + C::kCodesAt + st * C::kCode, bx, tok, bytes, vmap, pi.kvh, &c->code_full[st], policy);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->piece_empty[slot]);
+        if (pi.ntok == 0) return;
     }
 }
 
@@ -316,8 +450,6 @@ __device__ __forceinline__ Share share_of(const Piece& pi, int g, int per) {
         s.count = s.nb == 0 || last < g * per ? 0 : max(0, min(pi.hi, (pi.limit0 + last + kExtBlock - 1) / kExtBlock) - pi.lo);
     return s;
 }
-// The first block with places that some row of the tile does not see.
-__device__ __forceinline__ int first_masked(const Piece& pi) { return pi.limit0 / kExtBlock; }
 
 // One thread for each group: the products are asynchronous, and a thread's waits
 // hide behind the other's products.  PV(j) goes before QK(j + 1), which overwrites
@@ -437,72 +569,11 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
     }
 }
 
-// ------------------------------------------------------------------ V where masks end (bf16)
-
-// A weight of 0 does not hide an infinity or NaN in a product, so in blocks with
-// masked places V is cleaned before it is used: slots behind the row's end (which
-// may hold anything) become 0; so do infinities and NaN of tokens that some rows
-// see and others don't, which the rows that see them get back at the end.
-template <int D>
-__device__ __forceinline__ void fix_values(const ExtendParams& p, Ctl* c, uint8_t* smem) {
-    using C = Cfg<D, false>;
-    const int lane = threadIdx.x & 31;
-    uint32_t n = 0;
-    for (uint32_t pc = 0;; ++pc) {
-        const int slot = pc % kPieceRing;
-        if (!wait_warp(&c->piece_full[slot], (pc / kPieceRing) & 1, &c->abort)) return;
-        const Piece pi = c->piece[slot];
-        const int ntok = pi.ntok, lo = pi.lo, hi = pi.bad || ntok == 0 ? pi.lo : pi.hi, masked = first_masked(pi);
-        const int len = pi.len;
-        for (int j = lo; j < hi; ++j, n += 2) {
-            // (every block is waited for, in order: a parity tells a phase from the next one only)
-            if (!wait_warp(&c->full[n % C::kStages], (n / C::kStages) & 1, &c->abort)) return;
-            const uint32_t vn = n + 1, st = vn % C::kStages;
-            if (!wait_warp(&c->full[st], (vn / C::kStages) & 1, &c->abort)) return;
-            if (j < masked) continue;
-            // rows that only some of the tile's rows see, then those behind the row's end
-            const int seen = max(pi.limit0 - j * kExtBlock, 0), valid = min(len - j * kExtBlock, kExtBlock);
-            const uint32_t tile = smem_addr(smem) + C::kQ + st * C::kTile;
-            constexpr int kPer = C::kHalves * 8;   // 16-byte pieces of a token
-            auto at = [&](int i) { return tile + i / (8 * kPer) * C::kGroup + i / 8 % C::kHalves * 1024 + i / kPer % 8 * 128 + i % 8 * 16; };
-            uint32_t any = 0;
-#pragma unroll 8
-            for (int i = seen * kPer + lane; i < valid * kPer; i += 32) {
-                uint32_t v[4];
-                lds128(v, at(i));
-#pragma unroll
-                for (int k = 0; k < 4; ++k) any |= (v[k] & 0x7f807f80u) + 0x00800080u;
-            }
-            const bool odd = __any_sync(kFull, (any & 0x80008000u) != 0);
-            if (odd) {
-                for (int i = seen * kPer + lane; i < valid * kPer; i += 32) {
-                    uint32_t v[4];
-                    lds128(v, at(i));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if ((v[k] & 0x7f80u) == 0x7f80u) v[k] &= 0xffff0000u;
-                        if ((v[k] & 0x7f800000u) == 0x7f800000u) v[k] &= 0x0000ffffu;
-                    }
-                    sts128(at(i), v[0], v[1], v[2], v[3]);
-                }
-            }
-            for (int i = valid * kPer + lane; i < kExtBlock * kPer; i += 32) sts128(at(i), 0, 0, 0, 0);
-            if (odd && lane == 0) c->found[slot].nonfinite = 1;
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c->fixed[st]);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->piece_empty[slot]);
-        if (ntok == 0) return;
-    }
-}
-
 // ------------------------------------------------------------------ e4m3 to bf16
 
 // V's codes become bf16 exactly (4 bits of significand into 8); their scales join the
 // weights in fp32.  (K's go into the product as they are.)  In blocks with masked
-// places NaN codes become 0, as infinities and NaN do in fix_values.
+// places NaN codes become 0, as infinities and NaN do in clean_values.
 template <int D>
 __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* smem) {
     using C = Cfg<D, true>;
@@ -651,7 +722,7 @@ __device__ __forceinline__ RowOut row_out(const ExtendParams& p, const Piece& pi
     }
     return o;
 }
-// What fix_values took out of V and this row sees, tokens [t0, t1), is added to what
+// What clean_values took out of V and this row sees, tokens [t0, t1), is added to what
 // the row has written: an infinity or NaN of its own value.  Rare, so V is read from
 // the pages again.
 template <int D, bool Q8>
@@ -1064,12 +1135,12 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
         }
         c->abort = 0;
         c->late = 0;
-        c->issued = 0;
+        c->keys_issued = c->values_issued = 0;
         c->q_loads = 0;
         fence_mbar_init();
     }
     if (warp == C::kMma) tmem_alloc(&c->tmem, 512);
-    if (warp == C::kProducer && lane < 3) prefetch_map(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap);
+    if (warp == C::kLoad && lane < 3) prefetch_map(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap);
     grid_dependency_wait();
     launch_dependents();
 
@@ -1129,17 +1200,20 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
                 asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
             else
                 asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-            if (warp == C::kProducer) {
+            uint64_t policy;
+            asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+            if (warp == C::kLoad) {
                 ExtWalk w;
                 w.begin(parts, cta, p.B, p.Hkv, rows.tt, c->row0, c->row, c->row_unit);
-                uint64_t policy;
-                asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
-                produce<D, Q8>(p, c, smem, &qmap, &kmap, &vmap, w, rows, policy);
+                load<D, Q8>(p, c, smem, &qmap, &kmap, &vmap, w, rows, policy);
+            } else if (warp == C::kValues) {
+                if constexpr (Q8)
+                    load_values<D>(p, c, smem, &vmap, policy);
+                else
+                    clean<D>(p, c, smem);
             } else if (warp == C::kMma || warp == C::kMma + 1) {
                 if (lane == 0) multiply<D, Q8>(p, c, smem, warp - C::kMma);
                 __syncwarp();
-            } else if (warp == C::kFixer) {
-                if constexpr (!Q8) fix_values<D>(p, c, smem);
             }
         }
     }
@@ -1150,11 +1224,16 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
             atomicOr(p.status, static_cast<uint32_t>(PKV_DEV_TIMEOUT));
             umma_commit(&c->drain);
             wait_for(&c->drain, 0, &c->late);
-            const uint32_t n = c->issued;
-            for (uint32_t i = n > 16 ? n - 16 : 0; i < n; ++i) {   // (more than any ring holds; those before have landed)
-                const uint32_t at = Q8 ? i / 2 : i, ring = Q8 ? (i % 2 ? C::kCodes : C::kKeys) : C::kStages;
-                uint64_t* full = Q8 ? (i % 2 ? c->code_full : c->key_full) : c->full;
-                if (at + ring >= (Q8 ? (n + 1) / 2 : n)) wait_for(&full[at % ring], (at / ring) & 1, &c->late);
+            constexpr uint32_t kRing = Q8 ? C::kKeys : C::kStages, kValueRing = Q8 ? C::kCodes : C::kStages;
+            for (uint32_t i = max(c->keys_issued - 10, 0); i < c->keys_issued; ++i) {   // (as many as any ring holds)
+                const uint32_t at = Q8 ? i : 2 * i;
+                if (at + kRing >= (Q8 ? c->keys_issued : 2 * c->keys_issued))
+                    wait_for(Q8 ? &c->key_full[at % kRing] : &c->full[at % kRing], (at / kRing) & 1, &c->late);
+            }
+            for (uint32_t i = max(c->values_issued - 10, 0); i < c->values_issued; ++i) {
+                const uint32_t at = Q8 ? i : 2 * i + 1;
+                if (at + kValueRing >= (Q8 ? c->values_issued : 2 * c->values_issued))
+                    wait_for(Q8 ? &c->code_full[at % kValueRing] : &c->full[at % kValueRing], (at / kValueRing) & 1, &c->late);
             }
             if (c->q_loads) wait_for(&c->q_full, (c->q_loads - 1) & 1, &c->late);
         }
