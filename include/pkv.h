@@ -423,14 +423,17 @@ int pkv_extend_reserve(pkv_plan_t plan);
  * one plan share its memory and have to be ordered on the GPU, as decodes have;
  * they may overlap its decodes and appends.  Two kernels on `stream`.
  *
- * Products take bf16 factors (8-bit codes are exact in it) and fp32 sums; the
- * softmax is fp32 with the weights rounded once to bf16 for the product with V
- * (after their V scale in the 8-bit cache) and summed before that rounding; the
- * output is rounded once to bf16.  The order of all sums is fixed by the lengths,
+ * Products have fp32 sums and bf16 factors; 8-bit codes are exact, and a query
+ * meets them in two e4m3 parts, exact for elements down to 2^-10 of its largest and
+ * off by at most 2^-18 of the largest below that.  The softmax is fp32, with weights
+ * below 2^-126 of the largest left out, and the weights rounded once to bf16 for the
+ * product with V (after their V scale in the 8-bit cache) and summed before that
+ * rounding; the output is rounded once to bf16.  The order of all sums is fixed by the lengths,
  * so a repeated call gives the same bits.  A query whose scores are all -inf has
- * output 0 and lse -inf.  Slots behind a row's last token may hold anything.  An
- * infinity or NaN in a token's V reaches the queries that see the token and no
- * others.  Tokens of q that belong to no row, and their outputs, are left as they are.
+ * output 0 and lse -inf; one with a NaN element is NaN (in the 8-bit cache one with
+ * an infinite element too).  Slots behind a row's last token may hold anything.  An
+ * infinity or NaN in a token's V, or a V scale, reaches the queries that see the
+ * token (of the scale's block) and no others.  Tokens of q that belong to no row, and their outputs, are left as they are.
  *
  * A row whose n_b exceeds seq_lens_d[b], or whose length exceeds its table, sets
  * PKV_DEV_PLAN_MISMATCH and its outputs are NaN; offsets outside [0, total_tokens]

@@ -1,8 +1,10 @@
 """pkv_extend and pkv_extend_q8 on the GPU against the definition in 64 bits.
 
 Tolerances, element by element.  Let A = sum_t w_t |v_t| with the exact weights w, and n the tokens seen.
-* A score is an fp32 dot product of exact bf16 factors (codes are exact in bf16, their scale joins in fp32):
-  off by at most d = (2 D + 16) 2^-23 max_t sum_e |q_e k_te| / sqrt(D).
+* A score is an fp32 dot product: off by at most d = (2 D + 16) 2^-23 max_t sum_e |q_e k_te| / sqrt(D).  In the 8-bit
+  cache (exact codes, their scale joins in fp32) the query is two e4m3 numbers, scaled so that its largest element lies
+  in [2^7, 2^8): the second holds the first's remainder to half of e4m3's smallest step, 2^-10 of 2^7, which adds
+  2^-17 max_e |q_e| sum_e |k_te| / sqrt(D) at most.
 * A weight is off by a factor of 2 d + 2^-20 (score and reference, ex2, V scale), then rounded to bf16: 2^-8.
   Sums of n terms in fp32 add n 2^-23.  So |out error| <= (2^-8 + 2 (2 d + 2^-20 + n 2^-23)) A (numerator and
   denominator), and rounding the output to bf16 adds 2^-8 |out|, or half a subnormal step.
@@ -100,6 +102,9 @@ class Problem:
                 w = torch.softmax(z, 1)
                 ref, A = w @ vh, w @ vh.abs()
                 d = (2 * D + 16) * 2.0 ** -23 * size.amax(1)
+                if self.q8:
+                    far = kh.abs().sum(1).expand(a, n).masked_fill(hidden, 0).amax(1)
+                    d = d + 2.0 ** -17 * q.abs().amax(1) * far / math.sqrt(D)
                 f = 2 * (2 * d + 2.0 ** -20 + n * 2.0 ** -23)
                 tol = (2.0 ** -8 + f)[:, None] * A + 2.0 ** -8 * ref.abs() + 2.0 ** -133 + n * 2.0 ** -126 * vh.abs().max()
                 got = out[here, h].double()
@@ -200,6 +205,42 @@ def test_scales_of_any_kind():
     p.vs[int(p.table[0, 256 // 16])] = math.inf
     p.run()
     assert not p.out[56:90].isfinite().any() and p.lse.isfinite().all() and torch.equal(p.out[fine], was[0][fine])
+
+
+def test_queries_with_far_elements():
+    """8-bit cache: elements from 2^-30 to 2^30 times the others, all small, all zero, and powers of two apart."""
+    p = Problem([200], [70], q8=True, Hq=4, Hkv=2)
+    p.q[0:10] = (p.q[0:10].float() * 2.0 ** -100).bfloat16()
+    p.q[10:20, :, 3] *= 2.0 ** 6
+    p.q[20:30] = 0
+    p.q[30:40] = (p.q[30:40].float() * torch.exp2(torch.arange(128, device="cuda") % 13 - 12.0)).bfloat16()
+    p.q[40:50, :, 5] = (p.q[40:50, :, 5].float() * 2.0 ** -30).bfloat16()
+    p.run().check()
+    # elements above 2^-10 of the largest are exact: the score of such a query is as good as in fp32
+    p.q.copy_((torch.rand(70, 4, 128, device="cuda") + 0.01).bfloat16())
+    p.run()
+    k, _ = p.cached(0, 270)
+    z = torch.einsum("ahd,nhd->han", p.q.double(), k.repeat_interleave(2, 1)) / math.sqrt(128)
+    z = z.masked_fill(torch.ones(70, 270, dtype=torch.bool, device="cuda").triu(201), -math.inf)
+    ref = torch.logsumexp(z, 2).T
+    size = (p.q.double().abs().sum(2) * k.abs().amax() / math.sqrt(128))
+    assert ((p.lse.double() - ref).abs() <= 2 * 272 * 2.0 ** -23 * size + 270 * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -22 * ref.abs()).all()
+
+
+@BOTH
+def test_queries_that_are_not_finite(q8):
+    """A query with an element that is no number is none itself (with an infinite one too, in the 8-bit cache), and no other."""
+    p = Problem([200], [70], q8=q8, Hq=4, Hkv=2).run()
+    was = p.out.clone(), p.lse.clone()
+    p.q[7, 2, 11] = math.nan
+    if q8:
+        p.q[33, 1, 0] = -math.inf
+    p.run()
+    odd = torch.zeros(70, 4, dtype=torch.bool, device="cuda")
+    odd[7, 2] = True
+    odd[33, 1] = q8
+    assert p.out[odd].isnan().all() and p.lse[odd].isnan().all()
+    assert torch.equal(p.out[~odd], was[0][~odd]) and torch.equal(p.lse[~odd], was[1][~odd])
 
 
 def test_one_token_a_row_is_the_decode():
