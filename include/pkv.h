@@ -426,9 +426,10 @@ int pkv_extend_reserve(pkv_plan_t plan);
  * Products have fp32 sums and bf16 factors; 8-bit codes are exact, and a query
  * meets them in two e4m3 parts, exact for elements down to 2^-10 of its largest and
  * off by at most 2^-18 of the largest below that.  The softmax is fp32, with weights
- * below 2^-126 of the largest left out, and the weights rounded once to bf16 for the
- * product with V (after their V scale in the 8-bit cache) and summed before that
- * rounding; the output is rounded once to bf16.  The order of all sums is fixed by the lengths,
+ * below 2^-126 of the largest left out, and the weights rounded once for the product
+ * with V and summed before that rounding: to bf16, or, in the 8-bit cache and times
+ * their V scale, to f16 with a reference of their own (2^-11 of themselves, or 2^-31
+ * of the query's largest such product); the output is rounded once to bf16.  The order of all sums is fixed by the lengths,
  * so a repeated call gives the same bits.  A query whose scores are all -inf has
  * output 0 and lse -inf; one with a NaN element is NaN (in the 8-bit cache one with
  * an infinite element too).  Slots behind a row's last token may hold anything.  An

@@ -14,7 +14,7 @@
 // of 128; one KV block of 128 tokens serves both.  One CTA per SM, specialised
 // warps: one loads (TMA), two issue tcgen05.mma, two warpgroups do the softmax with
 // a row per thread, and one cleans V where masks end (bf16), or one loads V's codes
-// and four widen them to bf16 (8-bit).  Scores and outputs stay in tensor
+// and four widen them to f16 (8-bit).  Scores and outputs stay in tensor
 // memory: S0, S1, O0, O1 of 128 columns each; P replaces S, in place, as the
 // second product's first operand.  While one group is at its softmax the tensor
 // core works for the other.
@@ -38,7 +38,7 @@ struct Cfg {
     static constexpr int kTile = kExtBlock * D * 2;           // bytes of a K or V block in bf16
     static constexpr int kCode = kExtBlock * D;               // ... in e4m3
     static constexpr int kQ = kExtRows * D * 2;
-    // K and V take turns in one ring (bf16); or K's codes, V's codes and V in bf16 have a ring each (8-bit)
+    // K and V take turns in one ring (bf16); or K's codes, V's codes and V in f16 have a ring each (8-bit)
     static constexpr int kStages = Q8 ? (D == 128 ? 2 : 4) : (D == 128 ? 5 : 10);
     static constexpr int kKeys = Q8 ? (D == 128 ? 3 : 8) : 0;
     static constexpr int kCodes = Q8 ? (D == 128 ? 3 : 4) : 0;
@@ -77,12 +77,15 @@ struct Ctl {
     uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], pair_full, turn[2];
     // of shared rows: (8-bit, at first) what the first group has scaled the query's parts by; the second group's
     // reference and sum
-    float2 pair_ml[128];
+    union {
+        float2 pair_ml[128];
+        int64_t scan[20];   // (the schedule, before there are pieces)
+    };
+    float pair_u[128];      // (8-bit) the second group's reference of O
     uint64_t piece_full[kPieceRing], piece_empty[kPieceRing];
     Piece piece[kPieceRing];
     Found found[kPieceRing];
     float scales[kScaleRing][16];                  // 8 of K, 8 of V
-    int64_t scan[17];
     ExtRow row;                                    // the row that the CTA's part begins in, its first unit, its index
     int64_t row_unit;
     int32_t row0;
@@ -461,7 +464,7 @@ template <int D, bool Q8>
 __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t* smem, const int g) {
     using C = Cfg<D, Q8>;
     const int per = kExtRows / 2 / p.G;
-    constexpr uint32_t kIdQk = Q8 ? umma_idesc_e4m3(kExtBlock) : umma_idesc(kExtBlock, false), kIdPv = umma_idesc(D, true);
+    constexpr uint32_t kIdQk = Q8 ? umma_idesc_e4m3(kExtBlock) : umma_idesc(kExtBlock, false), kIdPv = umma_idesc(D, true, Q8);
     const uint32_t tS = c->tmem + g * 128, tO = tS + 256, base = smem_addr(smem);
     // descriptors count in 16 bytes: what is added to them never carries out of the address.  The parts of Q and the
     // codes of K are rows of D bytes.
@@ -569,9 +572,9 @@ __device__ __forceinline__ void multiply(const ExtendParams& p, Ctl* c, uint8_t*
     }
 }
 
-// ------------------------------------------------------------------ e4m3 to bf16
+// ------------------------------------------------------------------ e4m3 to f16
 
-// V's codes become bf16 exactly (4 bits of significand into 8); their scales join the
+// V's codes become f16, exactly and by one instruction for two; their scales join the
 // weights in fp32.  (K's go into the product as they are.)  In blocks with masked
 // places NaN codes become 0, as infinities and NaN do in clean_values.
 template <int D>
@@ -622,8 +625,8 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
                     uint32_t o[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        o[2 * k] = e4m3x2_bf16x2(static_cast<uint16_t>(v[h][k]));
-                        o[2 * k + 1] = e4m3x2_bf16x2(static_cast<uint16_t>(v[h][k] >> 16));
+                        o[2 * k] = e4m3x2_f16x2(static_cast<uint16_t>(v[h][k]));
+                        o[2 * k + 1] = e4m3x2_f16x2(static_cast<uint16_t>(v[h][k] >> 16));
                     }
                     const uint32_t first = (chunk % 4) * 2 + swap, at = dst + row / 8 * C::kGroup + row % 8 * 128;
                     const uint32_t a0 = at + ((first ^ (row & 7)) << 4), a1 = a0 ^ 16;
@@ -758,9 +761,24 @@ __device__ __forceinline__ void write_nan(const RowOut& o, int D) {
     }
 }
 
+// The row's output times f, where it lies.  (The block's product has not begun, and the
+// one before is done, as this block's scores came after it.)
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t tO, float f) {
+#pragma unroll 1
+    for (int k = 0; k < D; k += 32) {
+        uint32_t o[32];
+        tmem_ld32(o, tO + k);
+        tmem_wait_ld();
+        tmem_loaded32(o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tmem_st32(tO + k, o);
+    }
+}
+
 // Scores above the running reference m by more than 2^8 move it: the sum and the
-// output follow (the block's product has not begun, and the one before is done, as
-// this block's scores came after it).
+// output follow.
 template <int D>
 __device__ __forceinline__ void follow_maximum(float top, bool first, uint32_t tO, float& m, float& l) {
     if (first) {
@@ -770,16 +788,7 @@ __device__ __forceinline__ void follow_maximum(float top, bool first, uint32_t t
         const float f = to == -INFINITY ? 1.0f : ex2(m - to);
         l *= f;
         m = to;
-#pragma unroll 1
-        for (int k = 0; k < D; k += 32) {
-            uint32_t o[32];
-            tmem_ld32(o, tO + k);
-            tmem_wait_ld();
-            tmem_loaded32(o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st32(tO + k, o);
-        }
+        rescale<D>(tO, f);
     }
 }
 
@@ -861,14 +870,19 @@ __device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float cs
 
 // The same over the 8-bit cache: 16 scores share a scale of K, their weights one of
 // V.  `scales` has K's 8 (whose signs have gone into the scores) and V's 8; those of
-// blocks that the row does not see at all may be anything.  The scores are read
-// twice, as the widening warps leave too few registers to hold them.
+// blocks that the row does not see at all may be anything.
+// What goes into the product with V, 2^(c s - m) times V's scale, is rounded to f16
+// (11 bits where bf16 has 8: with scales that are no powers of two even the heaviest
+// weight is rounded) and has a reference u of its own in log2, since the heaviest token
+// may lie in a block of small scale: the largest product of the row is kept from 2^6 to
+// 2^14, f16 holds the others to 2^-11 of themselves or 2^-31 of it, and O counts in 2^u.
+// (Loops, and the scores read twice: the widening warps leave neither the registers
+// nor the room for instructions to do otherwise.)
 template <int D>
 __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float cs, const float* scales, int seen, bool first,
-                                                 float& m, float& l) {
-    float top = -INFINITY;
+                                                 float& m, float& l, float& u) {
+    float top = -INFINITY, topv = -INFINITY;
     uint32_t s[32];
-    // (loops, not straight code: three warps of a scheduler run three pieces of code, and instructions have to be near)
 #pragma unroll 1
     for (int k = 0; k < 128; k += 32) {
         tmem_ld32(s, tS + k);
@@ -877,15 +891,31 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
 #pragma unroll
         for (int i = 0; i < 32; i += 16) {
             const float* y = reinterpret_cast<const float*>(s + i);
-            float t = max3(y[0], y[1], y[2]), u = max3(y[3], y[4], y[5]);
-            t = max3(t, y[6], y[7]), u = max3(u, y[8], y[9]);
-            t = max3(t, y[10], y[11]), u = max3(u, y[12], y[13]);
-            t = max3(max3(t, y[14], y[15]), u, u);
-            top = fmaxf(top, t * (k + i < seen ? fabsf(scales[(k + i) / 16]) : 1.0f));
+            float a = max3(y[0], y[1], y[2]), b = max3(y[3], y[4], y[5]);
+            a = max3(a, y[6], y[7]), b = max3(b, y[8], y[9]);
+            a = max3(a, y[10], y[11]), b = max3(b, y[12], y[13]);
+            a = fmaxf(max3(a, y[14], y[15]), b);
+            const float t = a * (k + i < seen ? fabsf(scales[(k + i) / 16]) * cs : 1.0f);
+            top = fmaxf(top, t);
+            topv = fmaxf(topv, t + __log2f(fabsf(scales[8 + (k + i) / 16])));
         }
     }
-    follow_maximum<D>(top * cs, first, tO, m, l);
-    const float ref = m == -INFINITY ? 0.0f : -m;
+    topv -= 6.0f;
+    if (first) {
+        m = top;
+        u = topv;
+    } else {
+        if (top > m + kMoveAt) {
+            l *= ex2(m - top);
+            m = top;
+        }
+        if (__any_sync(kFull, topv > u + kMoveAt)) {
+            const float to = fmaxf(u, topv);
+            rescale<D>(tO, to == -INFINITY ? 1.0f : ex2(u - to));
+            u = to;
+        }
+    }
+    const float ref = m == -INFINITY ? 0.0f : -m, move = -ref - (u == -INFINITY ? 0.0f : u);
     const uint64_t ref2 = pack2(ref, ref);
     uint64_t sum[2] = {0, 0};
 #pragma unroll 1
@@ -895,7 +925,9 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
         tmem_loaded32(s);
 #pragma unroll
         for (int h = 0; h < 32; h += 16) {
-            const float ks = k + h < seen ? fabsf(scales[(k + h) / 16]) * cs : 1.0f, vs = k + h < seen ? scales[8 + (k + h) / 16] : 0.0f;
+            const float sv = scales[8 + (k + h) / 16];
+            const float ks = k + h < seen ? fabsf(scales[(k + h) / 16]) * cs : 1.0f;
+            const float vs = k + h < seen ? copysignf(ex2(__log2f(fabsf(sv)) + move), sv) : 0.0f;
             const uint64_t ks2 = pack2(ks, ks), vs2 = pack2(vs, vs);
 #pragma unroll
             for (int i = h; i < h + 16; i += 2) {
@@ -903,7 +935,7 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
                 const uint64_t y = pack2(ex2(e.x), ex2(e.y));
                 sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], y);
                 const F2 z = unpack2(mul2(y, vs2));
-                s[i / 2] = bf16x2(z.x, z.y);
+                s[i / 2] = f16x2(z.x, z.y);
             }
         }
         tmem_st16(tS + k / 2, s);
@@ -933,7 +965,7 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
         const bool warp_live = base_row + (row & ~31) < pi.ntok << shift;   // some row of the warp does
         const int limit = pi.limit0 + ((base_row + row) >> shift);          // tokens that the row sees
         const int masked = first_masked(pi);
-        float m = -INFINITY, l = 0.0f, cs = p.scale_log2;
+        float m = -INFINITY, l = 0.0f, u = -INFINITY, cs = p.scale_log2;
         if (Q8 && sh.nb > 0) {   // (every piece's load is waited for: a parity tells a phase from the next one only)
             const uint32_t phase = q_loads++ & 1;
             if (!wait_warp(&c->q_full, phase, &c->abort)) return false;
@@ -968,7 +1000,7 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
                 if (Q8 && __any_sync(kFull, scales[lane & 7] < 0.0f)) turn_scores(tS, scales);
                 if (cut) mask_scores(tS, seen);
                 if constexpr (Q8)
-                    softmax_block_q8<D>(tS, tO, cs, scales, cut ? seen : kExtBlock, j == 0, m, l);
+                    softmax_block_q8<D>(tS, tO, cs, scales, cut ? seen : kExtBlock, j == 0, m, l, u);
                 else
                     softmax_block<D>(tS, tO, cs, j == 0, m, l);
                 tmem_wait_st();
@@ -990,9 +1022,13 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
             tc_fence_after();
         }
         float f0 = 1.0f, f1 = 0.0f;   // the two groups' parts of shared rows
+        // 8-bit: O counts in 2^u where the sum counts in 2^m; in two steps, as 2^(u - m) may be far off
+        auto step = [](float u, float m) { return u == -INFINITY || m == -INFINITY ? 1.0f : ex2(0.5f * (u - m)); };
+        float h0 = Q8 ? step(u, m) : 1.0f, h1 = 1.0f;
         if (sh.pair) {
             if (g == 1) {
                 c->pair_ml[row] = make_float2(m, l);
+                if (Q8) c->pair_u[row] = u;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -1005,6 +1041,7 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
             ++pairs;
             tc_fence_after();
             const float2 other = c->pair_ml[row];
+            if (Q8) h1 = step(c->pair_u[row], other.x);
             const float to = fmaxf(m, other.x), ref = to == -INFINITY ? 0.0f : to;
             f0 = ex2(m - ref);
             f1 = ex2(other.x - ref);
@@ -1033,10 +1070,15 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
                         tmem_loaded32(y);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            x[i] = __float_as_uint(__uint_as_float(x[i]) * f0 + __uint_as_float(y[i]) * f1);
+                            x[i] = Q8 ? __float_as_uint(__uint_as_float(x[i]) * h0 * (h0 * f0) + __uint_as_float(y[i]) * h1 * (h1 * f1))
+                                      : __float_as_uint(__uint_as_float(x[i]) * f0 + __uint_as_float(y[i]) * f1);
                     } else {
                         tmem_wait_ld();
                         tmem_loaded32(x);
+                        if (Q8) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * h0 * h0);
+                        }
                     }
                     if (live && o.out) {
 #pragma unroll

@@ -71,10 +71,10 @@ __device__ __forceinline__ uint64_t umma_desc(uint32_t smem, uint32_t lead, uint
            static_cast<uint64_t>(group >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 
-// bf16 x bf16 -> fp32, 128 rows, `n` columns; B's rows are its outer dimension
-// (K-major), or its inner one (`b_mn`).
-__host__ __device__ constexpr uint32_t umma_idesc(int n, bool b_mn) {
-    return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
+// bf16 x bf16 (or f16 x f16) -> fp32, 128 rows, `n` columns; B's rows are its outer
+// dimension (K-major), or its inner one (`b_mn`).
+__host__ __device__ constexpr uint32_t umma_idesc(int n, bool b_mn, bool f16 = false) {
+    return 1u << 4 | (f16 ? 0u : 1u << 7 | 1u << 10) | (b_mn ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
 }
 
 // Operand in rows of D bytes (8-bit elements, K-major), 64 or 128, swizzled by as many.
@@ -163,7 +163,12 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// two e4m3 codes, exactly (through f16)
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// two e4m3 codes, exactly
 __device__ __forceinline__ F2 e4m3x2_f32(uint16_t codes) {
     uint32_t h;
     F2 r;
@@ -171,9 +176,10 @@ __device__ __forceinline__ F2 e4m3x2_f32(uint16_t codes) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(r.x), "=f"(r.y) : "r"(h));
     return r;
 }
-__device__ __forceinline__ uint32_t e4m3x2_bf16x2(uint16_t codes) {
-    const F2 r = e4m3x2_f32(codes);
-    return bf16x2(r.x, r.y);
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t codes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
+    return h;
 }
 // {lo, hi} rounded to e4m3, lo in the lower byte
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {

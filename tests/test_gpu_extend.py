@@ -5,9 +5,11 @@ Tolerances, element by element.  Let A = sum_t w_t |v_t| with the exact weights 
   cache (exact codes, their scale joins in fp32) the query is two e4m3 numbers, scaled so that its largest element lies
   in [2^7, 2^8): the second holds the first's remainder to half of e4m3's smallest step, 2^-10 of 2^7, which adds
   2^-17 max_e |q_e| sum_e |k_te| / sqrt(D) at most.
-* A weight is off by a factor of 2 d + 2^-20 (score and reference, ex2, V scale), then rounded to bf16: 2^-8.
-  Sums of n terms in fp32 add n 2^-23.  So |out error| <= (2^-8 + 2 (2 d + 2^-20 + n 2^-23)) A (numerator and
-  denominator), and rounding the output to bf16 adds 2^-8 |out|, or half a subnormal step.
+* A weight is off by a factor of 2 d + 2^-20 (score and reference, ex2, V scale), then rounded: r = 2^-8 of itself in
+  bf16; times its V scale in f16, 2^-11 of itself or half a step of 2^-24 where the largest such product is at least
+  2^6 (8-bit; and 2^-16 for the logarithm of the scale).  Sums of n terms in fp32 add n 2^-23.  So |out error| <= (r + 2 (2 d + 2^-20 + n 2^-23)) A (numerator
+  and denominator), for 8 bits and n tokens + n 2^-31 448 max_t w_t |scale_t|, and rounding the output to bf16 adds
+  2^-8 |out|, or half a subnormal step.
 * A weight below 2^-126, fp32's least normal number, against a largest one of 1 or more is 0: n 2^-126 max |v|.
 * |lse error| <= 2 d + 2^-20 + n 2^-23 + 2^-22 |lse|.
 """
@@ -106,7 +108,13 @@ class Problem:
                     far = kh.abs().sum(1).expand(a, n).masked_fill(hidden, 0).amax(1)
                     d = d + 2.0 ** -17 * q.abs().amax(1) * far / math.sqrt(D)
                 f = 2 * (2 * d + 2.0 ** -20 + n * 2.0 ** -23)
-                tol = (2.0 ** -8 + f)[:, None] * A + 2.0 ** -8 * ref.abs() + 2.0 ** -133 + n * 2.0 ** -126 * vh.abs().max()
+                r = 2.0 ** -11 + 2.0 ** -16 if self.q8 else 2.0 ** -8   # (2^-16: the logarithm of the V scale)
+                tol = (r + f)[:, None] * A + 2.0 ** -8 * ref.abs() + 2.0 ** -133 + n * 2.0 ** -126 * vh.abs().max()
+                if self.q8:
+                    t = torch.arange(n, device="cuda")
+                    blk = (self.table[b].long()[t // self.ps] * self.ps + t % self.ps) // 16
+                    heaviest = (w * self.vs.flatten(0, 1)[blk, h // G].double().abs()).amax(1)
+                    tol = tol + (n * 2.0 ** -31 * 448 * heaviest)[:, None]
                 got = out[here, h].double()
                 assert torch.isfinite(got).all(), (b, h)
                 over = ((got - ref).abs() / tol).max().item()
