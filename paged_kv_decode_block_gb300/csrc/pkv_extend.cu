@@ -28,7 +28,6 @@ namespace pkv {
 namespace {
 
 constexpr int kPieceRing = 4;
-constexpr int kScaleRing = 8;      // blocks whose scales are in shared memory
 constexpr float kMoveAt = 8.0f;    // log2 by which the maximum outgrows the reference
 
 template <int D, bool Q8>
@@ -50,6 +49,9 @@ struct Cfg {
     static constexpr int kReaders = Q8 ? 15 : 11;             // warps that read the piece ring
     static constexpr int kKeysAt = kQ + kStages * kTile, kCodesAt = kKeysAt + kKeys * kCode;
     static constexpr size_t kBytes = static_cast<size_t>(kCodesAt) + kCodes * kCode;
+    // Blocks whose scales are held: K's place of block b + kKeys is free when both groups have the scores of block b,
+    // whose scales the softmax reads after that, but those of block b - 1 it has read by then.
+    static constexpr int kScales = Q8 ? kKeys + 1 : 0;
 };
 
 struct alignas(16) Piece {
@@ -72,7 +74,7 @@ struct Ctl {
     uint64_t key_full[8], key_empty[8];            // blocks of K in e4m3
     uint64_t code_full[4], code_empty[4];          // ... of V
     uint64_t q_split[2];                           // the groups' queries in two e4m3 parts
-    uint64_t scale_full[kScaleRing];
+    uint64_t scale_full[9];
     uint64_t q_full, q_empty, drain;
     uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], pair_full, turn[2];
     // of shared rows: (8-bit, at first) what the first group has scaled the query's parts by; the second group's
@@ -85,7 +87,6 @@ struct Ctl {
     uint64_t piece_full[kPieceRing], piece_empty[kPieceRing];
     Piece piece[kPieceRing];
     Found found[kPieceRing];
-    float scales[kScaleRing][16];                  // 8 of K, 8 of V
     ExtRow row;                                    // the row that the CTA's part begins in, its first unit, its index
     int64_t row_unit;
     int32_t row0;
@@ -93,6 +94,8 @@ struct Ctl {
     uint32_t tmem;
     int32_t keys_issued, values_issued;            // blocks whose loads have begun
     int32_t q_loads;
+    float scales[1][24];                           // [kScales]: 8 of K, 8 of V, and log2 of their magnitudes
+    __device__ __forceinline__ float* scales_of(uint32_t i) { return scales[0] + i * 24; }
 };
 
 // Waits for a phase, for at most kWaitLimitNs: then every wait of the CTA gives up, and the kernel's end sets the
@@ -292,10 +295,11 @@ __device__ __forceinline__ void load(const ExtendParams& p, Ctl* c, uint8_t* sme
             const int tok = bx.token(j, page);
             const uint32_t at = Q8 ? blocks : 2 * blocks, st = at % kRing;
             if (at >= kRing && !wait_warp(&empty[st], (at / kRing - 1) & 1, &c->abort)) return;
-            if (Q8) {
-                if (lane < 16) c->scales[blocks % kScaleRing][lane] = sc;
+            if constexpr (Q8) {
+                if (lane < 16) c->scales_of(blocks % C::kScales)[lane] = sc;
+                if (lane >= 8 && lane < 16) c->scales_of(blocks % C::kScales)[8 + lane] = log2f(fabsf(sc));
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&c->scale_full[blocks % kScaleRing]);
+                if (lane == 0) mbar_arrive(&c->scale_full[blocks % C::kScales]);
             }
             if (lane == 0) c->keys_issued = blocks + 1;
             load_block<Q8>(smem + (Q8 ? C::kKeysAt : C::kQ) + st * kBlock, bx, tok, bytes, kmap, e.kvh, &full[st], policy);
@@ -897,7 +901,7 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
             a = fmaxf(max3(a, y[14], y[15]), b);
             const float t = a * (k + i < seen ? fabsf(scales[(k + i) / 16]) * cs : 1.0f);
             top = fmaxf(top, t);
-            topv = fmaxf(topv, t + __log2f(fabsf(scales[8 + (k + i) / 16])));
+            topv = fmaxf(topv, t + scales[16 + (k + i) / 16]);
         }
     }
     topv -= 6.0f;
@@ -917,6 +921,7 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
     }
     const float ref = m == -INFINITY ? 0.0f : -m, move = -ref - (u == -INFINITY ? 0.0f : u);
     const uint64_t ref2 = pack2(ref, ref);
+    const float by = ex2(0.5f * move);   // (twice, as 2^move may be out of range where the scales are far from 1)
     uint64_t sum[2] = {0, 0};
 #pragma unroll 1
     for (int k = 0; k < 128; k += 32) {
@@ -925,9 +930,8 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
         tmem_loaded32(s);
 #pragma unroll
         for (int h = 0; h < 32; h += 16) {
-            const float sv = scales[8 + (k + h) / 16];
             const float ks = k + h < seen ? fabsf(scales[(k + h) / 16]) * cs : 1.0f;
-            const float vs = k + h < seen ? copysignf(ex2(__log2f(fabsf(sv)) + move), sv) : 0.0f;
+            const float vs = k + h < seen ? scales[8 + (k + h) / 16] * by * by : 0.0f;
             const uint64_t ks2 = pack2(ks, ks), vs2 = pack2(vs, vs);
 #pragma unroll
             for (int i = h; i < h + 16; i += 2) {
@@ -992,10 +996,10 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
                 const int seen = limit - at * kExtBlock;   // columns of the block that the row sees
                 const bool cut = at >= masked;
                 const float* scales = nullptr;
-                if (Q8) {
+                if constexpr (Q8) {
                     const uint32_t b = blocks + sh.block(j);
-                    if (!wait_warp(&c->scale_full[b % kScaleRing], (b / kScaleRing) & 1, &c->abort)) return false;
-                    scales = c->scales[b % kScaleRing];
+                    if (!wait_warp(&c->scale_full[b % C::kScales], (b / C::kScales) & 1, &c->abort)) return false;
+                    scales = c->scales_of(b % C::kScales);
                 }
                 if (Q8 && __any_sync(kFull, scales[lane & 7] < 0.0f)) turn_scores(tS, scales);
                 if (cut) mask_scores(tS, seen);
@@ -1158,7 +1162,7 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
             mbar_init(&c->code_full[i], 1);
             mbar_init(&c->code_empty[i], 4);
         }
-        for (int i = 0; i < kScaleRing; ++i) mbar_init(&c->scale_full[i], 1);
+        for (int i = 0; i < C::kScales; ++i) mbar_init(&c->scale_full[i], 1);
         mbar_init(&c->q_full, 1);
         mbar_init(&c->q_empty, 2);
         mbar_init(&c->drain, 2);
@@ -1226,7 +1230,7 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
     if (work) {
         if (warp < 8) {
             if constexpr (Q8)
-                asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+                asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
             else
                 asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
             if (!attend<D, Q8>(p, c, smem)) {
@@ -1234,7 +1238,7 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
             }
         } else if (Q8 && warp < 12) {
             if constexpr (Q8) {
-                asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
+                asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
                 widen<D>(p, c, smem);
             }
         } else {
@@ -1372,7 +1376,7 @@ __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant
 template <int D, bool Q8>
 cudaError_t launch(const ExtendParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                    int ctas, cudaStream_t stream) {
-    constexpr size_t kSmem = Cfg<D, Q8>::kBytes + sizeof(Ctl);
+    constexpr size_t kSmem = Cfg<D, Q8>::kBytes + sizeof(Ctl) + Cfg<D, Q8>::kScales * 24 * sizeof(float);
     static_assert(kSmem <= 232448, "shared memory of a CTA");
     // (on every call, as a device reset drops it)
     cudaError_t e = cudaFuncSetAttribute(extend_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
