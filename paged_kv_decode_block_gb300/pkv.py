@@ -654,23 +654,25 @@ def copy_pages(pools, copies, page_size: int, stream=None):
         list_ = np.zeros((0, 3), np.int32)
     page_size = int(page_size)
     dev, num_pages, known, flat = torch.cuda.current_device(), None, {}, []
+    shape = dtype = None
     for t in pools:
         try:
             if t.get_device() != dev or not t.is_contiguous():
                 raise TypeError("pools must be contiguous tensors on the current CUDA device")
-            kind = (t.shape, t.dtype)
-            sizes = known.get(kind)
+            if t.dtype is not dtype or t.shape != shape:   # (mostly the last one's)
+                shape, dtype = t.shape, t.dtype
+                sizes = known.get((shape, dtype))
+                if sizes is None:
+                    n, entries = (tuple(shape) + (0, 0))[:2]
+                    if num_pages is None:
+                        num_pages = n
+                    if n != num_pages or n == 0 or entries == 0 or t.numel() == 0 or page_size <= 0 or page_size % entries:
+                        raise ValueError(f"pools: shape {tuple(shape)}, expected [{num_pages}][{page_size} / tokens an entry][...]")
+                    sizes = known[shape, dtype] = (t.numel() // n * t.element_size(), page_size // entries)
+                size, unit = sizes
         except AttributeError:
             raise TypeError("pools must be contiguous tensors on the current CUDA device") from None
-        if sizes is None:
-            n, entries = (t.shape + (0, 0))[:2]
-            if num_pages is None:
-                num_pages = n
-            if n != num_pages or n == 0 or entries == 0 or t.numel() == 0 or page_size <= 0 or page_size % entries:
-                raise ValueError(f"pools: shape {tuple(t.shape)}, expected [{num_pages}][{page_size} / tokens an entry][...]")
-            sizes = known[kind] = (t.numel() // n * t.element_size(), page_size // entries)
-        flat.append(t.data_ptr())
-        flat += sizes
+        flat += (t.data_ptr(), size, unit)
     if not flat:
         return
     rc = (_lib or load()).pkv_copy_pages(struct.pack("%dq" % len(flat), *flat), len(flat) // 3, list_.ctypes.data, len(list_),
