@@ -429,12 +429,13 @@ int pkv_extend_reserve(pkv_plan_t plan);
  * below 2^-126 of the largest left out, and the weights rounded once for the product
  * with V and summed before that rounding: to bf16, or, in the 8-bit cache and times
  * their V scale, to f16 with a reference of their own (2^-11 of themselves, or 2^-31
- * of the query's largest such product); the output is rounded once to bf16.  The order of all sums is fixed by the lengths,
- * so a repeated call gives the same bits.  A query whose scores are all -inf has
+ * of the query's largest such product); the output is rounded once to bf16.  The order
+ * of all sums is fixed by the lengths, so a repeated call gives the same bits.  A query whose scores are all -inf has
  * output 0 and lse -inf; one with a NaN element is NaN (in the 8-bit cache one with
  * an infinite element too).  Slots behind a row's last token may hold anything.  An
  * infinity or NaN in a token's V, or a V scale, reaches the queries that see the
- * token (of the scale's block) and no others.  Tokens of q that belong to no row, and their outputs, are left as they are.
+ * token (of the scale's block) and no others.  Tokens of q that belong to no row, and
+ * their outputs, are left as they are.
  *
  * A row whose n_b exceeds seq_lens_d[b], or whose length exceeds its table, sets
  * PKV_DEV_PLAN_MISMATCH and its outputs are NaN; offsets outside [0, total_tokens]
@@ -570,7 +571,7 @@ int pkv_profile_read(pkv_plan_t plan, float *ms, int32_t capacity, int32_t *coun
  *                       when `capacity` is too small (*n_copies is then what it takes;
  *                       half of the pool always suffices).  Nothing changes then.  The
  *                       device table has to follow before it is used again
- * A pool that a session is bound to is not compacted (its tables are the session's),
+ * A pool that a session was ever bound to is not compacted (its tables are the session's),
  * and once a session has taken the pages to the device (pkv_session_device_plan)
  * none of its pages is shared any more: both PKV_EINVAL.  That session refuses a
  * pool with shared pages too.

@@ -19,8 +19,21 @@
 // second product's first operand.  While one group is at its softmax the tensor
 // core works for the other.
 //
-// Bound: the tensor core (4 * 256 * 128 * D operations a block) when a KV head
-// has more than about 300 rows of scores to a byte of cache, HBM below.
+// Bound: a KV head's token is 4 D bytes (8-bit: 2 D) and 4 D operations for each row
+// of scores, so above about 280 rows (140) that read the same tokens it is the tensor
+// core, 2048 cycles a block at D = 128, and below them HBM.  Measured, 32 query and 8
+// KV heads, D = 128, bf16:
+//   2048 tokens after 30720          705-763 us   1.40-1.51 PFLOP/s, about 3000 cycles a
+//                                                 block: the gap between one group's products
+//                                                 and the other's, and the boxes of 16 tokens
+//   8 prompts of 128-4096            215 us       0.93 PFLOP/s: a tile of few blocks costs 17
+//                                                 thousand cycles besides (its masked blocks,
+//                                                 outputs, code that is not in the cache)
+//   5 tokens each after 512-32768    55 us        4.6 TB/s: 6 us until the stream runs, 6 us
+//                                                 to join the parts
+// and e4m3:
+//   4 tokens each, 56 rows of 1024-8192   219 us  softmax and widening, a warp's latencies
+//   8 rows, chunks of 512                 416 us  the same: 0.87 PFLOP/s
 #include "pkv_extend_schedule.h"
 #include "pkv_tcgen05.cuh"
 
@@ -49,8 +62,8 @@ struct Cfg {
     static constexpr int kReaders = Q8 ? 15 : 11;             // warps that read the piece ring
     static constexpr int kKeysAt = kQ + kStages * kTile, kCodesAt = kKeysAt + kKeys * kCode;
     static constexpr size_t kBytes = static_cast<size_t>(kCodesAt) + kCodes * kCode;
-    // Blocks whose scales are held: K's place of block b + kKeys is free when both groups have the scores of block b,
-    // whose scales the softmax reads after that, but those of block b - 1 it has read by then.
+    // Blocks whose scales are held.  Those of block b + kKeys are written once both groups' scores of block b are
+    // there; the softmax then still reads block b's, but is done with those of b - 1.
     static constexpr int kScales = Q8 ? kKeys + 1 : 0;
 };
 
@@ -201,7 +214,7 @@ struct Boxes {
     }
     // the page of this lane's 16 tokens of block j, or -2 past the row's end
     __device__ __forceinline__ int entry(int j) const {
-        const uint32_t t = j * kExtBlock + (threadIdx.x & 7) * 16;
+        const uint32_t t = static_cast<uint32_t>(j) * kExtBlock + (threadIdx.x & 7) * 16;
         return j < hi && t < static_cast<uint32_t>(len) ? row[t / static_cast<uint32_t>(page_size)] : -2;
     }
     __device__ __forceinline__ bool ok(int page) const { return page >= 0 && page < num_pages; }
@@ -454,7 +467,7 @@ __device__ __forceinline__ Share share_of(const Piece& pi, int g, int per) {
     if (s.pair)
         s.count = (s.nb + 1 - g) / 2;
     else
-        s.count = s.nb == 0 || last < g * per ? 0 : max(0, min(pi.hi, (pi.limit0 + last + kExtBlock - 1) / kExtBlock) - pi.lo);
+        s.count = s.nb == 0 || last < g * per ? 0 : max(0, min(pi.hi, static_cast<int>(ext_blocks(pi.limit0 + last))) - pi.lo);
     return s;
 }
 
@@ -605,50 +618,44 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
             const bool clean = j >= masked;
             const int seen = max(pi.limit0 - j * kExtBlock, 0), valid = len - j * kExtBlock;
             bool odd = false;
-            constexpr int kAtOnce = 1;
+            // (a loop: unrolled, its loads and stores overlap, but the code leaves the cache and the softmax waits for it)
 #pragma unroll 1
-            for (int i = 0; i < kPerRow; i += kAtOnce) {
-                uint32_t v[kAtOnce][4];   // (the loads first: the stores would hold them up)
-#pragma unroll
-                for (int h = 0; h < kAtOnce; ++h) lds128(v[h], src + (i + h) * 2048);
-                if (i + kAtOnce == kPerRow) {   // read: the next codes may come
+            for (int i = 0; i < kPerRow; ++i) {
+                uint32_t v[4];
+                lds128(v, src + i * 2048);
+                if (i + 1 == kPerRow) {   // read: the next codes may come
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&c->code_empty[cs]);
                 }
-#pragma unroll
-                for (int h = 0; h < kAtOnce; ++h) {
-                    const int row = tid / kPerRow + (i + h) * (128 / kPerRow);
-                    if (clean && row >= seen) {   // rows that not all of the tile's rows see, and what lies behind the row's end
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t nan = ((v[h][k] & 0x7f7f7f7fu) + 0x01010101u & 0x80808080u) >> 7;
-                            odd |= nan != 0 && row < valid;
-                            v[h][k] = row < valid ? v[h][k] & ~(nan * 0xffu) : 0;
-                        }
-                    }
-                    uint32_t o[8];
+                const int row = tid / kPerRow + i * (128 / kPerRow);
+                if (clean && row >= seen) {   // rows that not all of the tile's rows see, and what lies behind the row's end
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        o[2 * k] = e4m3x2_f16x2(static_cast<uint16_t>(v[h][k]));
-                        o[2 * k + 1] = e4m3x2_f16x2(static_cast<uint16_t>(v[h][k] >> 16));
+                        const uint32_t nan = ((v[k] & 0x7f7f7f7fu) + 0x01010101u & 0x80808080u) >> 7;
+                        odd |= nan != 0 && row < valid;
+                        v[k] = row < valid ? v[k] & ~(nan * 0xffu) : 0;
                     }
-                    const uint32_t first = (chunk % 4) * 2 + swap, at = dst + row / 8 * C::kGroup + row % 8 * 128;
-                    const uint32_t a0 = at + ((first ^ (row & 7)) << 4), a1 = a0 ^ 16;
-                    if (swap) {
-                        sts128(a0, o[4], o[5], o[6], o[7]);
-                        sts128(a1, o[0], o[1], o[2], o[3]);
-                    } else {
-                        sts128(a0, o[0], o[1], o[2], o[3]);
-                        sts128(a1, o[4], o[5], o[6], o[7]);
-                    }
+                }
+                uint32_t o[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    o[2 * k] = e4m3x2_f16x2(static_cast<uint16_t>(v[k]));
+                    o[2 * k + 1] = e4m3x2_f16x2(static_cast<uint16_t>(v[k] >> 16));
+                }
+                const uint32_t first = (chunk % 4) * 2 + swap, at = dst + row / 8 * C::kGroup + row % 8 * 128;
+                const uint32_t a0 = at + ((first ^ (row & 7)) << 4), a1 = a0 ^ 16;
+                if (swap) {
+                    sts128(a0, o[4], o[5], o[6], o[7]);
+                    sts128(a1, o[0], o[1], o[2], o[3]);
+                } else {
+                    sts128(a0, o[0], o[1], o[2], o[3]);
+                    sts128(a1, o[4], o[5], o[6], o[7]);
                 }
             }
             if (clean && __any_sync(kFull, odd) && lane == 0) c->found[slot].nonfinite = 1;
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&c->full[st]);
-            }
+            if (lane == 0) mbar_arrive(&c->full[st]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->piece_empty[slot]);
@@ -662,10 +669,9 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
 // two that brings its largest element to [2^7, 2^8): 4 bits of significand and the 4
 // that are left, exact for elements down to 2^-10 of the largest, and off by at most
 // 2^-18 of the largest below that.  Two e4m3 products cost what one of bf16 does, and
-// the cache's keys go into them untouched; widening them too took more of the
-// scheduler's slots than the softmax does (2048 tokens after 6144, 32/8 heads, D 128:
-// 252 us).  Returns what the scores are to be multiplied by; NaN if an element is not
-// finite.
+// the cache's keys go into them untouched; widening K as well as V is twice the work for
+// warps that a block waits for already.  Returns what the scores are to be multiplied
+// by; NaN if an element is not finite.
 template <int D>
 __device__ __forceinline__ float split_query(uint32_t at, int row, int barrier) {
     uint32_t q[D / 2];   // pairs
@@ -967,7 +973,8 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
         const int base_row = sh.pair ? 0 : g * 128;
         const bool live = base_row + row < pi.ntok << shift;                // this thread's row exists
         const bool warp_live = base_row + (row & ~31) < pi.ntok << shift;   // some row of the warp does
-        const int limit = pi.limit0 + ((base_row + row) >> shift);          // tokens that the row sees
+        // tokens that the row sees (rows that do not exist: no more than there are, which keeps them within 31 bits)
+        const int limit = static_cast<int>(min(static_cast<uint32_t>(pi.limit0) + ((base_row + row) >> shift), static_cast<uint32_t>(pi.len)));
         const int masked = first_masked(pi);
         float m = -INFINITY, l = 0.0f, u = -INFINITY, cs = p.scale_log2;
         if (Q8 && sh.nb > 0) {   // (every piece's load is waited for: a parity tells a phase from the next one only)
@@ -1105,7 +1112,8 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
                 }
                 if (c->found[slot].nonfinite && live)
                     add_nonfinite<D, Q8>(p, p.block_table + static_cast<size_t>(pi.b) * p.max_pages, pi.kvh,
-                                         max(lo, masked) * kExtBlock, min(limit, pi.hi * kExtBlock), o);
+                                         max(lo, masked) * kExtBlock,
+                                         static_cast<int>(min(static_cast<uint32_t>(limit), static_cast<uint32_t>(pi.hi) * kExtBlock)), o);
                 if (live && o.out && o.lse) *o.lse = kLn2 * (m + log2f(l));
                 if (live && !o.out) *o.ml = make_float2(m, l);
             }
@@ -1294,7 +1302,8 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
 // block per CTA that began such a tile and 32 of its rows; lanes are rows (the
 // layout in which the states were left).  What it waits for is memory: the
 // references and sums of all parts come in one round (warps take parts), then the
-// states, of which a warp takes an eighth of the columns and eight parts at once.
+// states, of which a warp takes an eighth of the columns with 16 loads in flight (5
+// drafted tokens over 8 rows, 150 parts: 5.8 us; with one part behind the other 9.5).
 template <int D>
 __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant__ ExtendParams p) {
     extern __shared__ float weights[];   // [part][32 rows]; -1: saw nothing, its state was not written

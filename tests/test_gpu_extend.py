@@ -529,3 +529,49 @@ def test_offsets_past_32_bits():
     p.table = torch.where(p.table >= 0, p.table + pages - p.pages, p.table)
     p.plan = pkv.Plan(p.after, None, ps, B=2, Hq=16, Hkv=Hkv, D=D, max_pages=p.table.shape[1], num_pages=pages)
     p.run().check()
+
+
+@pytest.mark.parametrize("G", [1, 4])
+@BOTH
+def test_a_row_of_almost_two_to_the_31(G, q8):
+    """A table as long as a plan takes, whose tokens before the last 32 lie in one page and weigh nothing (scores of
+    -448, the others within a few tens of 0): lengths and positions that a sign bit or a rounding up could break."""
+    p = Problem([12], [20], Hq=G, Hkv=1, D=64, q8=q8)
+    used = p.table[0, :2].clone()
+    far = next(i for i in range(p.pages) if i not in used.tolist())
+    p.q[..., 0] = 8.0
+    if q8:
+        p.k.view(torch.uint8)[far] = 0
+        p.k.view(torch.uint8)[far, ..., 0] = 0xfe
+        p.ks[far] = 1.0
+    else:
+        p.k[far] = 0.0
+        p.k[far, ..., 0] = -448.0
+    wide = 2 ** 27 - 1
+    table = torch.full((1, wide), far, dtype=torch.int32, device="cuda")
+    table[0, -2:] = used
+    lens = torch.full((1,), wide * 16, dtype=torch.int32, device="cuda")
+    plan = pkv.Plan([32], None, 16, B=1, Hq=G, Hkv=1, D=64, max_pages=wide, num_pages=p.pages)
+    short, p.plan = p.plan, plan
+    p.run(table=table, lens=lens)
+    torch.cuda.synchronize()
+    assert plan.status() == 0
+    p.plan = short
+    p.check()
+
+
+def test_decode_of_the_same_plan_at_the_same_time():
+    p = Problem([3000, 200, 8000], [40, 1, 300])
+    q = torch.randn(3, 8, 128, generator=p.gen, device="cuda").bfloat16()
+    alone, out = (torch.empty(3, 8, 128, device="cuda") for _ in range(2))
+    lse = torch.empty(3, 8, device="cuda")
+    pkv.decode(q, p.k, p.v, p.table, p.lens_d, p.plan, alone, lse)
+    p.plan.reserve_extend()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(10):
+        p.run()
+        pkv.decode(q, p.k, p.v, p.table, p.lens_d, p.plan, out, lse, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, alone)
+    p.check()
