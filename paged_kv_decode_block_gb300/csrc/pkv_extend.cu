@@ -23,7 +23,7 @@
 // of scores, so above about 280 rows (140) that read the same tokens it is the tensor
 // core, 2048 cycles a block at D = 128, and below them HBM.  Measured, 32 query and 8
 // KV heads, D = 128, bf16:
-//   2048 tokens after 30720          705-763 us   1.40-1.51 PFLOP/s, about 3000 cycles a
+//   2048 tokens after 30720          703-779 us   1.37-1.51 PFLOP/s, about 3000 cycles a
 //                                                 block: the gap between one group's products
 //                                                 and the other's, and the boxes of 16 tokens
 //   8 prompts of 128-4096            215 us       0.93 PFLOP/s: a tile of few blocks costs 17
@@ -32,8 +32,8 @@
 //   5 tokens each after 512-32768    55 us        4.6 TB/s: 6 us until the stream runs, 6 us
 //                                                 to join the parts
 // and e4m3:
-//   4 tokens each, 56 rows of 1024-8192   219 us  softmax and widening, a warp's latencies
-//   8 rows, chunks of 512                 416 us  the same: 0.87 PFLOP/s
+//   4 tokens each, 56 rows of 1024-8192   214 us  softmax and widening, a warp's latencies
+//   8 rows, chunks of 512                 411 us  the same: 0.88 PFLOP/s
 #include "pkv_extend_schedule.h"
 #include "pkv_tcgen05.cuh"
 
@@ -618,7 +618,8 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
             const bool clean = j >= masked;
             const int seen = max(pi.limit0 - j * kExtBlock, 0), valid = len - j * kExtBlock;
             bool odd = false;
-            // (a loop: unrolled, its loads and stores overlap, but the code leaves the cache and the softmax waits for it)
+            // (a short loop: loads ahead of their use, or two pieces at once, make the code longer, and these warps' and the
+            // softmax's together no longer fit the instruction cache: drafts over 56 rows 226 and 230 us against 215)
 #pragma unroll 1
             for (int i = 0; i < kPerRow; ++i) {
                 uint32_t v[4];
@@ -636,21 +637,18 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
                         v[k] = row < valid ? v[k] & ~(nan * 0xffu) : 0;
                     }
                 }
+                // the half that goes first, first
+                const uint32_t w[4] = {swap ? v[2] : v[0], swap ? v[3] : v[1], swap ? v[0] : v[2], swap ? v[1] : v[3]};
                 uint32_t o[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    o[2 * k] = e4m3x2_f16x2(static_cast<uint16_t>(v[k]));
-                    o[2 * k + 1] = e4m3x2_f16x2(static_cast<uint16_t>(v[k] >> 16));
+                    o[2 * k] = e4m3x2_f16x2(static_cast<uint16_t>(w[k]));
+                    o[2 * k + 1] = e4m3x2_f16x2(static_cast<uint16_t>(w[k] >> 16));
                 }
                 const uint32_t first = (chunk % 4) * 2 + swap, at = dst + row / 8 * C::kGroup + row % 8 * 128;
-                const uint32_t a0 = at + ((first ^ (row & 7)) << 4), a1 = a0 ^ 16;
-                if (swap) {
-                    sts128(a0, o[4], o[5], o[6], o[7]);
-                    sts128(a1, o[0], o[1], o[2], o[3]);
-                } else {
-                    sts128(a0, o[0], o[1], o[2], o[3]);
-                    sts128(a1, o[4], o[5], o[6], o[7]);
-                }
+                const uint32_t a0 = at + ((first ^ (row & 7)) << 4);
+                sts128(a0, o[0], o[1], o[2], o[3]);
+                sts128(a0 ^ 16, o[4], o[5], o[6], o[7]);
             }
             if (clean && __any_sync(kFull, odd) && lane == 0) c->found[slot].nonfinite = 1;
             fence_proxy_async_shared();
@@ -887,7 +885,8 @@ __device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float cs
 // may lie in a block of small scale: the largest product of the row is kept from 2^6 to
 // 2^14, f16 holds the others to 2^-11 of themselves or 2^-31 of it, and O counts in 2^u.
 // (Loops, and the scores read twice: the widening warps leave neither the registers
-// nor the room for instructions to do otherwise.)
+// nor the room for instructions to do otherwise.  64 columns at a time take 4 to 8 %
+// longer; 16 make drafts 4 % faster and chunks of 512 4 % slower.)
 template <int D>
 __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float cs, const float* scales, int seen, bool first,
                                                  float& m, float& l, float& u) {
