@@ -384,6 +384,7 @@ __device__ __forceinline__ bool clean_values(uint32_t tile, int seen, int valid)
 template <int D>
 __device__ __forceinline__ void clean(const ExtendParams& p, Ctl* c, uint8_t* smem) {
     using C = Cfg<D, false>;
+    const int lane = threadIdx.x & 31;
     uint32_t n = 0;
     for (uint32_t pc = 0;; ++pc) {
         const int slot = pc % kPieceRing;
@@ -391,22 +392,27 @@ __device__ __forceinline__ void clean(const ExtendParams& p, Ctl* c, uint8_t* sm
         const Piece pi = c->piece[slot];
         const int hi = pi.bad || pi.ntok == 0 ? pi.lo : pi.hi, masked = first_masked(pi);
         for (int j = pi.lo; j < hi; ++j, n += 2) {
-            // (every block is waited for, in order: a parity tells a phase from the next one only)
-            if (!wait_warp(&c->full[n % C::kStages], (n / C::kStages) & 1, &c->abort)) return;
-            const uint32_t vn = n + 1, st = vn % C::kStages;
+            // (every block is waited for, in order, and its place given back: a parity tells a phase from the next one only,
+            // so the ring must not go round without this warp)
+            const uint32_t kt = n % C::kStages, vn = n + 1, st = vn % C::kStages;
+            if (!wait_warp(&c->full[kt], (n / C::kStages) & 1, &c->abort)) return;
+            if (lane == 0) mbar_arrive(&c->empty[kt]);
             if (!wait_warp(&c->full[st], (vn / C::kStages) & 1, &c->abort)) return;
-            if (j < masked) continue;
-            const int first = j * kExtBlock;
-            const bool odd = clean_values<D>(smem_addr(smem) + C::kQ + st * C::kTile, max(pi.limit0 - first, 0), min(pi.len - first, kExtBlock));
-            fence_proxy_async_shared();
-            __syncwarp();
-            if ((threadIdx.x & 31) == 0) {
+            bool odd = false;
+            if (j >= masked) {
+                const int first = j * kExtBlock;
+                odd = clean_values<D>(smem_addr(smem) + C::kQ + st * C::kTile, max(pi.limit0 - first, 0), min(pi.len - first, kExtBlock));
+                fence_proxy_async_shared();
+                __syncwarp();
+            }
+            if (lane == 0) {
                 if (odd) c->found[slot].nonfinite = 1;
-                mbar_arrive(&c->fixed[st]);
+                if (j >= masked) mbar_arrive(&c->fixed[st]);
+                mbar_arrive(&c->empty[st]);
             }
         }
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(&c->piece_empty[slot]);
+        if (lane == 0) mbar_arrive(&c->piece_empty[slot]);
         if (pi.ntok == 0) return;
     }
 }
@@ -1158,7 +1164,7 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&c->full[i], Q8 ? 4 : 1);
-            mbar_init(&c->empty[i], 2);
+            mbar_init(&c->empty[i], Q8 ? 2 : 3);   // the products' two threads and (bf16) the warp that cleans
             mbar_init(&c->fixed[i], 1);
         }
         for (int i = 0; i < C::kKeys; ++i) {
