@@ -982,9 +982,11 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
         const int limit = static_cast<int>(min(static_cast<uint32_t>(pi.limit0) + ((base_row + row) >> shift), static_cast<uint32_t>(pi.len)));
         const int masked = first_masked(pi);
         float m = -INFINITY, l = 0.0f, u = -INFINITY, cs = p.scale_log2;
-        if (Q8 && sh.nb > 0) {   // (every piece's load is waited for: a parity tells a phase from the next one only)
+        if (Q8 && sh.nb > 0) {   // (every piece's load is waited for, and the next one follows every warp: a parity tells a
+                                 // phase from the next one only, and in a piece of one block the second group may have no rows)
             const uint32_t phase = q_loads++ & 1;
             if (!wait_warp(&c->q_full, phase, &c->abort)) return false;
+            if (lane == 0) mbar_arrive(&c->q_empty);
             if (sh.pair && g == 1) {
                 if (!wait_warp(&c->q_split[0], phase, &c->abort)) return false;
                 cs *= c->pair_ml[row].x;
@@ -1177,7 +1179,7 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
         }
         for (int i = 0; i < C::kScales; ++i) mbar_init(&c->scale_full[i], 1);
         mbar_init(&c->q_full, 1);
-        mbar_init(&c->q_empty, 2);
+        mbar_init(&c->q_empty, Q8 ? 2 + 8 : 2);   // the products' two threads and (8-bit) the softmax warps
         mbar_init(&c->drain, 2);
         mbar_init(&c->pair_full, 4);
         for (int g = 0; g < 2; ++g) {

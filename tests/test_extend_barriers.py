@@ -100,3 +100,50 @@ def test_the_cleaning_warp_never_falls_a_ring_behind(stages, slow):
         for x in full + empty + fixed:
             x.pending, x.phase = x.arrivals, 0
         play({"loads": loads(), "product 0": product(), "product 1": product(), "cleaning": cleaning()}, random.Random(seed), slow)
+
+
+@pytest.mark.parametrize("slow", [[], ["softmax 5"], ["softmax 4", "softmax 7"], ["softmax 0"], ["product 1"], ["loads"]])
+def test_the_second_group_never_falls_two_queries_behind(slow):
+    """8-bit: pieces of one block and few rows, in which the second group's warps have nothing to do but wait."""
+    pieces, ring = 40, 4
+    frees = "mbar_arrive(&c->q_empty)" in body("attend")
+    q_full, q_empty = Barrier(count("q_full", True)), Barrier(count("q_empty", True))
+    told, done = [Barrier(1) for _ in range(ring)], [Barrier(10) for _ in range(ring)]   # (the readers that matter here)
+    scores, outputs = Barrier(1), Barrier(4)   # of the first group
+
+    def loads():
+        for i in range(pieces):
+            if i >= ring:
+                yield done[i % ring], i // ring - 1
+            told[i % ring].arrive()
+            if i > 0:
+                yield q_empty, i - 1
+            q_full.arrive()
+
+    def product(g):
+        for i in range(pieces):
+            yield told[i % ring], i // ring
+            done[i % ring].arrive()
+            yield q_full, i
+            if g == 0:
+                if i > 0:
+                    yield outputs, i - 1
+                scores.arrive()
+            q_empty.arrive()
+
+    def softmax(g):
+        for i in range(pieces):
+            yield told[i % ring], i // ring
+            yield q_full, i
+            if frees:
+                q_empty.arrive()
+            if g == 0:
+                yield scores, i
+                outputs.arrive()
+            done[i % ring].arrive()
+
+    for seed in range(20):
+        for x in [q_full, q_empty, scores, outputs] + told + done:
+            x.pending, x.phase = x.arrivals, 0
+        play({"loads": loads(), **{f"product {g}": product(g) for g in range(2)}, **{f"softmax {w}": softmax(w // 4) for w in range(8)}},
+             random.Random(seed), slow)
