@@ -289,8 +289,7 @@ __device__ __forceinline__ void load(const ExtendParams& p, Ctl* c, uint8_t* sme
         auto scale = [&](int j, int page) {   // lanes 0..7: K's, 8..15: V's
             if (!Q8 || lane >= 16 || !bx.ok(page)) return 0.0f;
             const uint32_t blk = (j * kExtBlock + (lane & 7) * 16) % static_cast<uint32_t>(p.page_size) / kBlockRows;
-            const float x = (lane < 8 ? p.k_scales : p.v_scales)[(static_cast<size_t>(page) * (p.page_size / kBlockRows) + blk) * p.Hkv + e.kvh];
-            return lane < 8 && x == 0.0f ? 0x1p-120f : x;   // (a score of -inf in a place that is not seen stays one)
+            return (lane < 8 ? p.k_scales : p.v_scales)[(static_cast<size_t>(page) * (p.page_size / kBlockRows) + blk) * p.Hkv + e.kvh];
         };
         // pages are asked for two blocks ahead and scales one, so that no block waits for one load behind the other
         int next = bx.entry(e.lo), next2 = bx.entry(e.lo + 1);
@@ -882,6 +881,14 @@ __device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float cs
     l += a.x + a.y;
 }
 
+// What a score of codes is multiplied by: the magnitude of K's scale (its sign is in the score) times the row's
+// factor.  Never 0, or a score of -inf in a place that is not seen would not stay one; a score is below 2^24, so that
+// fp32's least normal number makes as little of it.  A scale that is no number stays none.
+__device__ __forceinline__ float key_factor(float scale, float cs) {
+    const float f = fabsf(scale) * cs;
+    return f < 0x1p-126f ? 0x1p-126f : f;
+}
+
 // The same over the 8-bit cache: 16 scores share a scale of K, their weights one of
 // V.  `scales` has K's 8 (whose signs have gone into the scores) and V's 8; those of
 // blocks that the row does not see at all may be anything.
@@ -910,7 +917,7 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
             a = max3(a, y[6], y[7]), b = max3(b, y[8], y[9]);
             a = max3(a, y[10], y[11]), b = max3(b, y[12], y[13]);
             a = fmaxf(max3(a, y[14], y[15]), b);
-            const float t = a * (k + i < seen ? fabsf(scales[(k + i) / 16]) * cs : 1.0f);
+            const float t = a * (k + i < seen ? key_factor(scales[(k + i) / 16], cs) : 1.0f);
             top = fmaxf(top, t);
             topv = fmaxf(topv, t + scales[16 + (k + i) / 16]);
         }
@@ -941,7 +948,7 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
         tmem_loaded32(s);
 #pragma unroll
         for (int h = 0; h < 32; h += 16) {
-            const float ks = k + h < seen ? fabsf(scales[(k + h) / 16]) * cs : 1.0f;
+            const float ks = k + h < seen ? key_factor(scales[(k + h) / 16], cs) : 1.0f;
             const float vs = k + h < seen ? scales[8 + (k + h) / 16] * by * by : 0.0f;
             const uint64_t ks2 = pack2(ks, ks), vs2 = pack2(vs, vs);
 #pragma unroll
