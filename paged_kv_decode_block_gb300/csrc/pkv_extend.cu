@@ -889,6 +889,13 @@ __device__ __forceinline__ float key_factor(float scale, float cs) {
     return f < 0x1p-126f ? 0x1p-126f : f;
 }
 
+// What a weight is multiplied by: V's scale times by^3.  No product is larger than 2^14, so where a finite scale's factor
+// is out of range the weights that meet it are below 2^-113, and left out: 0 rather than 0 times infinity.
+__device__ __forceinline__ float value_factor(float scale, float by) {
+    const float f = scale * by * by * by;
+    return fabsf(f) == INFINITY && fabsf(scale) != INFINITY ? 0.0f : f;
+}
+
 // The same over the 8-bit cache: 16 scores share a scale of K, their weights one of
 // V.  `scales` has K's 8 (whose signs have gone into the scores) and V's 8; those of
 // blocks that the row does not see at all may be anything.
@@ -937,9 +944,11 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
             u = to;
         }
     }
-    const float ref = m == -INFINITY ? 0.0f : -m, move = -ref - (u == -INFINITY ? 0.0f : u);
+    const float ref = m == -INFINITY ? 0.0f : -m, move = u == -INFINITY ? 0.0f : -ref - u;
     const uint64_t ref2 = pack2(ref, ref);
-    const float by = ex2(0.5f * move);   // (twice, as 2^move may be out of range where the scales are far from 1)
+    // 2^move in three steps, as it may be out of range where the scales are far from 1.  (Beyond 2^378 a scale is 0, or all
+    // weights are that meet it: least scale 2^-149, least weight 2^-126, products up to 2^14.)
+    const float by = ex2(fminf(move, 378.0f) * (1.0f / 3));
     uint64_t sum[2] = {0, 0};
 #pragma unroll 1
     for (int k = 0; k < 128; k += 32) {
@@ -949,7 +958,7 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
 #pragma unroll
         for (int h = 0; h < 32; h += 16) {
             const float ks = k + h < seen ? key_factor(scales[(k + h) / 16], cs) : 1.0f;
-            const float vs = k + h < seen ? scales[8 + (k + h) / 16] * by * by : 0.0f;
+            const float vs = k + h < seen ? value_factor(scales[8 + (k + h) / 16], by) : 0.0f;
             const uint64_t ks2 = pack2(ks, ks), vs2 = pack2(vs, vs);
 #pragma unroll
             for (int i = h; i < h + 16; i += 2) {

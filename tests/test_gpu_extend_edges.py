@@ -40,3 +40,64 @@ def test_queries_and_keys_of_next_to_nothing(scale, D):
     p.k.view(torch.uint8).zero_()   # an append's scale of a block of zeros is 2^-120
     p.q.zero_()
     p.run().check()
+
+
+def far_scores(p, b, c):
+    """Token t of row b gets score c[t]: D = 64, queries of 8 in element 0, keys of scale 1."""
+    assert p.D == 64 and len(c) == p.after[b]
+    k = torch.zeros(len(c), p.Hkv, 64, device="cuda")
+    k[..., 0] = torch.tensor(c, dtype=torch.float32, device="cuda")[:, None]
+    p.k.flatten(0, 1).view(torch.uint8)[slots(p, b, len(c))] = k.to(FP8).view(torch.uint8)
+
+
+@pytest.mark.parametrize("lens, new", [([200], [3]), ([130, 0], [200, 300]), ([20000], [5])])
+def test_values_of_scale_zero_or_far_apart(lens, new):
+    """8-bit: scales of V that are 0, where scores are high, and scales so far apart that the factor on a weight is out of
+    fp32's range where the weight itself is 0."""
+    p = Problem(lens, new, q8=True, Hq=4, Hkv=1, D=64)
+    p.q.zero_()
+    p.q[..., 0] = 8.0
+    p.ks.fill_(1.0)
+    was = p.vs.clone()
+    rng = torch.Generator().manual_seed(11)
+
+    def blocks(b, lo, hi):   # the scales' places of the row's tokens [lo, hi), both multiples of 16
+        return slots(p, b, p.after[b])[lo:hi:16] // 16
+
+    def scales(s):
+        p.vs.flatten(0, 1)[:] = s
+        return p.vs.flatten(0, 1)
+
+    for b, n in enumerate(p.after):
+        # high scores, and no scale of V but 0 in the first block of 128, or anywhere
+        far_scores(p, b, [240.0] * n)
+    s = scales(was.flatten(0, 1))
+    for b in range(p.B):
+        s[blocks(b, 0, 128)] = 0
+    p.run().check()
+    s.zero_()
+    p.run().check()
+    assert (p.out == 0).all()
+    # the heaviest token has a scale of V of 0, and all others weigh nothing
+    for b, n in enumerate(p.after):
+        far_scores(p, b, [448.0 if t == 5 else float(t % 11) for t in range(n)])
+    s = scales(was.flatten(0, 1))
+    for b in range(p.B):
+        s[blocks(b, 0, 16)] = 0
+    p.run().check()
+    # the heaviest token's scale is small, and those of tokens that weigh next to nothing are large; and the other way round
+    for heavy, light in ((2.0 ** -100, 2.0 ** 110), (2.0 ** 110, 2.0 ** -100), (2.0 ** -140, 1.0), (0.0, 2.0 ** 110)):
+        for far, near in ((60.0, 0.0), (80.0, 0.0), (88.0, 1.5), (104.0, 0.0)):
+            for b, n in enumerate(p.after):
+                far_scores(p, b, [far if t % 150 == 5 else near for t in range(n)])
+            s = scales(light)
+            for b, n in enumerate(p.after):
+                at = slots(p, b, n)[5::150] // 16
+                s[at] = heavy
+            p.run().check()
+    # anything
+    for b, n in enumerate(p.after):
+        far_scores(p, b, (torch.rand(n, generator=rng) * 160 - 80).tolist())
+    s = scales(torch.exp2(torch.rand(was.flatten(0, 1).shape, generator=rng).cuda() * 220 - 110))
+    s[::7] = 0
+    p.run().check()
