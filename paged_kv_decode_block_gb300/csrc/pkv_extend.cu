@@ -846,8 +846,11 @@ __device__ __forceinline__ void turn_scores(uint32_t tS, const float* scales) {
 
 // One block of a row's scores to weights: maximum, 2^(c s - m), sum; weights in
 // bf16 over the scores.  All 128 scores stay in registers between the two passes.
+// Rows that do not exist (not `live`) hold the queries of other rows of the call, or
+// what another CTA is writing over them: they have no maximum, and so no say in when
+// the warp's references move.
 template <int D>
-__device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float cs, bool first, float& m, float& l) {
+__device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float cs, bool live, bool first, float& m, float& l) {
     uint32_t s[128];
 #pragma unroll
     for (int k = 0; k < 4; ++k) tmem_ld32(s + 32 * k, tS + 32 * k);
@@ -861,7 +864,7 @@ __device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float cs
     for (int k = 8; k < 128; k += 8)
 #pragma unroll
         for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(s[k + i]), __uint_as_float(s[k + 4 + i]));
-    follow_maximum<D>(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs, first, tO, m, l);
+    follow_maximum<D>(live ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs : -INFINITY, first, tO, m, l);
     const float ref = m == -INFINITY ? 0.0f : -m;
     const uint64_t ref2 = pack2(ref, ref), cs2 = pack2(cs, cs);
     uint64_t sum[2] = {0, 0};
@@ -908,8 +911,8 @@ __device__ __forceinline__ float value_factor(float scale, float by) {
 // nor the room for instructions to do otherwise.  64 columns at a time take 4 to 8 %
 // longer; 16 make drafts 4 % faster and chunks of 512 4 % slower.)
 template <int D>
-__device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float cs, const float* scales, int seen, bool first,
-                                                 float& m, float& l, float& u) {
+__device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float cs, const float* scales, int seen, bool live,
+                                                 bool first, float& m, float& l, float& u) {
     float top = -INFINITY, topv = -INFINITY;
     uint32_t s[32];
 #pragma unroll 1
@@ -930,6 +933,7 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
         }
     }
     topv -= 6.0f;
+    if (!live) top = topv = -INFINITY;
     if (first) {
         m = top;
         u = topv;
@@ -1034,9 +1038,9 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
                 if (Q8 && __any_sync(kFull, scales[lane & 7] < 0.0f)) turn_scores(tS, scales);
                 if (cut) mask_scores(tS, seen);
                 if constexpr (Q8)
-                    softmax_block_q8<D>(tS, tO, cs, scales, cut ? seen : kExtBlock, j == 0, m, l, u);
+                    softmax_block_q8<D>(tS, tO, cs, scales, cut ? seen : kExtBlock, live, j == 0, m, l, u);
                 else
-                    softmax_block<D>(tS, tO, cs, j == 0, m, l);
+                    softmax_block<D>(tS, tO, cs, live, j == 0, m, l);
                 tmem_wait_st();
             }
             tc_fence_before();

@@ -101,3 +101,33 @@ def test_values_of_scale_zero_or_far_apart(lens, new):
     s = scales(torch.exp2(torch.rand(was.flatten(0, 1).shape, generator=rng).cuda() * 220 - 110))
     s[::7] = 0
     p.run().check()
+
+
+@BOTH
+@pytest.mark.parametrize("new", [3, 35])
+def test_a_row_does_not_depend_on_the_next_rows_queries(new, q8):
+    """A tile's box of queries goes on into the next row's.  Scores that rise by 2^3 a block move the reference now and
+    then; queries that are not the row's, in the same warp, have no say in when: the same bits."""
+    p = Problem([30000, 0], [new, 60], Hq=32, Hkv=8, q8=q8)
+    n = p.after[0]
+    ramp = (torch.arange(n, device="cuda") - (n - 1540)).clamp(min=0) * 0.00144
+    k = torch.randn(n, 8, 128, generator=p.gen, device="cuda") * 0.1 + ramp[:, None, None]
+    at = slots(p, 0, n)
+    if q8:
+        p.k.flatten(0, 1).view(torch.uint8)[at] = (k * 64).to(FP8).view(torch.uint8)
+        p.ks.fill_(2.0 ** -6)
+    else:
+        p.k.flatten(0, 1)[at] = k.bfloat16()
+    q = torch.rand(p.q.shape, generator=p.gen, device="cuda") * 0.5 + 0.75
+    results = []
+    for size in (0.0, 20.0, 1.0):
+        x = q.clone()
+        x[new:] *= size
+        p.q.copy_(x.bfloat16())
+        p.out.fill_(7.0), p.lse.fill_(7.0)
+        p.run().check()
+        results.append((p.out[:new].clone(), p.lse[:new].clone()))
+    for out, lse in results[1:]:
+        assert torch.equal(lse, results[0][1]) and torch.equal(out, results[0][0])
+    p.run(out=p.q)   # (the next row's outputs are being written over its queries)
+    assert torch.equal(p.q[:new], results[0][0]) and torch.equal(p.lse[:new], results[0][1])
