@@ -670,8 +670,9 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
 
 // A row's query, bf16, becomes the sum of two e4m3 numbers in place, times a power of
 // two that brings its largest element to [2^7, 2^8): 4 bits of significand and the 4
-// that are left, exact for elements down to 2^-10 of the largest, and off by at most
-// 2^-18 of the largest below that.  Two e4m3 products cost what one of bf16 does, and
+// that are left, whose last place is e4m3's least step of 2^-9 or more for elements from
+// 2^-2 on: those down to 2^-9 of the largest are exact, those below off by at most
+// half a step, 2^-17 of the largest.  Two e4m3 products cost what one of bf16 does, and
 // the cache's keys go into them untouched; widening K as well as V is twice the work for
 // warps that a block waits for already.  Returns what the scores are to be multiplied
 // by; NaN if an element is not finite.

@@ -131,3 +131,27 @@ def test_a_row_does_not_depend_on_the_next_rows_queries(new, q8):
         assert torch.equal(lse, results[0][1]) and torch.equal(out, results[0][0])
     p.run(out=p.q)   # (the next row's outputs are being written over its queries)
     assert torch.equal(p.q[:new], results[0][0]) and torch.equal(p.lse[:new], results[0][1])
+
+
+def test_elements_of_a_query_that_are_exact():
+    """8-bit: elements down to 2^-9 of the largest, a power of two here, are exact, and so is the score as far as fp32 is;
+    K is 0 where the largest element is.  The next ones below are off by at most 2^-17 of the largest."""
+    p = Problem([200], [70], q8=True, Hq=4, Hkv=2)
+    p.k.view(torch.uint8)[..., 0] = 0
+    for low, exact in ((2.0 ** -9, True), (2.0 ** -10, False)):
+        q = 128 * low * (1 + torch.randint(0, 128, (70, 4, 128), generator=p.gen, device="cuda") / 128)
+        q *= torch.where(torch.rand(q.shape, generator=p.gen, device="cuda") < 0.5, -1, 1)
+        q[..., 0] = 128
+        p.q.copy_(q.bfloat16())
+        assert torch.equal(p.q.float(), q.float())
+        p.run().check()
+        k, _ = p.cached(0, 270)
+        k = k.repeat_interleave(2, 1)
+        hidden = torch.ones(70, 270, dtype=torch.bool, device="cuda").triu(201)
+        z = torch.einsum("ahd,nhd->han", p.q.double(), k) / math.sqrt(128)
+        ref = torch.logsumexp(z.masked_fill(hidden, -math.inf), 2).T
+        size = torch.einsum("ahd,nhd->han", p.q.double().abs(), k.abs()).masked_fill(hidden, 0).amax(2).T / math.sqrt(128)
+        tol = 2 * 272 * 2.0 ** -23 * size + 270 * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -22 * ref.abs()
+        if not exact:
+            tol = tol + 128 * 2.0 ** -17 * k.abs().sum(2).amax(0) / math.sqrt(128)
+        assert ((p.lse.double() - ref).abs() <= tol).all()
