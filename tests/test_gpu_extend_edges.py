@@ -155,3 +155,21 @@ def test_elements_of_a_query_that_are_exact():
         if not exact:
             tol = tol + 128 * 2.0 ** -17 * k.abs().sum(2).amax(0) / math.sqrt(128)
         assert ((p.lse.double() - ref).abs() <= tol).all()
+
+
+@BOTH
+def test_what_bad_offsets_leave_alone(q8):
+    """Rows with offsets that cannot be are left out: tokens of no other row keep what they held, and the other rows are
+    answered."""
+    p = Problem([300, 100, 40], [60, 5, 30], q8=q8)
+    whole = {0: range(0, 60), 1: range(60, 65), 2: range(65, 95)}
+    for cu, good in (([0, 60, 65, 96], [0, 1]), ([-3, 60, 65, 95], [1, 2]), ([0, 60, 50, 50], [0]),
+                     ([0, 2 ** 31 - 1, 65, 95], [2]), ([0, 60, 2 ** 31 - 1, 2 ** 31 - 1], [0])):
+        p.out.fill_(7.0), p.lse.fill_(7.0)
+        p.run(cu_tokens=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+        assert p.plan.status() == pkv.DEV_PLAN_MISMATCH, cu
+        p.check(rows=good)
+        left = torch.ones(p.T, dtype=torch.bool, device="cuda")
+        for b in good:
+            left[list(whole[b])] = False
+        assert (p.out[left] == 7).all() and (p.lse[left] == 7).all(), cu
