@@ -173,3 +173,28 @@ def test_what_bad_offsets_leave_alone(q8):
         for b in good:
             left[list(whole[b])] = False
         assert (p.out[left] == 7).all() and (p.lse[left] == 7).all(), cu
+
+
+@BOTH
+@pytest.mark.parametrize("lens, new", [(0, 700), (9000, 60)])
+def test_each_token_in_its_turn(lens, new, q8):
+    """Queries that single a token out: its V is the answer, and nothing else can make up for it."""
+    p = Problem([lens], [new], Hq=8, Hkv=2, q8=q8, size=1.0)
+    n = lens + new
+    # (keys alike in size, so that a query along one of them scores highest there)
+    k = torch.where(torch.rand(n, 2, 128, generator=p.gen, device="cuda") < 0.5, -1.0, 1.0)
+    at = slots(p, 0, n)
+    if q8:
+        p.k.flatten(0, 1).view(torch.uint8)[at] = k.to(FP8).view(torch.uint8)
+        p.ks.fill_(1.0)
+    else:
+        p.k.flatten(0, 1)[at] = k.bfloat16()
+    limit = torch.arange(lens, n, device="cuda")
+    for part in range(4):   # the token itself, the first ones, and others it sees
+        pick = (limit if part == 0 else (limit - lens) if part == 1 else
+                (torch.rand(new, generator=p.gen, device="cuda") * (limit + 1)).long()).clamp(max=n - 1)
+        p.q.copy_((k[pick] * 4).repeat_interleave(4, 1).bfloat16())
+        p.run().check()
+        _, v = p.cached(0, n)
+        # 128 * 4 / sqrt(128) = 45 for the token, and few others above 20
+        assert ((p.out.double() - v[pick].repeat_interleave(4, 1)).abs() <= 2.0 ** -6 * v.abs().max()).all()
