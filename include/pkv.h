@@ -538,7 +538,8 @@ int pkv_profile_read(pkv_plan_t plan, float *ms, int32_t capacity, int32_t *coun
  * Host page pool: a FIFO free list of page ids, for callers that grow rows one
  * token at a time (the continuous-session workload).
  *   pkv_pool_create     copies `count` free page ids, handed out in that order
- *                       (PKV_EINVAL for an id outside [0, num_pages) or listed twice)
+ *                       (PKV_EINVAL for an id outside [0, num_pages) or listed twice;
+ *                       PKV_ENOMEM, with 5 bytes a page)
  *   pkv_pool_reserve    for every row whose next token (position seq_lens_h[b])
  *                       starts a new page whose table entry is still unassigned
  *                       (negative), pops a page into

@@ -1343,18 +1343,23 @@ int pkv_pool_create(const int32_t* free_pages, int32_t count, int32_t num_pages,
     *pool = nullptr;
     for (int32_t i = 0; i < count; ++i)
         if (free_pages[i] < 0 || free_pages[i] >= num_pages) return PKV_EINVAL;
-    pkv_pool_s* p = new (std::nothrow) pkv_pool_s;
-    if (!p) return PKV_ENOMEM;
-    p->is_free.assign(num_pages, 0);
-    p->shared.assign(num_pages, 0);
-    for (int32_t i = 0; i < count; ++i) {
-        if (p->is_free[free_pages[i]]) {   // listed twice
-            delete p;
-            return PKV_EINVAL;
+    pkv_pool_s* p = nullptr;
+    try {
+        p = new pkv_pool_s;
+        p->is_free.assign(num_pages, 0);
+        p->shared.assign(num_pages, 0);
+        for (int32_t i = 0; i < count; ++i) {
+            if (p->is_free[free_pages[i]]) {   // listed twice
+                delete p;
+                return PKV_EINVAL;
+            }
+            p->is_free[free_pages[i]] = 1;
         }
-        p->is_free[free_pages[i]] = 1;
+        p->free_list.assign(free_pages, free_pages + count);
+    } catch (const std::exception&) {
+        delete p;
+        return PKV_ENOMEM;
     }
-    p->free_list.assign(free_pages, free_pages + count);
     p->num_pages = num_pages;
     *pool = p;
     return PKV_OK;
