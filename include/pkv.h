@@ -426,8 +426,8 @@ int pkv_extend_reserve(pkv_plan_t plan);
  * Products have fp32 sums and bf16 factors; 8-bit codes are exact, and a query
  * meets them in two e4m3 parts, exact for elements down to 2^-9 of its largest and
  * off by at most 2^-17 of the largest below that.  The softmax is fp32, with weights
- * below 2^-126 of the largest left out (8-bit: those below 2^-113 where V's scale is so large
- * that their factor is out of range), and the weights rounded once for the product
+ * below 2^-126 of the largest left out (8-bit: those below 2^-113 may count for less where
+ * V's scale is so large that their factor is out of range), and the weights rounded once for the product
  * with V and summed before that rounding: to bf16, or, in the 8-bit cache and times
  * their V scale, to f16 with a reference of their own (2^-11 of themselves, or 2^-31
  * of the query's largest such product); the output is rounded once to bf16.  The order

@@ -289,7 +289,8 @@ __device__ __forceinline__ void load(const ExtendParams& p, Ctl* c, uint8_t* sme
         auto scale = [&](int j, int page) {   // lanes 0..7: K's, 8..15: V's
             if (!Q8 || lane >= 16 || !bx.ok(page)) return 0.0f;
             const uint32_t blk = (j * kExtBlock + (lane & 7) * 16) % static_cast<uint32_t>(p.page_size) / kBlockRows;
-            return (lane < 8 ? p.k_scales : p.v_scales)[(static_cast<size_t>(page) * (p.page_size / kBlockRows) + blk) * p.Hkv + e.kvh];
+            const float x = (lane < 8 ? p.k_scales : p.v_scales)[(static_cast<size_t>(page) * (p.page_size / kBlockRows) + blk) * p.Hkv + e.kvh];
+            return lane < 8 || fabsf(x) < INFINITY ? x : __uint_as_float(0x7fffffffu);   // (an infinite scale of V: NaN)
         };
         // pages are asked for two blocks ahead and scales one, so that no block waits for one load behind the other
         int next = bx.entry(e.lo), next2 = bx.entry(e.lo + 1);
@@ -792,12 +793,14 @@ __device__ __forceinline__ void rescale(uint32_t tO, float f) {
 }
 
 // Scores above the running reference m by more than 2^8 move it: the sum and the
-// output follow.
+// output follow, for the whole warp.  Rows that do not exist (not `live`) hold the
+// queries of other rows of the call, or what another CTA is writing over them: they
+// have no say in it.
 template <int D>
-__device__ __forceinline__ void follow_maximum(float top, bool first, uint32_t tO, float& m, float& l) {
+__device__ __forceinline__ void follow_maximum(float top, bool live, bool first, uint32_t tO, float& m, float& l) {
     if (first) {
         m = top;
-    } else if (__any_sync(kFull, top > m + kMoveAt)) {
+    } else if (__any_sync(kFull, live && top > m + kMoveAt)) {
         const float to = fmaxf(m, top);
         const float f = to == -INFINITY ? 1.0f : ex2(m - to);
         l *= f;
@@ -847,9 +850,6 @@ __device__ __forceinline__ void turn_scores(uint32_t tS, const float* scales) {
 
 // One block of a row's scores to weights: maximum, 2^(c s - m), sum; weights in
 // bf16 over the scores.  All 128 scores stay in registers between the two passes.
-// Rows that do not exist (not `live`) hold the queries of other rows of the call, or
-// what another CTA is writing over them: they have no maximum, and so no say in when
-// the warp's references move.
 template <int D>
 __device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float cs, bool live, bool first, float& m, float& l) {
     uint32_t s[128];
@@ -865,7 +865,7 @@ __device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float cs
     for (int k = 8; k < 128; k += 8)
 #pragma unroll
         for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(s[k + i]), __uint_as_float(s[k + 4 + i]));
-    follow_maximum<D>(live ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs : -INFINITY, first, tO, m, l);
+    follow_maximum<D>(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs, live, first, tO, m, l);
     const float ref = m == -INFINITY ? 0.0f : -m;
     const uint64_t ref2 = pack2(ref, ref), cs2 = pack2(cs, cs);
     uint64_t sum[2] = {0, 0};
@@ -886,18 +886,13 @@ __device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float cs
 }
 
 // What a score of codes is multiplied by: the magnitude of K's scale (its sign is in the score) times the row's
-// factor.  Never 0, or a score of -inf in a place that is not seen would not stay one; a score is below 2^24, so that
+// factor.  Not 0, or a score of -inf in a place that is not seen would not stay one; a score is below 2^24, so that
 // fp32's least normal number makes as little of it.  A scale that is no number stays none.
-__device__ __forceinline__ float key_factor(float scale, float cs) {
-    const float f = fabsf(scale) * cs;
-    return f < 0x1p-126f ? 0x1p-126f : f;
-}
-
-// What a weight is multiplied by: V's scale times by^3.  No product is larger than 2^14, so where a finite scale's factor
-// is out of range the weights that meet it are below 2^-113, and left out: 0 rather than 0 times infinity.
+__device__ __forceinline__ float key_factor(float scale, float cs) { return max_nan(fabsf(scale) * cs, 0x1p-126f); }
+// What a weight is multiplied by: V's scale times by^2.  No product is larger than 2^14, so where the factor is out of
+// range the weights that meet it are below 2^-113 and may count for less; but 0 times infinity must not come of it.
 __device__ __forceinline__ float value_factor(float scale, float by) {
-    const float f = scale * by * by * by;
-    return fabsf(f) == INFINITY && fabsf(scale) != INFINITY ? 0.0f : f;
+    return min_nan(max_nan(scale * by * by, -0x1.fffffep127f), 0x1.fffffep127f);
 }
 
 // The same over the 8-bit cache: 16 scores share a scale of K, their weights one of
@@ -928,13 +923,12 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
             a = max3(a, y[6], y[7]), b = max3(b, y[8], y[9]);
             a = max3(a, y[10], y[11]), b = max3(b, y[12], y[13]);
             a = fmaxf(max3(a, y[14], y[15]), b);
-            const float t = a * (k + i < seen ? key_factor(scales[(k + i) / 16], cs) : 1.0f);
+            const float t = a * (k + i < seen ? fabsf(scales[(k + i) / 16]) * cs : 1.0f);   // (finite times 0 at worst)
             top = fmaxf(top, t);
             topv = fmaxf(topv, t + scales[16 + (k + i) / 16]);
         }
     }
     topv -= 6.0f;
-    if (!live) top = topv = -INFINITY;
     if (first) {
         m = top;
         u = topv;
@@ -943,7 +937,7 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
             l *= ex2(m - top);
             m = top;
         }
-        if (__any_sync(kFull, topv > u + kMoveAt)) {
+        if (__any_sync(kFull, live && topv > u + kMoveAt)) {   // (see follow_maximum)
             const float to = fmaxf(u, topv);
             rescale<D>(tO, to == -INFINITY ? 1.0f : ex2(u - to));
             u = to;
@@ -951,9 +945,9 @@ __device__ __forceinline__ void softmax_block_q8(uint32_t tS, uint32_t tO, float
     }
     const float ref = m == -INFINITY ? 0.0f : -m, move = u == -INFINITY ? 0.0f : -ref - u;
     const uint64_t ref2 = pack2(ref, ref);
-    // 2^move in three steps, as it may be out of range where the scales are far from 1.  (Beyond 2^378 a scale is 0, or all
-    // weights are that meet it: least scale 2^-149, least weight 2^-126, products up to 2^14.)
-    const float by = ex2(fminf(move, 378.0f) * (1.0f / 3));
+    // 2^move in two steps, as it may be out of range where the scales are far from 1; beyond 2^252 no product makes a
+    // difference in the output, which is at most 2^(23 - move)
+    const float by = ex2(fminf(0.5f * move, 126.0f));
     uint64_t sum[2] = {0, 0};
 #pragma unroll 1
     for (int k = 0; k < 128; k += 32) {

@@ -103,6 +103,23 @@ def test_values_of_scale_zero_or_far_apart(lens, new):
     p.run().check()
 
 
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_scales_of_v_that_are_not_finite(value):
+    """8-bit: who sees a token of the scale's block answers no number, whatever the codes; the logarithm is K's alone."""
+    p = Problem([200, 0, 9000], [90, 300, 4], q8=True, scales="amax").run()
+    was = p.out.clone(), p.lse.clone()
+    odd = torch.zeros_like(p.out, dtype=torch.bool)
+    p.vs[int(p.table[0, 256 // 16]), 0, 1] = value    # tokens 256 to 271 of the first row, the second KV head
+    odd[56:90, 4:] = True
+    p.vs[int(p.table[2, 7]), 0, 0] = value            # seen by all of the third row's new tokens, in whole blocks
+    odd[390:394, :4] = True
+    p.v.view(torch.uint8)[int(p.table[2, 7])] = 0
+    p.run()
+    assert torch.equal(~p.out.isfinite(), odd)
+    assert torch.equal(p.out[:390][~odd[:390]], was[0][:390][~odd[:390]]) and torch.equal(p.lse, was[1])
+    p.check(rows=[1])
+
+
 @BOTH
 @pytest.mark.parametrize("new", [3, 35])
 def test_a_row_does_not_depend_on_the_next_rows_queries(new, q8):
