@@ -87,6 +87,7 @@ struct Ctl {
     uint64_t key_full[8], key_empty[8];            // blocks of K in e4m3
     uint64_t code_full[4], code_empty[4];          // ... of V
     uint64_t q_split[2];                           // the groups' queries in two e4m3 parts
+    uint64_t q_read[2];                            // (D = 64) all of a group's queries are in registers
     uint64_t scale_full[9];
     uint64_t q_full, q_empty, drain;
     uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], pair_full, turn[2];
@@ -675,10 +676,10 @@ __device__ __forceinline__ void widen(const ExtendParams& p, Ctl* c, uint8_t* sm
 // 2^-2 on: those down to 2^-9 of the largest are exact, those below off by at most
 // half a step, 2^-17 of the largest.  Two e4m3 products cost what one of bf16 does, and
 // the cache's keys go into them untouched; widening K as well as V is twice the work for
-// warps that a block waits for already.  Returns what the scores are to be multiplied
-// by; NaN if an element is not finite.
-template <int D>
-__device__ __forceinline__ float split_query(uint32_t at, int row, int barrier) {
+// warps that a block waits for already.  `scale` is what the scores are to be multiplied
+// by; NaN if an element is not finite.  False: a wait ran out.
+template <int D, class Read>
+__device__ __forceinline__ bool split_query(uint32_t at, int row, float& scale, const Read& all_read) {
     uint32_t q[D / 2];   // pairs
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
@@ -692,7 +693,7 @@ __device__ __forceinline__ float split_query(uint32_t at, int row, int barrier) 
     for (int i = 0; i < D / 2; ++i) most = max(most, max(q[i] & 0x7fff0000u, q[i] << 16 & 0x7fff0000u));
     const uint32_t e = max(most >> 23, 8u);   // exponent of the largest
     const float by = __uint_as_float((261 - e) << 23);
-    if (D == 64) named_barrier_sync(barrier, 128);   // rows of 64 bytes lie in other rows' places
+    if (D == 64 && !all_read()) return false;   // rows of 64 bytes lie in other rows' places
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
         uint32_t hi[4], lo[4];
@@ -715,7 +716,8 @@ __device__ __forceinline__ float split_query(uint32_t at, int row, int barrier) 
         sts128(to, hi[0], hi[1], hi[2], hi[3]);
         sts128(to + 128 * D, lo[0], lo[1], lo[2], lo[3]);
     }
-    return most >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __uint_as_float((e - 7) << 23);
+    scale = most >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __uint_as_float((e - 7) << 23);
+    return true;
 }
 
 // ------------------------------------------------------------------ softmax and outputs
@@ -981,7 +983,7 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
     const int shift = 31 - __clz(p.G), per = kExtRows / 2 >> shift;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
     const uint32_t tS = c->tmem + lanes + g * 128, tO = c->tmem + lanes + 256 + g * 128;
-    uint32_t done = 0, outs = 0, blocks = 0, pairs = 0, q_loads = 0;
+    uint32_t done = 0, outs = 0, blocks = 0, pairs = 0, q_loads = 0, splits = 0;
     if (!wait_warp(&c->piece_full[0], 0, &c->abort)) return false;
     Piece next = c->piece[0];   // (read ahead: shared memory is slow beside the products' operands)
     for (uint32_t pc = 0;; ++pc) {
@@ -1007,7 +1009,14 @@ __device__ __forceinline__ bool attend(const ExtendParams& p, Ctl* c, uint8_t* s
                 cs *= c->pair_ml[row].x;
             } else if (pi.ntok > g * per) {
                 if (D == 64 || warp_live) {
-                    const float scale = split_query<D>(smem_addr(smem) + g * (C::kQ / 2), row, 1 + g);
+                    // (a barrier of the hardware has no limit: warps that give up would leave the others there)
+                    auto all_read = [&] {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&c->q_read[g]);
+                        return wait_warp(&c->q_read[g], splits++ & 1, &c->abort);
+                    };
+                    float scale;
+                    if (!split_query<D>(smem_addr(smem) + g * (C::kQ / 2), row, scale, all_read)) return false;
                     if (sh.pair) c->pair_ml[row].x = scale;
                     cs *= scale;
                 }
@@ -1204,6 +1213,7 @@ extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CU
             mbar_init(&c->o_empty[g], 4);
             mbar_init(&c->turn[g], 1);
             mbar_init(&c->q_split[g], 4);
+            mbar_init(&c->q_read[g], 4);
         }
         for (int i = 0; i < kPieceRing; ++i) {
             mbar_init(&c->piece_full[i], 1);

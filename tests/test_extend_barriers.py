@@ -147,3 +147,12 @@ def test_the_second_group_never_falls_two_queries_behind(slow):
             x.pending, x.phase = x.arrivals, 0
         play({"loads": loads(), **{f"product {g}": product(g) for g in range(2)}, **{f"softmax {w}": softmax(w // 4) for w in range(8)}},
              random.Random(seed), slow)
+
+
+def test_the_warps_roles_have_no_wait_without_a_limit():
+    """A wait that runs out makes every warp return; one in a barrier of the hardware (bar.sync), which the warps that have
+    returned never reach, would stay there for ever."""
+    assert not re.search(r"named_barrier_sync|bar\.sync|barrier\.sync|barrier\.cta", source())
+    assert source().count("mbar_try_wait(") == 1 and "mbar_try_wait(" in body("wait_for")
+    for role in ("load", "load_values", "clean", "widen", "multiply", "split_query", "attend"):
+        assert "__syncthreads" not in body(role), role
