@@ -421,7 +421,9 @@ int pkv_extend_reserve(pkv_plan_t plan);
  * the page size, the status word and the reserved memory only, and may be stale;
  * a captured call may be replayed with other lengths and offsets.  Calls with
  * one plan share its memory and have to be ordered on the GPU, as decodes have;
- * they may overlap its decodes and appends.  Two kernels on `stream`.
+ * they may overlap its decodes and appends.  Two kernels on `stream`.  A CTA takes
+ * nearly all of an SM's shared memory, so a call enqueued while a resident kernel
+ * runs (pkv_resident_start) begins when that kernel yields or stops.
  *
  * Products have fp32 sums and bf16 factors; 8-bit codes are exact, and a query
  * meets them in two e4m3 parts, exact for elements down to 2^-9 of its largest and
@@ -434,8 +436,8 @@ int pkv_extend_reserve(pkv_plan_t plan);
  * of all sums is fixed by the lengths, so a repeated call gives the same bits.  A query whose scores are all -inf has
  * output 0 and lse -inf; one with a NaN element is NaN (in the 8-bit cache one with
  * an infinite element too).  Slots behind a row's last token may hold anything.  An
- * infinity or NaN in a token's V, or a V scale, reaches the queries that see the
- * token (of the scale's block) and no others.  Tokens of q that belong to no row, and
+ * infinity or NaN in a token's V, or a V scale (as NaN), reaches the queries that see
+ * the token (of the scale's block) and no others.  Tokens of q that belong to no row, and
  * their outputs, are left as they are.
  *
  * A row whose n_b exceeds seq_lens_d[b], or whose length exceeds its table, sets
@@ -466,7 +468,8 @@ int pkv_extend_q8(const pkv_queries *queries, const void *k_pages, const void *v
  * are on the current device, and no two of them overlap.
  * Errors: PKV_EINVAL (a page outside [0, num_pages), tokens outside [0,
  * page_size], a target twice or also a source, a null pointer, a pool whose sizes
- * or address are no multiples of 4 bytes or whose units do not divide the page),
+ * or address are no multiples of 4 bytes, whose units do not divide the page or whose
+ * page is larger than 2^24 bytes),
  * PKV_ENOMEM, PKV_ECUDA.  Nothing is enqueued on PKV_EINVAL.
  */
 typedef struct {

@@ -11,7 +11,8 @@
 // 1237 pages of 64 tokens in 8 layers of an 8-bit cache (2.6 GB moved) take 398 us, 6.5
 // TB/s; by the line, with less in flight, 428.  64 tails in 64 pools take 25 us on the GPU,
 // most of it the launch's parameter and one round of loads and stores; the call on the
-// host, which checks and writes the lists, 38-44.
+// host, which checks and writes the lists, 38-44 (from 33 copies on it marks pages
+// in an array of a byte for each page of the pool, so the pool's size counts too).
 #include "pkv_device.cuh"
 
 namespace pkv {

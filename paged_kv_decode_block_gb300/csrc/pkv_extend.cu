@@ -23,17 +23,17 @@
 // of scores, so above about 280 rows (140) that read the same tokens it is the tensor
 // core, 2048 cycles a block at D = 128, and below them HBM.  Measured, 32 query and 8
 // KV heads, D = 128, bf16:
-//   2048 tokens after 30720          703-779 us   1.37-1.51 PFLOP/s, about 3000 cycles a
+//   2048 tokens after 30720          703-783 us   1.37-1.51 PFLOP/s, about 3000 cycles a
 //                                                 block: the gap between one group's products
 //                                                 and the other's, and the boxes of 16 tokens
-//   8 prompts of 128-4096            215 us       0.93 PFLOP/s: a tile of few blocks costs 17
+//   8 prompts of 128-4096            216 us       0.93 PFLOP/s: a tile of few blocks costs 17
 //                                                 thousand cycles besides (its masked blocks,
 //                                                 outputs, code that is not in the cache)
 //   5 tokens each after 512-32768    55 us        4.6 TB/s: 6 us until the stream runs, 6 us
 //                                                 to join the parts
 // and e4m3:
-//   4 tokens each, 56 rows of 1024-8192   214 us  softmax and widening, a warp's latencies
-//   8 rows, chunks of 512                 411 us  the same: 0.88 PFLOP/s
+//   4 tokens each, 56 rows of 1024-8192   216 us  softmax and widening, a warp's latencies
+//   8 rows, chunks of 512                 419 us  the same: 0.87 PFLOP/s
 #include "pkv_extend_schedule.h"
 #include "pkv_tcgen05.cuh"
 
